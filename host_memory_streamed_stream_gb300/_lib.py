@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(_HERE, "libmt.so")
 
 c_int, c_i32, c_i64, c_u32, c_u64, c_f32, c_vp = (ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                                                   ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p)
+c_f64 = ctypes.c_double
 P = ctypes.POINTER
 
 
@@ -106,6 +107,15 @@ SIGNATURES = {
     "mtk_rmsnorm_bwd": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_int, c_vp]),
     "mtk_rmsnorm_bwd_noalloc": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_int, c_vp]),
     "mtk_rope": (c_int, [c_vp, c_i64, c_int, c_int, c_int, c_int, c_int, c_vp, c_int, c_vp]),
+    "mtk_rotary_inv_freq": (c_int, [c_int, c_f64, c_int, c_f64, c_f64, c_f64, c_f64, c_vp]),
+    "mtk_rotary_table": (c_int, [c_vp, c_int, c_int, c_f64, c_vp, c_vp]),
+    "mtk_rotary": (c_int, [c_vp, c_i64, c_vp, c_i64, c_int, c_int, c_int, c_int, c_int, c_vp, c_vp, c_int, c_int, c_vp,
+                           c_vp]),
+    "mtk_qk_norm_rope": (c_int, [c_vp, c_i64, c_vp, c_vp, c_vp, c_i64, c_vp, c_int, c_int, c_int, c_int, c_int, c_int,
+                                 c_f32, c_vp, c_vp, c_int, c_vp, c_vp]),
+    "mtk_qk_norm_rope_bwd_parts": (c_int, [c_int, c_int, c_int, c_int]),
+    "mtk_qk_norm_rope_bwd": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_int,
+                                     c_int, c_int, c_int, c_int, c_int, c_vp, c_vp, c_int, c_vp, c_vp]),
     "mtk_swiglu_fwd": (c_int, [c_vp, c_vp, c_int, c_int, c_vp]),
     "mtk_swiglu_bwd": (c_int, [c_vp, c_vp, c_vp, c_int, c_int, c_vp]),
     "mtk_embed_fwd": (c_int, [c_vp, c_vp, c_vp, c_int, c_int, c_vp]),

@@ -144,6 +144,56 @@ int mtk_rope(void* qkv, int64_t ld, int T, int seq, int n_heads, int n_kv_heads,
                      static_cast<const float*>(cos_sin), inverse != 0, S(stream)));
 }
 
+int mtk_rotary_inv_freq(int rot_dim, double theta, int scaling, double factor, double original_positions, double low,
+                        double high, double* inv_freq) {
+  return mt::rotary_inv_freq(rot_dim, theta, scaling, factor, original_positions, low, high, inv_freq) ? MT_OK
+                                                                                                       : MT_EINVAL;
+}
+
+int mtk_rotary_table(const double* inv_freq, int rot_dim, int n_pos, double amplitude, void* cos_sin, void* stream) {
+  if (!inv_freq || !cos_sin) return MT_EINVAL;
+  return rc(mt::rotary_table(inv_freq, rot_dim, n_pos, amplitude, static_cast<float*>(cos_sin), S(stream)));
+}
+
+int mtk_rotary(const void* x, int64_t ldx, void* y, int64_t ldy, int T, int heads, int head_dim, int rot_dim,
+               int interleaved, const void* positions, const void* cos_sin, int n_pos, int inverse, int* err_flag,
+               void* stream) {
+  if (!x || !y) return MT_EINVAL;
+  return rc(mt::rotary(static_cast<const bf16*>(x), ldx, static_cast<bf16*>(y), ldy, T, heads, head_dim, rot_dim,
+                       interleaved != 0, static_cast<const int32_t*>(positions), static_cast<const float*>(cos_sin),
+                       n_pos, inverse != 0, err_flag, S(stream)));
+}
+
+int mtk_qk_norm_rope(const void* x, int64_t ldx, const void* gq, const void* gk, void* y, int64_t ldy, void* rstd,
+                     int T, int n_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved, float eps,
+                     const void* positions, const void* cos_sin, int n_pos, int* err_flag, void* stream) {
+  if (!x || !gq || !gk || !y || !(eps >= 0.f)) return MT_EINVAL;
+  return rc(mt::qk_norm_rope(static_cast<const bf16*>(x), ldx, static_cast<const bf16*>(gq),
+                             static_cast<const bf16*>(gk), static_cast<bf16*>(y), ldy, static_cast<float*>(rstd), T,
+                             n_heads, n_kv_heads, head_dim, rot_dim, interleaved != 0, eps,
+                             static_cast<const int32_t*>(positions), static_cast<const float*>(cos_sin), n_pos,
+                             err_flag, S(stream)));
+}
+
+int mtk_qk_norm_rope_bwd_parts(int T, int n_heads, int n_kv_heads, int head_dim) {
+  if (T <= 0 || n_heads <= 0 || n_kv_heads <= 0 || (head_dim != 64 && head_dim != 128)) return 0;
+  return mt::qk_norm_rope_bwd_parts(T, n_heads, n_kv_heads, head_dim);
+}
+
+int mtk_qk_norm_rope_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* gq, const void* gk,
+                         const void* rstd, void* dx, int64_t lddx, void* partial, void* dgq, void* dgk, int T,
+                         int n_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved,
+                         const void* positions, const void* cos_sin, int n_pos, int* err_flag, void* stream) {
+  if (!dy || !x || !gq || !gk || !rstd || !dx || !partial || !dgq || !dgk) return MT_EINVAL;
+  return rc(mt::qk_norm_rope_bwd(static_cast<const bf16*>(dy), lddy, static_cast<const bf16*>(x), ldx,
+                                 static_cast<const bf16*>(gq), static_cast<const bf16*>(gk),
+                                 static_cast<const float*>(rstd), static_cast<bf16*>(dx), lddx,
+                                 static_cast<float*>(partial), static_cast<bf16*>(dgq), static_cast<bf16*>(dgk), T,
+                                 n_heads, n_kv_heads, head_dim, rot_dim, interleaved != 0,
+                                 static_cast<const int32_t*>(positions), static_cast<const float*>(cos_sin), n_pos,
+                                 err_flag, S(stream)));
+}
+
 int mtk_swiglu_fwd(const void* gu, void* act, int T, int f, void* stream) {
   if (!gu || !act || T <= 0 || f <= 0) return MT_EINVAL;
   return rc(mt::swiglu_fwd(static_cast<const bf16*>(gu), static_cast<bf16*>(act), T, f, S(stream)));

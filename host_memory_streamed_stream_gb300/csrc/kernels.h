@@ -110,6 +110,33 @@ cudaError_t cross_entropy(const float* logits, const int32_t* labels, bf16* dlog
 cudaError_t mean_reduce(const float* v, int n, float* out, cudaStream_t s);
 cudaError_t cast_f32_bf16(const float* x, bf16* y, int64_t n, cudaStream_t s);
 
+// ------------------------------------------------------------------ rotary positions, query/key norms
+// rot/2 scaled frequencies into a host array (rules and checks: mtk_rotary_inv_freq); false if refused.
+bool rotary_inv_freq(int rot, double theta, int scaling, double factor, double original, double low, double high,
+                     double* inv_freq);
+// Table fp32 [n_pos][rot/2][2] = amp * (cos, sin)(p * inv_freq[i]); inv_freq is a HOST array of
+// rot/2 finite radians per position (read before the call returns).
+constexpr int kRotaryMaxPairs = 128;
+cudaError_t rotary_table(const double* inv_freq, int rot, int n_pos, double amp, float* out, cudaStream_t s);
+// y = x with the first `rot` columns of each head rotated (pairs (2i, 2i+1) if interleaved, else
+// (i, i + rot/2)) at position positions[t], or t % n_pos without positions; inverse = the transpose.
+// y may be x. hd and rot multiples of 16.
+cudaError_t rotary(const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int T, int heads, int hd, int rot,
+                   bool interleaved, const int32_t* positions, const float* cs, int n_pos, bool inverse, int* err,
+                   cudaStream_t s);
+// RMSNorm of every query and key head (nh + nkv heads of hd columns, gains gq, gk [hd]), then the
+// rotation (rot = 0: none); rstd fp32 [T, nh + nkv] may be null. y may be x. hd 64 or 128.
+cudaError_t qk_norm_rope(const bf16* x, int64_t ldx, const bf16* gq, const bf16* gk, bf16* y, int64_t ldy, float* rstd,
+                         int T, int nh, int nkv, int hd, int rot, bool interleaved, float eps,
+                         const int32_t* positions, const float* cs, int n_pos, int* err, cudaStream_t s);
+// Its backward: dx (may be dy or x) and the gain gradients, through `partial` fp32 [parts][2][hd].
+constexpr int kQkNormParts = 608;
+int qk_norm_rope_bwd_parts(int T, int nh, int nkv, int hd);
+cudaError_t qk_norm_rope_bwd(const bf16* dy, int64_t lddy, const bf16* x, int64_t ldx, const bf16* gq, const bf16* gk,
+                             const float* rstd, bf16* dx, int64_t lddx, float* partial, bf16* dgq, bf16* dgk, int T,
+                             int nh, int nkv, int hd, int rot, bool interleaved, const int32_t* positions,
+                             const float* cs, int n_pos, int* err, cudaStream_t s);
+
 // ------------------------------------------------------------------ attention
 // Causal grouped-query flash attention over qkv [B*s, (nh + 2 nkv) hd] (q | k | v columns,
 // RoPE already applied). o bf16 [B*s, nh*hd]; lse fp32 [B, nh, s] in base-2 units of the

@@ -16,6 +16,7 @@ constexpr int kErrTimeoutAccFree = 4;    // MMA issuer waited too long for a dra
 constexpr int kErrTimeoutAttn = 5;       // an attention pipeline wait gave up
 constexpr int kErrTimeoutProbe = 6;      // the wait-expiry self-check gave up (as it is meant to)
 constexpr int kErrTimeoutSplit = 7;      // a GEMM tile's owner waited too long for a partial sum
+constexpr int kErrBadPosition = 8;       // a token's position lies outside the rotation table
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;  // 4 s: far above any legal wait
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {

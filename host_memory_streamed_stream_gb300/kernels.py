@@ -5,11 +5,13 @@ to one C entry point and raises on a nonzero status.
 """
 from __future__ import annotations
 
+import numpy as np
 import torch
 
 from . import MTError, _lib
 
 EPI_STORE_BF16, EPI_STORE_F32, EPI_ADD_F32 = 0, 1, 2
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 
 
 def _p(t):
@@ -111,6 +113,117 @@ def rope_(qkv, seq, n_heads, n_kv_heads, head_dim, cos_sin, inverse=False):
     _ok(_lib.load().mtk_rope(qkv.data_ptr(), qkv.stride(0), T, seq, n_heads, n_kv_heads, head_dim, cos_sin.data_ptr(),
                              int(inverse), _s()), "rope")
     return qkv
+
+
+# The calls below take views of larger buffers, so the types, shapes and strides that the C entry
+# cannot see are checked here (MTError with MT_EINVAL, like the entry's own refusals).
+def _need(ok, what):
+    if not ok:
+        raise MTError(-1, what)
+
+
+def _rows(t, n, cols, what):
+    """Row stride of a bf16 [n, >= cols] view on the current device with unit column stride."""
+    _need(t.dtype is torch.bfloat16 and t.dim() == 2 and t.shape[0] == n and t.shape[1] >= cols
+          and (t.stride(1) == 1 or t.shape[1] == 1) and t.is_cuda and t.get_device() == torch.cuda.current_device(),
+          f"{what}: a bf16 [{n}, >= {cols}] tensor with unit column stride on the current device")
+    return t.stride(0) if n > 1 else (cols + 7) // 8 * 8
+
+
+def _vec(t, n, dtype, like, what):
+    _need(t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.device == like.device,
+          f"{what}: a contiguous {dtype} tensor of {n} elements on {like.device}")
+    return t.data_ptr()
+
+
+def _table(cos_sin, like):
+    """(pointer, positions, rotated columns) of a rotation table; no table: no rotation."""
+    if cos_sin is None:
+        return None, 0, 0
+    _need(cos_sin.dim() == 3 and cos_sin.shape[2] == 2, "cos_sin: [n_pos, rot_dim/2, 2]")
+    return _vec(cos_sin, cos_sin.numel(), torch.float32, like, "cos_sin"), cos_sin.shape[0], 2 * cos_sin.shape[1]
+
+
+def rotary_inv_freq(rot_dim, theta=10000.0, scaling="plain", factor=1.0, original_positions=0, low=1.0, high=32.0):
+    """rot_dim/2 rotation frequencies (numpy float64, radians per position); see mtk_rotary_inv_freq
+    for the scalings "plain", "linear", "base" and "bands"."""
+    _need(scaling in ROTARY_SCALINGS, f"scaling: one of {sorted(ROTARY_SCALINGS)}")
+    out = np.empty(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    _ok(_lib.load().mtk_rotary_inv_freq(rot_dim, theta, ROTARY_SCALINGS[scaling], factor, original_positions, low, high,
+                                        out.ctypes.data), "rotary_inv_freq")
+    return out
+
+
+def rotary_table(inv_freq, n_pos, amplitude=1.0, out=None):
+    """fp32 [n_pos, rot_dim/2, 2] = amplitude * (cos, sin) of p * inv_freq[i] on the current device."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    _need(f.ndim == 1, "inv_freq: one frequency for each pair")
+    if out is None:
+        out = torch.empty(n_pos, f.size, 2, dtype=torch.float32, device="cuda")
+    _need(out.dtype is torch.float32 and out.is_cuda and out.is_contiguous() and tuple(out.shape) == (n_pos, f.size, 2),
+          "out: a contiguous fp32 [n_pos, rot_dim/2, 2] tensor")
+    _ok(_lib.load().mtk_rotary_table(f.ctypes.data, 2 * f.size, n_pos, amplitude, out.data_ptr(), _s()),
+        "rotary_table")
+    return out
+
+
+def rotary(x, heads, head_dim, cos_sin, positions=None, interleaved=False, inverse=False, out=None, err=None):
+    """x [T, heads*head_dim] with the first rot_dim (the table's) columns of every head rotated at
+    `positions` (int32 [T]; None: t % n_pos). out: a new tensor, another one, or x itself (in place)."""
+    T, cols = x.shape[0], heads * head_dim
+    ldx = _rows(x, T, cols, "x")
+    tab, n_pos, rot = _table(cos_sin, x)
+    if out is None:
+        out = torch.empty(T, cols, dtype=torch.bfloat16, device=x.device)
+    pos = None if positions is None else _vec(positions, T, torch.int32, x, "positions")
+    err = _err(err, x.device)
+    _ok(_lib.load().mtk_rotary(x.data_ptr(), ldx, out.data_ptr(), _rows(out, T, cols, "out"), T, heads, head_dim, rot,
+                               interleaved, pos, tab, n_pos, inverse, err.data_ptr(), _s()), "rotary")
+    return out
+
+
+def qk_norm_rope(x, gq, gk, n_heads, n_kv_heads, head_dim, cos_sin=None, positions=None, interleaved=False, eps=1e-5,
+                 out=None, err=None):
+    """RMSNorm of each query and key head of x [T, >= (nh+nkv)*hd] and the rotation (cos_sin None:
+    none): (y [T, (nh+nkv)*hd], rstd f32 [T, nh+nkv]). out: as for rotary."""
+    T, heads = x.shape[0], n_heads + n_kv_heads
+    cols = heads * head_dim
+    ldx = _rows(x, T, cols, "x")
+    tab, n_pos, rot = _table(cos_sin, x)
+    if out is None:
+        out = torch.empty(T, cols, dtype=torch.bfloat16, device=x.device)
+    rstd = torch.empty(T, heads, dtype=torch.float32, device=x.device)
+    pos = None if positions is None else _vec(positions, T, torch.int32, x, "positions")
+    err = _err(err, x.device)
+    _ok(_lib.load().mtk_qk_norm_rope(x.data_ptr(), ldx, _vec(gq, head_dim, torch.bfloat16, x, "gq"),
+                                     _vec(gk, head_dim, torch.bfloat16, x, "gk"), out.data_ptr(),
+                                     _rows(out, T, cols, "out"), rstd.data_ptr(), T, n_heads, n_kv_heads, head_dim, rot,
+                                     interleaved, eps, pos, tab, n_pos, err.data_ptr(), _s()), "qk_norm_rope")
+    return out, rstd
+
+
+def qk_norm_rope_bwd(dy, x, gq, gk, rstd, n_heads, n_kv_heads, head_dim, cos_sin=None, positions=None,
+                     interleaved=False, out=None, err=None):
+    """(dx [T, (nh+nkv)*hd], dgq, dgk) of qk_norm_rope; out: a new tensor for dx, another one, dy or x."""
+    T, heads = x.shape[0], n_heads + n_kv_heads
+    cols = heads * head_dim
+    ldx, lddy = _rows(x, T, cols, "x"), _rows(dy, T, cols, "dy")
+    tab, n_pos, rot = _table(cos_sin, x)
+    if out is None:
+        out = torch.empty(T, cols, dtype=torch.bfloat16, device=x.device)
+    lib = _lib.load()
+    parts = lib.mtk_qk_norm_rope_bwd_parts(T, n_heads, n_kv_heads, head_dim)
+    partial = torch.empty(parts, 2, head_dim, dtype=torch.float32, device=x.device)
+    dg = torch.empty(2, head_dim, dtype=torch.bfloat16, device=x.device)
+    pos = None if positions is None else _vec(positions, T, torch.int32, x, "positions")
+    err = _err(err, x.device)
+    _ok(lib.mtk_qk_norm_rope_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, _vec(gq, head_dim, torch.bfloat16, x, "gq"),
+                                 _vec(gk, head_dim, torch.bfloat16, x, "gk"),
+                                 _vec(rstd, T * heads, torch.float32, x, "rstd"), out.data_ptr(),
+                                 _rows(out, T, cols, "out"), partial.data_ptr(), dg[0].data_ptr(), dg[1].data_ptr(), T,
+                                 n_heads, n_kv_heads, head_dim, rot, interleaved, pos, tab, n_pos, err.data_ptr(),
+                                 _s()), "qk_norm_rope_bwd")
+    return out, dg[0], dg[1]
 
 
 def swiglu_fwd(gu, f):

@@ -110,6 +110,68 @@ int mtk_rmsnorm_bwd_noalloc(const void* dy, const void* x, const void* gamma, co
 int mtk_rope(void* qkv, int64_t ld, int T, int seq, int n_heads, int n_kv_heads, int head_dim, const void* cos_sin,
              int inverse, void* stream);
 
+/*
+ * Rotary positions in general: scaled frequencies, explicit positions (packed documents), part of
+ * the head, both pair layouts. (The pages name no model; mtk_rope is the layer template's form.)
+ *
+ * mtk_rotary_inv_freq: the frequencies f_i = theta^(-2i/rot_dim), i < rot_dim/2, in radians per
+ *   position, scaled for contexts `factor` times longer than the model was trained on. Host only
+ *   and pure: inv_freq is a HOST array of rot_dim/2 doubles.
+ *     MTK_ROTARY_PLAIN   f_i
+ *     MTK_ROTARY_LINEAR  f_i / factor (positions interpolated)
+ *     MTK_ROTARY_BASE    the base theta * factor^(rot_dim/(rot_dim-2)) instead of theta (the lowest
+ *                        frequency divided by factor, the highest kept); rot_dim > 2
+ *     MTK_ROTARY_BANDS   f_i (w + (1-w)/factor), w = (n_i - low)/(high - low) clamped to [0,1],
+ *                        n_i = original_positions * f_i / (2 pi) the turns over the trained
+ *                        context: high frequencies kept, low ones interpolated, a ramp between
+ *   MT_EINVAL unless rot_dim is even, 2..256, theta > 0 and, where they are used, factor > 0,
+ *   original_positions > 0 and high > low, all finite.
+ * mtk_rotary_table: cos_sin f32 [n_pos][rot_dim/2][2] = amplitude * (cos, sin)(p * inv_freq[i]) for
+ *   positions p = 0 .. n_pos-1. inv_freq is a HOST array, read before the call returns. Angles are
+ *   kept modulo whole turns in 64-bit fixed point, so far positions lose nothing.
+ * mtk_rotary: y bf16 [T, heads*head_dim] (row stride ldy) = x (row stride ldx) with the first
+ *   rot_dim columns of every head rotated: a' = a cos - b sin, b' = b cos + a sin on the pairs
+ *   (i, i + rot_dim/2), or (2i, 2i+1) if interleaved; inverse = 1 applies the transpose (the
+ *   backward pass). Token t is at positions[t] (int32 [T]), or at t % n_pos if positions is NULL.
+ *   y may be x (then ldy = ldx), else they must not overlap. head_dim and rot_dim are multiples
+ *   of 16, rot_dim <= head_dim <= 4096. A position outside [0, n_pos) sets *err_flag to 8 and
+ *   leaves that token unrotated. err_flag: device int, required.
+ */
+#define MTK_ROTARY_PLAIN 0
+#define MTK_ROTARY_LINEAR 1
+#define MTK_ROTARY_BASE 2
+#define MTK_ROTARY_BANDS 3
+int mtk_rotary_inv_freq(int rot_dim, double theta, int scaling, double factor, double original_positions, double low,
+                        double high, double* inv_freq);
+int mtk_rotary_table(const double* inv_freq, int rot_dim, int n_pos, double amplitude, void* cos_sin, void* stream);
+int mtk_rotary(const void* x, int64_t ldx, void* y, int64_t ldy, int T, int heads, int head_dim, int rot_dim,
+               int interleaved, const void* positions, const void* cos_sin, int n_pos, int inverse, int* err_flag,
+               void* stream);
+
+/*
+ * RMSNorm of each query and key head with the rotation in the same pass: for every token and head
+ * row x_h (head_dim columns) of the first n_heads + n_kv_heads heads of x,
+ *   rstd = 1/sqrt(mean(x_h^2) + eps),  y_h = R(x_h * rstd * g),  g = gq for query heads, gk for keys,
+ * with the rotation R of mtk_rotary (rot_dim = 0: no rotation; cos_sin, positions and err_flag may
+ * then be NULL). x, y bf16 with row strides ldx, ldy (columns past the key heads, such as v, are
+ * neither read nor written); gq, gk bf16 [head_dim]; rstd f32 [T][n_heads + n_kv_heads], or NULL.
+ * y may be x (then ldy = ldx). head_dim 64 or 128, rot_dim a multiple of 16.
+ *
+ * mtk_qk_norm_rope_bwd: from dy (row stride lddy), the forward's x and its rstd, with u = R^T dy and
+ * n = x_h * rstd: dx_h = rstd (u g - n mean(u g n)), dgq and dgk bf16 [head_dim] = the sums of u n
+ * over tokens and query (key) heads, added in a fixed order through `partial`, f32
+ * [mtk_qk_norm_rope_bwd_parts(...)][2][head_dim]. dx may be dy or x (with the same row stride). A
+ * bad position counts as no rotation, with *err_flag set to 8.
+ */
+int mtk_qk_norm_rope(const void* x, int64_t ldx, const void* gq, const void* gk, void* y, int64_t ldy, void* rstd,
+                     int T, int n_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved, float eps,
+                     const void* positions, const void* cos_sin, int n_pos, int* err_flag, void* stream);
+int mtk_qk_norm_rope_bwd_parts(int T, int n_heads, int n_kv_heads, int head_dim);
+int mtk_qk_norm_rope_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* gq, const void* gk,
+                         const void* rstd, void* dx, int64_t lddx, void* partial, void* dgq, void* dgk, int T,
+                         int n_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved,
+                         const void* positions, const void* cos_sin, int n_pos, int* err_flag, void* stream);
+
 /* SwiGLU on gu bf16 [T, 2f] = [g | u]: act bf16 [T,f] = silu(g)*u; backward dgu bf16 [T,2f]. */
 int mtk_swiglu_fwd(const void* gu, void* act, int T, int f, void* stream);
 int mtk_swiglu_bwd(const void* gu, const void* dact, void* dgu, int T, int f, void* stream);
