@@ -1,0 +1,129 @@
+// What the forward and backward of attention over spans share: the span of keys each query row
+// sees, its summary over a tile of rows, and the score's cap and distance bias.
+//
+// Query i sees the keys lo_i <= j < hi_i. Causal, document, prefix and two-sided masks are all of
+// this form, a tile's key range follows from its rows' smallest lo and largest hi, and a score's
+// visibility is two comparisons, so no mask is ever read or stored per pair.
+#pragma once
+#include <climits>
+#include <cstdint>
+#include <type_traits>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace mt {
+namespace span {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Spans {
+  const int32_t* lo;  // [B*s] or null: 0
+  const int32_t* hi;  // [B*s] or null: i + 1
+};
+
+// The span of row i of sequence b, clamped to the sequence; an empty one is (0, 0).
+__device__ __forceinline__ int2 load_span(const Spans& sp, int b, int i, int s) {
+  const int64_t at = static_cast<int64_t>(b) * s + i;
+  const int lo = sp.lo ? max(__ldg(sp.lo + at), 0) : 0;
+  const int hi = sp.hi ? min(__ldg(sp.hi + at), s) : i + 1;
+  return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// Summary of a tile of rows: the keys some row sees lie in [min_lo, max_hi); every row sees the
+// keys [max_lo, min_hi) (an empty row makes that range empty).
+struct Hull {
+  int min_lo, max_hi, max_lo, min_hi;
+};
+// What one row adds to it; a row past the end of the sequence (live = false) adds nothing.
+__device__ __forceinline__ Hull row_hull(int2 r, bool live) {
+  if (!live) return {INT_MAX, 0, 0, INT_MAX};
+  if (r.x >= r.y) return {INT_MAX, 0, INT_MAX, 0};
+  return {r.x, r.y, r.x, r.y};
+}
+__device__ __forceinline__ Hull warp_hull(Hull h) {
+  return {__reduce_min_sync(0xffffffffu, h.min_lo), __reduce_max_sync(0xffffffffu, h.max_hi),
+          __reduce_max_sync(0xffffffffu, h.max_lo), __reduce_min_sync(0xffffffffu, h.min_hi)};
+}
+__device__ __forceinline__ Hull join(const Hull& a, const Hull& b) {
+  return {min(a.min_lo, b.min_lo), max(a.max_hi, b.max_hi), max(a.max_lo, b.max_lo), min(a.min_hi, b.min_hi)};
+}
+// Whether all rows see all keys [k0, k1).
+__device__ __forceinline__ bool sees_all(const Hull& h, int k0, int k1) { return h.max_lo <= k0 && k1 <= h.min_hi; }
+
+// Bits [0, n) of a word, n clamped to 0..32.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// Bits of [lo, hi) relative to base.
+__device__ __forceinline__ uint32_t span_bits(int2 r, int base) { return bits_below(r.y - base) & ~bits_below(r.x - base); }
+
+// 32x32 bit transpose over the warp: bit c of lane r becomes bit r of lane c (five exchanges of
+// halves of shrinking blocks).
+__device__ __forceinline__ uint32_t warp_transpose(uint32_t x, int lane) {
+  uint32_t m = 0x0000ffffu;
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = (lane & j) ? ((x & ~m) | ((y & ~m) >> j)) : ((x & m) | ((y & m) << j));
+    m ^= m << (j >> 1);
+  }
+  return x;
+}
+
+__device__ __forceinline__ float ex2(float x) {  // hardware 2^x (ex2.approx, flush to zero)
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {  // hardware 1/x (1/inf = 0)
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {  // three-input max (sm_100+)
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Scores in log2 units from the raw products x = q.k. Plain: scale log2(e) x. Capped:
+// c log2(e) tanh(scale x / c), with tanh(y) = 1 - 2 r, r = 1/(1 + e^(2y)): one exponential and one
+// reciprocal, absolute error about c 2^-22, right at both ends (e^(2y) = 0 or inf); the derivative
+// 1 - tanh^2 is 4 r (1 - r).
+struct ScoreArgs {
+  float scale_log2;  // scale log2(e)
+  float scale;
+  float cap_in;      // 2 log2(e) scale / c: 2^(cap_in x) = e^(2y)
+  float cap_out;     // c log2(e)
+};
+inline ScoreArgs score_args(const AttnSpanArgs& g) {
+  return {g.scale * kLog2e, g.scale, g.cap > 0.f ? 2.f * kLog2e * g.scale / g.cap : 0.f, g.cap * kLog2e};
+}
+__device__ __forceinline__ float cap_r(float x, const ScoreArgs& a) { return rcp(1.f + ex2(x * a.cap_in)); }
+__device__ __forceinline__ float cap_score(float r, const ScoreArgs& a) { return fmaf(-2.f * a.cap_out, r, a.cap_out); }
+
+// Zero the 128 bytes of one 64-column slice of an operand row in shared memory. The 128-byte
+// swizzle moves 16-byte chunks within a row only, so it does not matter here.
+__device__ __forceinline__ void zero_slice_row(uint8_t* slice, int row) {
+  uint4* p = reinterpret_cast<uint4*>(slice + row * 128);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// One of the eight kernels of a direction: f(head_dim, capped, biased) as compile-time constants.
+template <class F>
+cudaError_t dispatch(const AttnSpanArgs& g, F&& f) {
+  auto pick = [&](auto hd) {
+    auto capped = [&](auto cap) {
+      return g.slopes ? f(hd, cap, std::true_type{}) : f(hd, cap, std::false_type{});
+    };
+    return g.cap > 0.f ? capped(std::true_type{}) : capped(std::false_type{});
+  };
+  return g.hd == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
+}
+
+}  // namespace span
+}  // namespace mt

@@ -31,6 +31,13 @@ inline int rc(cudaError_t e) {
   return MT_ECUDA;
 }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+mt::AttnSpanArgs span_args(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                           const void* lo, const void* hi, int B, int s, int nh, int nkv, int hd, float scale,
+                           float cap, const void* slopes) {
+  return {static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v), ldq, ldk, ldv, B, s,
+          nh, nkv, hd, static_cast<const int32_t*>(lo), static_cast<const int32_t*>(hi), scale, cap,
+          static_cast<const float*>(slopes)};
+}
 std::atomic<void*> g_gemm_ws{nullptr};  // workspace of the mtk_gemm_* calls (mtk_gemm_use_workspace)
 }  // namespace
 
@@ -247,6 +254,34 @@ int mtk_attn_bwd_rope(const void* qkv, const void* o, const void* lse, const voi
   return rc(mt::attn_bwd(static_cast<const bf16*>(qkv), static_cast<const bf16*>(o), static_cast<const float*>(lse),
                          static_cast<const bf16*>(dout), static_cast<bf16*>(dqkv), static_cast<float*>(delta),
                          static_cast<const float*>(cos_sin), B, s, nh, nkv, head_dim, err_flag, S(stream)));
+}
+
+int mtk_doc_spans(const int32_t* bounds, int n_docs, const int32_t* prefix, int B, int s, int32_t* lo, int32_t* hi,
+                  int32_t* positions) {
+  return mt::doc_spans(bounds, n_docs, prefix, B, s, lo, hi, positions) ? MT_OK : MT_EINVAL;
+}
+
+int mtk_attn_span_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                      const void* lo, const void* hi, void* o, int64_t ldo, void* lse, int B, int s, int nh, int nkv,
+                      int head_dim, float scale, float cap, const void* slopes, int* err_flag, void* stream) {
+  return rc(mt::attn_span_fwd(span_args(q, ldq, k, ldk, v, ldv, lo, hi, B, s, nh, nkv, head_dim, scale, cap, slopes),
+                              static_cast<bf16*>(o), ldo, static_cast<float*>(lse), err_flag, S(stream)));
+}
+
+uint64_t mtk_attn_span_bwd_scratch_bytes(int B, int s, int nh) {
+  return B > 0 && s > 0 && nh > 0 ? mt::attn_span_bwd_scratch(B, s, nh) : 0;
+}
+
+int mtk_attn_span_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                      const void* lo, const void* hi, const void* o, int64_t ldo, const void* lse, const void* dout,
+                      int64_t lddo, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,
+                      void* scratch, int B, int s, int nh, int nkv, int head_dim, float scale, float cap,
+                      const void* slopes, int* err_flag, void* stream) {
+  return rc(mt::attn_span_bwd(span_args(q, ldq, k, ldk, v, ldv, lo, hi, B, s, nh, nkv, head_dim, scale, cap, slopes),
+                              static_cast<const bf16*>(o), ldo, static_cast<const float*>(lse),
+                              static_cast<const bf16*>(dout), lddo, static_cast<bf16*>(dq), lddq,
+                              static_cast<bf16*>(dk), lddk, static_cast<bf16*>(dv), lddv, scratch, err_flag,
+                              S(stream)));
 }
 
 int mtk_bounded_wait_check(int* err_flag, int* gave_up, int64_t limit_ns, void* stream) {

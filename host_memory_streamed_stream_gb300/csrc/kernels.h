@@ -150,4 +150,29 @@ cudaError_t attn_fwd(const bf16* qkv, bf16* o, float* lse, int B, int s, int nh,
 cudaError_t attn_bwd(const bf16* qkv, const bf16* o, const float* lse, const bf16* dout, bf16* dqkv, float* delta,
                      const float* rope_cs, int B, int s, int nh, int nkv, int hd, int* err, cudaStream_t st);
 
+// ------------------------------------------------------------------ attention over spans
+// Query row i of each sequence sees the keys lo[i] <= j < hi[i] (null lo: 0, null hi: i + 1);
+// z = scale q.k, cap > 0: z = cap tanh(z / cap), slopes: z -= slopes[head] |i - j|. q, k, v are
+// separate [B*s] row matrices with their own row strides (multiples of 8).
+constexpr int kSpanMaxSeq = 1 << 22;
+struct AttnSpanArgs {
+  const bf16 *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  int B, s, nh, nkv, hd;
+  const int32_t *lo, *hi;
+  float scale, cap;
+  const float* slopes;
+};
+bool attn_span_ok(const AttnSpanArgs& g);  // sizes, strides and alignments the kernels take
+// o [B*s, nh*hd] (row stride ldo), lse fp32 [B, nh, s] as attn_fwd's; 0 and -inf for an empty span.
+cudaError_t attn_span_fwd(const AttnSpanArgs& g, bf16* o, int64_t ldo, float* lse, int* err, cudaStream_t st);
+// dq [B*s, nh*hd], dk and dv [B*s, nkv*hd]; scratch of attn_span_bwd_scratch() bytes.
+uint64_t attn_span_bwd_scratch(int B, int s, int nh);
+cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const float* lse, const bf16* dout,
+                          int64_t lddo, bf16* dq, int64_t lddq, bf16* dk, int64_t lddk, bf16* dv, int64_t lddv,
+                          void* scratch, int* err, cudaStream_t st);
+// Spans and positions of packed documents (host arrays; rules and checks: mtk_doc_spans).
+bool doc_spans(const int32_t* bounds, int n_docs, const int32_t* prefix, int B, int s, int32_t* lo, int32_t* hi,
+               int32_t* positions);
+
 }  // namespace mt

@@ -21,6 +21,10 @@ bool tma_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows
 // shared memory slice after slice, each [box_rows][64] with the 128-byte swizzle. TMA issue cost
 // is mostly per box and per 128-byte row, so one box per head-dim tile instead of one per slice
 // roughly doubles the load rate of 64-row tiles.
+// tma_map_heads is the same for a matrix of `slices` 64-column slices whose row stride is any
+// multiple of 8 elements (a column range of a wider buffer).
+bool tma_map_heads(CUtensorMap* map, const void* base, uint64_t rows, uint64_t batch, int64_t ld, int64_t bstride,
+                   uint64_t slices, uint32_t box_slices, uint32_t box_rows);
 bool tma_map_slices(CUtensorMap* map, const void* base, uint64_t rows, uint64_t batch, int64_t ld, int64_t bstride,
                     uint32_t box_slices, uint32_t box_rows);
 }  // namespace mt

@@ -291,3 +291,63 @@ def attn_bwd(qkv, o, lse, dout, B, s, nh, nkv, hd, err=None, cos_sin=None):
                                   delta.data_ptr(), cos_sin.data_ptr(), B, s, nh, nkv, hd, err.data_ptr(), _s()),
             "attn_bwd_rope")
     return dqkv
+
+
+def doc_spans(bounds, B, s, prefix=None):
+    """(lo, hi, positions) numpy int32 [B*s] of packed documents: document d holds the tokens
+    bounds[d] <= t < bounds[d+1]; prefix: how many of its first tokens all of it sees (None: causal)."""
+    bounds = np.ascontiguousarray(bounds, dtype=np.int32)
+    _need(bounds.ndim == 1 and bounds.size >= 1, "bounds: n_docs + 1 token indices")
+    if prefix is not None:
+        prefix = np.ascontiguousarray(prefix, dtype=np.int32)
+        _need(prefix.shape == (bounds.size - 1,), "prefix: one length for each document")
+    _need(B > 0 and s > 0, "B and s: positive")
+    out = np.empty((3, B * s), dtype=np.int32)
+    _ok(_lib.load().mtk_doc_spans(bounds.ctypes.data, bounds.size - 1, None if prefix is None else prefix.ctypes.data,
+                                  B, s, out[0].ctypes.data, out[1].ctypes.data, out[2].ctypes.data), "doc_spans")
+    return out[0], out[1], out[2]
+
+
+def _span_args(q, k, v, B, s, nh, nkv, hd, lo, hi, slopes):
+    T = B * s
+    return (q.data_ptr(), _rows(q, T, nh * hd, "q"), k.data_ptr(), _rows(k, T, nkv * hd, "k"), v.data_ptr(),
+            _rows(v, T, nkv * hd, "v"), None if lo is None else _vec(lo, T, torch.int32, q, "lo"),
+            None if hi is None else _vec(hi, T, torch.int32, q, "hi"),
+            None if slopes is None else _vec(slopes, nh, torch.float32, q, "slopes"))
+
+
+def attn_span_fwd(q, k, v, B, s, nh, nkv, hd, lo=None, hi=None, scale=None, cap=0.0, slopes=None, out=None, err=None):
+    """(o, lse) of attention in which row i sees the keys lo[i] <= j < hi[i] (int32 [B*s], see
+    doc_spans; None: causal). scale: 1/sqrt(hd) if None; cap: tanh cap of the scores (0: none);
+    slopes: fp32 [nh], lowers the scores by slopes[h] |i - j|. q, k, v may be column ranges of
+    wider tensors."""
+    *ptrs, sl = _span_args(q, k, v, B, s, nh, nkv, hd, lo, hi, slopes)
+    if out is None:
+        out = torch.empty(B * s, nh * hd, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty(B, nh, s, dtype=torch.float32, device=q.device)
+    err = _err(err, q.device)
+    _ok(_lib.load().mtk_attn_span_fwd(*ptrs, out.data_ptr(), _rows(out, B * s, nh * hd, "out"), lse.data_ptr(), B, s,
+                                      nh, nkv, hd, hd ** -0.5 if scale is None else scale, cap, sl, err.data_ptr(),
+                                      _s()), "attn_span_fwd")
+    return out, lse
+
+
+def attn_span_bwd(q, k, v, o, lse, dout, B, s, nh, nkv, hd, lo=None, hi=None, scale=None, cap=0.0, slopes=None,
+                  out=None, err=None):
+    """(dq, dk, dv) of attn_span_fwd; out: the three tensors (column ranges of one, for example) or
+    None for new ones."""
+    *ptrs, sl = _span_args(q, k, v, B, s, nh, nkv, hd, lo, hi, slopes)
+    T, dev = B * s, q.device
+    if out is None:
+        out = tuple(torch.empty(T, n * hd, dtype=torch.bfloat16, device=dev) for n in (nh, nkv, nkv))
+    dq, dk, dv = out
+    lib = _lib.load()
+    scratch = torch.empty(lib.mtk_attn_span_bwd_scratch_bytes(B, s, nh), dtype=torch.uint8, device=dev)
+    err = _err(err, dev)
+    _ok(lib.mtk_attn_span_bwd(*ptrs, o.data_ptr(), _rows(o, T, nh * hd, "o"),
+                              _vec(lse, T * nh, torch.float32, q, "lse"), dout.data_ptr(),
+                              _rows(dout, T, nh * hd, "dout"), dq.data_ptr(), _rows(dq, T, nh * hd, "dq"),
+                              dk.data_ptr(), _rows(dk, T, nkv * hd, "dk"), dv.data_ptr(),
+                              _rows(dv, T, nkv * hd, "dv"), scratch.data_ptr(), B, s, nh, nkv, hd,
+                              hd ** -0.5 if scale is None else scale, cap, sl, err.data_ptr(), _s()), "attn_span_bwd")
+    return dq, dk, dv

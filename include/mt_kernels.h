@@ -233,6 +233,47 @@ int mtk_attn_bwd(const void* qkv, const void* o, const void* lse, const void* do
 int mtk_attn_bwd_rope(const void* qkv, const void* o, const void* lse, const void* dout, void* dqkv, void* delta,
                       const void* cos_sin, int B, int s, int nh, int nkv, int head_dim, int* err_flag, void* stream);
 
+/*
+ * Attention over spans: self-attention in which query row i of its sequence sees the keys
+ * lo[i] <= j < hi[i], which covers causal, document, prefix and two-sided masks and padding. (An
+ * addition to the layer template's causal attention; the pages name no model.)
+ *   z_ij = scale q_i.k_j;  cap > 0: z = cap tanh(z / cap);  slopes: z -= slopes[head] |i - j|;
+ *   p_i = softmax of z_i over the span, o_i = sum_j p_ij v_j.
+ * q bf16 [B*s, nh*hd], k and v bf16 [B*s, nkv*hd] with row strides ldq, ldk, ldv (any column ranges
+ * of wider buffers); lo, hi int32 [B*s], positions inside the sequence, or NULL (lo 0, hi i + 1:
+ * causal); they are clamped to [0, s]. nkv divides nh, head_dim 64 or 128, s <= 4194304. scale > 0,
+ * cap >= 0 (0: none), slopes f32 [nh] or NULL, all finite; the cap's tanh is computed to about
+ * cap * 2^-22.
+ * An empty span (lo >= hi) makes row i padding: o_i = 0, lse_i = -inf, its gradients are 0, and no
+ * other row's span may contain it. Padding rows of q, k, v and dout may hold anything, NaN
+ * included, where the padding follows the documents of its sequence, precedes them, or lies between
+ * documents that are contiguous; all other rows must be finite.
+ *
+ * mtk_doc_spans: spans and positions of packed documents. HOST arrays, pure: documents d = 0 ..
+ *   n_docs-1 are the tokens bounds[d] <= t < bounds[d+1] of the B*s tokens (bounds int32
+ *   [n_docs+1], not decreasing; empty documents are allowed; tokens outside are padding). A document
+ *   that crosses the end of a sequence is cut there into two. Token t of a document part that starts
+ *   at t0 gets lo = t0, hi = max(t + 1, t0 + prefix[d]) up to the part's end, both inside the
+ *   sequence, and position t - t0. prefix int32 [n_docs] >= 0 or NULL (0: causal; the document's
+ *   length: two-sided). lo, hi int32 [B*s], positions int32 [B*s] or NULL; B*s < 2^31.
+ * mtk_attn_span_fwd: o bf16 [B*s, nh*hd] (row stride ldo), lse f32 [B, nh, s] in mtk_attn_fwd's
+ *   units (log2). err_flag: device int, required, as for all attention entries.
+ * mtk_attn_span_bwd: dq bf16 [B*s, nh*hd], dk, dv bf16 [B*s, nkv*hd] (row strides lddq, lddk, lddv;
+ *   every row is written) from dout, o and lse, deterministic, no atomics. scratch: device memory of
+ *   mtk_attn_span_bwd_scratch_bytes() bytes, 16-byte aligned. Gradients of slopes are not computed.
+ */
+int mtk_doc_spans(const int32_t* bounds, int n_docs, const int32_t* prefix, int B, int s, int32_t* lo, int32_t* hi,
+                  int32_t* positions);
+int mtk_attn_span_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                      const void* lo, const void* hi, void* o, int64_t ldo, void* lse, int B, int s, int nh, int nkv,
+                      int head_dim, float scale, float cap, const void* slopes, int* err_flag, void* stream);
+uint64_t mtk_attn_span_bwd_scratch_bytes(int B, int s, int nh);
+int mtk_attn_span_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                      const void* lo, const void* hi, const void* o, int64_t ldo, const void* lse, const void* dout,
+                      int64_t lddo, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,
+                      void* scratch, int B, int s, int nh, int nkv, int head_dim, float scale, float cap,
+                      const void* slopes, int* err_flag, void* stream);
+
 /* Block order of the causal attention grids (host-only, pure; no GPU needed). The forward, dQ
  * and dK/dV grids are one-dimensional with n_tiles * n_hb blocks (n_tiles 128-row tiles per
  * sequence; n_hb = heads * batch, KV heads for dK/dV). Block `lin` works on tile rank *rank
