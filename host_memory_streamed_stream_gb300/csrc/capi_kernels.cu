@@ -183,7 +183,9 @@ int mtk_qk_norm_rope(const void* x, int64_t ldx, const void* gq, const void* gk,
 }
 
 int mtk_qk_norm_rope_bwd_parts(int T, int n_heads, int n_kv_heads, int head_dim) {
-  if (T <= 0 || n_heads <= 0 || n_kv_heads <= 0 || (head_dim != 64 && head_dim != 128)) return 0;
+  if (T <= 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads > mt::kRotaryMaxHeads - n_kv_heads ||
+      (head_dim != 64 && head_dim != 128))
+    return 0;
   return mt::qk_norm_rope_bwd_parts(T, n_heads, n_kv_heads, head_dim);
 }
 

@@ -117,6 +117,7 @@ bool rotary_inv_freq(int rot, double theta, int scaling, double factor, double o
 // Table fp32 [n_pos][rot/2][2] = amp * (cos, sin)(p * inv_freq[i]); inv_freq is a HOST array of
 // rot/2 finite radians per position (read before the call returns).
 constexpr int kRotaryMaxPairs = 128;
+constexpr int kRotaryMaxHeads = 65536;
 cudaError_t rotary_table(const double* inv_freq, int rot, int n_pos, double amp, float* out, cudaStream_t s);
 // y = x with the first `rot` columns of each head rotated (pairs (2i, 2i+1) if interleaved, else
 // (i, i + rot/2)) at position positions[t], or t % n_pos without positions; inverse = the transpose.
@@ -129,7 +130,7 @@ cudaError_t rotary(const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int T, int 
 cudaError_t qk_norm_rope(const bf16* x, int64_t ldx, const bf16* gq, const bf16* gk, bf16* y, int64_t ldy, float* rstd,
                          int T, int nh, int nkv, int hd, int rot, bool interleaved, float eps,
                          const int32_t* positions, const float* cs, int n_pos, int* err, cudaStream_t s);
-// Its backward: dx (may be dy or x) and the gain gradients, through `partial` fp32 [parts][2][hd].
+// Its backward: dx (may be dy or x) and the gain gradients, through `partial` fp32 [parts][hd].
 constexpr int kQkNormParts = 608;
 int qk_norm_rope_bwd_parts(int T, int nh, int nkv, int hd);
 cudaError_t qk_norm_rope_bwd(const bf16* dy, int64_t lddy, const bf16* x, int64_t ldx, const bf16* gq, const bf16* gk,

@@ -134,7 +134,7 @@ int mtk_rope(void* qkv, int64_t ld, int T, int seq, int n_heads, int n_kv_heads,
  *   (i, i + rot_dim/2), or (2i, 2i+1) if interleaved; inverse = 1 applies the transpose (the
  *   backward pass). Token t is at positions[t] (int32 [T]), or at t % n_pos if positions is NULL.
  *   y may be x (then ldy = ldx), else they must not overlap. head_dim and rot_dim are multiples
- *   of 16, rot_dim <= head_dim <= 4096. A position outside [0, n_pos) sets *err_flag to 8 and
+ *   of 16, rot_dim <= head_dim <= 4096, heads <= 65536. A position outside [0, n_pos) sets *err_flag to 8 and
  *   leaves that token unrotated. err_flag: device int, required.
  */
 #define MTK_ROTARY_PLAIN 0
@@ -155,12 +155,12 @@ int mtk_rotary(const void* x, int64_t ldx, void* y, int64_t ldy, int T, int head
  * with the rotation R of mtk_rotary (rot_dim = 0: no rotation; cos_sin, positions and err_flag may
  * then be NULL). x, y bf16 with row strides ldx, ldy (columns past the key heads, such as v, are
  * neither read nor written); gq, gk bf16 [head_dim]; rstd f32 [T][n_heads + n_kv_heads], or NULL.
- * y may be x (then ldy = ldx). head_dim 64 or 128, rot_dim a multiple of 16.
+ * y may be x (then ldy = ldx). head_dim 64 or 128, rot_dim a multiple of 16, at most 65536 heads.
  *
  * mtk_qk_norm_rope_bwd: from dy (row stride lddy), the forward's x and its rstd, with u = R^T dy and
  * n = x_h * rstd: dx_h = rstd (u g - n mean(u g n)), dgq and dgk bf16 [head_dim] = the sums of u n
  * over tokens and query (key) heads, added in a fixed order through `partial`, f32
- * [mtk_qk_norm_rope_bwd_parts(...)][2][head_dim]. dx may be dy or x (with the same row stride). A
+ * [mtk_qk_norm_rope_bwd_parts(...)][head_dim]. dx may be dy or x (with the same row stride). A
  * bad position counts as no rotation, with *err_flag set to 8.
  */
 int mtk_qk_norm_rope(const void* x, int64_t ldx, const void* gq, const void* gk, void* y, int64_t ldy, void* rstd,
