@@ -1,17 +1,23 @@
 // Attention over spans, backward, on the tcgen05 tensor cores. Deterministic, no atomics.
 //
-// The kernels are those of the causal backward (attention_bwd_tc.cu): lsd pairs
-// (-lse2, -delta) per query row; dK/dV with one CTA per (128-key tile, kv head, sequence) walking
-// the 128-query tiles of its group's heads,
+// The tiles are worked on as in the causal backward (attention_bwd_tc.cu): lsd pairs
+// (-lse2, -delta) per query row; dK/dV per (128-key tile, kv head, sequence) over the 128-query
+// tiles of its group's heads,
 //     S^T = K Q^T, dP^T = V dO^T, P^T = 2^(z - lse2), dS^T = P^T (dP^T - delta) z',
 //     dV += P^T dO, dK += dS^T Q;
-// dQ with one CTA per (128-query tile, head, sequence) walking 128-key tiles, dQ += dS K; 128 x 128
-// tiles, two 128-column score slots in TMEM, P and dS written back over the scores as bf16 pairs
-// and read from TMEM, each in two halves of 64 columns. What differs:
+// dQ per (128-query tile, head, sequence) over 128-key tiles, dQ += dS K; 128 x 128 tiles, two
+// 128-column score slots in TMEM, P and dS written back over the scores as bf16 pairs and read from
+// TMEM, each in two halves of 64 columns. What differs:
 //  * z is the capped and biased score and z' the cap's derivative 1 - tanh^2 = 4 r (1 - r);
-//  * the delta kernel also writes each query tile's hull; a dQ CTA walks the key tiles of its hull,
-//    a dK/dV CTA the query tiles from the first to the last whose hull meets its keys, and a tile
-//    that meets nothing writes zeros;
+//  * the delta kernel also writes each query tile's hull; dQ walks the key tiles of its hull, dK/dV
+//    the query tiles from the first to the last whose hull meets its keys, and a tile that meets
+//    nothing writes zeros;
+//  * documents make these walks short (six tiles on average at a mean of 700 tokens, one for the
+//    shortest), and what a block spends around them (its start, the first loads and scores, the
+//    last products, the stores) cost more than the walks. The kernels are therefore persistent, one
+//    block per SM that takes items (a tile with its walk) from a counter, heaviest ranks first, and
+//    the roles run ahead across items: the next item's operands are loaded and its first scores
+//    computed while the last item's gradients are stored;
 //  * a tile that some row does not see whole is masked by words of 32 bits: a query row's span is a
 //    run of bits over its key columns; in dK/dV, where a thread holds a key row, 32 lanes make the
 //    runs of 32 query columns and transpose them through the warp;
@@ -31,7 +37,8 @@ namespace {
 
 using namespace span;
 
-constexpr int kThreads = 320;       // TMA warp, MMA warp, 8 elementwise warps
+// warps: 0 takes items and loads one ring, 1 issues MMAs, 2..9 elementwise, 10 and 11 load
+constexpr int kThreads = 384;
 constexpr int kElem = 256;          // elementwise threads
 constexpr int kCols = 32;           // score columns an elementwise warp takes per half tile
 constexpr int kElemWarps = kElem / 32;  // arrivals per barrier phase (one elected lane per warp)
@@ -86,16 +93,65 @@ __device__ __forceinline__ void half_row_out(uint32_t taddr, int part, float sca
   }
 }
 
+// ------------------------------------------------------------------ items
+// The items a block works on, handed from the warp that takes them to the others through two slots.
+struct Item {
+  int lin;    // index in the heaviest-first order, -1: no more
+  int first;  // first tile of the walk
+  int count;  // its tiles (per query head of the group in dK/dV)
+  Hull hull;  // dQ: of the query tile
+};
+struct ItemRing {
+  uint64_t* full;   // [2]
+  uint64_t* empty;  // [2]
+  Item* slot;       // [2]
+  int* err;
+};
+constexpr int kItemReaders = 11;  // lane 0 of every warp but the one that takes items
+
+// Publish item number n (one thread).
+__device__ __forceinline__ bool put_item(const ItemRing& r, int n, const Item& it) {
+  if (!mbar_wait(&r.empty[n & 1], ((n >> 1) & 1) ^ 1u, r.err, kErrTimeoutAttn)) return false;
+  r.slot[n & 1] = it;
+  mbar_arrive(&r.full[n & 1]);
+  return true;
+}
+// The same value in every lane, as a warp reduction's result: what the compiler can see to be uniform
+// stays in uniform registers. The MMA warp's descriptors follow from the items' tile counts, and
+// computed per lane they have to be moved for every MMA it issues.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// Item number n, for a whole warp; false if there is none.
+__device__ __forceinline__ bool get_item_warp(const ItemRing& r, int n, Item& it) {
+  if (!mbar_wait_warp(&r.full[n & 1], (n >> 1) & 1, r.err, kErrTimeoutAttn)) return false;
+  const Item s = r.slot[n & 1];
+  it.lin = uniform(s.lin);
+  it.first = uniform(s.first);
+  it.count = uniform(s.count);
+  it.hull = {uniform(s.hull.min_lo), uniform(s.hull.max_hi), uniform(s.hull.max_lo), uniform(s.hull.min_hi)};
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[n & 1]);
+  return it.lin >= 0;
+}
+// The same for a single thread.
+__device__ __forceinline__ bool get_item(const ItemRing& r, int n, Item& it) {
+  if (!mbar_wait(&r.full[n & 1], (n >> 1) & 1, r.err, kErrTimeoutAttn)) return false;
+  it = r.slot[n & 1];
+  mbar_arrive(&r.empty[n & 1]);
+  return it.lin >= 0;
+}
+
 // ------------------------------------------------------------------ delta and hulls
 // One block per 128 query rows of a (sequence, head): HD/8 lanes per row (16-byte loads). A row
 // whose span is empty (or past the end, or without a finite score) gets (-inf, -0): every
 // probability of it is 0. The blocks of head 0 also reduce their rows' spans to the tile's hull.
+// Block 0 clears the counters the next two kernels take their items from.
 template <int HD>
 __global__ void __launch_bounds__(256)
     span_delta_kernel(const bf16* __restrict__ o, int64_t ldo, const bf16* __restrict__ dout, int64_t lddo,
                       const float* __restrict__ lse, Spans spans, float2* __restrict__ lsd, Hull* __restrict__ hulls,
-                      int s, int nh, int n_t) {
+                      int* __restrict__ taken, int s, int nh, int n_t) {
   constexpr int kLanes = HD / 8;  // lanes per row
+  if (blockIdx.x == 0 && threadIdx.x < 2) taken[threadIdx.x] = 0;  // items taken by dQ and by dK/dV
   __shared__ Hull parts[4];
   const int tile = blockIdx.x % n_t;
   const int bh = blockIdx.x / n_t;  // b * nh + head
@@ -140,10 +196,12 @@ struct BwdArgs {
   Spans spans;
   const float* slopes;
   const float2* lsd;
-  const Hull* hulls;
+  const Hull* hulls;   // [B][tiles] of the query tiles
+  int2* q_ranges;      // [B][tiles] first and last query tile that meets a key tile (last -1: none)
+  int* taken;          // [2] items taken: dQ, dK/dV
   bf16 *dq, *dk, *dv;
   int64_t lddq, lddk, lddv;
-  int s, nh, nkv;
+  int B, s, nh, nkv;
   ScoreArgs score;
   int* err;
 };
@@ -185,7 +243,7 @@ struct SmemKV {
   static constexpr int DO = Q + QS * TILE;              // DS x (tile, then 128 (-lse2, -delta) pairs)
   static constexpr int DSTAGE = TILE + 1024;
   static constexpr int BAR = DO + DS * DSTAGE;
-  static constexpr int BYTES = BAR + 256;               // the dynamic window is 1024-aligned (checked)
+  static constexpr int BYTES = BAR + 320;               // the dynamic window is 1024-aligned (checked)
   static_assert(BYTES <= 232448, "dK/dV shared memory above the 227 KB per-CTA limit");
 };
 
@@ -205,32 +263,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint64_t* kv_full = bar + 0;
-  uint64_t* q_full = bar + 1;            // [QS]
-  uint64_t* q_empty = bar + 4;           // [QS]
-  uint64_t* d_full = bar + 7;            // [DS]
-  uint64_t* d_empty = bar + 9;           // [DS]
-  uint64_t* sdp_full = bar + 11;         // [2]: the tile's S^T and that half of its dP^T are complete
-  uint64_t* dp_free = bar + 13;          // every warp holds its dP^T columns in registers
-  uint64_t* p_half = bar + 14;           // [2]: every warp has written P^T/dS^T of that half
-  uint64_t* acc_done = bar + 16;         // the last tile's accumulating MMAs have completed
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 17);
-  int* q_range = reinterpret_cast<int*>(bar + 18);  // first and last query tile that meets the keys
+  uint64_t* kv_empty = bar + 1;          // every MMA that reads the item's K and V has completed
+  uint64_t* q_full = bar + 2;            // [QS]
+  uint64_t* q_empty = bar + 5;           // [QS]
+  uint64_t* d_full = bar + 8;            // [DS]
+  uint64_t* d_empty = bar + 10;          // [DS]
+  uint64_t* sdp_full = bar + 12;         // [2]: the tile's S^T and that half of its dP^T are complete
+  uint64_t* dp_free = bar + 14;          // every warp holds its dP^T columns in registers
+  uint64_t* p_half = bar + 15;           // [2]: every warp has written P^T/dS^T of that half
+  uint64_t* acc_full = bar + 17;         // the item's accumulating MMAs have completed
+  uint64_t* acc_empty = bar + 18;        // every warp has read its part of dK and dV
+  const ItemRing ring{bar + 19, bar + 21, reinterpret_cast<Item*>(bar + 24), err};
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 23);
 
   const int s = a.s, nh = a.nh, nkv = a.nkv;
-  const int n_t = (s + 127) / 128;
-  const TileSlot slot = heavy_first_slot(static_cast<int>(blockIdx.x), n_t, static_cast<int>(gridDim.x) / n_t);
-  const int kt = slot.rank;  // the first key tile is seen by the most queries under a causal mask
-  const int kvh = slot.hb % nkv, b = slot.hb / nkv;
+  const int n_t = (s + 127) / 128, n_hb = nkv * a.B;
   const int group = nh / nkv;
-  const int k0 = kt * 128;
   const int sp = pad128(s);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Hull* hulls = a.hulls + static_cast<int64_t>(b) * n_t;
+  // item -> key tile (the first key tile is seen by the most queries under a causal mask), head, sequence
+  struct Where {
+    int kt, kvh, b;
+  };
+  auto where = [&](int lin) -> Where {
+    const TileSlot slot = heavy_first_slot(lin, n_t, n_hb);
+    return {slot.rank, slot.hb % nkv, slot.hb / nkv};
+  };
 
   if (threadIdx.x == 0) {
-    q_range[0] = INT_MAX;
-    q_range[1] = -1;
     mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
     for (int i = 0; i < QS; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
@@ -244,7 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(dp_free, kElemWarps);
     mbar_init(&p_half[0], kElemWarps);
     mbar_init(&p_half[1], kElemWarps);
-    mbar_init(acc_done, 1);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, kElemWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ring.full[i], 1);
+      mbar_init(&ring.empty[i], kItemReaders);
+    }
     fence_mbar_init();
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
@@ -255,58 +322,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
-  __syncthreads();
-  {
-    int first = INT_MAX, last = -1;
-    for (int i = threadIdx.x; i < n_t; i += kThreads) {
-      const Hull h = hulls[i];
-      if (h.min_lo < k0 + 128 && h.max_hi > k0) {
-        first = min(first, i);
-        last = i;
-      }
-    }
-    first = __reduce_min_sync(0xffffffffu, first);
-    last = __reduce_max_sync(0xffffffffu, last);
-    if (lane == 0 && last >= 0) {
-      atomicMin(&q_range[0], first);
-      atomicMax(&q_range[1], last);
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tslot;
-  const int qt0 = q_range[0];
-  const int per_head = q_range[1] < 0 ? 0 : q_range[1] - qt0 + 1;
-  const int total = group * per_head;
   const uint32_t tdV = tbase + 256, tdK = tbase + 256 + HD;
-  auto s_slot = [&](int i) { return tbase + (i & 1) * 128; };        // S^T, then P^T | dS^T pairs
-  auto d_slot = [&](int i) { return tbase + ((i & 1) ^ 1) * 128; };  // dP^T
+  // g numbers the block's tiles across its items, n its items with a walk
+  auto s_slot = [&](int g) { return tbase + (g & 1) * 128; };        // S^T, then P^T | dS^T pairs
+  auto d_slot = [&](int g) { return tbase + ((g & 1) ^ 1) * 128; };  // dP^T
 
   if (warp == 0) {
-    // lane 0: K and V once, then the Q ring; lane 1: the dO ring with the (-lse2, -delta) pairs
-    if (lane == 0 && total > 0) {
-      mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
-      tma_load_4d(sm + L::K, &map_k, kv_full, 0, k0, kvh * (HD / 64), b);
-      tma_load_4d(sm + L::V, &map_v, kv_full, 0, k0, kvh * (HD / 64), b);
-      for (int i = 0; i < total; ++i) {
-        const int st = i % QS;
-        const int hq = kvh * group + i / per_head;
-        const int q0 = (qt0 + i % per_head) * 128;
-        if (!mbar_wait(&q_empty[st], ((i / QS) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
-        mbar_arrive_expect_tx(&q_full[st], L::TILE);
-        tma_load_4d(sm + L::Q + st * L::TILE, &map_q, &q_full[st], 0, q0, hq * (HD / 64), b);
+    // takes the items and loads the Q ring. The next item is taken when the last load of this one has
+    // been issued, up to QS tiles before its end: taken any earlier (with the item before), the items
+    // no longer go to the blocks that are done first (14B heads, 256 unequal items: 385 -> 470 us)
+    if (lane == 0) {
+      const int items = n_t * n_hb;
+      auto take = [&](int lin) -> Item {
+        Item it{-1, 0, 0, {0, 0, 0, 0}};
+        if (lin < items) {
+          const Where w = where(lin);
+          const int2 r = a.q_ranges[static_cast<int64_t>(w.b) * n_t + w.kt];
+          it.lin = lin;
+          it.first = r.x;
+          it.count = r.y < 0 ? 0 : r.y - r.x + 1;
+        }
+        return it;
+      };
+      Item cur = take(blockIdx.x);
+      bool ok = true;
+      for (int m = 0, g = 0; ok; ++m) {
+        if (!(ok = put_item(ring, m, cur)) || cur.lin < 0) break;
+        const Where w = where(cur.lin);
+        for (int i = 0; i < group * cur.count; ++i, ++g) {
+          const int st = g % QS;
+          if (!(ok = mbar_wait(&q_empty[st], ((g / QS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
+          mbar_arrive_expect_tx(&q_full[st], L::TILE);
+          tma_load_4d(sm + L::Q + st * L::TILE, &map_q, &q_full[st], 0, (cur.first + i % cur.count) * 128,
+                      (w.kvh * group + i / cur.count) * (HD / 64), w.b);
+        }
+        if (ok) cur = take(gridDim.x + atomicAdd(a.taken + 1, 1));
       }
-    } else if (lane == 1) {
-      for (int i = 0; i < total; ++i) {
-        const int st = i % DS;
-        const int hq = kvh * group + i / per_head;
-        const int q0 = (qt0 + i % per_head) * 128;
-        if (!mbar_wait(&d_empty[st], ((i / DS) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
-        mbar_arrive_expect_tx(&d_full[st], L::TILE + 1024);
-        uint8_t* base = sm + L::DO + st * L::DSTAGE;
-        tma_load_4d(base, &map_do, &d_full[st], 0, q0, hq * (HD / 64), b);
-        bulk_load_1d(base + L::TILE, a.lsd + (static_cast<int64_t>(b) * nh + hq) * sp + q0, 1024, &d_full[st]);
+    }
+  } else if (warp == 10) {
+    // the dO ring with the (-lse2, -delta) pairs
+    if (lane == 0) {
+      Item it;
+      bool ok = true;
+      for (int m = 0, g = 0; ok && get_item(ring, m, it); ++m) {
+        const Where w = where(it.lin);
+        for (int i = 0; i < group * it.count; ++i, ++g) {
+          const int st = g % DS;
+          const int hq = w.kvh * group + i / it.count, q0 = (it.first + i % it.count) * 128;
+          if (!(ok = mbar_wait(&d_empty[st], ((g / DS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
+          mbar_arrive_expect_tx(&d_full[st], L::TILE + 1024);
+          uint8_t* base = sm + L::DO + st * L::DSTAGE;
+          tma_load_4d(base, &map_do, &d_full[st], 0, q0, hq * (HD / 64), w.b);
+          bulk_load_1d(base + L::TILE, a.lsd + (static_cast<int64_t>(w.b) * nh + hq) * sp + q0, 1024, &d_full[st]);
+        }
+      }
+    }
+  } else if (warp == 11) {
+    // K and V, once per item
+    if (lane == 0) {
+      Item it;
+      for (int m = 0, n = 0; get_item(ring, m, it); ++m) {
+        if (it.count == 0) continue;
+        const Where w = where(it.lin);
+        if (!mbar_wait(kv_empty, (n & 1) ^ 1u, err, kErrTimeoutAttn)) break;
+        mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
+        tma_load_4d(sm + L::K, &map_k, kv_full, 0, w.kt * 128, w.kvh * (HD / 64), w.b);
+        tma_load_4d(sm + L::V, &map_v, kv_full, 0, w.kt * 128, w.kvh * (HD / 64), w.b);
+        ++n;
       }
     }
   } else if (warp == 1) {
@@ -316,160 +402,184 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, HD, false, true);
     const uint64_t kd = smem_desc_sw128(smem_addr(sm + L::K), 16, 1024);
     const uint64_t vd = smem_desc_sw128(smem_addr(sm + L::V), 16, 1024);
-    bool ok = total > 0 && mbar_wait_warp(kv_full, 0, err, kErrTimeoutAttn);
-    // S^T = K Q^T of tile i into TMEM slot t, once its Q tile is in
-    auto s_scores = [&](int i, uint32_t t) -> bool {
-      if (!mbar_wait_warp(&q_full[i % QS], (i / QS) & 1, err, kErrTimeoutAttn)) return false;
+    // S^T = K Q^T of tile g into its TMEM slot, once its Q tile is in
+    auto s_scores = [&](int g) -> bool {
+      if (!mbar_wait_warp(&q_full[g % QS], (g / QS) & 1, err, kErrTimeoutAttn)) return false;
       tc_fence_after();
-      const uint64_t bd = smem_desc_sw128(smem_addr(sm + L::Q + (i % QS) * L::TILE), 16, 1024);
+      const uint64_t bd = smem_desc_sw128(smem_addr(sm + L::Q + (g % QS) * L::TILE), 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk) {
         const uint32_t off = (kk >> 2) * kSlice128 + (kk & 3) * 32;
-        umma_bf16_warp(t, desc_advance(kd, off), desc_advance(bd, off), idesc_s, kk > 0 ? 1u : 0u);
+        umma_bf16_warp(s_slot(g), desc_advance(kd, off), desc_advance(bd, off), idesc_s, kk > 0 ? 1u : 0u);
       }
       return true;
     };
-    // half h of dP^T = V dO^T of tile i into columns [64 h, 64 h + 64) of TMEM slot t
-    auto dp_half = [&](int i, int h, uint32_t t) -> bool {
-      if (!mbar_wait_warp(&d_full[i % DS], (i / DS) & 1, err, kErrTimeoutAttn)) return false;
+    // half h of dP^T = V dO^T of tile g into columns [64 h, 64 h + 64) of its TMEM slot
+    auto dp_half = [&](int g, int h) -> bool {
+      if (!mbar_wait_warp(&d_full[g % DS], (g / DS) & 1, err, kErrTimeoutAttn)) return false;
       tc_fence_after();
-      const uint64_t bd = smem_desc_sw128(smem_addr(sm + L::DO + (i % DS) * L::DSTAGE), 16, 1024);
+      const uint64_t bd = smem_desc_sw128(smem_addr(sm + L::DO + (g % DS) * L::DSTAGE), 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk) {
         const uint32_t off = (kk >> 2) * kSlice128 + (kk & 3) * 32;
-        umma_bf16_warp(t + h * 64, desc_advance(vd, off), desc_advance(bd, off + h * 8192), idesc_dh,
+        umma_bf16_warp(d_slot(g) + h * 64, desc_advance(vd, off), desc_advance(bd, off + h * 8192), idesc_dh,
                        kk > 0 ? 1u : 0u);
       }
       return true;
     };
-    if (ok) ok = s_scores(0, s_slot(0)) && dp_half(0, 0, d_slot(0)) && dp_half(0, 1, d_slot(0));
-    if (ok) {
+    Item it;
+    bool ok = true;
+    for (int m = 0, n = 0, g = 0; ok && get_item_warp(ring, m, it); ++m) {
+      const int total = group * it.count;
+      if (total == 0) continue;
+      // the item's first scores: both TMEM slots are free of what the last item left in them once
+      // its products, issued before, have run and every warp holds its dP^T columns
+      if (!(ok = mbar_wait_warp(kv_full, n & 1, err, kErrTimeoutAttn))) break;
+      if (g > 0 && !(ok = mbar_wait_warp(dp_free, (g - 1) & 1, err, kErrTimeoutAttn))) break;
+      if (!(ok = s_scores(g) && dp_half(g, 0))) break;
       umma_commit_warp(&sdp_full[0]);
+      if (!(ok = dp_half(g, 1))) break;
       umma_commit_warp(&sdp_full[1]);
-    }
-    for (int i = 0; i < total && ok; ++i) {
-      // B operands of the accumulating MMAs: dO and Q tiles read MN-major (16 queries per step)
-      const uint64_t qd = smem_desc_sw128(smem_addr(sm + L::Q + (i % QS) * L::TILE), kSlice128, 1024);
-      const uint64_t dd = smem_desc_sw128(smem_addr(sm + L::DO + (i % DS) * L::DSTAGE), kSlice128, 1024);
-      const uint32_t ts = s_slot(i);
-      for (int h = 0; h < 2 && ok; ++h) {
-        if (h == 1 && i + 1 < total) {
-          // the next tile's first dP^T half over this tile's first P^T/dS^T pairs, after the MMAs
-          // reading them; then the next S^T into the dP^T slot, free once every warp holds its columns
-          if (!(ok = dp_half(i + 1, 0, d_slot(i + 1)))) break;
-          if (!(ok = mbar_wait_warp(dp_free, i & 1, err, kErrTimeoutAttn))) break;
+      if (total == 1) umma_commit_warp(kv_empty);
+      for (int i = 0; i < total && ok; ++i, ++g) {
+        // B operands of the accumulating MMAs: dO and Q tiles read MN-major (16 queries per step)
+        const uint64_t qd = smem_desc_sw128(smem_addr(sm + L::Q + (g % QS) * L::TILE), kSlice128, 1024);
+        const uint64_t dd = smem_desc_sw128(smem_addr(sm + L::DO + (g % DS) * L::DSTAGE), kSlice128, 1024);
+        const uint32_t ts = s_slot(g);
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (h == 1 && i + 1 < total) {
+            // the next tile's first dP^T half over this tile's first P^T/dS^T pairs, after the MMAs
+            // reading them; then the next S^T into the dP^T slot, free once every warp holds its columns
+            if (!(ok = dp_half(g + 1, 0))) break;
+            if (!(ok = mbar_wait_warp(dp_free, g & 1, err, kErrTimeoutAttn))) break;
+            tc_fence_after();
+            if (!(ok = s_scores(g + 1))) break;
+            umma_commit_warp(&sdp_full[0]);
+          }
+          if (!(ok = mbar_wait_warp(&p_half[h], g & 1, err, kErrTimeoutAttn))) break;
+          // the first product of an item overwrites the accumulators: the last item's have been read
+          if (h == 0 && i == 0 && n > 0 && !(ok = mbar_wait_warp(acc_empty, (n - 1) & 1, err, kErrTimeoutAttn))) break;
           tc_fence_after();
-          if (!(ok = s_scores(i + 1, s_slot(i + 1)))) break;
-          umma_commit_warp(&sdp_full[0]);
-        }
-        if (!(ok = mbar_wait_warp(&p_half[h], i & 1, err, kErrTimeoutAttn))) break;
-        tc_fence_after();
 #pragma unroll
-        for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {  // 16 queries per step; A (P^T, dS^T) from TMEM
-          const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
-          umma_bf16_tmem_a_warp(tdV, ts + kk * 16, desc_advance(dd, kk * 2048), idesc_acc, acc);
-          umma_bf16_tmem_a_warp(tdK, ts + kk * 16 + 8, desc_advance(qd, kk * 2048), idesc_acc, acc);
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {  // 16 queries per step; A (P^T, dS^T) from TMEM
+            const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
+            umma_bf16_tmem_a_warp(tdV, ts + kk * 16, desc_advance(dd, kk * 2048), idesc_acc, acc);
+            umma_bf16_tmem_a_warp(tdK, ts + kk * 16 + 8, desc_advance(qd, kk * 2048), idesc_acc, acc);
+          }
+        }
+        if (!ok) break;
+        umma_commit_warp(&q_empty[g % QS]);
+        umma_commit_warp(&d_empty[g % DS]);
+        if (i + 1 < total) {
+          // the next tile's second dP^T half over this tile's last P^T/dS^T pairs
+          if (!(ok = dp_half(g + 1, 1))) break;
+          umma_commit_warp(&sdp_full[1]);
+          if (i + 2 == total) umma_commit_warp(kv_empty);
+        } else {
+          umma_commit_warp(acc_full);
         }
       }
-      if (!ok) break;
-      umma_commit_warp(&q_empty[i % QS]);
-      umma_commit_warp(&d_empty[i % DS]);
-      if (i + 1 < total) {
-        // the next tile's second dP^T half over this tile's last P^T/dS^T pairs
-        if (!(ok = dp_half(i + 1, 1, d_slot(i + 1)))) break;
-        umma_commit_warp(&sdp_full[1]);
-      } else {
-        umma_commit_warp(acc_done);
-      }
+      ++n;
     }
   } else {
     const int sub = warp & 3;
     const int part = (warp - 2) >> 2;  // which 32 of each 64 query columns this warp takes
     const int row = sub * 32 + lane;
-    const int key = k0 + row;
     const int elem = threadIdx.x - 64;
     const uint32_t tl = static_cast<uint32_t>(sub * 32) << 16;
+    Item it;
     bool ok = true;
-    Hull hull = total > 0 ? hulls[qt0] : Hull{0, 0, 0, 0};
-    for (int i = 0; i < total && ok; ++i) {
-      const int q0 = (qt0 + i % per_head) * 128;
-      const bool all = sees_all(hull, k0, k0 + 128), padded = hull.max_lo == INT_MAX;
-      if (i + 1 < total) hull = hulls[qt0 + (i + 1) % per_head];
-      uint32_t vis[2] = {~0u, ~0u};  // visible query columns of this thread's key, per half
-      if (!all) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int q = q0 + h * 64 + part * kCols + lane;
-          const int2 seen = q < s ? load_span(a.spans, b, q, s) : make_int2(0, 0);
-          vis[h] = warp_transpose(span_bits(seen, k0 + sub * 32), lane);
-        }
-      }
-      const float slope2 = BIAS ? __ldg(a.slopes + kvh * group + i / per_head) * kLog2e : 0.f;
-      uint8_t* dstage = sm + L::DO + (i % DS) * L::DSTAGE;
-      const float4* lsd_s = reinterpret_cast<const float4*>(dstage + L::TILE);
-      // the pairs were copied with the tile's dO: observe that copy before reading them
-      if (!(ok = mbar_wait_warp(&d_full[i % DS], (i / DS) & 1, err, kErrTimeoutAttn))) break;
-      const uint32_t ts = s_slot(i) + tl, td = d_slot(i) + tl;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!ok) break;
-        if (!(ok = mbar_wait_warp(&sdp_full[h], i & 1, err, kErrTimeoutAttn))) break;
-        tc_fence_after();
-        const int cb = h * 64 + part * kCols;  // this warp's score columns [cb, cb + 32)
-        float sv[kCols], dv[kCols];
-        tmem_ld_2x32f(ts + cb, td + cb, sv, dv);
-        if (h == 1) {  // every dP^T column of the tile is now in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(dp_free);
-        }
-        const float d0 = static_cast<float>(q0 + cb - key);
-#pragma unroll
-        for (int k = 0; k < kCols / 2; ++k) {  // columns 2k, 2k+1: queries with (-lse2, -delta) in lv
-          const float4 lv = lsd_s[cb / 2 + k];
-          float2 x = make_float2(sv[2 * k], sv[2 * k + 1]), y = make_float2(dv[2 * k], dv[2 * k + 1]);
-          const float2 dist = make_float2(fabsf(d0 + (2 * k)), fabsf(d0 + (2 * k + 1)));
-          p_and_ds<CAP, BIAS>(x, y, make_float2(lv.x, lv.z), make_float2(lv.y, lv.w), dist, slope2, a.score);
-          sv[2 * k] = x.x;
-          sv[2 * k + 1] = x.y;
-          dv[2 * k] = y.x;
-          dv[2 * k + 1] = y.y;
-        }
+    for (int m = 0, n = 0, g = 0; ok && get_item_warp(ring, m, it); ++m) {
+      const Where w = where(it.lin);
+      const int k0 = w.kt * 128, key = k0 + row;
+      const int total = group * it.count;
+      const Hull* hulls = a.hulls + static_cast<int64_t>(w.b) * n_t;
+      Hull hull = total > 0 ? hulls[it.first] : Hull{0, 0, 0, 0};
+      for (int i = 0; i < total && ok; ++i, ++g) {
+        const int q0 = (it.first + i % it.count) * 128;
+        const bool all = sees_all(hull, k0, k0 + 128), padded = hull.max_lo == INT_MAX;
+        if (i + 1 < total) hull = hulls[it.first + (i + 1) % it.count];
+        uint32_t vis[2] = {~0u, ~0u};  // visible query columns of this thread's key, per half
         if (!all) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            const bool keep = vis[h] >> c & 1u;
-            sv[c] = keep ? sv[c] : 0.f;
-            dv[c] = keep ? dv[c] : 0.f;
+          for (int h = 0; h < 2; ++h) {
+            const int q = q0 + h * 64 + part * kCols + lane;
+            const int2 seen = q < s ? load_span(a.spans, w.b, q, s) : make_int2(0, 0);
+            vis[h] = warp_transpose(span_bits(seen, k0 + sub * 32), lane);
           }
         }
-        // P^T pairs then dS^T pairs over this warp's own 16 S^T columns: the A operands of
-        // K-step cb / 16 of the accumulating MMAs
+        const float slope2 = BIAS ? __ldg(a.slopes + w.kvh * group + i / it.count) * kLog2e : 0.f;
+        uint8_t* dstage = sm + L::DO + (g % DS) * L::DSTAGE;
+        const float4* lsd_s = reinterpret_cast<const float4*>(dstage + L::TILE);
+        // the pairs were copied with the tile's dO: observe that copy before reading them
+        if (!(ok = mbar_wait_warp(&d_full[g % DS], (g / DS) & 1, err, kErrTimeoutAttn))) break;
+        const uint32_t ts = s_slot(g) + tl, td = d_slot(g) + tl;
 #pragma unroll
-        for (int o = 0; o < kCols; o += 16) {
-          store_pairs16(ts + cb + o, sv, o);
-          store_pairs16(ts + cb + o + 8, dv, o);
-        }
-        tmem_st_wait();
-        if (padded) {  // this half's Q and dO rows that are padding: no product may read them
-          const int r = h * 64 + (elem & 63), which = elem >> 6;
-          if (which < 2 * L::NSL && reinterpret_cast<const float2*>(lsd_s)[r].x == -INFINITY) {
-            uint8_t* tile = which < L::NSL ? sm + L::Q + (i % QS) * L::TILE : dstage;
-            zero_slice_row(tile + (which % L::NSL) * kSlice128, r);
+        for (int h = 0; h < 2; ++h) {
+          if (!ok) break;
+          if (!(ok = mbar_wait_warp(&sdp_full[h], g & 1, err, kErrTimeoutAttn))) break;
+          tc_fence_after();
+          const int cb = h * 64 + part * kCols;  // this warp's score columns [cb, cb + 32)
+          float sv[kCols], dv[kCols];
+          tmem_ld_2x32f(ts + cb, td + cb, sv, dv);
+          if (h == 1) {  // every dP^T column of the tile is now in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dp_free);
           }
-          fence_proxy_async_smem();
+          const float d0 = static_cast<float>(q0 + cb - key);
+#pragma unroll
+          for (int k = 0; k < kCols / 2; ++k) {  // columns 2k, 2k+1: queries with (-lse2, -delta) in lv
+            const float4 lv = lsd_s[cb / 2 + k];
+            float2 x = make_float2(sv[2 * k], sv[2 * k + 1]), y = make_float2(dv[2 * k], dv[2 * k + 1]);
+            const float2 dist = make_float2(fabsf(d0 + (2 * k)), fabsf(d0 + (2 * k + 1)));
+            p_and_ds<CAP, BIAS>(x, y, make_float2(lv.x, lv.z), make_float2(lv.y, lv.w), dist, slope2, a.score);
+            sv[2 * k] = x.x;
+            sv[2 * k + 1] = x.y;
+            dv[2 * k] = y.x;
+            dv[2 * k + 1] = y.y;
+          }
+          if (!all) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+              const bool keep = vis[h] >> c & 1u;
+              sv[c] = keep ? sv[c] : 0.f;
+              dv[c] = keep ? dv[c] : 0.f;
+            }
+          }
+          // P^T pairs then dS^T pairs over this warp's own 16 S^T columns: the A operands of
+          // K-step cb / 16 of the accumulating MMAs
+#pragma unroll
+          for (int o = 0; o < kCols; o += 16) {
+            store_pairs16(ts + cb + o, sv, o);
+            store_pairs16(ts + cb + o + 8, dv, o);
+          }
+          tmem_st_wait();
+          if (padded) {  // this half's Q and dO rows that are padding: no product may read them
+            const int r = h * 64 + (elem & 63), which = elem >> 6;
+            if (which < 2 * L::NSL && reinterpret_cast<const float2*>(lsd_s)[r].x == -INFINITY) {
+              uint8_t* tile = which < L::NSL ? sm + L::Q + (g % QS) * L::TILE : dstage;
+              zero_slice_row(tile + (which % L::NSL) * kSlice128, r);
+            }
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_half[h]);
         }
+      }
+      if (!ok || (total > 0 && !mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
+      tc_fence_after();
+      const int64_t t = static_cast<int64_t>(w.b) * s + key;
+      half_row_out<HD>(tdK + tl, part, a.score.scale, a.dk + t * a.lddk + static_cast<int64_t>(w.kvh) * HD, key < s,
+                       total > 0);
+      half_row_out<HD>(tdV + tl, part, 1.f, a.dv + t * a.lddv + static_cast<int64_t>(w.kvh) * HD, key < s, total > 0);
+      if (total > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_half[h]);
+        if (lane == 0) mbar_arrive(acc_empty);
+        ++n;
       }
-    }
-    if (ok && (total == 0 || mbar_wait_warp(acc_done, 0, err, kErrTimeoutAttn))) {
-      tc_fence_after();
-      const int64_t t = static_cast<int64_t>(b) * s + key;
-      half_row_out<HD>(tdK + tl, part, a.score.scale, a.dk + t * a.lddk + static_cast<int64_t>(kvh) * HD, key < s,
-                       total > 0);
-      half_row_out<HD>(tdV + tl, part, 1.f, a.dv + t * a.lddv + static_cast<int64_t>(kvh) * HD, key < s, total > 0);
     }
   }
 
@@ -490,7 +600,7 @@ struct SmemQ {
   static constexpr int K = DO + TILE;                // KS tiles
   static constexpr int V = K + KS * TILE;            // VS tiles
   static constexpr int BAR = V + VS * TILE;
-  static constexpr int BYTES = BAR + 256;            // the dynamic window is 1024-aligned (checked)
+  static constexpr int BYTES = BAR + 320;            // the dynamic window is 1024-aligned (checked)
   static_assert(BYTES <= 232448, "dQ shared memory above the 227 KB per-CTA limit");
 };
 
@@ -510,41 +620,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint64_t* q_full = bar + 0;
-  uint64_t* k_full = bar + 1;            // [KS]
-  uint64_t* k_empty = bar + 4;           // [KS]
-  uint64_t* v_full = bar + 7;            // [VS]
-  uint64_t* v_empty = bar + 9;           // [VS]
-  uint64_t* sdp_full = bar + 11;         // the tile's S and dP are complete
-  uint64_t* dp_free = bar + 12;          // every warp holds its dP columns in registers
-  uint64_t* ds_half = bar + 13;          // [2]
-  uint64_t* dq_done = bar + 15;          // the last tile's dQ MMAs have completed
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 16);
-  uint32_t* empty_rows = reinterpret_cast<uint32_t*>(bar + 18);  // [4] bit r: row r of the 32 is padding
+  uint64_t* q_empty = bar + 1;           // every MMA that reads the item's Q and dO has completed
+  uint64_t* k_full = bar + 2;            // [KS]
+  uint64_t* k_empty = bar + 5;           // [KS]
+  uint64_t* v_full = bar + 8;            // [VS]
+  uint64_t* v_empty = bar + 10;          // [VS]
+  uint64_t* sdp_full = bar + 12;         // the tile's S and dP are complete
+  uint64_t* dp_free = bar + 13;          // every warp holds its dP columns in registers
+  uint64_t* ds_half = bar + 14;          // [2]
+  uint64_t* acc_full = bar + 16;         // the item's dQ MMAs have completed
+  uint64_t* acc_empty = bar + 17;        // every warp has read its part of dQ
+  const ItemRing ring{bar + 18, bar + 20, reinterpret_cast<Item*>(bar + 23), err};
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 22);
 
   const int s = a.s, nh = a.nh;
-  const int n_t = (s + 127) / 128;
-  const TileSlot slot = heavy_first_slot(static_cast<int>(blockIdx.x), n_t, static_cast<int>(gridDim.x) / n_t);
-  const int qt = n_t - 1 - slot.rank;  // the last query tile sees the most keys under a causal mask
-  const int head = slot.hb % nh, b = slot.hb / nh;
-  const int kvh = head / (nh / a.nkv);
-  const int q0 = qt * 128;
-  const Hull hull = a.hulls[static_cast<int64_t>(b) * n_t + qt];
-  const int j0 = hull.min_lo / 128;
-  const int n_kv = hull.max_hi > 0 ? (hull.max_hi + 127) / 128 - j0 : 0;  // key tiles j0 .. j0 + n_kv - 1
+  const int n_t = (s + 127) / 128, n_hb = nh * a.B;
+  const int group = nh / a.nkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp & 3;
-  const int part = (warp - 2) >> 2;  // which 32 of each 64 key columns this elementwise warp takes
-  const int row = sub * 32 + lane;
-  const int q = q0 + row;
-  int2 seen = make_int2(0, 0);
-  if (warp >= 2) {
-    if (q < s) seen = load_span(a.spans, b, q, s);
-    const uint32_t none = __ballot_sync(0xffffffffu, seen.x >= seen.y);
-    if (lane == 0 && part == 0) empty_rows[sub] = none;
-  }
+  // item -> query tile (the last one sees the most keys under a causal mask), head, sequence
+  struct Where {
+    int qt, head, b;
+  };
+  auto where = [&](int lin) -> Where {
+    const TileSlot slot = heavy_first_slot(lin, n_t, n_hb);
+    return {n_t - 1 - slot.rank, slot.hb % nh, slot.hb / nh};
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int i = 0; i < KS; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -557,7 +661,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(dp_free, kElemWarps);
     mbar_init(&ds_half[0], kElemWarps);
     mbar_init(&ds_half[1], kElemWarps);
-    mbar_init(dq_done, 1);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, kElemWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ring.full[i], 1);
+      mbar_init(&ring.empty[i], kItemReaders);
+    }
     fence_mbar_init();
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
@@ -573,26 +682,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = *tslot;
   const uint32_t tdP = tbase + 256, tdQ = tbase + 384;
-  auto s_slot = [&](int j) { return tbase + (j & 1) * 128; };
+  // g numbers the block's tiles across its items, n its items with a walk
+  auto s_slot = [&](int g) { return tbase + (g & 1) * 128; };
 
   if (warp == 0) {
-    // lane 0: Q and dO once, then the K ring; lane 1: the V ring
-    if (lane == 0 && n_kv > 0) {
-      mbar_arrive_expect_tx(q_full, 2 * L::TILE);
-      tma_load_4d(sm + L::Q, &map_q, q_full, 0, q0, head * (HD / 64), b);
-      tma_load_4d(sm + L::DO, &map_do, q_full, 0, q0, head * (HD / 64), b);
-      for (int j = 0; j < n_kv; ++j) {
-        const int st = j % KS;
-        if (!mbar_wait(&k_empty[st], ((j / KS) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
-        mbar_arrive_expect_tx(&k_full[st], L::TILE);
-        tma_load_4d(sm + L::K + st * L::TILE, &map_k, &k_full[st], 0, (j0 + j) * 128, kvh * (HD / 64), b);
+    // takes the items, each when the last load of the one before has been issued, and loads the K ring
+    if (lane == 0) {
+      const int items = n_t * n_hb;
+      auto take = [&](int lin) -> Item {
+        Item it{-1, 0, 0, {0, 0, 0, 0}};
+        if (lin < items) {
+          const Where w = where(lin);
+          it.lin = lin;
+          it.hull = a.hulls[static_cast<int64_t>(w.b) * n_t + w.qt];
+          it.first = it.hull.min_lo / 128;
+          it.count = it.hull.max_hi > 0 ? (it.hull.max_hi + 127) / 128 - it.first : 0;
+        }
+        return it;
+      };
+      Item cur = take(blockIdx.x);
+      bool ok = true;
+      for (int m = 0, g = 0; ok; ++m) {
+        if (!(ok = put_item(ring, m, cur)) || cur.lin < 0) break;
+        const Where w = where(cur.lin);
+        for (int j = 0; j < cur.count; ++j, ++g) {
+          const int st = g % KS;
+          if (!(ok = mbar_wait(&k_empty[st], ((g / KS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
+          mbar_arrive_expect_tx(&k_full[st], L::TILE);
+          tma_load_4d(sm + L::K + st * L::TILE, &map_k, &k_full[st], 0, (cur.first + j) * 128,
+                      w.head / group * (HD / 64), w.b);
+        }
+        if (ok) cur = take(gridDim.x + atomicAdd(a.taken, 1));
       }
-    } else if (lane == 1) {
-      for (int j = 0; j < n_kv; ++j) {
-        const int st = j % VS;
-        if (!mbar_wait(&v_empty[st], ((j / VS) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
-        mbar_arrive_expect_tx(&v_full[st], L::TILE);
-        tma_load_4d(sm + L::V + st * L::TILE, &map_v, &v_full[st], 0, (j0 + j) * 128, kvh * (HD / 64), b);
+    }
+  } else if (warp == 10) {
+    if (lane == 0) {  // the V ring
+      Item it;
+      bool ok = true;
+      for (int m = 0, g = 0; ok && get_item(ring, m, it); ++m) {
+        const Where w = where(it.lin);
+        for (int j = 0; j < it.count; ++j, ++g) {
+          const int st = g % VS;
+          if (!(ok = mbar_wait(&v_empty[st], ((g / VS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
+          mbar_arrive_expect_tx(&v_full[st], L::TILE);
+          tma_load_4d(sm + L::V + st * L::TILE, &map_v, &v_full[st], 0, (it.first + j) * 128,
+                      w.head / group * (HD / 64), w.b);
+        }
+      }
+    }
+  } else if (warp == 11) {
+    // Q and dO, once per item; first this block's share of the query ranges that dK/dV walks
+    for (int64_t i = blockIdx.x; i < static_cast<int64_t>(a.B) * n_t; i += gridDim.x) {
+      const Hull* hulls = a.hulls + i / n_t * n_t;
+      const int k0 = static_cast<int>(i % n_t) * 128;
+      int first = INT_MAX, last = -1;
+      for (int q = lane; q < n_t; q += 32) {
+        const Hull h = hulls[q];
+        if (h.min_lo < k0 + 128 && h.max_hi > k0) {
+          first = min(first, q);
+          last = q;
+        }
+      }
+      first = __reduce_min_sync(0xffffffffu, first);
+      last = __reduce_max_sync(0xffffffffu, last);
+      if (lane == 0) a.q_ranges[i] = make_int2(first, last);
+    }
+    if (lane == 0) {
+      Item it;
+      for (int m = 0, n = 0; get_item(ring, m, it); ++m) {
+        if (it.count == 0) continue;
+        const Where w = where(it.lin);
+        if (!mbar_wait(q_empty, (n & 1) ^ 1u, err, kErrTimeoutAttn)) break;
+        mbar_arrive_expect_tx(q_full, 2 * L::TILE);
+        tma_load_4d(sm + L::Q, &map_q, q_full, 0, w.qt * 128, w.head * (HD / 64), w.b);
+        tma_load_4d(sm + L::DO, &map_do, q_full, 0, w.qt * 128, w.head * (HD / 64), w.b);
+        ++n;
       }
     }
   } else if (warp == 1) {
@@ -601,113 +765,146 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, HD, false, true);
     const uint64_t qd = smem_desc_sw128(smem_addr(sm + L::Q), 16, 1024);
     const uint64_t dd = smem_desc_sw128(smem_addr(sm + L::DO), 16, 1024);
-    bool ok = n_kv > 0 && mbar_wait_warp(q_full, 0, err, kErrTimeoutAttn);
-    // S = Q K^T (dp = false) or dP = dO V^T of tile j into TMEM slot t, once its operand is in;
+    // S = Q K^T (dp = false) or dP = dO V^T of tile g into TMEM slot t, once its operand is in;
     // a V stage is released as soon as its dP has run
-    auto scores = [&](int j, bool dp, uint32_t t) -> bool {
-      uint64_t* full = dp ? &v_full[j % VS] : &k_full[j % KS];
-      const uint32_t parity = dp ? (j / VS) & 1 : (j / KS) & 1;
+    auto scores = [&](int g, bool dp, uint32_t t) -> bool {
+      uint64_t* full = dp ? &v_full[g % VS] : &k_full[g % KS];
+      const uint32_t parity = dp ? (g / VS) & 1 : (g / KS) & 1;
       if (!mbar_wait_warp(full, parity, err, kErrTimeoutAttn)) return false;
       tc_fence_after();
       const uint64_t ad = dp ? dd : qd;
       const uint64_t bd =
-          smem_desc_sw128(smem_addr(dp ? sm + L::V + (j % VS) * L::TILE : sm + L::K + (j % KS) * L::TILE), 16, 1024);
+          smem_desc_sw128(smem_addr(dp ? sm + L::V + (g % VS) * L::TILE : sm + L::K + (g % KS) * L::TILE), 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk) {
         const uint32_t off = (kk >> 2) * kSlice128 + (kk & 3) * 32;
         umma_bf16_warp(t, desc_advance(ad, off), desc_advance(bd, off), idesc_s, kk > 0 ? 1u : 0u);
       }
-      if (dp) umma_commit_warp(&v_empty[j % VS]);
+      if (dp) umma_commit_warp(&v_empty[g % VS]);
       return true;
     };
-    if (ok) ok = scores(0, false, s_slot(0)) && scores(0, true, tdP);
-    if (ok) umma_commit_warp(sdp_full);
-    for (int j = 0; j < n_kv && ok; ++j) {
-      // B operand of the dQ MMAs: the K tile read MN-major (16 keys per step)
-      const uint64_t kd = smem_desc_sw128(smem_addr(sm + L::K + (j % KS) * L::TILE), kSlice128, 1024);
-      // the next tile's S into the other S slot, whose dS was read by MMAs issued earlier
-      if (j + 1 < n_kv && !(ok = scores(j + 1, false, s_slot(j + 1)))) break;
-      for (int h = 0; h < 2 && ok; ++h) {
-        if (h == 1 && j + 1 < n_kv) {  // the dP slot is free once every warp holds its columns
-          if (!(ok = mbar_wait_warp(dp_free, j & 1, err, kErrTimeoutAttn))) break;
+    Item it;
+    bool ok = true;
+    for (int m = 0, n = 0, g = 0; ok && get_item_warp(ring, m, it); ++m) {
+      const int total = it.count;
+      if (total == 0) continue;
+      // the item's first scores: its S slot was last read by products issued before, the dP slot is
+      // free once every warp holds the last tile's columns
+      if (!(ok = mbar_wait_warp(q_full, n & 1, err, kErrTimeoutAttn))) break;
+      if (!(ok = scores(g, false, s_slot(g)))) break;
+      if (g > 0 && !(ok = mbar_wait_warp(dp_free, (g - 1) & 1, err, kErrTimeoutAttn))) break;
+      if (!(ok = scores(g, true, tdP))) break;
+      umma_commit_warp(sdp_full);
+      if (total == 1) umma_commit_warp(q_empty);
+      for (int j = 0; j < total && ok; ++j, ++g) {
+        // B operand of the dQ MMAs: the K tile read MN-major (16 keys per step)
+        const uint64_t kd = smem_desc_sw128(smem_addr(sm + L::K + (g % KS) * L::TILE), kSlice128, 1024);
+        // the next tile's S into the other S slot, whose dS was read by MMAs issued earlier
+        if (j + 1 < total && !(ok = scores(g + 1, false, s_slot(g + 1)))) break;
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (h == 1 && j + 1 < total) {  // the dP slot is free once every warp holds its columns
+            if (!(ok = mbar_wait_warp(dp_free, g & 1, err, kErrTimeoutAttn))) break;
+            tc_fence_after();
+            if (!(ok = scores(g + 1, true, tdP))) break;
+            umma_commit_warp(sdp_full);
+            if (j + 2 == total) umma_commit_warp(q_empty);
+          }
+          if (!(ok = mbar_wait_warp(&ds_half[h], g & 1, err, kErrTimeoutAttn))) break;
+          // the first product of an item overwrites the accumulator: the last item's has been read
+          if (h == 0 && j == 0 && n > 0 && !(ok = mbar_wait_warp(acc_empty, (n - 1) & 1, err, kErrTimeoutAttn))) break;
           tc_fence_after();
-          if (!(ok = scores(j + 1, true, tdP))) break;
-          umma_commit_warp(sdp_full);
-        }
-        if (!(ok = mbar_wait_warp(&ds_half[h], j & 1, err, kErrTimeoutAttn))) break;
-        tc_fence_after();
 #pragma unroll
-        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)  // 16 keys per step; A (dS) from TMEM
-          umma_bf16_tmem_a_warp(tdQ, s_slot(j) + kk * 16, desc_advance(kd, kk * 2048), idesc_acc,
-                                (j > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)  // 16 keys per step; A (dS) from TMEM
+            umma_bf16_tmem_a_warp(tdQ, s_slot(g) + kk * 16, desc_advance(kd, kk * 2048), idesc_acc,
+                                  (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (!ok) break;
+        umma_commit_warp(&k_empty[g % KS]);
+        if (j + 1 == total) umma_commit_warp(acc_full);
       }
-      if (!ok) break;
-      umma_commit_warp(&k_empty[j % KS]);
-      if (j == n_kv - 1) umma_commit_warp(dq_done);
+      ++n;
     }
   } else {
+    const int sub = warp & 3;
+    const int part = (warp - 2) >> 2;  // which 32 of each 64 key columns this warp takes
+    const int row = sub * 32 + lane;
     const int elem = threadIdx.x - 64;
-    const bool padded = (empty_rows[0] | empty_rows[1] | empty_rows[2] | empty_rows[3]) != 0;
     const uint32_t tl = static_cast<uint32_t>(sub * 32) << 16;
-    const float2 lq = a.lsd[(static_cast<int64_t>(b) * nh + head) * pad128(s) + q];  // padded: q is inside
-    const float2 nl2 = make_float2(lq.x, lq.x), ndl = make_float2(lq.y, lq.y);
-    const float slope2 = BIAS ? a.slopes[head] * kLog2e : 0.f;
+    Item it;
     bool ok = true;
-    for (int j = 0; j < n_kv && ok; ++j) {
-      if (!(ok = mbar_wait_warp(sdp_full, j & 1, err, kErrTimeoutAttn))) break;
-      tc_fence_after();
-      const uint32_t ts = s_slot(j) + tl;
-      const int key_tile = (j0 + j) * 128;
-      const bool all = sees_all(hull, key_tile, key_tile + 128);
-      // rows of K that nothing here may see: outside the hull, or padding among the tile's own rows
-      const bool own = padded && key_tile == q0;
-      const bool clean = own || key_tile < hull.min_lo || key_tile + 128 > hull.max_hi;
+    for (int m = 0, n = 0, g = 0; ok && get_item_warp(ring, m, it); ++m) {
+      const Where w = where(it.lin);
+      const int q0 = w.qt * 128, q = q0 + row;
+      const Hull hull = it.hull;
+      const int2 seen = q < s ? load_span(a.spans, w.b, q, s) : make_int2(0, 0);
+      const float2 lq = a.lsd[(static_cast<int64_t>(w.b) * nh + w.head) * pad128(s) + q];  // padded: q is inside
+      const float2 nl2 = make_float2(lq.x, lq.x), ndl = make_float2(lq.y, lq.y);
+      const float slope2 = BIAS ? a.slopes[w.head] * kLog2e : 0.f;
+      const bool padded = hull.max_lo == INT_MAX;
+      for (int j = 0; j < it.count && ok; ++j, ++g) {
+        if (!(ok = mbar_wait_warp(sdp_full, g & 1, err, kErrTimeoutAttn))) break;
+        tc_fence_after();
+        const uint32_t ts = s_slot(g) + tl;
+        const int key_tile = (it.first + j) * 128;
+        const bool all = sees_all(hull, key_tile, key_tile + 128);
+        // rows of K that nothing here may see: outside the hull, or padding among the tile's own rows
+        const bool own = padded && key_tile == q0;
+        const bool clean = own || key_tile < hull.min_lo || key_tile + 128 > hull.max_hi;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int cb = h * 64 + part * kCols;
-        float sv[kCols], dv[kCols];
-        tmem_ld_2x32f(ts + cb, tdP + tl + cb, sv, dv);
-        if (h == 1) {  // every dP column of the tile is now in registers
+        for (int h = 0; h < 2; ++h) {
+          const int cb = h * 64 + part * kCols;
+          float sv[kCols], dv[kCols];
+          tmem_ld_2x32f(ts + cb, tdP + tl + cb, sv, dv);
+          if (h == 1) {  // every dP column of the tile is now in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dp_free);
+          }
+          const int key0 = key_tile + cb;
+          const float d0 = static_cast<float>(q - key0);
+#pragma unroll
+          for (int k = 0; k < kCols / 2; ++k) {  // dS = P (dP - delta) z', two columns at a time
+            float2 x = make_float2(sv[2 * k], sv[2 * k + 1]), y = make_float2(dv[2 * k], dv[2 * k + 1]);
+            const float2 dist = make_float2(fabsf(d0 - (2 * k)), fabsf(d0 - (2 * k + 1)));
+            p_and_ds<CAP, BIAS>(x, y, nl2, ndl, dist, slope2, a.score);
+            dv[2 * k] = y.x;
+            dv[2 * k + 1] = y.y;
+          }
+          if (!all) {
+            const uint32_t vis = span_bits(seen, key0);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) dv[c] = vis >> c & 1u ? dv[c] : 0.f;
+          }
+          // dS goes back into TMEM over this warp's S columns (A operand of K-step cb / 16)
+#pragma unroll
+          for (int o = 0; o < kCols; o += 16) store_pairs16(ts + cb + o, dv, o);
+          tmem_st_wait();
+          if (clean) {
+            const int r = h * 64 + (elem & 63), which = elem >> 6, key = key_tile + r;
+            bool gone = key < hull.min_lo || key >= hull.max_hi;
+            if (own && !gone) {
+              const int2 its = load_span(a.spans, w.b, key, s);  // key < max_hi <= s
+              gone = its.x >= its.y;
+            }
+            if (which < L::NSL && gone) zero_slice_row(sm + L::K + (g % KS) * L::TILE + which * kSlice128, r);
+            fence_proxy_async_smem();
+          }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(dp_free);
+          if (lane == 0) mbar_arrive(&ds_half[h]);
         }
-        const int key0 = key_tile + cb;
-        const float d0 = static_cast<float>(q - key0);
-#pragma unroll
-        for (int k = 0; k < kCols / 2; ++k) {  // dS = P (dP - delta) z', two columns at a time
-          float2 x = make_float2(sv[2 * k], sv[2 * k + 1]), y = make_float2(dv[2 * k], dv[2 * k + 1]);
-          const float2 dist = make_float2(fabsf(d0 - (2 * k)), fabsf(d0 - (2 * k + 1)));
-          p_and_ds<CAP, BIAS>(x, y, nl2, ndl, dist, slope2, a.score);
-          dv[2 * k] = y.x;
-          dv[2 * k + 1] = y.y;
-        }
-        if (!all) {
-          const uint32_t vis = span_bits(seen, key0);
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) dv[c] = vis >> c & 1u ? dv[c] : 0.f;
-        }
-        // dS goes back into TMEM over this warp's S columns (A operand of K-step cb / 16)
-#pragma unroll
-        for (int o = 0; o < kCols; o += 16) store_pairs16(ts + cb + o, dv, o);
-        tmem_st_wait();
-        if (clean) {
-          const int r = h * 64 + (elem & 63), which = elem >> 6, key = key_tile + r;
-          const bool pad = own && (empty_rows[r >> 5] >> (r & 31) & 1u);
-          if (which < L::NSL && (key < hull.min_lo || key >= hull.max_hi || pad))
-            zero_slice_row(sm + L::K + (j % KS) * L::TILE + which * kSlice128, r);
-          fence_proxy_async_smem();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ds_half[h]);
       }
-    }
-    if (ok && (n_kv == 0 || mbar_wait_warp(dq_done, 0, err, kErrTimeoutAttn))) {
+      if (!ok || (it.count > 0 && !mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
       tc_fence_after();
       half_row_out<HD>(tdQ + tl, part, a.score.scale,
-                       a.dq + (static_cast<int64_t>(b) * s + q) * a.lddq + static_cast<int64_t>(head) * HD, q < s,
-                       n_kv > 0);
+                       a.dq + (static_cast<int64_t>(w.b) * s + q) * a.lddq + static_cast<int64_t>(w.head) * HD, q < s,
+                       it.count > 0);
+      if (it.count > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+        ++n;
+      }
     }
   }
 
@@ -722,7 +919,7 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
                    BwdArgs a, float2* lsd, Hull* hulls, cudaStream_t st) {
   const int n_t = (g.s + 127) / 128;
   span_delta_kernel<HD><<<static_cast<unsigned>(n_t) * g.nh * g.B, 256, 0, st>>>(o, ldo, dout, lddo, lse, a.spans, lsd,
-                                                                                 hulls, g.s, g.nh, n_t);
+                                                                                 hulls, a.taken, g.s, g.nh, n_t);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   constexpr uint32_t nsl = HD / 64;  // one box carries every head_dim slice of a tile
@@ -737,13 +934,15 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
   auto* dq = &attn_span_dq_kernel<HD, CAP, BIAS>;
   e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemQ<HD>::BYTES);
   if (e != cudaSuccess) return e;
-  dq<<<static_cast<unsigned>(n_t) * g.nh * g.B, kThreads, SmemQ<HD>::BYTES, st>>>(mq, mk, mv, md, a);
+  const int sms = gemm_num_sms();
+  const int64_t q_items = static_cast<int64_t>(n_t) * g.nh * g.B, k_items = static_cast<int64_t>(n_t) * g.nkv * g.B;
+  dq<<<static_cast<unsigned>(q_items < sms ? q_items : sms), kThreads, SmemQ<HD>::BYTES, st>>>(mq, mk, mv, md, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS>;
   e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemKV<HD>::BYTES);
   if (e != cudaSuccess) return e;
-  dkdv<<<static_cast<unsigned>(n_t) * g.nkv * g.B, kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, a);
+  dkdv<<<static_cast<unsigned>(k_items < sms ? k_items : sms), kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, a);
   return cudaGetLastError();
 }
 
@@ -751,7 +950,7 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
 
 uint64_t attn_span_bwd_scratch(int B, int s, int nh) {
   const uint64_t sp = static_cast<uint64_t>(pad128(s));
-  return static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * sizeof(Hull));
+  return static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * (sizeof(Hull) + sizeof(int2))) + 16;
 }
 
 cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const float* lse, const bf16* dout,
@@ -768,7 +967,10 @@ cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, con
     return cudaErrorInvalidValue;
   float2* lsd = static_cast<float2*>(scratch);
   Hull* hulls = reinterpret_cast<Hull*>(lsd + static_cast<int64_t>(g.B) * g.nh * pad128(g.s));
-  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, dq, dk, dv, lddq, lddk, lddv, g.s, g.nh, g.nkv, score_args(g), err};
+  const int64_t tiles = static_cast<int64_t>(g.B) * (pad128(g.s) / 128);
+  int2* q_ranges = reinterpret_cast<int2*>(hulls + tiles);
+  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_ranges, reinterpret_cast<int*>(q_ranges + tiles), dq, dk, dv,
+                  lddq, lddk, lddv, g.B, g.s, g.nh, g.nkv, score_args(g), err};
   return dispatch(g, [&](auto hd, auto cap, auto bias) {
     return launch<decltype(hd)::value, decltype(cap)::value, decltype(bias)::value>(g, o, ldo, lse, dout, lddo, a, lsd,
                                                                                     hulls, st);

