@@ -300,27 +300,28 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_after();
       const bool some = l != 0.f;  // NaN counts as something
       const float inv = 1.f / l;
-      bf16* orow = a.o + (static_cast<int64_t>(b) * s + q) * a.ldo + static_cast<int64_t>(head) * HD;
+      // the warp's 32 rows, 64 columns at a time
+      bf16* o0 = a.o + (static_cast<int64_t>(b) * s + q0 + sub * 32) * a.ldo + static_cast<int64_t>(head) * HD;
 #pragma unroll
-      for (int c4 = 0; c4 < HD / 32; ++c4) {
-        uint32_t r[32] = {};
-        if (n_kv > 0) {
-          tmem_ld_32cols(tO + tl + c4 * 32, r);
-          tmem_ld_wait();
-        }
-        if (q < s) {
+      for (int c64 = 0; c64 < HD / 64; ++c64) {
+        uint4 out[8];
+#pragma unroll
+        for (int c4 = 0; c4 < 2; ++c4) {
+          uint32_t r[32] = {};
+          if (n_kv > 0) {
+            tmem_ld_32cols(tO + tl + c64 * 64 + c4 * 32, r);
+            tmem_ld_wait();
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) r[i] = some ? __float_as_uint(__uint_as_float(r[i]) * inv) : 0u;
 #pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4) {
-            uint4 v;
-            v.x = pack_bf16(__uint_as_float(r[8 * v4 + 0]), __uint_as_float(r[8 * v4 + 1]));
-            v.y = pack_bf16(__uint_as_float(r[8 * v4 + 2]), __uint_as_float(r[8 * v4 + 3]));
-            v.z = pack_bf16(__uint_as_float(r[8 * v4 + 4]), __uint_as_float(r[8 * v4 + 5]));
-            v.w = pack_bf16(__uint_as_float(r[8 * v4 + 6]), __uint_as_float(r[8 * v4 + 7]));
-            reinterpret_cast<uint4*>(orow + c4 * 32)[v4] = v;
-          }
+          for (int v = 0; v < 4; ++v)
+            out[4 * c4 + v] = make_uint4(pack_bf16(__uint_as_float(r[8 * v + 0]), __uint_as_float(r[8 * v + 1])),
+                                         pack_bf16(__uint_as_float(r[8 * v + 2]), __uint_as_float(r[8 * v + 3])),
+                                         pack_bf16(__uint_as_float(r[8 * v + 4]), __uint_as_float(r[8 * v + 5])),
+                                         pack_bf16(__uint_as_float(r[8 * v + 6]), __uint_as_float(r[8 * v + 7])));
         }
+        store_rows<8>(o0 + c64 * 64, a.ldo, s - q0 - sub * 32, out, lane);
       }
       if (q < s) a.lse[(static_cast<int64_t>(b) * nh + head) * s + q] = some ? m_ref + log2f(l) : -INFINITY;
     }

@@ -22,12 +22,20 @@ struct Spans {
   const int32_t* hi;  // [B*s] or null: i + 1
 };
 
-// The span of row i of sequence b, clamped to the sequence; an empty one is (0, 0).
-__device__ __forceinline__ int2 load_span(const Spans& sp, int b, int i, int s) {
+// The span of row i of sequence b as given (a row past the end has none). Loaded ahead of its use and
+// clamped where it is used: an operation on the loaded values would wait for them.
+__device__ __forceinline__ int2 fetch_span(const Spans& sp, int b, int i, int s) {
+  if (i >= s) return make_int2(0, 0);
   const int64_t at = static_cast<int64_t>(b) * s + i;
-  const int lo = sp.lo ? max(__ldg(sp.lo + at), 0) : 0;
-  const int hi = sp.hi ? min(__ldg(sp.hi + at), s) : i + 1;
+  return make_int2(sp.lo ? __ldg(sp.lo + at) : 0, sp.hi ? __ldg(sp.hi + at) : i + 1);
+}
+// Clamped to the sequence; an empty one is (0, 0).
+__device__ __forceinline__ int2 clamp_span(int2 r, int s) {
+  const int lo = max(r.x, 0), hi = min(r.y, s);
   return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+__device__ __forceinline__ int2 load_span(const Spans& sp, int b, int i, int s) {
+  return clamp_span(fetch_span(sp, b, i, s), s);
 }
 
 // Summary of a tile of rows: the keys some row sees lie in [min_lo, max_hi); every row sees the
@@ -104,6 +112,32 @@ inline ScoreArgs score_args(const AttnSpanArgs& g) {
 }
 __device__ __forceinline__ float cap_r(float x, const ScoreArgs& a) { return rcp(1.f + ex2(x * a.cap_in)); }
 __device__ __forceinline__ float cap_score(float r, const ScoreArgs& a) { return fmaf(-2.f * a.cap_out, r, a.cap_out); }
+
+// Store 32 rows of NC 16-byte chunks, lane l holding row l: transposed within groups of NC lanes
+// (log2 NC exchanges) so that a store instruction writes 32 / NC rows' whole runs of NC chunks.
+// base: row 0, chunk 0; rows past `rows` are left out.
+template <int NC>
+__device__ __forceinline__ void store_rows(bf16* base, int64_t ld, int rows, uint4 (&c)[NC], int lane) {
+#pragma unroll
+  for (int b = 1; b < NC; b <<= 1) {
+    const bool up = (lane & b) != 0;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      if (k & b) continue;
+      uint4& lo = c[k];
+      uint4& hi = c[k | b];
+      const uint4 give = make_uint4(up ? lo.x : hi.x, up ? lo.y : hi.y, up ? lo.z : hi.z, up ? lo.w : hi.w);
+      const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, b), __shfl_xor_sync(0xffffffffu, give.y, b),
+                                   __shfl_xor_sync(0xffffffffu, give.z, b), __shfl_xor_sync(0xffffffffu, give.w, b));
+      lo = up ? got : lo;
+      hi = up ? hi : got;
+    }
+  }
+  const int first = lane / NC * NC;
+#pragma unroll
+  for (int k = 0; k < NC; ++k)
+    if (first + k < rows) *reinterpret_cast<uint4*>(base + (first + k) * ld + (lane % NC) * 8) = c[k];
+}
 
 // Zero the 128 bytes of one 64-column slice of an operand row in shared memory. The 128-byte
 // swizzle moves 16-byte chunks within a row only, so it does not matter here.

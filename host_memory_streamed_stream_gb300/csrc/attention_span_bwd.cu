@@ -68,19 +68,20 @@ __device__ __forceinline__ void tmem_ld_2x32f(uint32_t ta, uint32_t tb, float (&
   }
 }
 
-// Half of one TMEM lane's fp32 row (columns [part*HD/2, +HD/2)), times `scale`, as bf16 to dst.
-// acc = false: the accumulator was never written, the row is zero.
+// An item's gradients leave through shared memory: each thread converts half of its row (columns
+// [part*HD/2, +HD/2)) of the accumulator and writes it to the ring stage that the item's last tile
+// was read from, in the swizzled layout of a TMA store, which the warp that loads the items' own operands issues. (Each lane storing
+// its own row to global memory touches 32 lines an instruction: 7500 cycles for the two 128 x 128
+// gradients of a key tile, two tiles' work. Rows transposed through the warp first: 4700.)
 template <int HD>
-__device__ __forceinline__ void half_row_out(uint32_t taddr, int part, float scale, bf16* dst, bool store, bool acc) {
+__device__ __forceinline__ void stage_half_row(uint32_t taddr, int part, float scale, uint8_t* tile, int row) {
 #pragma unroll
-  for (int c = 0; c < HD / 2; c += 32) {
-    uint32_t r[32] = {};
-    if (acc) {
-      tmem_ld_32cols(taddr + part * (HD / 2) + c, r);
-      tmem_ld_wait();
-    }
-    if (!store) continue;
-    uint4* d = reinterpret_cast<uint4*>(dst + part * (HD / 2) + c);
+  for (int c = 0; c < HD / 64; ++c) {
+    uint32_t r[32];
+    const int col = part * (HD / 2) + c * 32;
+    tmem_ld_32cols(taddr + col, r);
+    tmem_ld_wait();
+    uint8_t* line = tile + (col >> 6) * kSlice128 + row * 128;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       uint4 u;
@@ -88,9 +89,16 @@ __device__ __forceinline__ void half_row_out(uint32_t taddr, int part, float sca
       u.y = pack_bf16(__uint_as_float(r[8 * v + 2]) * scale, __uint_as_float(r[8 * v + 3]) * scale);
       u.z = pack_bf16(__uint_as_float(r[8 * v + 4]) * scale, __uint_as_float(r[8 * v + 5]) * scale);
       u.w = pack_bf16(__uint_as_float(r[8 * v + 6]) * scale, __uint_as_float(r[8 * v + 7]) * scale);
-      d[v] = u;
+      *reinterpret_cast<uint4*>(line + ((((col & 63) >> 3) + v) ^ (row & 7)) * 16) = u;
     }
   }
+}
+
+// Zeros to `rows` rows of HD columns (an item without a walk): the elementwise threads, 16 bytes each.
+template <int HD>
+__device__ __forceinline__ void zero_rows(bf16* dst, int64_t ld, int rows, int elem) {
+  for (int i = elem; i < rows * (HD / 8); i += kElem)
+    *reinterpret_cast<uint4*>(dst + i / (HD / 8) * ld + i % (HD / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ------------------------------------------------------------------ items
@@ -107,6 +115,7 @@ struct ItemRing {
   Item* slot;       // [2]
   int* err;
 };
+constexpr int kTakeAhead = 2;     // the next item is taken with the last this many loads of an item
 constexpr int kItemReaders = 11;  // lane 0 of every warp but the one that takes items
 
 // Publish item number n (one thread).
@@ -251,6 +260,7 @@ template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_span_dkdv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                          const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv,
                           const __grid_constant__ BwdArgs a) {
   using L = SmemKV<HD>;
   constexpr int QS = L::QS, DS = L::DS;
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* dp_free = bar + 14;          // every warp holds its dP^T columns in registers
   uint64_t* p_half = bar + 15;           // [2]: every warp has written P^T/dS^T of that half
   uint64_t* acc_full = bar + 17;         // the item's accumulating MMAs have completed
-  uint64_t* acc_empty = bar + 18;        // every warp has read its part of dK and dV
+  uint64_t* acc_empty = bar + 18;        // every warp has read its part of dK and dV and staged it
   const ItemRing ring{bar + 19, bar + 21, reinterpret_cast<Item*>(bar + 24), err};
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 23);
 
@@ -332,9 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto d_slot = [&](int g) { return tbase + ((g & 1) ^ 1) * 128; };  // dP^T
 
   if (warp == 0) {
-    // takes the items and loads the Q ring. The next item is taken when the last load of this one has
-    // been issued, up to QS tiles before its end: taken any earlier (with the item before), the items
-    // no longer go to the blocks that are done first (14B heads, 256 unequal items: 385 -> 470 us)
+    // takes the items and loads the Q ring. The next item is taken with the last loads of this one, a
+    // few tiles before its end: taken with the item itself, the items no longer go to the blocks that
+    // are done first (14B heads, 256 unequal items: 385 -> 470 us); taken any later, the next item's
+    // first loads come late
     if (lane == 0) {
       const int items = n_t * n_hb;
       auto take = [&](int lin) -> Item {
@@ -349,18 +360,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         return it;
       };
       Item cur = take(blockIdx.x);
-      bool ok = true;
-      for (int m = 0, g = 0; ok; ++m) {
-        if (!(ok = put_item(ring, m, cur)) || cur.lin < 0) break;
+      bool ok = put_item(ring, 0, cur);
+      for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
         const Where w = where(cur.lin);
-        for (int i = 0; i < group * cur.count; ++i, ++g) {
+        const int total = group * cur.count, early = max(total - kTakeAhead, 0);
+        Item next;
+        auto hand_on = [&] {
+          next = take(gridDim.x + atomicAdd(a.taken + 1, 1));
+          return put_item(ring, m, next);
+        };
+        if (total == 0 && !(ok = hand_on())) break;
+        for (int i = 0; i < total; ++i, ++g) {
+          if (i == early && !(ok = hand_on())) break;
           const int st = g % QS;
           if (!(ok = mbar_wait(&q_empty[st], ((g / QS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
           mbar_arrive_expect_tx(&q_full[st], L::TILE);
           tma_load_4d(sm + L::Q + st * L::TILE, &map_q, &q_full[st], 0, (cur.first + i % cur.count) * 128,
                       (w.kvh * group + i / cur.count) * (HD / 64), w.b);
         }
-        if (ok) cur = take(gridDim.x + atomicAdd(a.taken + 1, 1));
+        cur = next;
       }
     }
   } else if (warp == 10) {
@@ -382,18 +400,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 11) {
-    // K and V, once per item
+    // K and V, once per item; and the gradients of the item before, from the stages of its last tile,
+    // which are released when they have been read
     if (lane == 0) {
       Item it;
-      for (int m = 0, n = 0; get_item(ring, m, it); ++m) {
-        if (it.count == 0) continue;
+      Where out{0, 0, 0};
+      bool ok = true;
+      auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
+        if (!mbar_wait(acc_empty, n & 1, err, kErrTimeoutAttn)) return false;
+        tma_store_4d(&map_dk, sm + L::Q + (g % QS) * L::TILE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
+        tma_store_4d(&map_dv, sm + L::DO + (g % DS) * L::DSTAGE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(&q_empty[g % QS]);
+        mbar_arrive(&d_empty[g % DS]);
+        return true;
+      };
+      int n = 0, g = 0, stored = 0;
+      for (int m = 0; ok && get_item(ring, m, it); ++m) {
         const Where w = where(it.lin);
-        if (!mbar_wait(kv_empty, (n & 1) ^ 1u, err, kErrTimeoutAttn)) break;
-        mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
-        tma_load_4d(sm + L::K, &map_k, kv_full, 0, w.kt * 128, w.kvh * (HD / 64), w.b);
-        tma_load_4d(sm + L::V, &map_v, kv_full, 0, w.kt * 128, w.kvh * (HD / 64), w.b);
-        ++n;
+        const int last = g - 1;
+        if (it.count > 0) {
+          if (!(ok = mbar_wait(kv_empty, (n & 1) ^ 1u, err, kErrTimeoutAttn))) break;
+          mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
+          tma_load_4d(sm + L::K, &map_k, kv_full, 0, w.kt * 128, w.kvh * (HD / 64), w.b);
+          tma_load_4d(sm + L::V, &map_v, kv_full, 0, w.kt * 128, w.kvh * (HD / 64), w.b);
+        }
+        if (stored < n) ok = store(stored++, last);
+        if (it.count > 0) {
+          out = w;
+          g += group * it.count;
+          ++n;
+        }
       }
+      if (ok && stored < n) store(stored, g - 1);
+      bulk_wait();
     }
   } else if (warp == 1) {
     // the whole warp runs the issuing loop; elect.sync picks the lane that issues each MMA
@@ -468,9 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        umma_commit_warp(&q_empty[g % QS]);
-        umma_commit_warp(&d_empty[g % DS]);
-        if (i + 1 < total) {
+        if (i + 1 < total) {  // the last tile's stages are released once the gradients have left them
+          umma_commit_warp(&q_empty[g % QS]);
+          umma_commit_warp(&d_empty[g % DS]);
           // the next tile's second dP^T half over this tile's last P^T/dS^T pairs
           if (!(ok = dp_half(g + 1, 1))) break;
           umma_commit_warp(&sdp_full[1]);
@@ -487,28 +528,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = sub * 32 + lane;
     const int elem = threadIdx.x - 64;
     const uint32_t tl = static_cast<uint32_t>(sub * 32) << 16;
-    Item it;
-    bool ok = true;
-    for (int m = 0, n = 0, g = 0; ok && get_item_warp(ring, m, it); ++m) {
-      const Where w = where(it.lin);
+    // A tile's hull and its query rows' spans (of this lane's column in each half) are loaded a tile
+    // ahead, an item's first ones before the last item's gradients are stored: a load here costs
+    // the block 800 cycles.
+    struct Ahead {
+      Hull hull;
+      int2 seen[2];
+    };
+    auto look = [&](int b, int qt) -> Ahead {
+      Ahead r;
+      r.hull = a.hulls[static_cast<int64_t>(b) * n_t + qt];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) r.seen[h] = fetch_span(a.spans, b, qt * 128 + h * 64 + part * kCols + lane, s);
+      return r;
+    };
+    Item it, next_it;
+    Where next_w{0, 0, 0};
+    Ahead ahead{};
+    bool ok = true, more = get_item_warp(ring, 0, next_it);
+    if (more) {
+      next_w = where(next_it.lin);
+      if (next_it.count > 0) ahead = look(next_w.b, next_it.first);
+    }
+    for (int m = 1, n = 0, g = 0; ok && more; ++m) {
+      it = next_it;
+      const Where w = next_w;
       const int k0 = w.kt * 128, key = k0 + row;
       const int total = group * it.count;
-      const Hull* hulls = a.hulls + static_cast<int64_t>(w.b) * n_t;
-      Hull hull = total > 0 ? hulls[it.first] : Hull{0, 0, 0, 0};
-      for (int i = 0; i < total && ok; ++i, ++g) {
-        const int q0 = (it.first + i % it.count) * 128;
-        const bool all = sees_all(hull, k0, k0 + 128), padded = hull.max_lo == INT_MAX;
-        if (i + 1 < total) hull = hulls[it.first + (i + 1) % it.count];
+      for (int i = 0, qt = it.first, hq = w.kvh * group; i < total && ok; ++i, ++g) {
+        const int q0 = qt * 128;
+        const bool all = sees_all(ahead.hull, k0, k0 + 128), padded = ahead.hull.max_lo == INT_MAX;
         uint32_t vis[2] = {~0u, ~0u};  // visible query columns of this thread's key, per half
         if (!all) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int q = q0 + h * 64 + part * kCols + lane;
-            const int2 seen = q < s ? load_span(a.spans, w.b, q, s) : make_int2(0, 0);
-            vis[h] = warp_transpose(span_bits(seen, k0 + sub * 32), lane);
-          }
+          for (int h = 0; h < 2; ++h) vis[h] = warp_transpose(span_bits(clamp_span(ahead.seen[h], s), k0 + sub * 32), lane);
         }
-        const float slope2 = BIAS ? __ldg(a.slopes + w.kvh * group + i / it.count) * kLog2e : 0.f;
+        const float slope2 = BIAS ? __ldg(a.slopes + hq) * kLog2e : 0.f;
+        if (++qt == it.first + it.count) {  // the walk of the group's next head
+          qt = it.first;
+          ++hq;
+        }
+        if (i + 1 < total) ahead = look(w.b, qt);
         uint8_t* dstage = sm + L::DO + (g % DS) * L::DSTAGE;
         const float4* lsd_s = reinterpret_cast<const float4*>(dstage + L::TILE);
         // the pairs were copied with the tile's dO: observe that copy before reading them
@@ -568,18 +628,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&p_half[h]);
         }
       }
-      if (!ok || (total > 0 && !mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
-      tc_fence_after();
-      const int64_t t = static_cast<int64_t>(w.b) * s + key;
-      half_row_out<HD>(tdK + tl, part, a.score.scale, a.dk + t * a.lddk + static_cast<int64_t>(w.kvh) * HD, key < s,
-                       total > 0);
-      half_row_out<HD>(tdV + tl, part, 1.f, a.dv + t * a.lddv + static_cast<int64_t>(w.kvh) * HD, key < s, total > 0);
-      if (total > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
-        ++n;
+      if (!ok) break;
+      more = get_item_warp(ring, m, next_it);
+      if (more) {
+        next_w = where(next_it.lin);
+        if (next_it.count > 0) ahead = look(next_w.b, next_it.first);
       }
+      if (total == 0) {
+        const int64_t t = static_cast<int64_t>(w.b) * s + k0;
+        zero_rows<HD>(a.dk + t * a.lddk + static_cast<int64_t>(w.kvh) * HD, a.lddk, min(128, s - k0), elem);
+        zero_rows<HD>(a.dv + t * a.lddv + static_cast<int64_t>(w.kvh) * HD, a.lddv, min(128, s - k0), elem);
+        continue;
+      }
+      if (!(ok = mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
+      tc_fence_after();
+      uint8_t* out_k = sm + L::Q + ((g - 1) % QS) * L::TILE;
+      uint8_t* out_v = sm + L::DO + ((g - 1) % DS) * L::DSTAGE;
+      stage_half_row<HD>(tdK + tl, part, a.score.scale, out_k, row);
+      stage_half_row<HD>(tdV + tl, part, 1.f, out_v, row);
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      ++n;
     }
   }
 
@@ -608,7 +679,7 @@ template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_span_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
-                        const __grid_constant__ BwdArgs a) {
+                        const __grid_constant__ CUtensorMap map_dq, const __grid_constant__ BwdArgs a) {
   using L = SmemQ<HD>;
   constexpr int KS = L::KS, VS = L::VS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -629,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* dp_free = bar + 13;          // every warp holds its dP columns in registers
   uint64_t* ds_half = bar + 14;          // [2]
   uint64_t* acc_full = bar + 16;         // the item's dQ MMAs have completed
-  uint64_t* acc_empty = bar + 17;        // every warp has read its part of dQ
+  uint64_t* acc_empty = bar + 17;        // every warp has read its part of dQ and staged it
   const ItemRing ring{bar + 18, bar + 20, reinterpret_cast<Item*>(bar + 23), err};
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 22);
 
@@ -686,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_slot = [&](int g) { return tbase + (g & 1) * 128; };
 
   if (warp == 0) {
-    // takes the items, each when the last load of the one before has been issued, and loads the K ring
+    // takes the items, each with the last loads of the one before, and loads the K ring
     if (lane == 0) {
       const int items = n_t * n_hb;
       auto take = [&](int lin) -> Item {
@@ -701,18 +772,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         return it;
       };
       Item cur = take(blockIdx.x);
-      bool ok = true;
-      for (int m = 0, g = 0; ok; ++m) {
-        if (!(ok = put_item(ring, m, cur)) || cur.lin < 0) break;
+      bool ok = put_item(ring, 0, cur);
+      for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
         const Where w = where(cur.lin);
+        const int early = max(cur.count - kTakeAhead, 0);
+        Item next;
+        auto hand_on = [&] {
+          next = take(gridDim.x + atomicAdd(a.taken, 1));
+          return put_item(ring, m, next);
+        };
+        if (cur.count == 0 && !(ok = hand_on())) break;
         for (int j = 0; j < cur.count; ++j, ++g) {
+          if (j == early && !(ok = hand_on())) break;
           const int st = g % KS;
           if (!(ok = mbar_wait(&k_empty[st], ((g / KS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
           mbar_arrive_expect_tx(&k_full[st], L::TILE);
           tma_load_4d(sm + L::K + st * L::TILE, &map_k, &k_full[st], 0, (cur.first + j) * 128,
                       w.head / group * (HD / 64), w.b);
         }
-        if (ok) cur = take(gridDim.x + atomicAdd(a.taken, 1));
+        cur = next;
       }
     }
   } else if (warp == 10) {
@@ -731,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 11) {
-    // Q and dO, once per item; first this block's share of the query ranges that dK/dV walks
+    // Q and dO, once per item, and the gradient of the item before, from the K stage of its last tile,
+    // which is released when it has been read; first this block's share of the query ranges that dK/dV walks
     for (int64_t i = blockIdx.x; i < static_cast<int64_t>(a.B) * n_t; i += gridDim.x) {
       const Hull* hulls = a.hulls + i / n_t * n_t;
       const int k0 = static_cast<int>(i % n_t) * 128;
@@ -749,15 +828,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       Item it;
-      for (int m = 0, n = 0; get_item(ring, m, it); ++m) {
-        if (it.count == 0) continue;
+      Where out{0, 0, 0};
+      bool ok = true;
+      auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
+        if (!mbar_wait(acc_empty, n & 1, err, kErrTimeoutAttn)) return false;
+        tma_store_4d(&map_dq, sm + L::K + (g % KS) * L::TILE, 0, out.qt * 128, out.head * (HD / 64), out.b);
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(&k_empty[g % KS]);
+        return true;
+      };
+      int n = 0, g = 0, stored = 0;
+      for (int m = 0; ok && get_item(ring, m, it); ++m) {
         const Where w = where(it.lin);
-        if (!mbar_wait(q_empty, (n & 1) ^ 1u, err, kErrTimeoutAttn)) break;
-        mbar_arrive_expect_tx(q_full, 2 * L::TILE);
-        tma_load_4d(sm + L::Q, &map_q, q_full, 0, w.qt * 128, w.head * (HD / 64), w.b);
-        tma_load_4d(sm + L::DO, &map_do, q_full, 0, w.qt * 128, w.head * (HD / 64), w.b);
-        ++n;
+        const int last = g - 1;
+        if (it.count > 0) {
+          if (!(ok = mbar_wait(q_empty, (n & 1) ^ 1u, err, kErrTimeoutAttn))) break;
+          mbar_arrive_expect_tx(q_full, 2 * L::TILE);
+          tma_load_4d(sm + L::Q, &map_q, q_full, 0, w.qt * 128, w.head * (HD / 64), w.b);
+          tma_load_4d(sm + L::DO, &map_do, q_full, 0, w.qt * 128, w.head * (HD / 64), w.b);
+        }
+        if (stored < n) ok = store(stored++, last);
+        if (it.count > 0) {
+          out = w;
+          g += it.count;
+          ++n;
+        }
       }
+      if (ok && stored < n) store(stored, g - 1);
+      bulk_wait();
     }
   } else if (warp == 1) {
     // the whole warp runs the issuing loop; elect.sync picks the lane that issues each MMA
@@ -819,8 +918,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   (j > 0 || kk > 0) ? 1u : 0u);
         }
         if (!ok) break;
-        umma_commit_warp(&k_empty[g % KS]);
-        if (j + 1 == total) umma_commit_warp(acc_full);
+        // the last tile's K stage is released once the gradient has left it
+        if (j + 1 < total) umma_commit_warp(&k_empty[g % KS]);
+        else umma_commit_warp(acc_full);
       }
       ++n;
     }
@@ -830,15 +930,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = sub * 32 + lane;
     const int elem = threadIdx.x - 64;
     const uint32_t tl = static_cast<uint32_t>(sub * 32) << 16;
-    Item it;
-    bool ok = true;
-    for (int m = 0, n = 0, g = 0; ok && get_item_warp(ring, m, it); ++m) {
-      const Where w = where(it.lin);
+    // a row's span and (-lse2, -delta) are loaded before the last item's gradient is stored
+    struct Ahead {
+      int2 seen;
+      float2 lq;
+    };
+    auto look = [&](const Where& w) -> Ahead {
+      const int q = w.qt * 128 + row;
+      return {fetch_span(a.spans, w.b, q, s),
+              a.lsd[(static_cast<int64_t>(w.b) * nh + w.head) * pad128(s) + q]};  // padded: q is inside
+    };
+    Item it, next_it;
+    Where next_w{0, 0, 0};
+    Ahead ahead{};
+    bool ok = true, more = get_item_warp(ring, 0, next_it);
+    if (more) {
+      next_w = where(next_it.lin);
+      ahead = look(next_w);
+    }
+    for (int m = 1, n = 0, g = 0; ok && more; ++m) {
+      it = next_it;
+      const Where w = next_w;
       const int q0 = w.qt * 128, q = q0 + row;
       const Hull hull = it.hull;
-      const int2 seen = q < s ? load_span(a.spans, w.b, q, s) : make_int2(0, 0);
-      const float2 lq = a.lsd[(static_cast<int64_t>(w.b) * nh + w.head) * pad128(s) + q];  // padded: q is inside
-      const float2 nl2 = make_float2(lq.x, lq.x), ndl = make_float2(lq.y, lq.y);
+      const int2 seen = clamp_span(ahead.seen, s);
+      const float2 nl2 = make_float2(ahead.lq.x, ahead.lq.x), ndl = make_float2(ahead.lq.y, ahead.lq.y);
       const float slope2 = BIAS ? a.slopes[w.head] * kLog2e : 0.f;
       const bool padded = hull.max_lo == INT_MAX;
       for (int j = 0; j < it.count && ok; ++j, ++g) {
@@ -894,17 +1010,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&ds_half[h]);
         }
       }
-      if (!ok || (it.count > 0 && !mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
-      tc_fence_after();
-      half_row_out<HD>(tdQ + tl, part, a.score.scale,
-                       a.dq + (static_cast<int64_t>(w.b) * s + q) * a.lddq + static_cast<int64_t>(w.head) * HD, q < s,
-                       it.count > 0);
-      if (it.count > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
-        ++n;
+      if (!ok) break;
+      more = get_item_warp(ring, m, next_it);
+      if (more) {
+        next_w = where(next_it.lin);
+        ahead = look(next_w);
       }
+      if (it.count == 0) {
+        zero_rows<HD>(a.dq + (static_cast<int64_t>(w.b) * s + q0) * a.lddq + static_cast<int64_t>(w.head) * HD, a.lddq,
+                      min(128, s - q0), elem);
+        continue;
+      }
+      if (!(ok = mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
+      tc_fence_after();
+      uint8_t* out = sm + L::K + ((g - 1) % KS) * L::TILE;
+      stage_half_row<HD>(tdQ + tl, part, a.score.scale, out, row);
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      ++n;
     }
   }
 
@@ -925,24 +1050,28 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
   constexpr uint32_t nsl = HD / 64;  // one box carries every head_dim slice of a tile
   const int64_t s = g.s;
   const uint64_t qs = static_cast<uint64_t>(g.nh) * nsl, ks = static_cast<uint64_t>(g.nkv) * nsl;
-  CUtensorMap mq, mk, mv, md;
+  CUtensorMap mq, mk, mv, md, mdq, mdk, mdv;
   if (!tma_map_heads(&mq, g.q, s, g.B, g.ldq, s * g.ldq, qs, nsl, 128) ||
       !tma_map_heads(&mk, g.k, s, g.B, g.ldk, s * g.ldk, ks, nsl, 128) ||
       !tma_map_heads(&mv, g.v, s, g.B, g.ldv, s * g.ldv, ks, nsl, 128) ||
-      !tma_map_heads(&md, dout, s, g.B, lddo, s * lddo, qs, nsl, 128))
+      !tma_map_heads(&md, dout, s, g.B, lddo, s * lddo, qs, nsl, 128) ||
+      !tma_map_heads(&mdq, a.dq, s, g.B, a.lddq, s * a.lddq, qs, nsl, 128) ||
+      !tma_map_heads(&mdk, a.dk, s, g.B, a.lddk, s * a.lddk, ks, nsl, 128) ||
+      !tma_map_heads(&mdv, a.dv, s, g.B, a.lddv, s * a.lddv, ks, nsl, 128))
     return cudaErrorInvalidValue;
   auto* dq = &attn_span_dq_kernel<HD, CAP, BIAS>;
   e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemQ<HD>::BYTES);
   if (e != cudaSuccess) return e;
   const int sms = gemm_num_sms();
   const int64_t q_items = static_cast<int64_t>(n_t) * g.nh * g.B, k_items = static_cast<int64_t>(n_t) * g.nkv * g.B;
-  dq<<<static_cast<unsigned>(q_items < sms ? q_items : sms), kThreads, SmemQ<HD>::BYTES, st>>>(mq, mk, mv, md, a);
+  dq<<<static_cast<unsigned>(q_items < sms ? q_items : sms), kThreads, SmemQ<HD>::BYTES, st>>>(mq, mk, mv, md, mdq, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS>;
   e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemKV<HD>::BYTES);
   if (e != cudaSuccess) return e;
-  dkdv<<<static_cast<unsigned>(k_items < sms ? k_items : sms), kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, a);
+  dkdv<<<static_cast<unsigned>(k_items < sms ? k_items : sms), kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, mdk, mdv,
+                                                                                                       a);
   return cudaGetLastError();
 }
 
@@ -963,7 +1092,8 @@ cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, con
     return cudaErrorInvalidValue;
   const int64_t qc = static_cast<int64_t>(g.nh) * g.hd, kc = static_cast<int64_t>(g.nkv) * g.hd;
   if (!rows(o, ldo, qc) || !rows(dout, lddo, qc) || !rows(dq, lddq, qc) || !rows(dk, lddk, kc) || !rows(dv, lddv, kc) ||
-      static_cast<double>(g.s) * 2 * lddo >= 1e12)
+      static_cast<double>(g.s) * 2 * lddo >= 1e12 || static_cast<double>(g.s) * 2 * lddq >= 1e12 ||
+      static_cast<double>(g.s) * 2 * lddk >= 1e12 || static_cast<double>(g.s) * 2 * lddv >= 1e12)
     return cudaErrorInvalidValue;
   float2* lsd = static_cast<float2*>(scratch);
   Hull* hulls = reinterpret_cast<Hull*>(lsd + static_cast<int64_t>(g.B) * g.nh * pad128(g.s));
