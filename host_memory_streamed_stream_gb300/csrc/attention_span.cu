@@ -221,17 +221,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int i = 0; i < 32; ++i) sc[c4 * 32 + i] = __uint_as_float(r[i]);
       }
-      if constexpr (CAP) {
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c) sc[c] = cap_score(cap_r(sc[c], a.score), a.score);
-      }
+      if constexpr (CAP) cap_tanh<kKeys>(sc, a.score);
+      const float to_log2 = CAP ? a.score.cap_log2 : a.score.scale_log2;  // sc times this: log2 units
       if constexpr (BIAS) {
         const float d0 = static_cast<float>(q - key0);
 #pragma unroll
         for (int c = 0; c < kKeys; ++c)
-          sc[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), CAP ? sc[c] : sc[c] * a.score.scale_log2);
+          sc[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), sc[c] * to_log2);
       }
-      constexpr bool kScaled = CAP || BIAS;  // the scores are in log2 units already
       if (!sees_all(hull, key0, key0 + kKeys)) {
 #pragma unroll
         for (int c4 = 0; c4 < kKeys / 32; ++c4) {
@@ -244,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       float r = sc[0];
 #pragma unroll
       for (int c = 1; c + 1 < kKeys; c += 2) r = fmax3(r, sc[c], sc[c + 1]);
-      const float mx = fmaxf(r, sc[kKeys - 1]) * (kScaled ? 1.f : a.score.scale_log2);
+      const float mx = fmaxf(r, sc[kKeys - 1]) * (BIAS ? 1.f : to_log2);
       const bool need = mx > m_ref + kLazyRescale;
       const float m_new = need ? mx : m_ref;
       // rescale O only when a row's max grew past the lazy threshold; O += P_{j-1} V_{j-1} must
@@ -267,13 +264,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       m_ref = m_new;
       uint32_t pw[kKeys / 2];  // P_j as bf16 pairs: key 2c in the low half of column c
-      const float mul = kScaled ? 1.f : a.score.scale_log2, neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-      const float2 sl = make_float2(mul, mul), nm = make_float2(neg_m, neg_m);
+      const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+      const float2 sl = make_float2(to_log2, to_log2), nm = make_float2(neg_m, neg_m);
       float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < kKeys / 2; ++c) {
         const float2 x = make_float2(sc[2 * c], sc[2 * c + 1]);
-        const float2 v = kScaled ? __fadd2_rn(x, nm) : __ffma2_rn(x, sl, nm);
+        const float2 v = BIAS ? __fadd2_rn(x, nm) : __ffma2_rn(x, sl, nm);
         const float2 pp = make_float2(ex2(v.x), ex2(v.y));
         acc = __fadd2_rn(acc, pp);
         pw[c] = pack_bf16(pp.x, pp.y);
@@ -364,7 +361,8 @@ bool attn_span_ok(const AttnSpanArgs& g) {
   if ((reinterpret_cast<uintptr_t>(g.lo) | reinterpret_cast<uintptr_t>(g.hi) | reinterpret_cast<uintptr_t>(g.slopes)) & 3)
     return false;
   if (!std::isfinite(g.scale) || !(g.scale > 0.f) || !std::isfinite(g.cap) || g.cap < 0.f) return false;
-  if (g.cap > 0.f && (!std::isnormal(g.cap) || !std::isfinite(2.f * kLog2e * g.scale / g.cap) || !std::isfinite(2.f * kLog2e * g.cap))) return false;
+  if (g.cap > 0.f && (!std::isnormal(g.cap) || !std::isfinite(g.scale / g.cap) || !std::isfinite(kLog2e * g.cap)))
+    return false;
   if (!std::isfinite(kLog2e * g.scale)) return false;
   // batch * tiles * heads blocks, and tensor-map strides below 2^40 bytes
   return (g.s + 127) / 128 * nh * g.B <= INT_MAX && static_cast<double>(g.s) * 2 * g.ldq < 1e12 &&

@@ -8,7 +8,7 @@
 // dQ per (128-query tile, head, sequence) over 128-key tiles, dQ += dS K; 128 x 128 tiles, two
 // 128-column score slots in TMEM, P and dS written back over the scores as bf16 pairs and read from
 // TMEM, each in two halves of 64 columns. What differs:
-//  * z is the capped and biased score and z' the cap's derivative 1 - tanh^2 = 4 r (1 - r);
+//  * z is the capped and biased score and z' the cap's derivative 1 - tanh^2;
 //  * the delta kernel also writes each query tile's hull; dQ walks the key tiles of its hull, dK/dV
 //    the query tiles from the first to the last whose hull meets its keys, and a tile that meets
 //    nothing writes zeros;
@@ -37,53 +37,68 @@ namespace {
 
 using namespace span;
 
-// warps: 0 takes items and loads one ring, 1 issues MMAs, 2..9 elementwise, 10 and 11 load
-constexpr int kThreads = 384;
-constexpr int kElem = 256;          // elementwise threads
-constexpr int kCols = 32;           // score columns an elementwise warp takes per half tile
-constexpr int kElemWarps = kElem / 32;  // arrivals per barrier phase (one elected lane per warp)
+// Warps of a block with EW elementwise warps (8 or 16): 0 takes items and loads one ring, 1 issues
+// MMAs, 2 .. EW+1 elementwise (EW/4 on each TMEM lane quadrant), the last two load.
+template <int EW>
+struct Roles {
+  static constexpr int kElem = EW * 32;      // elementwise threads
+  static constexpr int kCols = 256 / EW;     // score columns an elementwise warp takes per half tile
+  static constexpr int kRingWarp = EW + 2;   // loads the other ring
+  static constexpr int kItemWarp = EW + 3;   // loads an item's own operands, stores its gradients
+  static constexpr int kThreads = EW * 32 + 128;
+  static constexpr int kItemReaders = EW + 3;  // lane 0 of every warp but the one that takes items
+};
 constexpr int kSlice128 = 128 * 128;  // bytes of a [128 rows][64 bf16] swizzle-atom-wide slice
 
 __host__ __device__ __forceinline__ int pad128(int s) { return (s + 127) & ~127; }
 
 // Pack the 16 values v[o .. o + 15] into 8 bf16 pairs and store them to 8 TMEM columns of this
 // thread's lane (the A-operand layout: element k of a row in column k/2, even k in the low half).
-__device__ __forceinline__ void store_pairs16(uint32_t taddr, const float (&v)[kCols], int o) {
+template <int N>
+__device__ __forceinline__ void store_pairs16(uint32_t taddr, const float (&v)[N], int o) {
   uint32_t w[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) w[c] = pack_bf16(v[o + 2 * c], v[o + 2 * c + 1]);
   tmem_st_8cols(taddr, w);
 }
 
-// Two 32-column TMEM loads (S and dP of one row) behind a single wait.
-__device__ __forceinline__ void tmem_ld_2x32f(uint32_t ta, uint32_t tb, float (&a)[kCols], float (&b)[kCols]) {
-  uint32_t ra[32], rb[32];
-  tmem_ld_32cols(ta, ra);
-  tmem_ld_32cols(tb, rb);
+// N (16 or 32) columns of S and of dP of one row behind a single wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_pair(uint32_t ta, uint32_t tb, float (&a)[N], float (&b)[N]) {
+  uint32_t ra[N], rb[N];
+  if constexpr (N == 32) {
+    tmem_ld_32cols(ta, ra);
+    tmem_ld_32cols(tb, rb);
+  } else {
+    tmem_ld_16cols(ta, ra);
+    tmem_ld_16cols(tb, rb);
+  }
   tmem_ld_wait();
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < N; ++i) {
     a[i] = __uint_as_float(ra[i]);
     b[i] = __uint_as_float(rb[i]);
   }
 }
 
-// An item's gradients leave through shared memory: each thread converts half of its row (columns
-// [part*HD/2, +HD/2)) of the accumulator and writes it to the ring stage that the item's last tile
+// An item's gradients leave through shared memory: each thread converts its share of a row (W columns
+// from col0) of the accumulator and writes it to the ring stage that the item's last tile
 // was read from, in the swizzled layout of a TMA store, which the warp that loads the items' own operands issues. (Each lane storing
 // its own row to global memory touches 32 lines an instruction: 7500 cycles for the two 128 x 128
 // gradients of a key tile, two tiles' work. Rows transposed through the warp first: 4700.)
-template <int HD>
-__device__ __forceinline__ void stage_half_row(uint32_t taddr, int part, float scale, uint8_t* tile, int row) {
+template <int W>
+__device__ __forceinline__ void stage_cols(uint32_t taddr, int col0, float scale, uint8_t* tile, int row) {
+  constexpr int N = W < 32 ? 16 : 32;
 #pragma unroll
-  for (int c = 0; c < HD / 64; ++c) {
-    uint32_t r[32];
-    const int col = part * (HD / 2) + c * 32;
-    tmem_ld_32cols(taddr + col, r);
+  for (int c = 0; c < W; c += N) {
+    uint32_t r[N];
+    const int col = col0 + c;
+    if constexpr (N == 32) tmem_ld_32cols(taddr + col, r);
+    else tmem_ld_16cols(taddr + col, r);
     tmem_ld_wait();
     uint8_t* line = tile + (col >> 6) * kSlice128 + row * 128;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    for (int v = 0; v < N / 8; ++v) {
       uint4 u;
       u.x = pack_bf16(__uint_as_float(r[8 * v + 0]) * scale, __uint_as_float(r[8 * v + 1]) * scale);
       u.y = pack_bf16(__uint_as_float(r[8 * v + 2]) * scale, __uint_as_float(r[8 * v + 3]) * scale);
@@ -96,8 +111,8 @@ __device__ __forceinline__ void stage_half_row(uint32_t taddr, int part, float s
 
 // Zeros to `rows` rows of HD columns (an item without a walk): the elementwise threads, 16 bytes each.
 template <int HD>
-__device__ __forceinline__ void zero_rows(bf16* dst, int64_t ld, int rows, int elem) {
-  for (int i = elem; i < rows * (HD / 8); i += kElem)
+__device__ __forceinline__ void zero_rows(bf16* dst, int64_t ld, int rows, int elem, int threads) {
+  for (int i = elem; i < rows * (HD / 8); i += threads)
     *reinterpret_cast<uint4*>(dst + i / (HD / 8) * ld + i % (HD / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
 }
 
@@ -116,7 +131,6 @@ struct ItemRing {
   int* err;
 };
 constexpr int kTakeAhead = 2;     // the next item is taken with the last this many loads of an item
-constexpr int kItemReaders = 11;  // lane 0 of every warp but the one that takes items
 
 // Publish item number n (one thread).
 __device__ __forceinline__ bool put_item(const ItemRing& r, int n, const Item& it) {
@@ -215,27 +229,17 @@ struct BwdArgs {
   int* err;
 };
 
-// P and dS of one pair of columns: raw scores and dP in, P and dS out. nl = -lse2, nd = -delta of
-// the columns' (or the row's) queries; dist = |i - j| where there is a bias.
+// P and dS of one pair of columns: scores (capped: their tanh) and dP in, P and dS out. nl = -lse2,
+// nd = -delta of the columns' (or the row's) queries; dist = |i - j| where there is a bias.
 template <bool CAP, bool BIAS>
 __device__ __forceinline__ void p_and_ds(float2& sv, float2& dv, float2 nl, float2 nd, float2 dist, float slope2,
                                          const ScoreArgs& a) {
-  float2 e, r;
-  if constexpr (CAP) {
-    r = make_float2(cap_r(sv.x, a), cap_r(sv.y, a));
-    e = make_float2(cap_score(r.x, a), cap_score(r.y, a));
-    if constexpr (BIAS) e = __ffma2_rn(make_float2(-slope2, -slope2), dist, e);
-    e = __fadd2_rn(e, nl);
-  } else {
-    if constexpr (BIAS) nl = __ffma2_rn(make_float2(-slope2, -slope2), dist, nl);
-    e = __ffma2_rn(sv, make_float2(a.scale_log2, a.scale_log2), nl);
-  }
+  const float to_log2 = CAP ? a.cap_log2 : a.scale_log2;
+  if constexpr (BIAS) nl = __ffma2_rn(make_float2(-slope2, -slope2), dist, nl);
+  const float2 e = __ffma2_rn(sv, make_float2(to_log2, to_log2), nl);
   const float2 p = make_float2(ex2(e.x), ex2(e.y));
   float2 d = __fmul2_rn(p, __fadd2_rn(dv, nd));
-  if constexpr (CAP) {
-    const float2 r4 = __fmul2_rn(r, make_float2(4.f, 4.f));
-    d = __fmul2_rn(d, __ffma2_rn(make_float2(-r4.x, -r4.y), r, r4));
-  }
+  if constexpr (CAP) d = __fmul2_rn(d, __ffma2_rn(make_float2(-sv.x, -sv.y), sv, make_float2(1.f, 1.f)));
   sv = p;
   dv = d;
 }
@@ -256,13 +260,15 @@ struct SmemKV {
   static_assert(BYTES <= 232448, "dK/dV shared memory above the 227 KB per-CTA limit");
 };
 
-template <int HD, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int HD, bool CAP, bool BIAS, int EW>
+__global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     attn_span_dkdv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                           const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv,
                           const __grid_constant__ BwdArgs a) {
   using L = SmemKV<HD>;
+  using R = Roles<EW>;
+  constexpr int kCols = R::kCols;
   constexpr int QS = L::QS, DS = L::DS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
@@ -313,14 +319,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sdp_full[0], 1);
     mbar_init(&sdp_full[1], 1);
-    mbar_init(dp_free, kElemWarps);
-    mbar_init(&p_half[0], kElemWarps);
-    mbar_init(&p_half[1], kElemWarps);
+    mbar_init(dp_free, EW);
+    mbar_init(&p_half[0], EW);
+    mbar_init(&p_half[1], EW);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, kElemWarps);
+    mbar_init(acc_empty, EW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ring.full[i], 1);
-      mbar_init(&ring.empty[i], kItemReaders);
+      mbar_init(&ring.empty[i], R::kItemReaders);
     }
     fence_mbar_init();
     tma_prefetch_map(&map_q);
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur = next;
       }
     }
-  } else if (warp == 10) {
+  } else if (warp == R::kRingWarp) {
     // the dO ring with the (-lse2, -delta) pairs
     if (lane == 0) {
       Item it;
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 11) {
+  } else if (warp == R::kItemWarp) {
     // K and V, once per item; and the gradients of the item before, from the stages of its last tile,
     // which are released when they have been read
     if (lane == 0) {
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int sub = warp & 3;
-    const int part = (warp - 2) >> 2;  // which 32 of each 64 query columns this warp takes
+    const int part = (warp - 2) >> 2;  // which kCols of each 64 query columns this warp takes
     const int row = sub * 32 + lane;
     const int elem = threadIdx.x - 64;
     const uint32_t tl = static_cast<uint32_t>(sub * 32) << 16;
@@ -579,14 +585,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (!(ok = mbar_wait_warp(&sdp_full[h], g & 1, err, kErrTimeoutAttn))) break;
           tc_fence_after();
-          const int cb = h * 64 + part * kCols;  // this warp's score columns [cb, cb + 32)
+          const int cb = h * 64 + part * kCols;  // this warp's score columns [cb, cb + kCols)
           float sv[kCols], dv[kCols];
-          tmem_ld_2x32f(ts + cb, td + cb, sv, dv);
+          tmem_ld_pair<kCols>(ts + cb, td + cb, sv, dv);
           if (h == 1) {  // every dP^T column of the tile is now in registers
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(dp_free);
           }
+          if constexpr (CAP) cap_tanh<kCols>(sv, a.score);
           const float d0 = static_cast<float>(q0 + cb - key);
 #pragma unroll
           for (int k = 0; k < kCols / 2; ++k) {  // columns 2k, 2k+1: queries with (-lse2, -delta) in lv
@@ -611,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // K-step cb / 16 of the accumulating MMAs
 #pragma unroll
           for (int o = 0; o < kCols; o += 16) {
-            store_pairs16(ts + cb + o, sv, o);
-            store_pairs16(ts + cb + o + 8, dv, o);
+            store_pairs16<kCols>(ts + cb + o, sv, o);
+            store_pairs16<kCols>(ts + cb + o + 8, dv, o);
           }
           tmem_st_wait();
           if (padded) {  // this half's Q and dO rows that are padding: no product may read them
@@ -636,16 +643,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (total == 0) {
         const int64_t t = static_cast<int64_t>(w.b) * s + k0;
-        zero_rows<HD>(a.dk + t * a.lddk + static_cast<int64_t>(w.kvh) * HD, a.lddk, min(128, s - k0), elem);
-        zero_rows<HD>(a.dv + t * a.lddv + static_cast<int64_t>(w.kvh) * HD, a.lddv, min(128, s - k0), elem);
+        zero_rows<HD>(a.dk + t * a.lddk + static_cast<int64_t>(w.kvh) * HD, a.lddk, min(128, s - k0), elem, R::kElem);
+        zero_rows<HD>(a.dv + t * a.lddv + static_cast<int64_t>(w.kvh) * HD, a.lddv, min(128, s - k0), elem, R::kElem);
         continue;
       }
       if (!(ok = mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
       tc_fence_after();
       uint8_t* out_k = sm + L::Q + ((g - 1) % QS) * L::TILE;
       uint8_t* out_v = sm + L::DO + ((g - 1) % DS) * L::DSTAGE;
-      stage_half_row<HD>(tdK + tl, part, a.score.scale, out_k, row);
-      stage_half_row<HD>(tdV + tl, part, 1.f, out_v, row);
+      stage_cols<HD * 4 / EW>(tdK + tl, part * (HD * 4 / EW), a.score.scale, out_k, row);
+      stage_cols<HD * 4 / EW>(tdV + tl, part * (HD * 4 / EW), 1.f, out_v, row);
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
@@ -675,12 +682,14 @@ struct SmemQ {
   static_assert(BYTES <= 232448, "dQ shared memory above the 227 KB per-CTA limit");
 };
 
-template <int HD, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int HD, bool CAP, bool BIAS, int EW>
+__global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     attn_span_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                         const __grid_constant__ CUtensorMap map_dq, const __grid_constant__ BwdArgs a) {
   using L = SmemQ<HD>;
+  using R = Roles<EW>;
+  constexpr int kCols = R::kCols;
   constexpr int KS = L::KS, VS = L::VS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
@@ -729,14 +738,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_empty[i], 1);
     }
     mbar_init(sdp_full, 1);
-    mbar_init(dp_free, kElemWarps);
-    mbar_init(&ds_half[0], kElemWarps);
-    mbar_init(&ds_half[1], kElemWarps);
+    mbar_init(dp_free, EW);
+    mbar_init(&ds_half[0], EW);
+    mbar_init(&ds_half[1], EW);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, kElemWarps);
+    mbar_init(acc_empty, EW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ring.full[i], 1);
-      mbar_init(&ring.empty[i], kItemReaders);
+      mbar_init(&ring.empty[i], R::kItemReaders);
     }
     fence_mbar_init();
     tma_prefetch_map(&map_q);
@@ -793,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur = next;
       }
     }
-  } else if (warp == 10) {
+  } else if (warp == R::kRingWarp) {
     if (lane == 0) {  // the V ring
       Item it;
       bool ok = true;
@@ -808,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 11) {
+  } else if (warp == R::kItemWarp) {
     // Q and dO, once per item, and the gradient of the item before, from the K stage of its last tile,
     // which is released when it has been read; first this block's share of the query ranges that dK/dV walks
     for (int64_t i = blockIdx.x; i < static_cast<int64_t>(a.B) * n_t; i += gridDim.x) {
@@ -926,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int sub = warp & 3;
-    const int part = (warp - 2) >> 2;  // which 32 of each 64 key columns this warp takes
+    const int part = (warp - 2) >> 2;  // which kCols of each 64 key columns this warp takes
     const int row = sub * 32 + lane;
     const int elem = threadIdx.x - 64;
     const uint32_t tl = static_cast<uint32_t>(sub * 32) << 16;
@@ -970,13 +979,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
           const int cb = h * 64 + part * kCols;
           float sv[kCols], dv[kCols];
-          tmem_ld_2x32f(ts + cb, tdP + tl + cb, sv, dv);
+          tmem_ld_pair<kCols>(ts + cb, tdP + tl + cb, sv, dv);
           if (h == 1) {  // every dP column of the tile is now in registers
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(dp_free);
           }
           const int key0 = key_tile + cb;
+          if constexpr (CAP) cap_tanh<kCols>(sv, a.score);
           const float d0 = static_cast<float>(q - key0);
 #pragma unroll
           for (int k = 0; k < kCols / 2; ++k) {  // dS = P (dP - delta) z', two columns at a time
@@ -993,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // dS goes back into TMEM over this warp's S columns (A operand of K-step cb / 16)
 #pragma unroll
-          for (int o = 0; o < kCols; o += 16) store_pairs16(ts + cb + o, dv, o);
+          for (int o = 0; o < kCols; o += 16) store_pairs16<kCols>(ts + cb + o, dv, o);
           tmem_st_wait();
           if (clean) {
             const int r = h * 64 + (elem & 63), which = elem >> 6, key = key_tile + r;
@@ -1018,13 +1028,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (it.count == 0) {
         zero_rows<HD>(a.dq + (static_cast<int64_t>(w.b) * s + q0) * a.lddq + static_cast<int64_t>(w.head) * HD, a.lddq,
-                      min(128, s - q0), elem);
+                      min(128, s - q0), elem, R::kElem);
         continue;
       }
       if (!(ok = mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
       tc_fence_after();
       uint8_t* out = sm + L::K + ((g - 1) % KS) * L::TILE;
-      stage_half_row<HD>(tdQ + tl, part, a.score.scale, out, row);
+      stage_cols<HD * 4 / EW>(tdQ + tl, part * (HD * 4 / EW), a.score.scale, out, row);
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
@@ -1059,18 +1069,19 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
       !tma_map_heads(&mdk, a.dk, s, g.B, a.lddk, s * a.lddk, ks, nsl, 128) ||
       !tma_map_heads(&mdv, a.dv, s, g.B, a.lddv, s * a.lddv, ks, nsl, 128))
     return cudaErrorInvalidValue;
-  auto* dq = &attn_span_dq_kernel<HD, CAP, BIAS>;
+  constexpr int kQWarps = CAP ? 16 : 8, kKWarps = CAP ? 16 : 8;
+  auto* dq = &attn_span_dq_kernel<HD, CAP, BIAS, kQWarps>;
   e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemQ<HD>::BYTES);
   if (e != cudaSuccess) return e;
   const int sms = gemm_num_sms();
   const int64_t q_items = static_cast<int64_t>(n_t) * g.nh * g.B, k_items = static_cast<int64_t>(n_t) * g.nkv * g.B;
-  dq<<<static_cast<unsigned>(q_items < sms ? q_items : sms), kThreads, SmemQ<HD>::BYTES, st>>>(mq, mk, mv, md, mdq, a);
+  dq<<<static_cast<unsigned>(q_items < sms ? q_items : sms), Roles<kQWarps>::kThreads, SmemQ<HD>::BYTES, st>>>(mq, mk, mv, md, mdq, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS>;
+  auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps>;
   e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemKV<HD>::BYTES);
   if (e != cudaSuccess) return e;
-  dkdv<<<static_cast<unsigned>(k_items < sms ? k_items : sms), kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, mdk, mdv,
+  dkdv<<<static_cast<unsigned>(k_items < sms ? k_items : sms), Roles<kKWarps>::kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, mdk, mdv,
                                                                                                        a);
   return cudaGetLastError();
 }

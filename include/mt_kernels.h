@@ -242,8 +242,8 @@ int mtk_attn_bwd_rope(const void* qkv, const void* o, const void* lse, const voi
  * q bf16 [B*s, nh*hd], k and v bf16 [B*s, nkv*hd] with row strides ldq, ldk, ldv (any column ranges
  * of wider buffers); lo, hi int32 [B*s], positions inside the sequence, or NULL (lo 0, hi i + 1:
  * causal); they are clamped to [0, s]. nkv divides nh, head_dim 64 or 128, s <= 4194304. scale > 0,
- * cap >= 0 (0: none), slopes f32 [nh] or NULL, all finite; the cap's tanh is computed to about
- * cap * 2^-22.
+ * cap >= 0 (0: none), slopes f32 [nh] or NULL, all finite; capped scores are right to about cap * 2^-22
+ * (relative 2^-22 while they stay below the cap before it is applied).
  * An empty span (lo >= hi) makes row i padding: o_i = 0, lse_i = -inf, its gradients are 0, and no
  * other row's span may contain it. Padding rows of q, k, v and dout may hold anything, NaN
  * included, where the padding follows the documents of its sequence, precedes them, or lies between
