@@ -128,7 +128,7 @@ SIGNATURES = {
     "mtk_doc_spans": (c_int, [c_vp, c_int, c_vp, c_int, c_int, c_vp, c_vp, c_vp]),
     "mtk_attn_span_fwd": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_i64, c_vp, c_int, c_int,
                                   c_int, c_int, c_int, c_f32, c_f32, c_vp, c_vp, c_vp]),
-    "mtk_attn_span_bwd_scratch_bytes": (c_u64, [c_int, c_int, c_int]),
+    "mtk_attn_span_bwd_scratch_bytes": (c_u64, [c_int, c_int, c_int, c_int, c_int]),
     "mtk_attn_span_bwd": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64,
                                   c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_int, c_int, c_int, c_int, c_int,
                                   c_f32, c_f32, c_vp, c_vp, c_vp]),

@@ -340,7 +340,8 @@ cudaError_t launch(const AttnSpanArgs& g, bf16* o, int64_t ldo, float* lse, int*
       !tma_map_heads(&mv, g.v, s, g.B, g.ldv, s * g.ldv, static_cast<uint64_t>(g.nkv) * L::NSL, L::NSL, kKeys))
     return cudaErrorInvalidValue;
   auto* kernel = &attn_span_fwd_kernel<HD, CAP, BIAS>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(kernel, L::BYTES, ready);
   if (e != cudaSuccess) return e;
   const FwdArgs a{{g.lo, g.hi}, g.slopes, o, ldo, lse, g.s, g.nh, g.nkv, score_args(g), err};
   kernel<<<static_cast<unsigned>((s + 127) / 128 * g.nh * g.B), kThreads, L::BYTES, st>>>(mq, mk, mv, a);

@@ -5,6 +5,7 @@
 // this form, a tile's key range follows from its rows' smallest lo and largest hi, and a score's
 // visibility is two comparisons, so no mask is ever read or stored per pair.
 #pragma once
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <type_traits>
@@ -180,6 +181,17 @@ __device__ __forceinline__ void zero_slice_row(uint8_t* slice, int row) {
   uint4* p = reinterpret_cast<uint4*>(slice + row * 128);
 #pragma unroll
   for (int i = 0; i < 8; ++i) p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Allow a kernel its dynamic shared memory, once for each device (a bit of `ready`).
+template <class K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (ready.load() >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) ready.fetch_or(uint64_t{1} << dev);
+  return e;
 }
 
 // One of the eight kernels of a direction: f(head_dim, capped, biased) as compile-time constants.

@@ -109,6 +109,25 @@ __device__ __forceinline__ void stage_cols(uint32_t taddr, int col0, float scale
   }
 }
 
+// W columns (from col0) of one row of an fp32 accumulator to the item's partial sums, laid out [group of
+// 4 columns][128 rows][4]: a warp's 32 rows are 512 contiguous bytes an instruction.
+template <int W>
+__device__ __forceinline__ void partial_cols(uint32_t taddr, int col0, float* dst, int row) {
+  constexpr int N = W < 32 ? 16 : 32;
+#pragma unroll
+  for (int c = 0; c < W; c += N) {
+    uint32_t r[N];
+    if constexpr (N == 32) tmem_ld_32cols(taddr + col0 + c, r);
+    else tmem_ld_16cols(taddr + col0 + c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int v = 0; v < N / 4; ++v)
+      reinterpret_cast<float4*>(dst)[((col0 + c) / 4 + v) * 128 + row] =
+          make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]), __uint_as_float(r[4 * v + 2]),
+                      __uint_as_float(r[4 * v + 3]));
+  }
+}
+
 // Zeros to `rows` rows of HD columns (an item without a walk): the elementwise threads, 16 bytes each.
 template <int HD>
 __device__ __forceinline__ void zero_rows(bf16* dst, int64_t ld, int rows, int elem, int threads) {
@@ -222,6 +241,7 @@ struct BwdArgs {
   const Hull* hulls;   // [B][tiles] of the query tiles
   int2* q_ranges;      // [B][tiles] first and last query tile that meets a key tile (last -1: none)
   int* taken;          // [2] items taken: dQ, dK/dV
+  float* partial;      // dK/dV by query head: [B][nh][tiles][2][HD/4][128][4], else null
   bf16 *dq, *dk, *dv;
   int64_t lddq, lddk, lddv;
   int B, s, nh, nkv;
@@ -260,7 +280,7 @@ struct SmemKV {
   static_assert(BYTES <= 232448, "dK/dV shared memory above the 227 KB per-CTA limit");
 };
 
-template <int HD, bool CAP, bool BIAS, int EW>
+template <int HD, bool CAP, bool BIAS, int EW, bool PARTIAL>
 __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     attn_span_dkdv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
@@ -293,17 +313,20 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 23);
 
   const int s = a.s, nh = a.nh, nkv = a.nkv;
-  const int n_t = (s + 127) / 128, n_hb = nkv * a.B;
   const int group = nh / nkv;
+  const int heads = PARTIAL ? 1 : group;  // query heads an item walks
+  const int n_t = (s + 127) / 128, n_hb = nh / heads * a.B;
   const int sp = pad128(s);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // item -> key tile (the first key tile is seen by the most queries under a causal mask), head, sequence
+  // item -> key tile (the first key tile is seen by the most queries under a causal mask), first query
+  // head, key head, sequence
   struct Where {
-    int kt, kvh, b;
+    int kt, hq, kvh, b;
   };
   auto where = [&](int lin) -> Where {
     const TileSlot slot = heavy_first_slot(lin, n_t, n_hb);
-    return {slot.rank, slot.hb % nkv, slot.hb / nkv};
+    const int per_b = nh / heads, hq = slot.hb % per_b * heads;
+    return {slot.rank, hq, hq / group, slot.hb / per_b};
   };
 
   if (threadIdx.x == 0) {
@@ -369,7 +392,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       bool ok = put_item(ring, 0, cur);
       for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
         const Where w = where(cur.lin);
-        const int total = group * cur.count, early = max(total - kTakeAhead, 0);
+        const int total = heads * cur.count, early = max(total - kTakeAhead, 0);
         Item next;
         auto hand_on = [&] {
           next = take(gridDim.x + atomicAdd(a.taken + 1, 1));
@@ -382,7 +405,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
           if (!(ok = mbar_wait(&q_empty[st], ((g / QS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
           mbar_arrive_expect_tx(&q_full[st], L::TILE);
           tma_load_4d(sm + L::Q + st * L::TILE, &map_q, &q_full[st], 0, (cur.first + i % cur.count) * 128,
-                      (w.kvh * group + i / cur.count) * (HD / 64), w.b);
+                      (w.hq + i / cur.count) * (HD / 64), w.b);
         }
         cur = next;
       }
@@ -394,9 +417,9 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       bool ok = true;
       for (int m = 0, g = 0; ok && get_item(ring, m, it); ++m) {
         const Where w = where(it.lin);
-        for (int i = 0; i < group * it.count; ++i, ++g) {
+        for (int i = 0; i < heads * it.count; ++i, ++g) {
           const int st = g % DS;
-          const int hq = w.kvh * group + i / it.count, q0 = (it.first + i % it.count) * 128;
+          const int hq = w.hq + i / it.count, q0 = (it.first + i % it.count) * 128;
           if (!(ok = mbar_wait(&d_empty[st], ((g / DS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
           mbar_arrive_expect_tx(&d_full[st], L::TILE + 1024);
           uint8_t* base = sm + L::DO + st * L::DSTAGE;
@@ -410,14 +433,16 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     // which are released when they have been read
     if (lane == 0) {
       Item it;
-      Where out{0, 0, 0};
+      Where out{0, 0, 0, 0};
       bool ok = true;
       auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
         if (!mbar_wait(acc_empty, n & 1, err, kErrTimeoutAttn)) return false;
-        tma_store_4d(&map_dk, sm + L::Q + (g % QS) * L::TILE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
-        tma_store_4d(&map_dv, sm + L::DO + (g % DS) * L::DSTAGE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
-        bulk_commit();
-        bulk_wait_read();
+        if constexpr (!PARTIAL) {
+          tma_store_4d(&map_dk, sm + L::Q + (g % QS) * L::TILE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
+          tma_store_4d(&map_dv, sm + L::DO + (g % DS) * L::DSTAGE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
+          bulk_commit();
+          bulk_wait_read();
+        }
         mbar_arrive(&q_empty[g % QS]);
         mbar_arrive(&d_empty[g % DS]);
         return true;
@@ -435,7 +460,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         if (stored < n) ok = store(stored++, last);
         if (it.count > 0) {
           out = w;
-          g += group * it.count;
+          g += heads * it.count;
           ++n;
         }
       }
@@ -477,7 +502,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     Item it;
     bool ok = true;
     for (int m = 0, n = 0, g = 0; ok && get_item_warp(ring, m, it); ++m) {
-      const int total = group * it.count;
+      const int total = heads * it.count;
       if (total == 0) continue;
       // the item's first scores: both TMEM slots are free of what the last item left in them once
       // its products, issued before, have run and every warp holds its dP^T columns
@@ -549,7 +574,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       return r;
     };
     Item it, next_it;
-    Where next_w{0, 0, 0};
+    Where next_w{0, 0, 0, 0};
     Ahead ahead{};
     bool ok = true, more = get_item_warp(ring, 0, next_it);
     if (more) {
@@ -560,8 +585,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       it = next_it;
       const Where w = next_w;
       const int k0 = w.kt * 128, key = k0 + row;
-      const int total = group * it.count;
-      for (int i = 0, qt = it.first, hq = w.kvh * group; i < total && ok; ++i, ++g) {
+      const int total = heads * it.count;
+      for (int i = 0, qt = it.first, hq = w.hq; i < total && ok; ++i, ++g) {
         const int q0 = qt * 128;
         const bool all = sees_all(ahead.hull, k0, k0 + 128), padded = ahead.hull.max_lo == INT_MAX;
         uint32_t vis[2] = {~0u, ~0u};  // visible query columns of this thread's key, per half
@@ -641,6 +666,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         next_w = where(next_it.lin);
         if (next_it.count > 0) ahead = look(next_w.b, next_it.first);
       }
+      if (PARTIAL && total == 0) continue;  // the kernel that adds the heads writes the zeros
       if (total == 0) {
         const int64_t t = static_cast<int64_t>(w.b) * s + k0;
         zero_rows<HD>(a.dk + t * a.lddk + static_cast<int64_t>(w.kvh) * HD, a.lddk, min(128, s - k0), elem, R::kElem);
@@ -649,6 +675,16 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       }
       if (!(ok = mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
       tc_fence_after();
+      if constexpr (PARTIAL) {
+        float* p = a.partial + ((static_cast<int64_t>(w.b) * nh + w.hq) * n_t + w.kt) * (2 * 128 * HD);
+        partial_cols<HD * 4 / EW>(tdK + tl, part * (HD * 4 / EW), p, row);
+        partial_cols<HD * 4 / EW>(tdV + tl, part * (HD * 4 / EW), p + 128 * HD, row);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+        ++n;
+        continue;
+      }
       uint8_t* out_k = sm + L::Q + ((g - 1) % QS) * L::TILE;
       uint8_t* out_v = sm + L::DO + ((g - 1) % DS) * L::DSTAGE;
       stage_cols<HD * 4 / EW>(tdK + tl, part * (HD * 4 / EW), a.score.scale, out_k, row);
@@ -665,6 +701,32 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tbase, 512);
+}
+
+// dK and dV of one key tile: the sums of its query heads' partial sums, added in head order.
+template <int HD>
+__global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ BwdArgs a, int n_t) {
+  const int kt = blockIdx.x % n_t, hb = blockIdx.x / n_t;
+  const int c = blockIdx.y * 2 + (threadIdx.x >> 7);  // 4 columns of dK, then of dV
+  const int kvh = hb % a.nkv, b = hb / a.nkv, group = a.nh / a.nkv;
+  const int row = threadIdx.x & 127, key = kt * 128 + row;
+  if (key >= a.s) return;
+  const bool some = a.q_ranges[static_cast<int64_t>(b) * n_t + kt].y >= 0;
+  const int64_t head_step = static_cast<int64_t>(n_t) * (2 * 128 * HD);
+  const float* p = a.partial + (static_cast<int64_t>(b) * a.nh + kvh * group) * head_step + kt * static_cast<int64_t>(2 * 128 * HD);
+  const int64_t t = static_cast<int64_t>(b) * a.s + key;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (some) {
+    for (int h = 0; h < group; ++h) {
+      const float4 x = reinterpret_cast<const float4*>(p + h * head_step)[c * 128 + row];
+      sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+    }
+  }
+  const bool is_k = c < HD / 4;
+  const float m = is_k ? a.score.scale : 1.f;
+  bf16* dst = is_k ? a.dk + t * a.lddk + kvh * static_cast<int64_t>(HD) + 4 * c
+                   : a.dv + t * a.lddv + kvh * static_cast<int64_t>(HD) + 4 * (c - HD / 4);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum.x * m, sum.y * m), pack_bf16(sum.z * m, sum.w * m));
 }
 
 // ------------------------------------------------------------------ dQ (Q-outer)
@@ -1071,26 +1133,48 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
     return cudaErrorInvalidValue;
   constexpr int kQWarps = CAP ? 16 : 8, kKWarps = CAP ? 16 : 8;
   auto* dq = &attn_span_dq_kernel<HD, CAP, BIAS, kQWarps>;
-  e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemQ<HD>::BYTES);
+  static std::atomic<uint64_t> dq_ready{0}, dkdv_ready[2] = {{0}, {0}};
+  e = allow_smem(dq, SmemQ<HD>::BYTES, dq_ready);
   if (e != cudaSuccess) return e;
   const int sms = gemm_num_sms();
-  const int64_t q_items = static_cast<int64_t>(n_t) * g.nh * g.B, k_items = static_cast<int64_t>(n_t) * g.nkv * g.B;
+  const int64_t q_items = static_cast<int64_t>(n_t) * g.nh * g.B;
+  const int64_t k_items = static_cast<int64_t>(n_t) * (a.partial ? g.nh : g.nkv) * g.B;
   dq<<<static_cast<unsigned>(q_items < sms ? q_items : sms), Roles<kQWarps>::kThreads, SmemQ<HD>::BYTES, st>>>(mq, mk, mv, md, mdq, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps>;
-  e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemKV<HD>::BYTES);
+  const unsigned blocks = static_cast<unsigned>(k_items < sms ? k_items : sms);
+  if (!a.partial) {
+    auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, false>;
+    e = allow_smem(dkdv, SmemKV<HD>::BYTES, dkdv_ready[0]);
+    if (e != cudaSuccess) return e;
+    dkdv<<<blocks, Roles<kKWarps>::kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, mdk, mdv, a);
+    return cudaGetLastError();
+  }
+  auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, true>;
+  e = allow_smem(dkdv, SmemKV<HD>::BYTES, dkdv_ready[1]);
   if (e != cudaSuccess) return e;
-  dkdv<<<static_cast<unsigned>(k_items < sms ? k_items : sms), Roles<kKWarps>::kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, mdk, mdv,
-                                                                                                       a);
+  dkdv<<<blocks, Roles<kKWarps>::kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, mdk, mdv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  span_join_kernel<HD><<<dim3(static_cast<unsigned>(n_t) * g.nkv * g.B, HD / 4), 256, 0, st>>>(a, n_t);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-uint64_t attn_span_bwd_scratch(int B, int s, int nh) {
+// With few key tiles the groups' heads are walked by different blocks, whose fp32 sums another kernel
+// adds: where the tiles would leave half of the 152 SMs idle. (B 2, s 333, 4 query heads on one key
+// head: dK/dV 37 us in 6 blocks of up to 12 tiles each, 14 + 4 us in 24 blocks.) With more tiles the
+// sums' traffic, 1 KB a key and query head, costs more than the even load saves.
+static bool split_heads(int B, int s, int nh, int nkv) {
+  return nh > nkv && static_cast<int64_t>(pad128(s) / 128) * nkv * B <= 152 / 2;
+}
+
+uint64_t attn_span_bwd_scratch(int B, int s, int nh, int nkv, int hd) {
   const uint64_t sp = static_cast<uint64_t>(pad128(s));
-  return static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * (sizeof(Hull) + sizeof(int2))) + 16;
+  const uint64_t lists = static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * (sizeof(Hull) + sizeof(int2))) + 16;
+  const uint64_t sums = split_heads(B, s, nh, nkv) ? static_cast<uint64_t>(B) * nh * sp * 2 * hd * sizeof(float) : 0;
+  return (lists + 15) / 16 * 16 + sums;
 }
 
 cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const float* lse, const bf16* dout,
@@ -1110,8 +1194,12 @@ cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, con
   Hull* hulls = reinterpret_cast<Hull*>(lsd + static_cast<int64_t>(g.B) * g.nh * pad128(g.s));
   const int64_t tiles = static_cast<int64_t>(g.B) * (pad128(g.s) / 128);
   int2* q_ranges = reinterpret_cast<int2*>(hulls + tiles);
-  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_ranges, reinterpret_cast<int*>(q_ranges + tiles), dq, dk, dv,
-                  lddq, lddk, lddv, g.B, g.s, g.nh, g.nkv, score_args(g), err};
+  const uint64_t all = attn_span_bwd_scratch(g.B, g.s, g.nh, g.nkv, g.hd);
+  const uint64_t sums = static_cast<uint64_t>(g.B) * g.nh * pad128(g.s) * 2 * g.hd * sizeof(float);
+  float* partial = split_heads(g.B, g.s, g.nh, g.nkv)
+                       ? reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + (all - sums)) : nullptr;
+  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_ranges, reinterpret_cast<int*>(q_ranges + tiles), partial, dq,
+                  dk, dv, lddq, lddk, lddv, g.B, g.s, g.nh, g.nkv, score_args(g), err};
   return dispatch(g, [&](auto hd, auto cap, auto bias) {
     return launch<decltype(hd)::value, decltype(cap)::value, decltype(bias)::value>(g, o, ldo, lse, dout, lddo, a, lsd,
                                                                                     hulls, st);

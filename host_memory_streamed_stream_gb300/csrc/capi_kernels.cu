@@ -270,8 +270,9 @@ int mtk_attn_span_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, co
                               static_cast<bf16*>(o), ldo, static_cast<float*>(lse), err_flag, S(stream)));
 }
 
-uint64_t mtk_attn_span_bwd_scratch_bytes(int B, int s, int nh) {
-  return B > 0 && s > 0 && nh > 0 ? mt::attn_span_bwd_scratch(B, s, nh) : 0;
+uint64_t mtk_attn_span_bwd_scratch_bytes(int B, int s, int nh, int nkv, int head_dim) {
+  if (B <= 0 || s <= 0 || s > mt::kSpanMaxSeq || nh <= 0 || nkv <= 0 || head_dim <= 0) return 0;
+  return mt::attn_span_bwd_scratch(B, s, nh, nkv, head_dim);
 }
 
 int mtk_attn_span_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,

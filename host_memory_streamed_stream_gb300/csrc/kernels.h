@@ -168,7 +168,7 @@ bool attn_span_ok(const AttnSpanArgs& g);  // sizes, strides and alignments the 
 // o [B*s, nh*hd] (row stride ldo), lse fp32 [B, nh, s] as attn_fwd's; 0 and -inf for an empty span.
 cudaError_t attn_span_fwd(const AttnSpanArgs& g, bf16* o, int64_t ldo, float* lse, int* err, cudaStream_t st);
 // dq [B*s, nh*hd], dk and dv [B*s, nkv*hd]; scratch of attn_span_bwd_scratch() bytes.
-uint64_t attn_span_bwd_scratch(int B, int s, int nh);
+uint64_t attn_span_bwd_scratch(int B, int s, int nh, int nkv, int hd);
 cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const float* lse, const bf16* dout,
                           int64_t lddo, bf16* dq, int64_t lddq, bf16* dk, int64_t lddk, bf16* dv, int64_t lddv,
                           void* scratch, int* err, cudaStream_t st);

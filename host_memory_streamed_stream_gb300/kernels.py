@@ -5,6 +5,8 @@ to one C entry point and raises on a nonzero status.
 """
 from __future__ import annotations
 
+import functools
+
 import numpy as np
 import torch
 
@@ -162,7 +164,8 @@ def _table(cos_sin, dev):
 def rotary_inv_freq(rot_dim, theta=10000.0, scaling="plain", factor=1.0, original_positions=0, low=1.0, high=32.0):
     """rot_dim/2 rotation frequencies (numpy float64, radians per position); see mtk_rotary_inv_freq
     for the scalings "plain", "linear", "base" and "bands"."""
-    _need(scaling in ROTARY_SCALINGS, f"scaling: one of {sorted(ROTARY_SCALINGS)}")
+    if scaling not in ROTARY_SCALINGS:
+        raise MTError(-1, f"scaling: one of {sorted(ROTARY_SCALINGS)}")
     out = np.empty(max(int(rot_dim) // 2, 1), dtype=np.float64)
     _ok(_lib.load().mtk_rotary_inv_freq(rot_dim, theta, ROTARY_SCALINGS[scaling], factor, original_positions, low, high,
                                         out.ctypes.data), "rotary_inv_freq")
@@ -228,8 +231,7 @@ def qk_norm_rope_bwd(dy, x, gq, gk, rstd, n_heads, n_kv_heads, head_dim, cos_sin
     if out is None:
         out = torch.empty((T, cols), dtype=torch.bfloat16, device=x.device)
     lib = _lib.load()
-    parts = lib.mtk_qk_norm_rope_bwd_parts(T, n_heads, n_kv_heads, head_dim)
-    partial = torch.empty((parts, head_dim), dtype=torch.float32, device=x.device)
+    partial = torch.empty((lib.mtk_qk_norm_rope_bwd_parts(T, n_heads, n_kv_heads, head_dim), head_dim), dtype=torch.float32, device=x.device)
     dgq, dgk = torch.empty_like(gq), torch.empty_like(gk)
     pos = None if positions is None else _vec(positions, T, torch.int32, "positions", dev)
     err = _err(err, x.device)
@@ -350,6 +352,11 @@ def attn_span_fwd(q, k, v, B, s, nh, nkv, hd, lo=None, hi=None, scale=None, cap=
     return out, lse
 
 
+@functools.lru_cache(maxsize=256)
+def _span_scratch(B, s, nh, nkv, hd):
+    return _lib.load().mtk_attn_span_bwd_scratch_bytes(B, s, nh, nkv, hd)
+
+
 def attn_span_bwd(q, k, v, o, lse, dout, B, s, nh, nkv, hd, lo=None, hi=None, scale=None, cap=0.0, slopes=None,
                   out=None, err=None):
     """(dq, dk, dv) of attn_span_fwd; out: three tensors to write, None: the column ranges of one new
@@ -362,7 +369,7 @@ def attn_span_bwd(q, k, v, o, lse, dout, B, s, nh, nkv, hd, lo=None, hi=None, sc
         out = out.split((nh * hd, nkv * hd, nkv * hd), 1)
     dq, dk, dv = out
     lib = _lib.load()
-    scratch = torch.empty(lib.mtk_attn_span_bwd_scratch_bytes(B, s, nh), dtype=torch.uint8, device=q.device)
+    scratch = torch.empty(_span_scratch(B, s, nh, nkv, hd), dtype=torch.uint8, device=q.device)
     err = _err(err, q.device)
     _ok(lib.mtk_attn_span_bwd(*ptrs, o.data_ptr(), _rows(o, T, nh * hd, "o", dev),
                               _vec(lse, T * nh, torch.float32, "lse", dev), dout.data_ptr(),

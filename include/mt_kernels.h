@@ -267,7 +267,7 @@ int mtk_doc_spans(const int32_t* bounds, int n_docs, const int32_t* prefix, int 
 int mtk_attn_span_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
                       const void* lo, const void* hi, void* o, int64_t ldo, void* lse, int B, int s, int nh, int nkv,
                       int head_dim, float scale, float cap, const void* slopes, int* err_flag, void* stream);
-uint64_t mtk_attn_span_bwd_scratch_bytes(int B, int s, int nh);
+uint64_t mtk_attn_span_bwd_scratch_bytes(int B, int s, int nh, int nkv, int head_dim);
 int mtk_attn_span_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
                       const void* lo, const void* hi, const void* o, int64_t ldo, const void* lse, const void* dout,
                       int64_t lddo, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,

@@ -118,5 +118,6 @@ def test_attn_span_refusals(lib):
                dict(dq=p + 2), dict(lddq=256), dict(lddk=128), dict(lddv=254), dict(scratch=None),
                dict(scratch=p + 8)):
         assert call_bwd(**kw) == -1, kw
-    assert lib.mtk_attn_span_bwd_scratch_bytes(0, 1, 1) == 0
-    assert lib.mtk_attn_span_bwd_scratch_bytes(2, 129, 3) >= 2 * 3 * 256 * 8
+    assert lib.mtk_attn_span_bwd_scratch_bytes(0, 1, 1, 1, 64) == 0
+    assert lib.mtk_attn_span_bwd_scratch_bytes(1, 4194305, 1, 1, 64) == 0
+    assert lib.mtk_attn_span_bwd_scratch_bytes(2, 129, 4, 2, 64) >= 2 * 4 * 256 * 8
