@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "attention_span.cuh"
+#include "follow.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "tile_order.cuh"
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(256)
                       const float* __restrict__ lse, Spans spans, float2* __restrict__ lsd, Hull* __restrict__ hulls,
                       int* __restrict__ taken, int s, int nh, int n_t) {
   constexpr int kLanes = HD / 8;  // lanes per row
+  let_next_start();  // (dQ and dK/dV do not: the next one's blocks among theirs cost 17 us of 362 at 7B)
   if (blockIdx.x == 0 && threadIdx.x < 2) taken[threadIdx.x] = 0;  // items taken by dQ and by dK/dV
   __shared__ Hull parts[4];
   const int tile = blockIdx.x % n_t;
@@ -361,6 +363,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -706,6 +709,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
 // dK and dV of one key tile: the sums of its query heads' partial sums, added in head order.
 template <int HD>
 __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ BwdArgs a, int n_t) {
+  wait_for_previous();
   const int kt = blockIdx.x % n_t, hb = blockIdx.x / n_t;
   const int c = blockIdx.y * 2 + (threadIdx.x >> 7);  // 4 columns of dK, then of dV
   const int kvh = hb % a.nkv, b = hb / a.nkv, group = a.nh / a.nkv;
@@ -819,6 +823,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1139,25 +1144,17 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
   const int sms = gemm_num_sms();
   const int64_t q_items = static_cast<int64_t>(n_t) * g.nh * g.B;
   const int64_t k_items = static_cast<int64_t>(n_t) * (a.partial ? g.nh : g.nkv) * g.B;
-  dq<<<static_cast<unsigned>(q_items < sms ? q_items : sms), Roles<kQWarps>::kThreads, SmemQ<HD>::BYTES, st>>>(mq, mk, mv, md, mdq, a);
-  e = cudaGetLastError();
+  e = launch_following(dq, dim3(static_cast<unsigned>(q_items < sms ? q_items : sms)), Roles<kQWarps>::kThreads,
+                       SmemQ<HD>::BYTES, st, mq, mk, mv, md, mdq, a);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>(k_items < sms ? k_items : sms);
-  if (!a.partial) {
-    auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, false>;
-    e = allow_smem(dkdv, SmemKV<HD>::BYTES, dkdv_ready[0]);
-    if (e != cudaSuccess) return e;
-    dkdv<<<blocks, Roles<kKWarps>::kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, mdk, mdv, a);
-    return cudaGetLastError();
-  }
-  auto* dkdv = &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, true>;
-  e = allow_smem(dkdv, SmemKV<HD>::BYTES, dkdv_ready[1]);
+  auto* dkdv = a.partial ? &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, true>
+                         : &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, false>;
+  e = allow_smem(dkdv, SmemKV<HD>::BYTES, dkdv_ready[a.partial != nullptr]);
   if (e != cudaSuccess) return e;
-  dkdv<<<blocks, Roles<kKWarps>::kThreads, SmemKV<HD>::BYTES, st>>>(mq, mk, mv, md, mdk, mdv, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  span_join_kernel<HD><<<dim3(static_cast<unsigned>(n_t) * g.nkv * g.B, HD / 4), 256, 0, st>>>(a, n_t);
-  return cudaGetLastError();
+  e = launch_following(dkdv, dim3(static_cast<unsigned>(k_items < sms ? k_items : sms)), Roles<kKWarps>::kThreads,
+                       SmemKV<HD>::BYTES, st, mq, mk, mv, md, mdk, mdv, a);
+  if (e != cudaSuccess || !a.partial) return e;
+  return launch_following(span_join_kernel<HD>, dim3(static_cast<unsigned>(n_t) * g.nkv * g.B, HD / 4), 256, 0, st, a, n_t);
 }
 
 }  // namespace

@@ -131,7 +131,7 @@ cudaError_t qk_norm_rope(const bf16* x, int64_t ldx, const bf16* gq, const bf16*
                          int T, int nh, int nkv, int hd, int rot, bool interleaved, float eps,
                          const int32_t* positions, const float* cs, int n_pos, int* err, cudaStream_t s);
 // Its backward: dx (may be dy or x) and the gain gradients, through `partial` fp32 [parts][hd].
-constexpr int kQkNormParts = 608;
+constexpr int kQkNormParts = 304;  // blocks of the backward: two on each SM
 int qk_norm_rope_bwd_parts(int T, int nh, int nkv, int hd);
 cudaError_t qk_norm_rope_bwd(const bf16* dy, int64_t lddy, const bf16* x, int64_t ldx, const bf16* gq, const bf16* gk,
                              const float* rstd, bf16* dx, int64_t lddx, float* partial, bf16* dgq, bf16* dgk, int T,

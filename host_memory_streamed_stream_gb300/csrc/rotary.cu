@@ -12,6 +12,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "follow.cuh"
 #include "kernels.h"
 #include "mt_kernels.h"
 #include "ptx.cuh"
@@ -23,24 +24,54 @@ namespace {
 constexpr int kRotThreads = 256;
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
-struct Vec16 {  // 16 columns of one head's row, as loaded
-  uint4 a, b;
+// A unit's 16 values in fp32, arranged for the rotation: a[i] pairs with b[i], i < 8. In the half layout
+// a is the first vector and b the second; in the interleaved one a holds the even elements of both
+// and b the odd ones. Two neighbouring i at a time go through the packed fp32 units: with scalar
+// arithmetic these kernels are bound by instructions (19 to 27 an element for the norms), not HBM.
+struct Row16 {
+  float2 a[4], b[4];
 };
-
-__device__ __forceinline__ void unpack8(const uint4& w, float* v) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+template <bool INTER>
+__device__ __forceinline__ Row16 unpack(const uint4& v0, const uint4& v1) {
+  const uint32_t x[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  Row16 r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(x[j] << 16);
-    v[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (INTER) {
+      r.a[i] = make_float2(bf_lo(x[2 * i]), bf_lo(x[2 * i + 1]));
+      r.b[i] = make_float2(bf_hi(x[2 * i]), bf_hi(x[2 * i + 1]));
+    } else {
+      r.a[i] = make_float2(bf_lo(x[i]), bf_hi(x[i]));
+      r.b[i] = make_float2(bf_lo(x[4 + i]), bf_hi(x[4 + i]));
+    }
   }
+  return r;
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+template <bool INTER>
+__device__ __forceinline__ void pack(const Row16& r, uint4& v0, uint4& v1) {
+  uint32_t x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (INTER) {
+      x[2 * i] = pack2(r.a[i].x, r.b[i].x);
+      x[2 * i + 1] = pack2(r.a[i].y, r.b[i].y);
+    } else {
+      x[i] = pack2(r.a[i].x, r.a[i].y);
+      x[4 + i] = pack2(r.b[i].x, r.b[i].y);
+    }
+  }
+  v0 = make_uint4(x[0], x[1], x[2], x[3]);
+  v1 = make_uint4(x[4], x[5], x[6], x[7]);
+}
+// Column (within the unit's vectors) of value i of a (half 0) or b (half 1): vector, element.
+__device__ __forceinline__ int2 place_of(int half, int i, bool interleaved) {
+  return interleaved ? make_int2(i >> 2, 2 * (i & 3) + half) : make_int2(half, i);
 }
 
 // Where a unit's two vectors lie in the head's row, and whether it is rotated.
@@ -54,99 +85,90 @@ __device__ __forceinline__ Unit unit_of(int u, int hd, int rot) {
   return {c, c + (hd - rot) / 2, false};
 }
 
-// Cosine and sine of the unit's 8 rotation indices at a token's position; a position outside the
-// table raises the error flag and leaves the token as it is (angle 0).
-__device__ __forceinline__ void load_angles(const float* __restrict__ cs, const int32_t* __restrict__ positions,
-                                            int64_t t, int n_pos, int rot, bool interleaved, int u, int* err,
-                                            float4 (&r)[4]) {
-  const int p = positions ? positions[t] : static_cast<int>(t % n_pos);
-  if (p < 0 || p >= n_pos) {
-    atomicCAS(err, 0, kErrBadPosition);
+// Cosines and sines of the unit's 8 rotation indices, in pairs like Row16.
+struct Angles {
+  float2 c[4], s[4];
+};
+struct RawAngles {
+  float4 r[4];
+};
+__device__ __forceinline__ Angles angles_of(const RawAngles& w) {
+  Angles g;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = make_float4(1.f, 0.f, 1.f, 0.f);
-    return;
+  for (int k = 0; k < 4; ++k) {
+    g.c[k] = make_float2(w.r[k].x, w.r[k].z);
+    g.s[k] = make_float2(w.r[k].y, w.r[k].w);
   }
-  const float* q = cs + static_cast<int64_t>(p) * rot + (interleaved ? 8 : 16) * u;
-  const int second = interleaved ? rot / 2 : 8;  // floats to the angles of the unit's last 4 pairs
-#pragma unroll
-  for (int k = 0; k < 4; ++k) r[k] = __ldg(reinterpret_cast<const float4*>(q + (k >> 1) * second) + (k & 1));
+  return g;
 }
 
-// The rotation on the unit's 16 values (v[0..8) from the first vector); sgn -1 for the transpose.
-__device__ __forceinline__ void rotate(float (&v)[16], const float4 (&r)[4], bool interleaved, float sgn) {
+struct Rotation {
+  const float* cs;
+  const int32_t* positions;
+  int n_pos, rot;
+  int* err;
+};
+// Position of token t (T stays below 2^31), -1 if it is outside the table.
+__device__ __forceinline__ int position_of(const Rotation& q, uint32_t t) {
+  return q.positions ? q.positions[t] : static_cast<int>(t % static_cast<uint32_t>(q.n_pos));
+}
+// The unit's angles at a position; one outside the table raises the error flag and leaves the token
+// as it is (angle 0).
+template <bool INTER>
+__device__ __forceinline__ RawAngles load_angles(const Rotation& q, int p, int u) {
+  RawAngles w;
+  if (p < 0 || p >= q.n_pos) {
+    atomicCAS(q.err, 0, kErrBadPosition);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float c = (i & 1) ? r[i / 2].z : r[i / 2].x;
-    const float s = sgn * ((i & 1) ? r[i / 2].w : r[i / 2].y);
-    if (interleaved) {
-      const float a = v[2 * i], b = v[2 * i + 1];
-      v[2 * i] = a * c - b * s;
-      v[2 * i + 1] = b * c + a * s;
-    } else {
-      const float a = v[i], b = v[8 + i];
-      v[i] = a * c - b * s;
-      v[8 + i] = b * c + a * s;
-    }
+    for (int k = 0; k < 4; ++k) w.r[k] = make_float4(1.f, 0.f, 1.f, 0.f);
+    return w;
+  }
+  const float* row = q.cs + static_cast<int64_t>(p) * q.rot + (INTER ? 8 : 16) * u;
+  const int second = INTER ? q.rot / 2 : 8;  // floats to the angles of the unit's last 4 pairs
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w.r[k] = __ldg(reinterpret_cast<const float4*>(row + (k >> 1) * second) + (k & 1));
+  return w;
+}
+
+// a' = a c - b s, b' = b c + a s; INVERSE the transpose.
+template <bool INVERSE>
+__device__ __forceinline__ void rotate(Row16& v, const Angles& g) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 as = __fmul2_rn(v.a[k], g.s[k]), bs = __fmul2_rn(v.b[k], g.s[k]);
+    const float2 neg_as = make_float2(-as.x, -as.y), neg_bs = make_float2(-bs.x, -bs.y);
+    v.a[k] = __ffma2_rn(v.a[k], g.c[k], INVERSE ? bs : neg_bs);
+    v.b[k] = __ffma2_rn(v.b[k], g.c[k], INVERSE ? neg_as : as);
   }
 }
 
-// Threads of a block: unit (fastest), head slot, token slot. A thread takes the heads of its slot one
-// after the other; the slots are as few as give that many turns, so that the turns are even (48
-// heads of 8 units: 24 slots, two turns, not 32 and a half-empty second turn).
+// How a block's threads take rows: unit (fastest), head slot, token slot. A thread takes the heads of its
+// slot in turns and keeps its token's angles for them.
 struct RowSplit {
   int units, head_slots, token_slots;
-  int rows() const { return units * head_slots * token_slots; }
-  int threads() const { return (rows() + 31) / 32 * 32; }  // whole warps, for the row sums
+  __host__ __device__ int rows() const { return head_slots * token_slots; }
 };
-RowSplit row_split(int heads, int hd) {
-  RowSplit s;
-  s.units = hd / 16;
+// The split that leaves the fewest threads idle over the turns; among equals the one with the most
+// turns, up to most_turns, for angles loaded once a token (two turns, for few tokens, to spread
+// them). 8192 x 64 heads rotated in 4 turns 43.1 us, in 8 44.8, in 2 45.4; 4096 x 48 heads normed in up
+// to 8 turns 24.6 us, in up to 4 28.6.
+RowSplit row_split(int T, int heads, int hd, int most_turns) {
+  RowSplit s{hd / 16, 1, 1};
   const int slots = kRotThreads / s.units;
-  const int turns = (heads + slots - 1) / slots;
-  s.head_slots = (heads + turns - 1) / turns;
-  s.token_slots = slots / s.head_slots;
-  return s;
-}
-
-// Two heads a turn: both rows' loads are in flight together, and before the angles are needed.
-constexpr int kHeadsPerTurn = 2;
-
-__global__ void __launch_bounds__(kRotThreads)
-    rotary_kernel(const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int T, int heads, int hd, int rot, bool interleaved,
-                  const int32_t* __restrict__ positions, const float* __restrict__ cs, int n_pos, float sgn, int units,
-                  int head_slots, int token_slots, int* err) {
-  const int u = threadIdx.x % units, slot = threadIdx.x / units;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * token_slots + slot / head_slots;
-  if (t >= T || slot >= head_slots * token_slots) return;
-  const Unit w = unit_of(u, hd, rot);
-  if (!w.rotated && x == y) return;
-  float4 r[4];
-  if (w.rotated) load_angles(cs, positions, t, n_pos, rot, interleaved, u, err, r);
-  for (int h = slot % head_slots; h < heads; h += kHeadsPerTurn * head_slots) {
-    uint4 a[kHeadsPerTurn], b[kHeadsPerTurn];
-#pragma unroll
-    for (int k = 0; k < kHeadsPerTurn; ++k) {
-      if (h + k * head_slots >= heads) break;
-      const bf16* xr = x + t * ldx + static_cast<int64_t>(h + k * head_slots) * hd;
-      a[k] = *reinterpret_cast<const uint4*>(xr + w.c0);
-      b[k] = *reinterpret_cast<const uint4*>(xr + w.c1);
-    }
-#pragma unroll
-    for (int k = 0; k < kHeadsPerTurn; ++k) {
-      if (h + k * head_slots >= heads) break;
-      if (w.rotated) {
-        float v[16];
-        unpack8(a[k], v);
-        unpack8(b[k], v + 8);
-        rotate(v, r, interleaved, sgn);
-        a[k] = pack8(v);
-        b[k] = pack8(v + 8);
-      }
-      bf16* yr = y + t * ldy + static_cast<int64_t>(h + k * head_slots) * hd;
-      *reinterpret_cast<uint4*>(yr + w.c0) = a[k];
-      *reinterpret_cast<uint4*>(yr + w.c1) = b[k];
+  if (T < 152 * 16) most_turns = 2;
+  double best = -1.0;
+  for (int hs = heads < slots ? heads : slots; hs >= 1; --hs) {
+    const int turns = (heads + hs - 1) / hs;
+    if (turns > most_turns && best >= 0.0) break;
+    const int ts = slots / hs;
+    const double used = static_cast<double>(heads) * ts / (static_cast<double>(turns) * slots);
+    if (used >= best) {
+      best = used;
+      s.head_slots = hs;
+      s.token_slots = ts;
     }
   }
+  return s;
 }
 
 // Sum over the HD/16 threads of a head's row (consecutive lanes).
@@ -157,185 +179,261 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// y = R(x rstd g), rstd = 1/sqrt(mean x^2 + eps), one row per head. Threads past the last head or
-// token stay for the row sums (their rows are empty).
-template <int HD>
-__global__ void __launch_bounds__(kRotThreads)
-    qk_norm_rope_kernel(const bf16* x, int64_t ldx, const bf16* __restrict__ gq, const bf16* __restrict__ gk, bf16* y,
-                        int64_t ldy, float* __restrict__ rstd, int T, int nh, int heads, int rot, bool interleaved,
-                        float eps, const int32_t* __restrict__ positions, const float* __restrict__ cs, int n_pos,
-                        int head_slots, int token_slots, int* err) {
-  constexpr int kUnits = HD / 16;
-  const int u = threadIdx.x % kUnits, slot = threadIdx.x / kUnits;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * token_slots + slot / head_slots;
-  const bool live = t < T && slot < head_slots * token_slots;
-  const Unit w = unit_of(u, HD, rot);
+struct RowArgs {
+  const bf16* x;
+  int64_t ldx;
+  bf16* y;
+  int64_t ldy;
+  int T, heads, hd;
+  RowSplit split;
+  Rotation rotation;
+  // the norms'
+  int nh;
+  const bf16 *gq, *gk;
+  float* rstd;
+  float eps;
+};
+
+// One pass over rows: the rotation (HD = 0: any head size), or, with HD, y = R(x rstd g), rstd =
+// 1/sqrt(mean x^2 + eps), one row per head. A block takes token_slots tokens, a thread two heads a
+// turn: both rows' loads are in flight together, the first ones before the token's position and
+// angles, which depend on each other. What hides the rest of the latency is the number of threads, so
+// the gains are read again for every row (from L1) and the registers kept to four blocks an SM.
+// Threads past the last head or token stay for the row sums.
+constexpr int kHeadsPerTurn = 2;
+template <int HD, bool INTER, bool INVERSE>
+__global__ void __launch_bounds__(kRotThreads, 4) row_kernel(const __grid_constant__ RowArgs p) {
+  const int units = HD ? HD / 16 : p.split.units, hd = HD ? HD : p.hd, head_slots = p.split.head_slots;
+  const int u = threadIdx.x % units, slot = threadIdx.x / units;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * p.split.token_slots + slot / head_slots;
+  const Unit w = unit_of(u, hd, p.rotation.rot);
+  const bool live = t < p.T && slot < p.split.rows() && (HD || w.rotated || p.x != p.y);
+  if (!HD && !live) return;
   const int h0 = slot % head_slots;
-  float4 r[4];
-  if (live && w.rotated) load_angles(cs, positions, t, n_pos, rot, interleaved, u, err, r);
-  for (int hb = 0; hb < heads; hb += kHeadsPerTurn * head_slots) {  // the same trip count in every thread
-    uint4 a[kHeadsPerTurn], b[kHeadsPerTurn];
+  const int64_t step = static_cast<int64_t>(head_slots) * hd;
+  const bf16* xr = p.x + t * p.ldx + static_cast<int64_t>(h0) * hd;
+  bf16* yr = p.y + t * p.ldy + static_cast<int64_t>(h0) * hd;
+  uint4 v0[kHeadsPerTurn], v1[kHeadsPerTurn];
+  auto load = [&](int h) {
 #pragma unroll
     for (int k = 0; k < kHeadsPerTurn; ++k) {
-      const int h = hb + h0 + k * head_slots;
-      a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && h < heads) {
-        const bf16* xr = x + t * ldx + static_cast<int64_t>(h) * HD;
-        a[k] = *reinterpret_cast<const uint4*>(xr + w.c0);
-        b[k] = *reinterpret_cast<const uint4*>(xr + w.c1);
+      v0[k] = v1[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && h + k * head_slots < p.heads) {
+        v0[k] = *reinterpret_cast<const uint4*>(xr + k * step + w.c0);
+        v1[k] = *reinterpret_cast<const uint4*>(xr + k * step + w.c1);
       }
     }
+    xr += kHeadsPerTurn * step;
+  };
+  load(h0);
+  Angles ang{};
+  if (live && w.rotated) {
+    const int pos = position_of(p.rotation, static_cast<uint32_t>(t));
+    ang = angles_of(load_angles<INTER>(p.rotation, pos, u));
+  }
+  for (int hb = 0; hb < p.heads; hb += kHeadsPerTurn * head_slots) {  // the same turns in every thread
+    if (hb > 0) load(hb + h0);
 #pragma unroll
     for (int k = 0; k < kHeadsPerTurn; ++k) {
       const int h = hb + h0 + k * head_slots;
-      float v[16];
-      unpack8(a[k], v);
-      unpack8(b[k], v + 8);
-      float ss = 0.f;
+      const bool on = live && h < p.heads;
+      if constexpr (HD > 0) {
+        Row16 v = unpack<INTER>(v0[k], v1[k]);
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ss += v[i] * v[i];
-      const float rs = rsqrtf(row_sum<HD>(ss) * (1.f / HD) + eps);
-      if (!(live && h < heads)) continue;
-      const bf16* gain = h < nh ? gq : gk;
-      float g[16];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(gain + w.c0)), g);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(gain + w.c1)), g + 8);
+        for (int i = 0; i < 4; ++i) ss = __ffma2_rn(v.a[i], v.a[i], __ffma2_rn(v.b[i], v.b[i], ss));
+        const float rs = rsqrtf(row_sum<HD>(ss.x + ss.y) * (1.f / HD) + p.eps);
+        const bf16* gain = h < p.nh ? p.gq : p.gk;
+        const Row16 g = unpack<INTER>(__ldg(reinterpret_cast<const uint4*>(gain + w.c0)),
+                                      __ldg(reinterpret_cast<const uint4*>(gain + w.c1)));
+        const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = v[i] * rs * g[i];
-      if (w.rotated) rotate(v, r, interleaved, 1.f);
-      bf16* yr = y + t * ldy + static_cast<int64_t>(h) * HD;
-      *reinterpret_cast<uint4*>(yr + w.c0) = pack8(v);
-      *reinterpret_cast<uint4*>(yr + w.c1) = pack8(v + 8);
-      if (rstd && u == 0) rstd[t * heads + h] = rs;
+        for (int i = 0; i < 4; ++i) {
+          v.a[i] = __fmul2_rn(__fmul2_rn(v.a[i], rs2), g.a[i]);
+          v.b[i] = __fmul2_rn(__fmul2_rn(v.b[i], rs2), g.b[i]);
+        }
+        if (w.rotated) rotate<false>(v, ang);
+        pack<INTER>(v, v0[k], v1[k]);
+        if (on && p.rstd && u == 0) p.rstd[t * p.heads + h] = rs;
+      } else if (w.rotated) {
+        Row16 v = unpack<INTER>(v0[k], v1[k]);
+        rotate<INVERSE>(v, ang);
+        pack<INTER>(v, v0[k], v1[k]);
+      }
+      if (on) {
+        *reinterpret_cast<uint4*>(yr + k * step + w.c0) = v0[k];
+        *reinterpret_cast<uint4*>(yr + k * step + w.c1) = v1[k];
+      }
     }
+    yr += kHeadsPerTurn * step;
   }
 }
 
-// The backward's blocks take either query heads or key heads: blocks [0, blocks_q) the former, the
-// rest the latter, in proportion to the heads. A thread then sums one gain gradient only.
-struct BwdSide {
+template <int HD>
+cudaError_t launch_rows(const RowArgs& a, bool interleaved, bool inverse, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.T) + a.split.token_slots - 1) / a.split.token_slots);
+  auto* kernel = interleaved ? (inverse ? row_kernel<HD, true, HD == 0> : row_kernel<HD, true, false>)
+                             : (inverse ? row_kernel<HD, false, HD == 0> : row_kernel<HD, false, false>);
+  kernel<<<blocks, (a.split.units * a.split.rows() + 31) / 32 * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ backward of the query/key norms
+// Blocks take either query heads or key heads: blocks [0, q.blocks) the former, the rest the latter, in
+// proportion to the heads. A thread then has one gain, kept in registers, and one gain gradient.
+struct NormSide {
   RowSplit split;
   int blocks;
 };
-struct BwdSplit {
-  BwdSide q, k;
+struct NormSplit {
+  NormSide q, k;
 };
-BwdSplit bwd_split(int T, int nh, int nkv, int hd) {
-  BwdSplit s{{row_split(nh, hd), 0}, {row_split(nkv, hd), 0}};
+NormSplit norm_split(int T, int nh, int nkv, int hd) {
+  constexpr int blocks = kQkNormParts;
+  NormSplit s{{row_split(T, nh, hd, 8), 0}, {row_split(T, nkv, hd, 8), 0}};
   auto most = [T](const RowSplit& r) { return (T - 1) / r.token_slots + 1; };
-  const int share = static_cast<int>(static_cast<int64_t>(kQkNormParts) * nh / (nh + nkv)), q = share > 0 ? share : 1;
-  const int k = kQkNormParts > q ? kQkNormParts - q : 1;
+  const int share = static_cast<int>(static_cast<int64_t>(blocks) * nh / (nh + nkv)), q = share > 0 ? share : 1;
+  const int k = blocks > q ? blocks - q : 1;
   s.q.blocks = most(s.q.split) < q ? most(s.q.split) : q;
   s.k.blocks = most(s.k.split) < k ? most(s.k.split) : k;
   return s;
 }
 
+struct BwdArgs {
+  const bf16 *x, *dy;
+  int64_t ldx, lddy;
+  bf16* dx;
+  int64_t lddx;
+  const bf16 *gq, *gk;
+  const float* rstd;
+  float* partial;
+  int T, nh, heads;
+  Rotation rotation;
+};
+
 // One row's operands as loaded, a turn ahead of their use.
-struct RowPair {
-  uint4 d0, d1, x0, x1;
+struct RawRow {
+  uint4 x0, x1, d0, d1;
   float rs;
 };
 
-// With u = R^T dy and n = x rstd: dx = rstd (u g - n mean(u g n)) per head row, and each block's
-// share of dg = sum over tokens and heads of u n. A thread keeps its 16 columns for every row it
-// takes, so the gain sums stay in registers; at the end they are added over the block's slots in
-// slot order and written to the block's row of `partial` [blocks][HD]: fixed order, no atomics. The
-// next row and, with a new token, its angles are loaded before the current row is worked on.
-template <int HD>
+// With u = R^T dy and n = x rstd: dx = rstd (u g - n mean(u g n)) per head row, and the block's share
+// of dg = sum over its rows of u n: a thread keeps its 16 columns for every row it takes, so the sums
+// stay in registers; at the end they are added over the block's slots in slot order and written to the
+// block's row of `partial` [blocks][HD]: fixed order, no atomics.
+// The next row and, with a new token, its angles are loaded before the current row is worked on, and
+// the position of the token after that.
+template <int HD, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, 2)
-    qk_norm_rope_bwd_kernel(const bf16* dy, int64_t lddy, const bf16* x, int64_t ldx, const bf16* __restrict__ gq,
-                            const bf16* __restrict__ gk, const float* __restrict__ rstd, bf16* dx, int64_t lddx,
-                            float* __restrict__ partial, int T, int nh, int all_heads, int rot, bool interleaved,
-                            const int32_t* __restrict__ positions, const float* __restrict__ cs, int n_pos,
-                            const __grid_constant__ BwdSplit bs, int* err) {
+    qk_norm_bwd_kernel(const __grid_constant__ BwdArgs p, const __grid_constant__ NormSplit bs) {
   constexpr int kUnits = HD / 16;
   __shared__ float sums[kRotThreads][17];
+  let_next_start();
   const bool is_q = static_cast<int>(blockIdx.x) < bs.q.blocks;
-  const BwdSide& side = is_q ? bs.q : bs.k;
+  const NormSide& side = is_q ? bs.q : bs.k;
   const int head_slots = side.split.head_slots, token_slots = side.split.token_slots;
-  const int heads = is_q ? nh : all_heads - nh, first = is_q ? 0 : nh;
+  const int heads = is_q ? p.nh : p.heads - p.nh, first = is_q ? 0 : p.nh;
   const int block = is_q ? blockIdx.x : blockIdx.x - bs.q.blocks;
   const int u = threadIdx.x % kUnits, slot = threadIdx.x / kUnits;
+  const int h0 = slot % head_slots;
   const bool in = slot < head_slots * token_slots;
-  const Unit w = unit_of(u, HD, rot);
-  const int h0 = slot % head_slots, tslot = slot / head_slots;
-  const uint4 g0 = __ldg(reinterpret_cast<const uint4*>((is_q ? gq : gk) + w.c0));
-  const uint4 g1 = __ldg(reinterpret_cast<const uint4*>((is_q ? gq : gk) + w.c1));
-  float acc[16];
+  const Unit w = unit_of(u, HD, p.rotation.rot);
+  const bool turns_on = in && w.rotated;
+  const uint32_t T = static_cast<uint32_t>(p.T);
+  const bf16* gain = is_q ? p.gq : p.gk;
+  const Row16 g = unpack<INTER>(__ldg(reinterpret_cast<const uint4*>(gain + w.c0)),
+                                __ldg(reinterpret_cast<const uint4*>(gain + w.c1)));
+  Row16 acc;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int k = 0; k < 4; ++k) acc.a[k] = acc.b[k] = make_float2(0.f, 0.f);
 
-  int64_t t = static_cast<int64_t>(block) * token_slots + tslot;  // the row being loaded
-  int hb = 0;
-  const int64_t step = static_cast<int64_t>(side.blocks) * token_slots;
+  uint32_t t = static_cast<uint32_t>(block) * token_slots + slot / head_slots;  // the row being loaded: token,
+  int hb = 0;                                                                 // head - h0
+  const uint32_t step = static_cast<uint32_t>(side.blocks) * token_slots;
   const int turns = (heads + head_slots - 1) / head_slots;
-  const int64_t token_turns = (T - 1 - static_cast<int64_t>(block) * token_slots) / step + 1;  // >= 1
-  auto load = [&](RowPair& p) {
-    p.d0 = p.d1 = p.x0 = p.x1 = make_uint4(0u, 0u, 0u, 0u);
-    p.rs = 0.f;
+  const uint32_t tokens = (T - 1 - static_cast<uint32_t>(block) * token_slots) / step + 1;  // >= 1
+  auto load = [&](RawRow& r) {
+    r.x0 = r.x1 = r.d0 = r.d1 = make_uint4(0u, 0u, 0u, 0u);
+    r.rs = 0.f;
     if (in && t < T && hb + h0 < heads) {
       const int64_t col = static_cast<int64_t>(first + hb + h0) * HD;
-      const bf16 *dr = dy + t * lddy + col, *xr = x + t * ldx + col;
-      p.d0 = *reinterpret_cast<const uint4*>(dr + w.c0);
-      p.d1 = *reinterpret_cast<const uint4*>(dr + w.c1);
-      p.x0 = *reinterpret_cast<const uint4*>(xr + w.c0);
-      p.x1 = *reinterpret_cast<const uint4*>(xr + w.c1);
-      p.rs = rstd[t * all_heads + first + hb + h0];
+      const bf16* xr = p.x + t * p.ldx + col;
+      r.x0 = *reinterpret_cast<const uint4*>(xr + w.c0);
+      r.x1 = *reinterpret_cast<const uint4*>(xr + w.c1);
+      const bf16* dr = p.dy + t * p.lddy + col;
+      r.d0 = *reinterpret_cast<const uint4*>(dr + w.c0);
+      r.d1 = *reinterpret_cast<const uint4*>(dr + w.c1);
+      r.rs = p.rstd[static_cast<int64_t>(t) * p.heads + first + hb + h0];
     }
   };
-  float4 r[4], r_next[4];
-  RowPair next;
+  RawRow next;
+  RawAngles raw{};
+  Angles ang{};
+  int pos = turns_on && t < T ? position_of(p.rotation, t) : 0;
   load(next);
-  if (in && t < T && w.rotated) load_angles(cs, positions, t, n_pos, rot, interleaved, u, err, r_next);
-  for (int64_t it = 0; it < token_turns * turns; ++it) {
-    const RowPair cur = next;
-    const int64_t tc = t;
-    const int hc = hb + h0;
-    const bool on = in && t < T && hc < heads;
-    if (hb == 0) {
+  if (turns_on && t < T) raw = load_angles<INTER>(p.rotation, pos, u);
+  if (turns_on && t + step < T) pos = position_of(p.rotation, t + step);
+  for (uint32_t it = 0; it < tokens; ++it) {
+    ang = angles_of(raw);
+    for (int turn = 0; turn < turns; ++turn) {
+      const RawRow cur = next;
+      const uint32_t tc = t;
+      const int hc = hb + h0;
+      const bool on = in && t < T && hc < heads;
+      hb += head_slots;
+      if (turn + 1 == turns) {
+        hb = 0;
+        t += step;
+        if (turns_on && t < T) {
+          raw = load_angles<INTER>(p.rotation, pos, u);
+          if (t + step < T) pos = position_of(p.rotation, t + step);
+        }
+      }
+      load(next);
+      Row16 n = unpack<INTER>(cur.x0, cur.x1);
+      Row16 d = unpack<INTER>(cur.d0, cur.d1);
+      if (w.rotated) rotate<true>(d, ang);
+      const float2 rs2 = make_float2(cur.rs, cur.rs);
+      float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) r[k] = r_next[k];
-    }
-    hb += head_slots;
-    if (hb >= heads) {
-      hb = 0;
-      t += step;
-      if (in && t < T && w.rotated) load_angles(cs, positions, t, n_pos, rot, interleaved, u, err, r_next);
-    }
-    load(next);
-    float d[16], n[16], g[16];
-    unpack8(cur.d0, d);
-    unpack8(cur.d1, d + 8);
-    unpack8(cur.x0, n);
-    unpack8(cur.x1, n + 8);
-    unpack8(g0, g);
-    unpack8(g1, g + 8);
-    if (on && w.rotated) rotate(d, r, interleaved, -1.f);
-    float dot = 0.f;
+      for (int k = 0; k < 4; ++k) {
+        n.a[k] = __fmul2_rn(n.a[k], rs2);
+        n.b[k] = __fmul2_rn(n.b[k], rs2);
+        acc.a[k] = __ffma2_rn(d.a[k], n.a[k], acc.a[k]);
+        acc.b[k] = __ffma2_rn(d.b[k], n.b[k], acc.b[k]);
+        d.a[k] = __fmul2_rn(d.a[k], g.a[k]);
+        d.b[k] = __fmul2_rn(d.b[k], g.b[k]);
+        dot = __ffma2_rn(d.a[k], n.a[k], __ffma2_rn(d.b[k], n.b[k], dot));
+      }
+      const float m = row_sum<HD>(dot.x + dot.y) * (-1.f / HD);
+      const float2 m2 = make_float2(m, m);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      n[i] *= cur.rs;
-      acc[i] += d[i] * n[i];
-      d[i] *= g[i];
-      dot += d[i] * n[i];
+      for (int k = 0; k < 4; ++k) {
+        n.a[k] = __fmul2_rn(rs2, __ffma2_rn(n.a[k], m2, d.a[k]));
+        n.b[k] = __fmul2_rn(rs2, __ffma2_rn(n.b[k], m2, d.b[k]));
+      }
+      if (on) {
+        bf16* o = p.dx + tc * p.lddx + static_cast<int64_t>(first + hc) * HD;
+        uint4 v0, v1;
+        pack<INTER>(n, v0, v1);
+        *reinterpret_cast<uint4*>(o + w.c0) = v0;
+        *reinterpret_cast<uint4*>(o + w.c1) = v1;
+      }
     }
-    const float m = row_sum<HD>(dot) * (1.f / HD);
-    if (!on) continue;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) d[i] = cur.rs * (d[i] - n[i] * m);
-    bf16* o = dx + tc * lddx + static_cast<int64_t>(first + hc) * HD;
-    *reinterpret_cast<uint4*>(o + w.c0) = pack8(d);
-    *reinterpret_cast<uint4*>(o + w.c1) = pack8(d + 8);
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sums[threadIdx.x][i] = acc[i];
+  for (int i = 0; i < 8; ++i) {
+    sums[threadIdx.x][i] = (i & 1) ? acc.a[i / 2].y : acc.a[i / 2].x;
+    sums[threadIdx.x][8 + i] = (i & 1) ? acc.b[i / 2].y : acc.b[i / 2].x;
+  }
   __syncthreads();
   if (threadIdx.x < HD) {  // one thread per (unit, value) pair
     const int un = threadIdx.x / 16, i = threadIdx.x % 16;
     float s = 0.f;
     for (int k = 0; k < head_slots * token_slots; ++k) s += sums[k * kUnits + un][i];
-    const Unit q = unit_of(un, HD, rot);
-    partial[static_cast<int64_t>(blockIdx.x) * HD + (i < 8 ? q.c0 + i : q.c1 + i - 8)] = s;
+    const Unit q = unit_of(un, HD, p.rotation.rot);
+    const int2 at = place_of(i >> 3, i & 7, INTER);
+    p.partial[static_cast<int64_t>(blockIdx.x) * HD + (at.x ? q.c1 : q.c0) + at.y] = s;
   }
 }
 
@@ -351,6 +449,7 @@ __global__ void __launch_bounds__(1024)
   const int j = threadIdx.x % HD, g = threadIdx.x / HD;
   const int p0 = blockIdx.x ? blocks_q : 0, p1 = blockIdx.x ? blocks_q + blocks_k : blocks_q;
   float s = 0.f;
+  wait_for_previous();
   for (int p = p0 + g; p < p1; p += kGroups) s += partial[static_cast<int64_t>(p) * HD + j];
   acc[g][j] = s;
   __syncthreads();
@@ -472,32 +571,34 @@ cudaError_t rotary(const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int T, int 
   if (!vec_aligned(x, ldx) || !vec_aligned(y, ldy) || ldx < static_cast<int64_t>(heads) * hd ||
       ldy < static_cast<int64_t>(heads) * hd || (x == y && ldx != ldy))
     return cudaErrorInvalidValue;
-  const RowSplit sp = row_split(heads, hd);
-  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(T) + sp.token_slots - 1) / sp.token_slots);
-  rotary_kernel<<<blocks, sp.threads(), 0, s>>>(x, ldx, y, ldy, T, heads, hd, rot, interleaved, positions, cs, n_pos,
-                                                inverse ? -1.f : 1.f, sp.units, sp.head_slots, sp.token_slots, err);
-  return cudaGetLastError();
+  const RowArgs a{x, ldx, y, ldy, T, heads, hd, row_split(T, heads, hd, 4), {cs, positions, n_pos, rot, err},
+                  0, nullptr, nullptr, nullptr, 0.f};
+  return launch_rows<0>(a, interleaved, inverse, s);
 }
+
+namespace {
+bool norm_ok(int T, int nh, int nkv, int hd, int rot, const float* cs, int n_pos, const int32_t* positions,
+             const bf16* gq, const bf16* gk, const int* err) {
+  return T > 0 && nh > 0 && nkv > 0 && heads_ok(static_cast<int64_t>(nh) + nkv) && (hd == 64 || hd == 128) &&
+         rotation_ok(hd, rot, cs, n_pos, positions, err) && vec_aligned(gq, 0) && vec_aligned(gk, 0);
+}
+}  // namespace
 
 cudaError_t qk_norm_rope(const bf16* x, int64_t ldx, const bf16* gq, const bf16* gk, bf16* y, int64_t ldy, float* rstd,
                          int T, int nh, int nkv, int hd, int rot, bool interleaved, float eps,
                          const int32_t* positions, const float* cs, int n_pos, int* err, cudaStream_t s) {
-  if (T <= 0 || nh <= 0 || nkv <= 0 || !heads_ok(static_cast<int64_t>(nh) + nkv) || (hd != 64 && hd != 128) || !rotation_ok(hd, rot, cs, n_pos, positions, err))
-    return cudaErrorInvalidValue;
+  if (!norm_ok(T, nh, nkv, hd, rot, cs, n_pos, positions, gq, gk, err)) return cudaErrorInvalidValue;
   const int heads = nh + nkv;
-  if (!vec_aligned(x, ldx) || !vec_aligned(y, ldy) || !vec_aligned(gq, 0) || !vec_aligned(gk, 0) ||
-      ldx < static_cast<int64_t>(heads) * hd || ldy < static_cast<int64_t>(heads) * hd || (x == y && ldx != ldy))
+  const int64_t cols = static_cast<int64_t>(heads) * hd;
+  if (!vec_aligned(x, ldx) || !vec_aligned(y, ldy) || ldx < cols || ldy < cols || (x == y && ldx != ldy))
     return cudaErrorInvalidValue;
-  const RowSplit sp = row_split(heads, hd);
-  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(T) + sp.token_slots - 1) / sp.token_slots);
-  (hd == 64 ? qk_norm_rope_kernel<64> : qk_norm_rope_kernel<128>)<<<blocks, sp.threads(), 0, s>>>(
-      x, ldx, gq, gk, y, ldy, rstd, T, nh, heads, rot, interleaved, eps, positions, cs, n_pos, sp.head_slots,
-      sp.token_slots, err);
-  return cudaGetLastError();
+  const RowArgs a{x, ldx, y, ldy, T, heads, hd, row_split(T, heads, hd, 8), {cs, positions, n_pos, rot, err},
+                  nh, gq, gk, rstd, eps};
+  return hd == 64 ? launch_rows<64>(a, interleaved, false, s) : launch_rows<128>(a, interleaved, false, s);
 }
 
 int qk_norm_rope_bwd_parts(int T, int nh, int nkv, int hd) {
-  const BwdSplit s = bwd_split(T, nh, nkv, hd);
+  const NormSplit s = norm_split(T, nh, nkv, hd);
   return s.q.blocks + s.k.blocks;
 }
 
@@ -505,23 +606,21 @@ cudaError_t qk_norm_rope_bwd(const bf16* dy, int64_t lddy, const bf16* x, int64_
                              const float* rstd, bf16* dx, int64_t lddx, float* partial, bf16* dgq, bf16* dgk, int T,
                              int nh, int nkv, int hd, int rot, bool interleaved, const int32_t* positions,
                              const float* cs, int n_pos, int* err, cudaStream_t s) {
-  if (T <= 0 || nh <= 0 || nkv <= 0 || !heads_ok(static_cast<int64_t>(nh) + nkv) || (hd != 64 && hd != 128) || !rotation_ok(hd, rot, cs, n_pos, positions, err))
-    return cudaErrorInvalidValue;
+  if (!norm_ok(T, nh, nkv, hd, rot, cs, n_pos, positions, gq, gk, err)) return cudaErrorInvalidValue;
   const int heads = nh + nkv;
   const int64_t cols = static_cast<int64_t>(heads) * hd;
-  if (!vec_aligned(dy, lddy) || !vec_aligned(x, ldx) || !vec_aligned(dx, lddx) || !vec_aligned(gq, 0) ||
-      !vec_aligned(gk, 0) || lddy < cols || ldx < cols || lddx < cols || (dx == dy && lddx != lddy) ||
-      (dx == x && lddx != ldx))
+  if (!vec_aligned(dy, lddy) || !vec_aligned(x, ldx) || !vec_aligned(dx, lddx) || lddy < cols || ldx < cols ||
+      lddx < cols || (dx == dy && lddx != lddy) || (dx == x && lddx != ldx))
     return cudaErrorInvalidValue;
-  const BwdSplit sp = bwd_split(T, nh, nkv, hd);
-  (hd == 64 ? qk_norm_rope_bwd_kernel<64> : qk_norm_rope_bwd_kernel<128>)<<<sp.q.blocks + sp.k.blocks, kRotThreads, 0,
-                                                                            s>>>(
-      dy, lddy, x, ldx, gq, gk, rstd, dx, lddx, partial, T, nh, heads, rot, interleaved, positions, cs, n_pos, sp, err);
+  const NormSplit sp = norm_split(T, nh, nkv, hd);
+  const BwdArgs a{x, dy, ldx, lddy, dx, lddx, gq, gk, rstd, partial, T, nh, heads, {cs, positions, n_pos, rot, err}};
+  auto* kernel = hd == 64 ? (interleaved ? qk_norm_bwd_kernel<64, true> : qk_norm_bwd_kernel<64, false>)
+                          : (interleaved ? qk_norm_bwd_kernel<128, true> : qk_norm_bwd_kernel<128, false>);
+  kernel<<<sp.q.blocks + sp.k.blocks, kRotThreads, 0, s>>>(a, sp);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  (hd == 64 ? qk_gain_reduce_kernel<64> : qk_gain_reduce_kernel<128>)<<<2, 1024, 0, s>>>(
-      partial, sp.q.blocks, sp.k.blocks, dgq, dgk);
-  return cudaGetLastError();
+  return launch_following(hd == 64 ? qk_gain_reduce_kernel<64> : qk_gain_reduce_kernel<128>, dim3(2), 1024, 0, s, partial,
+                          sp.q.blocks, sp.k.blocks, dgq, dgk);
 }
 
 }  // namespace mt
