@@ -29,11 +29,17 @@ namespace {
 
 using namespace span;
 
-constexpr int kThreads = 192;
 constexpr int kKeys = 64;              // keys per tile
 constexpr int kSlice128 = 128 * 128;   // [128 rows][64 bf16]: one 128-byte swizzle atom wide
 constexpr int kSlice64 = 64 * 128;     // [64 rows][64 bf16]
 constexpr float kLazyRescale = 8.f;    // log2 units
+// Capped scores lie in [-c log2(e), c log2(e)]. Up to kBounded log2 units (c <= 69) the exponentials
+// need no running maximum: 2^(z - kBoundedRef) stays between 2^-108 and 2^92, and the sums of 2^22 keys
+// and values below 2^14 within fp32. Without it a row's two halves of a tile have nothing to tell
+// each other, so two threads share a row (eight softmax warps): the tanh's polynomial is long, and
+// four warps a block left the FMA units idle half of the time (16384 tokens, 8/2 heads, capped:
+// 691 us with the running maximum and one thread a row).
+constexpr float kBounded = 100.f, kBoundedRef = 8.f;
 constexpr int kKStages = 3;            // K ring depth
 constexpr int kVStages = 2;            // V ring depth
 
@@ -60,11 +66,13 @@ struct FwdArgs {
   int* err;
 };
 
-template <int HD, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int HD, bool CAP, bool BIAS, bool BOUNDED>
+__global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
     attn_span_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ FwdArgs a) {
   using L = Smem<HD>;
+  constexpr int kCols = BOUNDED ? 32 : 64;      // score columns of a softmax thread
+  constexpr int kSoftmax = BOUNDED ? 256 : 128;  // softmax threads
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   int* err = a.err;
@@ -103,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (q < s) seen = load_span(a.spans, b, q, s);
     const Hull h = warp_hull(row_hull(seen, q < s));
     const uint32_t none = __ballot_sync(0xffffffffu, seen.x >= seen.y);
-    if (lane == 0) {
+    if (lane == 0 && warp < 6) {
       hulls[sub] = h;
       empty_rows[sub] = none;
     }
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], kSoftmax);
     }
     mbar_init(pv_done, 1);
     mbar_init(o_done, 1);
@@ -194,98 +202,106 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint64_t vd = smem_desc_sw128(smem_addr(sm + L::V + vs * L::TILE), kSlice64, 1024);
 #pragma unroll
       for (int kk = 0; kk < kKeys / 16; ++kk)  // A = P_j from TMEM: 16 keys = 8 columns per step
-        umma_bf16_tmem_a_warp(tO, tS0 + st * kKeys + kk * 8, desc_advance(vd, kk * 2048), idesc_o,
+        umma_bf16_tmem_a_warp(tO, tS0 + st * kKeys + (16 * kk / kCols) * kCols + 16 * kk % kCols / 2, desc_advance(vd, kk * 2048), idesc_o,
                               (j > 0 || kk > 0) ? 1u : 0u);
       umma_commit_warp(&v_empty[vs]);
       umma_commit_warp(pv_done);
       if (j == n_kv - 1) umma_commit_warp(o_done);
     }
   } else {
-    // ------------------------------------------------------------ softmax (warps 2..5)
+    // ------------------------------------------------------------ softmax (warps 2..5, or 2..9)
     const uint32_t tl = static_cast<uint32_t>(sub * 32) << 16;
+    const int part = (warp - 2) >> 2;  // which kCols of a tile's columns (0 with one thread a row)
+    const int elem = threadIdx.x - 64;
     const bool padded = (empty_rows[0] | empty_rows[1] | empty_rows[2] | empty_rows[3]) != 0;
     const float slope2 = BIAS ? a.slopes[head] * kLog2e : 0.f;
-    float m_ref = -INFINITY, l = 0.f;
+    const float to_log2 = CAP ? a.score.cap_log2 : a.score.scale_log2;  // a score times this: log2 units
+    float m_ref = BOUNDED ? kBoundedRef : -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n_kv; ++j) {
       const int st = j & 1;
       const int key0 = (j0 + j) * kKeys;
+      // this thread's scores and, over them, its part of P as bf16 pairs (key 2c in the low half of
+      // column c): a thread overwrites only columns that it has read
+      const uint32_t tS = tS0 + tl + st * kKeys + part * kCols;
       if (!(ok = mbar_wait_warp(&s_full[st], (j >> 1) & 1, err, kErrTimeoutAttn))) break;
       tc_fence_after();
-      float sc[kKeys];
+      float sc[kCols];
 #pragma unroll
-      for (int c4 = 0; c4 < kKeys / 32; ++c4) {
+      for (int c4 = 0; c4 < kCols / 32; ++c4) {
         uint32_t r[32];
-        tmem_ld_32cols(tS0 + tl + st * kKeys + c4 * 32, r);
+        tmem_ld_32cols(tS + c4 * 32, r);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) sc[c4 * 32 + i] = __uint_as_float(r[i]);
       }
-      if constexpr (CAP) cap_tanh<kKeys>(sc, a.score);
-      const float to_log2 = CAP ? a.score.cap_log2 : a.score.scale_log2;  // sc times this: log2 units
+      if constexpr (CAP) cap_tanh<kCols>(sc, a.score);
       if constexpr (BIAS) {
         const float d0 = static_cast<float>(q - key0);
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c)
+        for (int c = 0; c < kCols; ++c)
           sc[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), sc[c] * to_log2);
       }
       if (!sees_all(hull, key0, key0 + kKeys)) {
 #pragma unroll
-        for (int c4 = 0; c4 < kKeys / 32; ++c4) {
-          const uint32_t vis = span_bits(seen, key0 + c4 * 32);
+        for (int c4 = 0; c4 < kCols / 32; ++c4) {
+          const uint32_t vis = span_bits(seen, key0 + part * kCols + c4 * 32);
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (!(vis >> c & 1u)) sc[c4 * 32 + c] = -INFINITY;
         }
       }
-      float r = sc[0];
+      if constexpr (!BOUNDED) {
+        float r = sc[0];
 #pragma unroll
-      for (int c = 1; c + 1 < kKeys; c += 2) r = fmax3(r, sc[c], sc[c + 1]);
-      const float mx = fmaxf(r, sc[kKeys - 1]) * (BIAS ? 1.f : to_log2);
-      const bool need = mx > m_ref + kLazyRescale;
-      const float m_new = need ? mx : m_ref;
-      // rescale O only when a row's max grew past the lazy threshold; O += P_{j-1} V_{j-1} must
-      // have finished first (P_j may be written before it has: it goes to the other buffer)
-      if (j > 0 && __any_sync(0xffffffffu, need)) {
-        if (!(ok = mbar_wait_warp(pv_done, (j - 1) & 1, err, kErrTimeoutAttn))) break;
-        tc_fence_after();
-        const float factor = need ? ex2(m_ref - m_new) : 1.f;  // 0 where nothing was seen before
+        for (int c = 1; c + 1 < kCols; c += 2) r = fmax3(r, sc[c], sc[c + 1]);
+        const float mx = fmaxf(r, sc[kCols - 1]) * (BIAS ? 1.f : to_log2);
+        const bool need = mx > m_ref + kLazyRescale;
+        const float m_new = need ? mx : m_ref;
+        // rescale O only when a row's max grew past the lazy threshold; O += P_{j-1} V_{j-1} must
+        // have finished first (P_j may be written before it has: it goes to the other buffer)
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
+          if (!(ok = mbar_wait_warp(pv_done, (j - 1) & 1, err, kErrTimeoutAttn))) break;
+          tc_fence_after();
+          const float factor = need ? ex2(m_ref - m_new) : 1.f;  // 0 where nothing was seen before
 #pragma unroll
-        for (int c4 = 0; c4 < HD / 32; ++c4) {
-          uint32_t w[32];
-          tmem_ld_32cols(tO + tl + c4 * 32, w);
-          tmem_ld_wait();
+          for (int c4 = 0; c4 < HD / 32; ++c4) {
+            uint32_t w[32];
+            tmem_ld_32cols(tO + tl + c4 * 32, w);
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * factor);
-          tmem_st_32cols(tO + tl + c4 * 32, w);
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * factor);
+            tmem_st_32cols(tO + tl + c4 * 32, w);
+          }
+          tmem_st_wait();
+          l *= factor;
         }
-        tmem_st_wait();
-        l *= factor;
+        m_ref = m_new;
       }
-      m_ref = m_new;
-      uint32_t pw[kKeys / 2];  // P_j as bf16 pairs: key 2c in the low half of column c
+      uint32_t pw[kCols / 2];
       const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
       const float2 sl = make_float2(to_log2, to_log2), nm = make_float2(neg_m, neg_m);
       float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < kKeys / 2; ++c) {
+      for (int c = 0; c < kCols / 2; ++c) {
         const float2 x = make_float2(sc[2 * c], sc[2 * c + 1]);
         const float2 v = BIAS ? __fadd2_rn(x, nm) : __ffma2_rn(x, sl, nm);
         const float2 pp = make_float2(ex2(v.x), ex2(v.y));
         acc = __fadd2_rn(acc, pp);
         pw[c] = pack_bf16(pp.x, pp.y);
       }
-      tmem_st_32cols(tS0 + tl + st * kKeys, pw);
+      if constexpr (kCols == 64) tmem_st_32cols(tS, pw);
+      else tmem_st_16cols(tS, pw);
       tmem_st_wait();
       l += acc.x + acc.y;
       // rows of V that nothing here may see: outside the hull, or padding among the tile's own rows
       const bool own = padded && key0 < q0 + 128 && key0 + kKeys > q0;
       if (key0 < hull.min_lo || key0 + kKeys > hull.max_hi || own) {
         if (!(ok = mbar_wait_warp(&v_full[j % kVStages], (j / kVStages) & 1, err, kErrTimeoutAttn))) break;
-        const int kr = row & 63, key = key0 + kr, part = row >> 6;
+        const int kr = elem & 63, key = key0 + kr, which = elem >> 6;
         const bool pad = own && key >= q0 && key < q0 + 128 && (empty_rows[(key - q0) >> 5] >> ((key - q0) & 31) & 1u);
-        if ((key < hull.min_lo || key >= hull.max_hi || pad) && part < L::NSL)
-          zero_slice_row(sm + L::V + (j % kVStages) * L::TILE + part * kSlice64, kr);
+        if ((key < hull.min_lo || key >= hull.max_hi || pad) && which < L::NSL)
+          zero_slice_row(sm + L::V + (j % kVStages) * L::TILE + which * kSlice64, kr);
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -293,20 +309,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // the output waits on its own barrier: a parity wait on pv_done could not tell the last
     // product's phase from the one two before it
-    if (ok && (n_kv == 0 || mbar_wait_warp(o_done, 0, err, kErrTimeoutAttn))) {
-      tc_fence_after();
+    ok = ok && (n_kv == 0 || mbar_wait_warp(o_done, 0, err, kErrTimeoutAttn));
+    tc_fence_after();
+    if constexpr (BOUNDED) {  // the row's two sums, through Q's memory (every product has run)
+      float* sums = reinterpret_cast<float*>(sm + L::Q);
+      if (ok) sums[part * 128 + row] = l;
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory");
+      if (ok) l += sums[(part ^ 1) * 128 + row];
+    }
+    if (ok) {
       const bool some = l != 0.f;  // NaN counts as something
       const float inv = 1.f / l;
-      // the warp's 32 rows, 64 columns at a time
-      bf16* o0 = a.o + (static_cast<int64_t>(b) * s + q0 + sub * 32) * a.ldo + static_cast<int64_t>(head) * HD;
+      // the warp's 32 rows and this part's columns, up to 64 at a time
+      constexpr int kOut = BOUNDED ? HD / 2 : HD, kStep = kOut < 64 ? kOut : 64;
+      bf16* o0 = a.o + (static_cast<int64_t>(b) * s + q0 + sub * 32) * a.ldo + static_cast<int64_t>(head) * HD + part * kOut;
 #pragma unroll
-      for (int c64 = 0; c64 < HD / 64; ++c64) {
-        uint4 out[8];
+      for (int c = 0; c < kOut; c += kStep) {
+        uint4 out[kStep / 8];
 #pragma unroll
-        for (int c4 = 0; c4 < 2; ++c4) {
+        for (int c4 = 0; c4 < kStep / 32; ++c4) {
           uint32_t r[32] = {};
           if (n_kv > 0) {
-            tmem_ld_32cols(tO + tl + c64 * 64 + c4 * 32, r);
+            tmem_ld_32cols(tO + tl + part * kOut + c + c4 * 32, r);
             tmem_ld_wait();
           }
 #pragma unroll
@@ -318,9 +342,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                                          pack_bf16(__uint_as_float(r[8 * v + 4]), __uint_as_float(r[8 * v + 5])),
                                          pack_bf16(__uint_as_float(r[8 * v + 6]), __uint_as_float(r[8 * v + 7])));
         }
-        store_rows<8>(o0 + c64 * 64, a.ldo, s - q0 - sub * 32, out, lane);
+        store_rows<kStep / 8>(o0 + c, a.ldo, s - q0 - sub * 32, out, lane);
       }
-      if (q < s) a.lse[(static_cast<int64_t>(b) * nh + head) * s + q] = some ? m_ref + log2f(l) : -INFINITY;
+      if (q < s && part == 0)
+        a.lse[(static_cast<int64_t>(b) * nh + head) * s + q] = some ? m_ref + log2f(l) : -INFINITY;
     }
   }
 
@@ -339,13 +364,19 @@ cudaError_t launch(const AttnSpanArgs& g, bf16* o, int64_t ldo, float* lse, int*
       !tma_map_heads(&mk, g.k, s, g.B, g.ldk, s * g.ldk, static_cast<uint64_t>(g.nkv) * L::NSL, L::NSL, kKeys) ||
       !tma_map_heads(&mv, g.v, s, g.B, g.ldv, s * g.ldv, static_cast<uint64_t>(g.nkv) * L::NSL, L::NSL, kKeys))
     return cudaErrorInvalidValue;
-  auto* kernel = &attn_span_fwd_kernel<HD, CAP, BIAS>;
-  static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = allow_smem(kernel, L::BYTES, ready);
-  if (e != cudaSuccess) return e;
   const FwdArgs a{{g.lo, g.hi}, g.slopes, o, ldo, lse, g.s, g.nh, g.nkv, score_args(g), err};
-  kernel<<<static_cast<unsigned>((s + 127) / 128 * g.nh * g.B), kThreads, L::BYTES, st>>>(mq, mk, mv, a);
-  return cudaGetLastError();
+  auto run = [&](auto bounded) {
+    auto* kernel = &attn_span_fwd_kernel<HD, CAP, BIAS, decltype(bounded)::value>;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = allow_smem(kernel, L::BYTES, ready);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>((s + 127) / 128 * g.nh * g.B), decltype(bounded)::value ? 320 : 192, L::BYTES, st>>>(
+        mq, mk, mv, a);
+    return cudaGetLastError();
+  };
+  if constexpr (CAP && !BIAS)
+    if (a.score.cap_log2 <= kBounded) return run(std::true_type{});
+  return run(std::false_type{});
 }
 
 }  // namespace
