@@ -33,13 +33,13 @@ constexpr int kKeys = 64;              // keys per tile
 constexpr int kSlice128 = 128 * 128;   // [128 rows][64 bf16]: one 128-byte swizzle atom wide
 constexpr int kSlice64 = 64 * 128;     // [64 rows][64 bf16]
 constexpr float kLazyRescale = 8.f;    // log2 units
-// Capped scores lie in [-c log2(e), c log2(e)]. Up to kBounded log2 units (c <= 69) the exponentials
-// need no running maximum: 2^(z - kBoundedRef) stays between 2^-108 and 2^92, and the sums of 2^22 keys
-// and values below 2^14 within fp32. Without it a row's two halves of a tile have nothing to tell
+// Capped scores lie in [-c log2(e), c log2(e)]. Up to kBounded log2 units (c <= 50.5) the exponentials
+// need no running maximum: 2^(z - kBoundedRef) stays between 2^-81 and 2^65, so the sums over 2^22 keys
+// stay within fp32 for values between 2^-40 and 2^40. Without it a row's two halves of a tile have nothing to tell
 // each other, so two threads share a row (eight softmax warps): the tanh's polynomial is long, and
 // four warps a block left the FMA units idle half of the time (16384 tokens, 8/2 heads, capped:
 // 691 us with the running maximum and one thread a row).
-constexpr float kBounded = 100.f, kBoundedRef = 8.f;
+constexpr float kBounded = 73.f, kBoundedRef = 8.f;
 constexpr int kKStages = 3;            // K ring depth
 constexpr int kVStages = 2;            // V ring depth
 
@@ -402,8 +402,12 @@ bool attn_span_ok(const AttnSpanArgs& g) {
 }
 
 cudaError_t attn_span_fwd(const AttnSpanArgs& g, bf16* o, int64_t ldo, float* lse, int* err, cudaStream_t st) {
-  if (!attn_span_ok(g) || !o || !lse || !err || (reinterpret_cast<uintptr_t>(o) & 15) || ldo % 8 ||
-      ldo < static_cast<int64_t>(g.nh) * g.hd)
+  const int64_t qc = static_cast<int64_t>(g.nh) * g.hd, kc = static_cast<int64_t>(g.nkv) * g.hd;
+  const int64_t T = static_cast<int64_t>(g.B) * g.s;
+  if (!attn_span_ok(g) || !o || !lse || !err || (reinterpret_cast<uintptr_t>(o) & 15) || ldo % 8 || ldo < qc ||
+      ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(err)) & 3) ||
+      columns_overlap(o, ldo, qc, g.q, g.ldq, qc, T) || columns_overlap(o, ldo, qc, g.k, g.ldk, kc, T) ||
+      columns_overlap(o, ldo, qc, g.v, g.ldv, kc, T))
     return cudaErrorInvalidValue;
   return dispatch(g, [&](auto hd, auto cap, auto bias) {
     return launch<decltype(hd)::value, decltype(cap)::value, decltype(bias)::value>(g, o, ldo, lse, err, st);

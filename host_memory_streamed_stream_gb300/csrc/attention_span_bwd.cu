@@ -1185,8 +1185,24 @@ cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, con
   const int64_t qc = static_cast<int64_t>(g.nh) * g.hd, kc = static_cast<int64_t>(g.nkv) * g.hd;
   if (!rows(o, ldo, qc) || !rows(dout, lddo, qc) || !rows(dq, lddq, qc) || !rows(dk, lddk, kc) || !rows(dv, lddv, kc) ||
       static_cast<double>(g.s) * 2 * lddo >= 1e12 || static_cast<double>(g.s) * 2 * lddq >= 1e12 ||
-      static_cast<double>(g.s) * 2 * lddk >= 1e12 || static_cast<double>(g.s) * 2 * lddv >= 1e12)
+      static_cast<double>(g.s) * 2 * lddk >= 1e12 || static_cast<double>(g.s) * 2 * lddv >= 1e12 ||
+      ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(err)) & 3))
     return cudaErrorInvalidValue;
+  // the walk of one key tile, up to s/128 tiles for each of its query heads at 1.3 us, stays well below
+  // the limit of the waits for its end
+  if (static_cast<int64_t>(g.s) * (g.nh / g.nkv) > kSpanMaxWalk) return cudaErrorInvalidValue;
+  struct Columns {
+    const bf16* p;
+    int64_t ld, cols;
+  };
+  const Columns out[3] = {{dq, lddq, qc}, {dk, lddk, kc}, {dv, lddv, kc}};
+  const Columns other[8] = {{g.q, g.ldq, qc}, {g.k, g.ldk, kc}, {g.v, g.ldv, kc}, {o, ldo, qc},
+                            {dout, lddo, qc}, out[0], out[1], out[2]};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 5 + i; ++j)
+      if (columns_overlap(out[i].p, out[i].ld, out[i].cols, other[j].p, other[j].ld, other[j].cols,
+                          static_cast<int64_t>(g.B) * g.s))
+        return cudaErrorInvalidValue;
   float2* lsd = static_cast<float2*>(scratch);
   Hull* hulls = reinterpret_cast<Hull*>(lsd + static_cast<int64_t>(g.B) * g.nh * pad128(g.s));
   const int64_t tiles = static_cast<int64_t>(g.B) * (pad128(g.s) / 128);

@@ -110,6 +110,11 @@ cudaError_t cross_entropy(const float* logits, const int32_t* labels, bf16* dlog
 cudaError_t mean_reduce(const float* v, int n, float* out, cudaStream_t s);
 cudaError_t cast_f32_bf16(const float* x, bf16* y, int64_t n, cudaStream_t s);
 
+// Whether two ranges of columns (cols_a of rows with stride lda at a; the same of b) share an element.
+// With one stride they are compared as columns of one buffer, else as the memory they span.
+bool columns_overlap(const bf16* a, int64_t lda, int64_t cols_a, const bf16* b, int64_t ldb, int64_t cols_b,
+                     int64_t rows);
+
 // ------------------------------------------------------------------ rotary positions, query/key norms
 // rot/2 scaled frequencies into a host array (rules and checks: mtk_rotary_inv_freq); false if refused.
 bool rotary_inv_freq(int rot, double theta, int scaling, double factor, double original, double low, double high,
@@ -121,12 +126,12 @@ constexpr int kRotaryMaxHeads = 65536;
 cudaError_t rotary_table(const double* inv_freq, int rot, int n_pos, double amp, float* out, cudaStream_t s);
 // y = x with the first `rot` columns of each head rotated (pairs (2i, 2i+1) if interleaved, else
 // (i, i + rot/2)) at position positions[t], or t % n_pos without positions; inverse = the transpose.
-// y may be x. hd and rot multiples of 16.
+// y may be x, but not overlap it otherwise. hd and rot multiples of 16.
 cudaError_t rotary(const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int T, int heads, int hd, int rot,
                    bool interleaved, const int32_t* positions, const float* cs, int n_pos, bool inverse, int* err,
                    cudaStream_t s);
 // RMSNorm of every query and key head (nh + nkv heads of hd columns, gains gq, gk [hd]), then the
-// rotation (rot = 0: none); rstd fp32 [T, nh + nkv] may be null. y may be x. hd 64 or 128.
+// rotation (rot = 0: none); rstd fp32 [T, nh + nkv] may be null. y as above. hd 64 or 128.
 cudaError_t qk_norm_rope(const bf16* x, int64_t ldx, const bf16* gq, const bf16* gk, bf16* y, int64_t ldy, float* rstd,
                          int T, int nh, int nkv, int hd, int rot, bool interleaved, float eps,
                          const int32_t* positions, const float* cs, int n_pos, int* err, cudaStream_t s);
@@ -156,6 +161,7 @@ cudaError_t attn_bwd(const bf16* qkv, const bf16* o, const float* lse, const bf1
 // z = scale q.k, cap > 0: z = cap tanh(z / cap), slopes: z -= slopes[head] |i - j|. q, k, v are
 // separate [B*s] row matrices with their own row strides (multiples of 8).
 constexpr int kSpanMaxSeq = 1 << 22;
+constexpr int64_t kSpanMaxWalk = int64_t{1} << 27;  // s * query heads per key head, backward
 struct AttnSpanArgs {
   const bf16 *q, *k, *v;
   int64_t ldq, ldk, ldv;
@@ -167,7 +173,7 @@ struct AttnSpanArgs {
 bool attn_span_ok(const AttnSpanArgs& g);  // sizes, strides and alignments the kernels take
 // o [B*s, nh*hd] (row stride ldo), lse fp32 [B, nh, s] as attn_fwd's; 0 and -inf for an empty span.
 cudaError_t attn_span_fwd(const AttnSpanArgs& g, bf16* o, int64_t ldo, float* lse, int* err, cudaStream_t st);
-// dq [B*s, nh*hd], dk and dv [B*s, nkv*hd]; scratch of attn_span_bwd_scratch() bytes.
+// dq [B*s, nh*hd], dk and dv [B*s, nkv*hd], over no input; scratch of attn_span_bwd_scratch() bytes.
 uint64_t attn_span_bwd_scratch(int B, int s, int nh, int nkv, int hd);
 cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const float* lse, const bf16* dout,
                           int64_t lddo, bf16* dq, int64_t lddq, bf16* dk, int64_t lddk, bf16* dv, int64_t lddv,

@@ -108,7 +108,7 @@ struct Rotation {
   int n_pos, rot;
   int* err;
 };
-// Position of token t (T stays below 2^31), -1 if it is outside the table.
+// Position of token t (T stays below 2^31); not checked against the table.
 __device__ __forceinline__ int position_of(const Rotation& q, uint32_t t) {
   return q.positions ? q.positions[t] : static_cast<int>(t % static_cast<uint32_t>(q.n_pos));
 }
@@ -509,12 +509,16 @@ __global__ void __launch_bounds__(kRotThreads)
 // Heads that the kernels index with 32 bits.
 bool heads_ok(int64_t heads) { return heads > 0 && heads <= kRotaryMaxHeads; }
 bool vec_aligned(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
+bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+// Whether y may be written while x is read: they are one row matrix, or share nothing.
+bool may_write(const bf16* y, int64_t ldy, const bf16* x, int64_t ldx, int64_t cols, int T) {
+  return (x == y && ldx == ldy) || !columns_overlap(x, ldx, cols, y, ldy, cols, T);
+}
 
 bool rotation_ok(int hd, int rot, const float* cs, int n_pos, const int32_t* positions, const int* err) {
   if (rot < 0 || rot > hd || rot % 16) return false;
   if (rot == 0) return true;
-  return cs && (reinterpret_cast<uintptr_t>(cs) & 15) == 0 && (reinterpret_cast<uintptr_t>(positions) & 3) == 0 &&
-         n_pos > 0 && err;
+  return cs && aligned(cs, 16) && aligned(positions, 4) && n_pos > 0 && err && aligned(err, 4);
 }
 
 }  // namespace
@@ -545,7 +549,8 @@ bool rotary_inv_freq(int rot, double theta, int scaling, double factor, double o
 }
 
 cudaError_t rotary_table(const double* inv_freq, int rot, int n_pos, double amp, float* out, cudaStream_t s) {
-  if (rot <= 0 || rot % 2 || rot / 2 > kRotaryMaxPairs || n_pos <= 0 || (reinterpret_cast<uintptr_t>(out) & 15))
+  if (rot <= 0 || rot % 2 || rot / 2 > kRotaryMaxPairs || n_pos <= 0 || (reinterpret_cast<uintptr_t>(out) & 15) ||
+      !std::isfinite(static_cast<float>(amp)))
     return cudaErrorInvalidValue;
   TurnTable f{};
   for (int i = 0; i < rot / 2; ++i) {
@@ -568,8 +573,8 @@ cudaError_t rotary(const bf16* x, int64_t ldx, bf16* y, int64_t ldy, int T, int 
   if (T <= 0 || !heads_ok(heads) || hd <= 0 || hd % 16 || hd > 16 * kRotThreads || rot == 0 ||
       !rotation_ok(hd, rot, cs, n_pos, positions, err))
     return cudaErrorInvalidValue;
-  if (!vec_aligned(x, ldx) || !vec_aligned(y, ldy) || ldx < static_cast<int64_t>(heads) * hd ||
-      ldy < static_cast<int64_t>(heads) * hd || (x == y && ldx != ldy))
+  const int64_t cols = static_cast<int64_t>(heads) * hd;
+  if (!vec_aligned(x, ldx) || !vec_aligned(y, ldy) || ldx < cols || ldy < cols || !may_write(y, ldy, x, ldx, cols, T))
     return cudaErrorInvalidValue;
   const RowArgs a{x, ldx, y, ldy, T, heads, hd, row_split(T, heads, hd, 4), {cs, positions, n_pos, rot, err},
                   0, nullptr, nullptr, nullptr, 0.f};
@@ -590,7 +595,8 @@ cudaError_t qk_norm_rope(const bf16* x, int64_t ldx, const bf16* gq, const bf16*
   if (!norm_ok(T, nh, nkv, hd, rot, cs, n_pos, positions, gq, gk, err)) return cudaErrorInvalidValue;
   const int heads = nh + nkv;
   const int64_t cols = static_cast<int64_t>(heads) * hd;
-  if (!vec_aligned(x, ldx) || !vec_aligned(y, ldy) || ldx < cols || ldy < cols || (x == y && ldx != ldy))
+  if (!vec_aligned(x, ldx) || !vec_aligned(y, ldy) || ldx < cols || ldy < cols || !aligned(rstd, 4) ||
+      !may_write(y, ldy, x, ldx, cols, T))
     return cudaErrorInvalidValue;
   const RowArgs a{x, ldx, y, ldy, T, heads, hd, row_split(T, heads, hd, 8), {cs, positions, n_pos, rot, err},
                   nh, gq, gk, rstd, eps};
@@ -610,7 +616,8 @@ cudaError_t qk_norm_rope_bwd(const bf16* dy, int64_t lddy, const bf16* x, int64_
   const int heads = nh + nkv;
   const int64_t cols = static_cast<int64_t>(heads) * hd;
   if (!vec_aligned(dy, lddy) || !vec_aligned(x, ldx) || !vec_aligned(dx, lddx) || lddy < cols || ldx < cols ||
-      lddx < cols || (dx == dy && lddx != lddy) || (dx == x && lddx != ldx))
+      lddx < cols || !aligned(rstd, 4) || !aligned(partial, 4) || !aligned(dgq, 2) || !aligned(dgk, 2) ||
+      !may_write(dx, lddx, dy, lddy, cols, T) || !may_write(dx, lddx, x, ldx, cols, T))
     return cudaErrorInvalidValue;
   const NormSplit sp = norm_split(T, nh, nkv, hd);
   const BwdArgs a{x, dy, ldx, lddy, dx, lddx, gq, gk, rstd, partial, T, nh, heads, {cs, positions, n_pos, rot, err}};

@@ -1,11 +1,21 @@
 // Spans and positions of packed documents: host arrays in, host arrays out, like the token ids they
-// go with.
+// go with. And the check that an entry's outputs do not lie over its inputs.
 #include <algorithm>
 #include <cstdint>
 
 #include "kernels.h"
 
 namespace mt {
+
+bool columns_overlap(const bf16* a, int64_t lda, int64_t cols_a, const bf16* b, int64_t ldb, int64_t cols_b,
+                     int64_t rows) {
+  using Wide = __int128;  // any stride times any number of rows
+  const Wide pa = reinterpret_cast<uintptr_t>(a) / sizeof(bf16), pb = reinterpret_cast<uintptr_t>(b) / sizeof(bf16);
+  if (pa + Wide(rows - 1) * lda + cols_a <= pb || pb + Wide(rows - 1) * ldb + cols_b <= pa) return false;
+  if (lda != ldb) return true;
+  const Wide d = ((pb - pa) % lda + lda) % lda;  // b's first column in rows that start at a
+  return d < cols_a || d + cols_b > lda;
+}
 
 bool doc_spans(const int32_t* bounds, int n_docs, const int32_t* prefix, int B, int s, int32_t* lo, int32_t* hi,
                int32_t* positions) {

@@ -127,7 +127,7 @@ int mtk_rope(void* qkv, int64_t ld, int T, int seq, int n_heads, int n_kv_heads,
  *   MT_EINVAL unless rot_dim is even, 2..256, theta > 0 and, where they are used, factor > 0,
  *   original_positions > 0 and high > low, all finite.
  * mtk_rotary_table: cos_sin f32 [n_pos][rot_dim/2][2] = amplitude * (cos, sin)(p * inv_freq[i]) for
- *   positions p = 0 .. n_pos-1. inv_freq is a HOST array, read before the call returns. Angles are
+ *   positions p = 0 .. n_pos-1 (amplitude finite). inv_freq is a HOST array, read before the call returns. Angles are
  *   kept modulo whole turns in 64-bit fixed point, so far positions lose nothing.
  * mtk_rotary: y bf16 [T, heads*head_dim] (row stride ldy) = x (row stride ldx) with the first
  *   rot_dim columns of every head rotated: a' = a cos - b sin, b' = b cos + a sin on the pairs
@@ -155,12 +155,12 @@ int mtk_rotary(const void* x, int64_t ldx, void* y, int64_t ldy, int T, int head
  * with the rotation R of mtk_rotary (rot_dim = 0: no rotation; cos_sin, positions and err_flag may
  * then be NULL). x, y bf16 with row strides ldx, ldy (columns past the key heads, such as v, are
  * neither read nor written); gq, gk bf16 [head_dim]; rstd f32 [T][n_heads + n_kv_heads], or NULL.
- * y may be x (then ldy = ldx). head_dim 64 or 128, rot_dim a multiple of 16, at most 65536 heads.
+ * y may be x (then ldy = ldx), else they must not overlap. head_dim 64 or 128, rot_dim a multiple of 16, at most 65536 heads.
  *
  * mtk_qk_norm_rope_bwd: from dy (row stride lddy), the forward's x and its rstd, with u = R^T dy and
  * n = x_h * rstd: dx_h = rstd (u g - n mean(u g n)), dgq and dgk bf16 [head_dim] = the sums of u n
  * over tokens and query (key) heads, added in a fixed order through `partial`, f32
- * [mtk_qk_norm_rope_bwd_parts(...)][head_dim]. dx may be dy or x (with the same row stride). A
+ * [mtk_qk_norm_rope_bwd_parts(...)][head_dim]. dx may be dy or x (with the same row stride), else it overlaps neither. A
  * bad position counts as no rotation, with *err_flag set to 8.
  */
 int mtk_qk_norm_rope(const void* x, int64_t ldx, const void* gq, const void* gk, void* y, int64_t ldy, void* rstd,
@@ -243,7 +243,9 @@ int mtk_attn_bwd_rope(const void* qkv, const void* o, const void* lse, const voi
  * of wider buffers); lo, hi int32 [B*s], positions inside the sequence, or NULL (lo 0, hi i + 1:
  * causal); they are clamped to [0, s]. nkv divides nh, head_dim 64 or 128, s <= 4194304. scale > 0,
  * cap >= 0 (0: none), slopes f32 [nh] or NULL, all finite; capped scores are right to about cap * 2^-22
- * (relative 2^-22 while they stay below the cap before it is applied).
+ * (relative 2^-22 while they stay below the cap before it is applied). Capped up to 50.5 without slopes, v is
+ * taken to lie between 2^-40 and 2^40 in size (or 0): beyond, products with the unnormalised
+ * probabilities may leave fp32.
  * An empty span (lo >= hi) makes row i padding: o_i = 0, lse_i = -inf, its gradients are 0, and no
  * other row's span may contain it. Padding rows of q, k, v and dout may hold anything, NaN
  * included, where the padding follows the documents of its sequence, precedes them, or lies between
@@ -256,11 +258,14 @@ int mtk_attn_bwd_rope(const void* qkv, const void* o, const void* lse, const voi
  *   at t0 gets lo = t0, hi = max(t + 1, t0 + prefix[d]) up to the part's end, both inside the
  *   sequence, and position t - t0. prefix int32 [n_docs] >= 0 or NULL (0: causal; the document's
  *   length: two-sided). lo, hi int32 [B*s], positions int32 [B*s] or NULL; B*s < 2^31.
+ * Outputs may be column ranges of one buffer with the inputs or each other but share no element with them
+ * (MT_EINVAL).
  * mtk_attn_span_fwd: o bf16 [B*s, nh*hd] (row stride ldo), lse f32 [B, nh, s] in mtk_attn_fwd's
  *   units (log2). err_flag: device int, required, as for all attention entries.
  * mtk_attn_span_bwd: dq bf16 [B*s, nh*hd], dk, dv bf16 [B*s, nkv*hd] (row strides lddq, lddk, lddv;
  *   every row is written) from dout, o and lse, deterministic, no atomics. scratch: device memory of
- *   mtk_attn_span_bwd_scratch_bytes() bytes, 16-byte aligned. Gradients of slopes are not computed.
+ *   mtk_attn_span_bwd_scratch_bytes() bytes, 16-byte aligned, not shared by calls that may run at the same
+ *   time. s * (nh / nkv) <= 2^27. Gradients of slopes are not computed.
  */
 int mtk_doc_spans(const int32_t* bounds, int n_docs, const int32_t* prefix, int B, int s, int32_t* lo, int32_t* hi,
                   int32_t* positions);

@@ -175,6 +175,37 @@ def test_backward(K, B, s, nh, nkv, hd, kind, cap, bias):
     assert int(kw["err"].item()) == 0
 
 
+@pytest.mark.parametrize("cap", [30.0, 50.0, 60.0])
+@pytest.mark.parametrize("size", [2.0 ** -30, 1.0, 2.0 ** 30])
+def test_scores_at_the_cap(K, cap, size):
+    """Scores of +-1152 before the cap: documents whose scores are all at -cap, all at +cap, at both,
+    with small and large values. One fused buffer holds q, k, v, the output and the gradients."""
+    rng = np.random.default_rng(int(cap))
+    B, s, nh, nkv, hd = 1, 330, 2, 1, 128
+    row, key = np.where(np.arange(s) % 3 == 1, -1.0, 1.0), np.ones(s)
+    row[:70], row[70:140] = -1.0, 1.0
+    key[200:] = np.where(np.arange(s)[200:] % 5 < 2, -1.0, 1.0)
+    u = np.where(rng.random(hd) < 0.5, -3.0, 3.0)
+    q = np.broadcast_to((row[:, None] * u)[:, None], (s, nh, hd))
+    k = (key[:, None] * u)[:, None]
+    v, _ = _bf16(rng, (s, 1, hd))
+    v = v * size
+    do, dot = _bf16(rng, (s, nh * hd))
+    buf = torch.zeros(s, 11 * hd, dtype=torch.bfloat16, device="cuda")
+    buf[:, :4 * hd] = torch.tensor(np.concatenate([q, k, v], 1).reshape(s, 4 * hd)).to(torch.bfloat16).cuda()
+    cols = [buf[:, a * hd:b * hd] for a, b in ((0, 2), (2, 3), (3, 4), (4, 6), (6, 8), (8, 9), (9, 10))]
+    lo, hi, _ = K.doc_spans([0, 70, 140, 330], B, s)
+    kw = dict(lo=_i32(lo), hi=_i32(hi), scale=1.0, cap=cap, err=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    o, lse = K.attn_span_fwd(*cols[:3], B, s, nh, nkv, hd, out=cols[3], **kw)
+    got = K.attn_span_bwd(*cols[:3], o, lse, dot, B, s, nh, nkv, hd, out=cols[4:], **kw)
+    assert int(kw["err"].item()) == 0 and bool((buf[:, 10 * hd:] == 0).all())
+    x, vis = (q[None], k[None], v[None]), [osp.visible(lo, hi, s)]
+    on = _np(o).reshape(B, s, nh, hd)
+    _check_forward(on, lse, x, vis, 1.0, cap, np.zeros(nh), B, s, nh, nkv, hd)
+    _check_backward([_np(t).reshape(B, s, -1, hd) for t in got], x, on, lse, do.reshape(B, s, nh, hd), vis, 1.0, cap,
+                    np.zeros(nh), B, s, nh, nkv, hd)
+
+
 @pytest.mark.parametrize("kind", ["docs_padded", "gaps", "prefix"])
 @pytest.mark.parametrize("hd,s", [(64, 333), (128, 300)])
 def test_padding_may_hold_anything(K, kind, hd, s):

@@ -91,6 +91,10 @@ def test_attn_span_refusals(lib):
     fwd = dict(q=p, ldq=512, k=p, ldk=256, v=p, ldv=256, lo=p, hi=p, o=p, ldo=512, lse=p, B=2, s=64, nh=4, nkv=2,
                hd=128, scale=0.1, cap=0.0, slopes=None, err=p)
     bwd = dict(fwd, dout=p, lddo=512, dq=p, lddq=512, dk=p, lddk=256, dv=p, lddv=256, scratch=p)
+    for i, name in enumerate(("q", "k", "v", "o", "dout", "dq", "dk", "dv")):  # no two overlap
+        if name in fwd:
+            fwd[name] = p + (i << 20)
+        bwd[name] = p + (i << 20)
 
     def call_fwd(**kw):
         a = dict(fwd, **kw)
@@ -118,6 +122,21 @@ def test_attn_span_refusals(lib):
                dict(dq=p + 2), dict(lddq=256), dict(lddk=128), dict(lddv=254), dict(scratch=None),
                dict(scratch=p + 8)):
         assert call_bwd(**kw) == -1, kw
+    # outputs over an input or another output: the same memory, shifted by a row, columns that meet in
+    # rows of one stride (128 rows of 512 columns: 131072 bytes), and strides that differ
+    for name in ("q", "k", "v"):
+        for kw in (dict(o=fwd[name]), dict(o=fwd[name] + 1024), dict(o=fwd[name] - 131072 + 1024),
+                   dict(o=fwd[name] + 496, ldo=1024, ldq=1024, ldk=1024, ldv=1024)):
+            assert call_fwd(**kw) == -1, (name, kw)
+    for out in ("dq", "dk", "dv"):
+        for name in ("q", "k", "v", "o", "dout", "dq", "dk", "dv"):
+            if name != out:
+                assert call_bwd(**{out: bwd[name]}) == -1, (out, name)
+                assert call_bwd(**{out: bwd[name] + 512}) == -1, (out, name)
+    for kw in (dict(lse=p + 2), dict(err=p + 1)):
+        assert call_fwd(**kw) == -1 and call_bwd(**kw) == -1, kw
+    # the longest walk of a key tile
+    assert call_bwd(B=1, s=1 << 22, nh=64, nkv=1, ldq=8192, ldo=8192, lddo=8192, lddq=8192) == -1
     assert lib.mtk_attn_span_bwd_scratch_bytes(0, 1, 1, 1, 64) == 0
     assert lib.mtk_attn_span_bwd_scratch_bytes(1, 4194305, 1, 1, 64) == 0
     assert lib.mtk_attn_span_bwd_scratch_bytes(2, 129, 4, 2, 64) >= 2 * 4 * 256 * 8

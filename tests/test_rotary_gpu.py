@@ -111,6 +111,28 @@ def test_rotary(K, T, heads, hd, rot, inter, inverse):
     assert torch.equal(a, b) and int(err.item()) == 0
 
 
+def test_into_other_columns_of_the_same_buffer(K):
+    """The input's own buffer may hold the output, next to it."""
+    rng = np.random.default_rng(4)
+    T, hd, nh, nkv = 70, 64, 3, 2
+    cols = (nh + nkv) * hd
+    tab, _ = _table(K, hd, 100)
+    x, buf = _bf16(rng, (T, 2 * cols + 8))
+    gain = torch.ones(hd, dtype=torch.bfloat16, device="cuda")
+    a, b = buf[:, :cols], buf[:, cols + 8:]
+    keep = a.clone()
+    want = K.rotary(a, nh + nkv, hd, tab)
+    assert torch.equal(K.rotary(a, nh + nkv, hd, tab, out=b), want) and torch.equal(a, keep)
+    wy, wr = K.qk_norm_rope(a, gain, gain, nh, nkv, hd, tab)
+    y, r = K.qk_norm_rope(a, gain, gain, nh, nkv, hd, tab, out=b)
+    assert torch.equal(y, wy) and torch.equal(r, wr) and torch.equal(a, keep)
+    from host_memory_streamed_stream_gb300 import MTError
+
+    for out in (buf[:, 8:8 + cols], buf[:, cols - 64:2 * cols - 64]):
+        with pytest.raises(MTError):
+            K.rotary(a, nh + nkv, hd, tab, out=out)
+
+
 def test_rotary_bad_position_is_flagged_and_left(K):
     rng = np.random.default_rng(3)
     tab, cs = _table(K, 32, 20)

@@ -74,6 +74,8 @@ def test_entry_refusals(lib):
     for rot, n, out, src in ((63, 16, p, f), (0, 16, p, f), (258, 16, p, f), (64, 0, p, f), (64, 16, p + 8, f),
                              (64, 16, p, bad)):
         assert lib.mtk_rotary_table(src, rot, n, 1.0, out, None) == -1
+    for amp in (float("nan"), float("inf"), 1e39):
+        assert lib.mtk_rotary_table(f, 64, 16, amp, p, None) == -1
 
     def rotary(x=p, ldx=256, y=e, ldy=256, T=4, heads=2, hd=128, rot=64, pos=None, cs=p, n_pos=8, err=p):
         return lib.mtk_rotary(x, ldx, y, ldy, T, heads, hd, rot, 0, pos, cs, n_pos, 0, err, None)
@@ -81,7 +83,8 @@ def test_entry_refusals(lib):
     for kw in (dict(x=None), dict(y=None), dict(x=p + 2), dict(y=e + 8), dict(ldx=252), dict(ldx=248), dict(ldy=0),
                dict(T=0), dict(T=-1), dict(heads=0), dict(hd=0), dict(hd=120), dict(hd=8192, ldx=16384, ldy=16384),
                dict(rot=0), dict(rot=24), dict(rot=144), dict(rot=-16), dict(cs=None), dict(cs=p + 4), dict(n_pos=0),
-               dict(err=None), dict(pos=p + 2), dict(y=p, ldy=512)):
+               dict(err=None), dict(err=p + 2), dict(pos=p + 2), dict(y=p, ldy=512), dict(y=p + 512),
+               dict(y=p + 496, ldx=512, ldy=512), dict(y=p + 528, ldx=512, ldy=512), dict(y=p - 1024, ldy=512)):
         assert rotary(**kw) == -1, kw
 
     def norm(x=p, ldx=512, gq=p, gk=p, y=e, ldy=384, rstd=p, T=4, nh=2, nkv=1, hd=128, rot=64, eps=1e-5, cs=p, n_pos=8,
@@ -92,17 +95,20 @@ def test_entry_refusals(lib):
     for kw in (dict(x=None), dict(gq=None), dict(gk=None), dict(y=None), dict(gq=p + 2), dict(gk=p + 8), dict(ldx=376),
                dict(ldy=380), dict(T=0), dict(nh=0), dict(nkv=0), dict(hd=96), dict(hd=256, ldx=1024, ldy=1024),
                dict(rot=8), dict(rot=160), dict(eps=-1.0), dict(eps=float("nan")), dict(cs=None), dict(n_pos=0),
-               dict(err=None), dict(y=p)):
+               dict(err=None), dict(y=p), dict(rstd=p + 2), dict(y=p + 1024, ldy=512)):
         assert norm(**kw) == -1, kw
 
-    def back(dy=p, lddy=384, x=p, ldx=512, gq=p, gk=p, rstd=p, dx=e, lddx=384, part=p, dgq=p, dgk=p, T=4, hd=128,
+    d = 1 << 22
+
+    def back(dy=d, lddy=384, x=p, ldx=512, gq=p, gk=p, rstd=p, dx=e, lddx=384, part=p, dgq=p, dgk=p, T=4, hd=128,
              rot=64, cs=p):
         return lib.mtk_qk_norm_rope_bwd(dy, lddy, x, ldx, gq, gk, rstd, dx, lddx, part, dgq, dgk, T, 2, 1, hd, rot, 0,
                                         None, cs, 8, p, None)
 
     for kw in (dict(dy=None), dict(x=None), dict(rstd=None), dict(dx=None), dict(part=None), dict(dgq=None),
                dict(dgk=None), dict(lddy=376), dict(lddx=388), dict(T=0), dict(hd=32), dict(rot=40), dict(cs=None),
-               dict(dx=p, x=e, lddx=512), dict(dx=p, dy=e)):
+               dict(dx=p, lddx=384), dict(dx=d, lddx=512), dict(dx=d + 768), dict(dx=p + 1024, lddx=512),
+               dict(rstd=p + 1), dict(part=p + 2), dict(dgq=p + 1), dict(dgk=p + 1)):
         assert back(**kw) == -1, kw
     assert lib.mtk_qk_norm_rope_bwd_parts(0, 2, 1, 128) == 0
     assert lib.mtk_qk_norm_rope_bwd_parts(5, 2, 1, 96) == 0
