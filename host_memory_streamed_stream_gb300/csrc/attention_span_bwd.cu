@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
                           const __grid_constant__ BwdArgs a) {
   using L = SmemKV<HD>;
   using R = Roles<EW>;
+  constexpr int kUnroll = CAP ? 2 : 1;  // of a tile's halves
   constexpr int kCols = R::kCols;
   constexpr int QS = L::QS, DS = L::DS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         // the pairs were copied with the tile's dO: observe that copy before reading them
         if (!(ok = mbar_wait_warp(&d_full[g % DS], (g / DS) & 1, err, kErrTimeoutAttn))) break;
         const uint32_t ts = s_slot(g) + tl, td = d_slot(g) + tl;
-#pragma unroll
+#pragma unroll kUnroll
         for (int h = 0; h < 2; ++h) {
           if (!ok) break;
           if (!(ok = mbar_wait_warp(&sdp_full[h], g & 1, err, kErrTimeoutAttn))) break;
@@ -635,9 +636,10 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
             dv[2 * k + 1] = y.y;
           }
           if (!all) {
+            const uint32_t seen = h ? vis[1] : vis[0];
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
-              const bool keep = vis[h] >> c & 1u;
+              const bool keep = seen >> c & 1u;
               sv[c] = keep ? sv[c] : 0.f;
               dv[c] = keep ? dv[c] : 0.f;
             }
@@ -755,6 +757,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
                         const __grid_constant__ CUtensorMap map_dq, const __grid_constant__ BwdArgs a) {
   using L = SmemQ<HD>;
   using R = Roles<EW>;
+  constexpr int kUnroll = CAP ? 2 : 1;  // of a tile's halves
   constexpr int kCols = R::kCols;
   constexpr int KS = L::KS, VS = L::VS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1042,7 +1045,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         // rows of K that nothing here may see: outside the hull, or padding among the tile's own rows
         const bool own = padded && key_tile == q0;
         const bool clean = own || key_tile < hull.min_lo || key_tile + 128 > hull.max_hi;
-#pragma unroll
+#pragma unroll kUnroll
         for (int h = 0; h < 2; ++h) {
           const int cb = h * 64 + part * kCols;
           float sv[kCols], dv[kCols];
