@@ -5,7 +5,7 @@
 // The pipeline is that of the causal kernel (attention_tc.cu): one CTA per (128-query tile, query
 // head, sequence), two CTAs per SM; warp 0 loads Q once and K and V tiles of 64 keys into two
 // rings, warp 1 issues S_j = Q K_j^T into one of two TMEM score buffers and O += P_j V_j, warps
-// 2..5 hold one query row per thread. What differs:
+// 2..5 hold one query row per thread (or, see kBounded, warps 2..9 half a row). What differs:
 //  * the softmax warps first reduce their rows' spans to the tile's hull; the key tiles that are
 //    loaded and multiplied are those of [min_lo, max_hi), the masked path is taken where some row
 //    does not see the whole tile, and a tile of empty rows writes zeros and loads nothing;
@@ -14,6 +14,14 @@
 //  * rows of V that no query row of the tile may see (keys outside the hull, padding rows inside
 //    the tile's own range) are zeroed in shared memory before the product, as 0 x NaN is NaN:
 //    padding may hold anything.
+//
+// Measured (head size 128): two 4096-token sequences of 32 heads, packed documents of 700 tokens on
+// average, 110 us (1.28 times the visible scores are computed in the tiles, at 875 TFLOP/s: blocks are
+// eleven tiles long, two of five tiles take the masked path, and the longest blocks end last); the same
+// sequences causal 213 us, 1290 TFLOP/s; 16384 tokens, 8/2 heads, causal 345 us, 1590 TFLOP/s, capped with
+// a prefix 600 us, 980 TFLOP/s, bound by the elementwise warps' instructions. Blocks that go on to further
+// items (taken over from the grid) instead of ending came out slower, 135 us for the packed documents:
+// the look-ahead costs the tile loop more than the second CTA of an SM leaves uncovered.
 #include <cmath>
 #include <cstdint>
 

@@ -9,6 +9,9 @@
 // same unit, and so the same cosines and sines, for every head of its token. Neighbouring threads
 // read neighbouring vectors in both accesses (with 16 adjacent columns per thread instead, every
 // access covers half of each 32-byte sector: 53 us instead of 51 for 8192 x 64 interleaved heads).
+// Measured (head size 128; a plain copy reaches 6.77 TB/s): rotation of 8192 x 64 heads 43.1 us, 6.3
+// TB/s; norm forward of 4096 x 48 heads 24.6 us (21 us of it on the device, half of it in start and tail), its backward of
+// 8192 x 64 heads 74.7 us, 5.4 TB/s. A single token takes 3 us on the device and is bound by the call.
 #include <cmath>
 #include <cstdint>
 
@@ -439,7 +442,8 @@ __global__ void __launch_bounds__(kRotThreads, 2)
 
 // Block 0: dgq[j] = sum of the query blocks' partial[p][j], block 1: dgk from the key blocks': the
 // rows dealt to 1024/HD groups of threads (group g: rows g, g + groups, ...), then the groups added
-// in order.
+// in order. One latency after another is all it is: with ten loads in flight a lone backward call takes 102
+// us instead of 105 (8192 x 64 heads).
 template <int HD>
 __global__ void __launch_bounds__(1024)
     qk_gain_reduce_kernel(const float* __restrict__ partial, int blocks_q, int blocks_k, bf16* __restrict__ dgq,
@@ -450,7 +454,15 @@ __global__ void __launch_bounds__(1024)
   const int p0 = blockIdx.x ? blocks_q : 0, p1 = blockIdx.x ? blocks_q + blocks_k : blocks_q;
   float s = 0.f;
   wait_for_previous();
-  for (int p = p0 + g; p < p1; p += kGroups) s += partial[static_cast<int64_t>(p) * HD + j];
+  constexpr int kAhead = 10;  // loads in flight; the sum keeps its order
+  for (int p = p0 + g; p < p1; p += kAhead * kGroups) {
+    float v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      v[k] = p + k * kGroups < p1 ? partial[static_cast<int64_t>(p + k * kGroups) * HD + j] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) s += v[k];
+  }
   acc[g][j] = s;
   __syncthreads();
   if (g == 0) {
@@ -465,7 +477,8 @@ __global__ void __launch_bounds__(1024)
 // per position times 2^64, p F mod 2^64 is the angle of position p without the whole turns, exact
 // for every p up to the rounding of F itself (2^-53 of the frequency), where p f in fp32 would lose
 // all of it for far positions and fp64 arithmetic is slow on this part. The top 32 bits, less the
-// nearest quarter turn, convert to fp32 with an error below 2^-26 turns.
+// nearest quarter turn, convert to fp32 with an error below 2^-26 turns. The kernel is bound by
+// instructions: 131072 x 64 angles take 14 us, 4.8 TB/s, below the 20 us of the host's calls.
 struct TurnTable {
   uint64_t turns[kRotaryMaxPairs];
 };
