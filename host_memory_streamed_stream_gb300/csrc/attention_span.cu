@@ -16,12 +16,13 @@
 //    padding may hold anything.
 //
 // Measured (head size 128): two 4096-token sequences of 32 heads, packed documents of 700 tokens on
-// average, 110 us (1.28 times the visible scores are computed in the tiles, at 875 TFLOP/s: blocks are
+// average, 108 us (1.28 times the visible scores are computed in the tiles, at 890 TFLOP/s: blocks are
 // eleven tiles long, two of five tiles take the masked path, and the longest blocks end last); the same
-// sequences causal 213 us, 1290 TFLOP/s; 16384 tokens, 8/2 heads, causal 345 us, 1590 TFLOP/s, capped with
+// sequences causal 209 us, 1310 TFLOP/s; 16384 tokens, 8/2 heads, causal 345 us, 1590 TFLOP/s, capped with
 // a prefix 600 us, 980 TFLOP/s, bound by the elementwise warps' instructions. Blocks that go on to further
 // items (taken over from the grid) instead of ending came out slower, 135 us for the packed documents:
 // the look-ahead costs the tile loop more than the second CTA of an SM leaves uncovered.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -69,7 +70,7 @@ struct FwdArgs {
   bf16* o;
   int64_t ldo;
   float* lse;
-  int s, nh, nkv;
+  int s, nh, nkv, head_group;
   ScoreArgs score;
   int* err;
 };
@@ -104,7 +105,8 @@ __global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
 
   const int s = a.s, nh = a.nh;
   const int n_qt = (s + 127) / 128;
-  const TileSlot slot = heavy_first_slot(static_cast<int>(blockIdx.x), n_qt, static_cast<int>(gridDim.x) / n_qt);
+  const TileSlot slot = heavy_first_slot(static_cast<int>(blockIdx.x), n_qt, static_cast<int>(gridDim.x) / n_qt,
+                                         a.head_group);
   const int qt = n_qt - 1 - slot.rank;  // the last query tile sees the most keys under a causal mask
   const int head = slot.hb % nh, b = slot.hb / nh;
   const int kvh = head / (nh / a.nkv);
@@ -372,7 +374,15 @@ cudaError_t launch(const AttnSpanArgs& g, bf16* o, int64_t ldo, float* lse, int*
       !tma_map_heads(&mk, g.k, s, g.B, g.ldk, s * g.ldk, static_cast<uint64_t>(g.nkv) * L::NSL, L::NSL, kKeys) ||
       !tma_map_heads(&mv, g.v, s, g.B, g.ldv, s * g.ldv, static_cast<uint64_t>(g.nkv) * L::NSL, L::NSL, kKeys))
     return cudaErrorInvalidValue;
-  const FwdArgs a{{g.lo, g.hi}, g.slopes, o, ldo, lse, g.s, g.nh, g.nkv, score_args(g), err};
+  // Blocks go heaviest first over as many (head, sequence) pairs as keep their K and V in half of the L2,
+  // 16 at least: the more pairs, the less the last ones' long blocks stand alone at the end, until
+  // the pairs' keys push one another out. (16, 32, 64 pairs: 4096 tokens, 40/8 heads, 0.4 MB of K and V a
+  // pair of them, 144, 147, 134 us, capped 223, 221, 195; two sequences of 32 heads, 2 MB a pair, 214, 212,
+  // 217, as packed documents 110, 109, 108.)
+  constexpr int64_t kGroupBytes = 64 << 20;
+  const int64_t pairs = std::min<int64_t>(kGroupBytes / (s * HD * 4) * (g.nh / g.nkv), static_cast<int64_t>(g.nh) * g.B);
+  const FwdArgs a{{g.lo, g.hi}, g.slopes, o, ldo, lse, g.s, g.nh, g.nkv, static_cast<int>(std::max<int64_t>(pairs, kHeadGroup)),
+                  score_args(g), err};
   auto run = [&](auto bounded) {
     auto* kernel = &attn_span_fwd_kernel<HD, CAP, BIAS, decltype(bounded)::value>;
     static std::atomic<uint64_t> ready{0};

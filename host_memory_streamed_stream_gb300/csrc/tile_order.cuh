@@ -22,13 +22,13 @@ struct TileSlot {
   int hb;    // head + n_heads * batch
 };
 
-// Slot of block `lin` in a grid of n_tiles x n_hb blocks.
-__host__ __device__ inline TileSlot heavy_first_slot(int lin, int n_tiles, int n_hb) {
-  const int per_group = n_tiles * kHeadGroup;
+// Slot of block `lin` in a grid of n_tiles x n_hb blocks, in groups of `group` (head, batch) pairs.
+__host__ __device__ inline TileSlot heavy_first_slot(int lin, int n_tiles, int n_hb, int group = kHeadGroup) {
+  const int per_group = n_tiles * group;
   const int g = lin / per_group;
   const int within = lin - g * per_group;
-  const int gsz = (n_hb - g * kHeadGroup) < kHeadGroup ? (n_hb - g * kHeadGroup) : kHeadGroup;
-  return {within / gsz, g * kHeadGroup + within % gsz};
+  const int gsz = (n_hb - g * group) < group ? (n_hb - g * group) : group;
+  return {within / gsz, g * group + within % gsz};
 }
 
 }  // namespace mt
