@@ -31,6 +31,7 @@
 // moves 192 KB of operands, 64 KB of TMA writes and 845 wavefronts of ordinary accesses (most of them the
 // pairs' broadcasts) through shared memory; smaller products that start earlier (S^T by halves) move
 // more and end later: 349 us.
+#include <algorithm>
 #include <cstdint>
 
 #include "attention_span.cuh"
@@ -57,6 +58,7 @@ struct Roles {
   static constexpr int kThreads = EW * 32 + 128;
   static constexpr int kItemReaders = EW + 3;  // lane 0 of every warp but the one that takes items
 };
+constexpr int kMaxParts = 512;        // of a key tile's walk
 constexpr int kSlice128 = 128 * 128;  // bytes of a [128 rows][64 bf16] swizzle-atom-wide slice
 
 __host__ __device__ __forceinline__ int pad128(int s) { return (s + 127) & ~127; }
@@ -150,6 +152,8 @@ struct Item {
   int lin;    // index in the heaviest-first order, -1: no more
   int first;  // first tile of the walk
   int count;  // its tiles (per query head of the group in dK/dV)
+  int begin;  // dK/dV: first step of the item's part of the walk over the group's heads
+  int steps;  // and its steps
   Hull hull;  // dQ: of the query tile
 };
 struct ItemRing {
@@ -179,6 +183,8 @@ __device__ __forceinline__ bool get_item_warp(const ItemRing& r, int n, Item& it
   it.lin = uniform(s.lin);
   it.first = uniform(s.first);
   it.count = uniform(s.count);
+  it.begin = uniform(s.begin);
+  it.steps = uniform(s.steps);
   it.hull = {uniform(s.hull.min_lo), uniform(s.hull.max_hi), uniform(s.hull.max_lo), uniform(s.hull.min_hi)};
   if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[n & 1]);
   return it.lin >= 0;
@@ -251,13 +257,21 @@ struct BwdArgs {
   const Hull* hulls;   // [B][tiles] of the query tiles
   int2* q_ranges;      // [B][tiles] first and last query tile that meets a key tile (last -1: none)
   int* taken;          // [2] items taken: dQ, dK/dV
-  float* partial;      // dK/dV by query head: [B][nh][tiles][2][HD/4][128][4], else null
+  int parts;           // parts of a key tile's walk
+  float* partial;      // with more than one, their sums: [B][nkv][parts][tiles][2][HD/4][128][4]
   bf16 *dq, *dk, *dv;
   int64_t lddq, lddk, lddv;
   int B, s, nh, nkv;
   ScoreArgs score;
   int* err;
 };
+
+// Query tiles of a key tile's walk (per query head of the group), and where part `k` of `parts` of `steps`
+// steps begins.
+__device__ __forceinline__ int walk_tiles(int2 range) { return range.y < 0 ? 0 : range.y - range.x + 1; }
+__device__ __forceinline__ int part_begin(int steps, int k, int parts) {
+  return static_cast<uint32_t>(steps * k) / static_cast<uint32_t>(parts);  // steps <= 2^19, parts <= kMaxParts
+}
 
 // P and dS of one pair of columns: scores (capped: their tanh) and dP in, P and dS out. nl = -lse2,
 // nd = -delta of the columns' (or the row's) queries; dist = |i - j| where there is a bias.
@@ -327,19 +341,19 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
 
   const int s = a.s, nh = a.nh, nkv = a.nkv;
   const int group = nh / nkv;
-  const int heads = PARTIAL ? 1 : group;  // query heads an item walks
-  const int n_t = (s + 127) / 128, n_hb = nh / heads * a.B;
+  const int parts = PARTIAL ? a.parts : 1;  // items that share the walk of a key tile
+  const int n_t = (s + 127) / 128, n_hb = nkv * parts * a.B;
   const int sp = pad128(s);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // item -> key tile (the first key tile is seen by the most queries under a causal mask), first query
-  // head, key head, sequence
+  // item -> key tile (the first key tile is seen by the most queries under a causal mask), part of its
+  // walk, key head, sequence
   struct Where {
-    int kt, hq, kvh, b;
+    int kt, part, kvh, b;
   };
   auto where = [&](int lin) -> Where {
     const TileSlot slot = heavy_first_slot(lin, n_t, n_hb);
-    const int per_b = nh / heads, hq = slot.hb % per_b * heads;
-    return {slot.rank, hq, hq / group, slot.hb / per_b};
+    const int hb = slot.hb / parts;
+    return {slot.rank, slot.hb % parts, hb % nkv, hb / nkv};
   };
 
   if (threadIdx.x == 0) {
@@ -392,13 +406,15 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     if (lane == 0) {
       const int items = n_t * n_hb;
       auto take = [&](int lin) -> Item {
-        Item it{-1, 0, 0, {0, 0, 0, 0}};
+        Item it{-1, 0, 0, 0, 0, {0, 0, 0, 0}};
         if (lin < items) {
           const Where w = where(lin);
           const int2 r = a.q_ranges[static_cast<int64_t>(w.b) * n_t + w.kt];
           it.lin = lin;
           it.first = r.x;
-          it.count = r.y < 0 ? 0 : r.y - r.x + 1;
+          it.count = walk_tiles(r);
+          it.begin = part_begin(group * it.count, w.part, parts);
+          it.steps = part_begin(group * it.count, w.part + 1, parts) - it.begin;
         }
         return it;
       };
@@ -406,7 +422,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       bool ok = put_item(ring, 0, cur);
       for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
         const Where w = where(cur.lin);
-        const int total = heads * cur.count, early = max(total - kTakeAhead, 0);
+        const int total = cur.steps, early = max(total - kTakeAhead, 0);
         Item next;
         auto hand_on = [&] {
           next = take(gridDim.x + atomicAdd(a.taken + 1, 1));
@@ -418,8 +434,9 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
           const int st = g % QS;
           if (!(ok = mbar_wait(&q_empty[st], ((g / QS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
           mbar_arrive_expect_tx(&q_full[st], L::TILE);
-          tma_load_4d(sm + L::Q + st * L::TILE, &map_q, &q_full[st], 0, (cur.first + i % cur.count) * 128,
-                      (w.hq + i / cur.count) * (HD / 64), w.b);
+          const int x = (PARTIAL ? cur.begin : 0) + i;
+          tma_load_4d(sm + L::Q + st * L::TILE, &map_q, &q_full[st], 0, (cur.first + x % cur.count) * 128,
+                      (w.kvh * group + x / cur.count) * (HD / 64), w.b);
         }
         cur = next;
       }
@@ -431,9 +448,10 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       bool ok = true;
       for (int m = 0, g = 0; ok && get_item(ring, m, it); ++m) {
         const Where w = where(it.lin);
-        for (int i = 0; i < heads * it.count; ++i, ++g) {
+        const int begin = PARTIAL ? it.begin : 0;
+        for (int i = begin; i < begin + it.steps; ++i, ++g) {
           const int st = g % DS;
-          const int hq = w.hq + i / it.count, q0 = (it.first + i % it.count) * 128;
+          const int hq = w.kvh * group + i / it.count, q0 = (it.first + i % it.count) * 128;
           if (!(ok = mbar_wait(&d_empty[st], ((g / DS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
           mbar_arrive_expect_tx(&d_full[st], L::TILE + 1024);
           uint8_t* base = sm + L::DO + st * L::DSTAGE;
@@ -465,16 +483,16 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       for (int m = 0; ok && get_item(ring, m, it); ++m) {
         const Where w = where(it.lin);
         const int last = g - 1;
-        if (it.count > 0) {
+        if (it.steps > 0) {
           if (!(ok = mbar_wait(kv_empty, (n & 1) ^ 1u, err, kErrTimeoutAttn))) break;
           mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
           tma_load_4d(sm + L::K, &map_k, kv_full, 0, w.kt * 128, w.kvh * (HD / 64), w.b);
           tma_load_4d(sm + L::V, &map_v, kv_full, 0, w.kt * 128, w.kvh * (HD / 64), w.b);
         }
         if (stored < n) ok = store(stored++, last);
-        if (it.count > 0) {
+        if (it.steps > 0) {
           out = w;
-          g += heads * it.count;
+          g += it.steps;
           ++n;
         }
       }
@@ -516,7 +534,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     Item it;
     bool ok = true;
     for (int m = 0, n = 0, g = 0; ok && get_item_warp(ring, m, it); ++m) {
-      const int total = heads * it.count;
+      const int total = it.steps;
       if (total == 0) continue;
       // the item's first scores: both TMEM slots are free of what the last item left in them once
       // its products, issued before, have run and every warp holds its dP^T columns
@@ -587,20 +605,26 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       for (int h = 0; h < 2; ++h) r.seen[h] = fetch_span(a.spans, b, qt * 128 + h * 64 + part * kCols + lane, s);
       return r;
     };
+    auto first_tile = [](const Item& x) { return x.first + (PARTIAL ? x.begin % x.count : 0); };
     Item it, next_it;
     Where next_w{0, 0, 0, 0};
     Ahead ahead{};
     bool ok = true, more = get_item_warp(ring, 0, next_it);
     if (more) {
       next_w = where(next_it.lin);
-      if (next_it.count > 0) ahead = look(next_w.b, next_it.first);
+      if (next_it.steps > 0) ahead = look(next_w.b, first_tile(next_it));
     }
     for (int m = 1, n = 0, g = 0; ok && more; ++m) {
       it = next_it;
       const Where w = next_w;
       const int k0 = w.kt * 128, key = k0 + row;
-      const int total = heads * it.count;
-      for (int i = 0, qt = it.first, hq = w.hq; i < total && ok; ++i, ++g) {
+      const int total = it.steps;
+      int qt = it.first, hq = w.kvh * group;
+      if (PARTIAL && total > 0) {
+        qt += it.begin % it.count;
+        hq += it.begin / it.count;
+      }
+      for (int i = 0; i < total && ok; ++i, ++g) {
         const int q0 = qt * 128;
         const bool all = sees_all(ahead.hull, k0, k0 + 128), padded = ahead.hull.max_lo == INT_MAX;
         uint32_t vis[2] = {~0u, ~0u};  // visible query columns of this thread's key, per half
@@ -679,9 +703,9 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       more = get_item_warp(ring, m, next_it);
       if (more) {
         next_w = where(next_it.lin);
-        if (next_it.count > 0) ahead = look(next_w.b, next_it.first);
+        if (next_it.steps > 0) ahead = look(next_w.b, first_tile(next_it));
       }
-      if (PARTIAL && total == 0) continue;  // the kernel that adds the heads writes the zeros
+      if (PARTIAL && total == 0) continue;  // the kernel that adds the parts writes the zeros
       if (total == 0) {
         const int64_t t = static_cast<int64_t>(w.b) * s + k0;
         zero_rows<HD>(a.dk + t * a.lddk + static_cast<int64_t>(w.kvh) * HD, a.lddk, min(128, s - k0), elem, R::kElem);
@@ -691,7 +715,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       if (!(ok = mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
       tc_fence_after();
       if constexpr (PARTIAL) {
-        float* p = a.partial + ((static_cast<int64_t>(w.b) * nh + w.hq) * n_t + w.kt) * (2 * 128 * HD);
+        float* p = a.partial + (((static_cast<int64_t>(w.b) * nkv + w.kvh) * parts + w.part) * n_t + w.kt) * (2 * 128 * HD);
         partial_cols<HD * 4 / EW>(tdK + tl, part * (HD * 4 / EW), p, row);
         partial_cols<HD * 4 / EW>(tdV + tl, part * (HD * 4 / EW), p + 128 * HD, row);
         tc_fence_before();
@@ -718,7 +742,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   if (warp == 1) tmem_dealloc(tbase, 512);
 }
 
-// dK and dV of one key tile: the sums of its query heads' partial sums, added in head order.
+// dK and dV of one key tile: the sums of its walk's parts, added in their order.
 template <int HD>
 __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ BwdArgs a, int n_t) {
   wait_for_previous();
@@ -727,16 +751,15 @@ __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ 
   const int kvh = hb % a.nkv, b = hb / a.nkv, group = a.nh / a.nkv;
   const int row = threadIdx.x & 127, key = kt * 128 + row;
   if (key >= a.s) return;
-  const bool some = a.q_ranges[static_cast<int64_t>(b) * n_t + kt].y >= 0;
-  const int64_t head_step = static_cast<int64_t>(n_t) * (2 * 128 * HD);
-  const float* p = a.partial + (static_cast<int64_t>(b) * a.nh + kvh * group) * head_step + kt * static_cast<int64_t>(2 * 128 * HD);
+  const int steps = group * walk_tiles(a.q_ranges[static_cast<int64_t>(b) * n_t + kt]);
+  const int64_t part_size = static_cast<int64_t>(n_t) * (2 * 128 * HD);
+  const float* p = a.partial + (static_cast<int64_t>(b) * a.nkv + kvh) * a.parts * part_size + kt * static_cast<int64_t>(2 * 128 * HD);
   const int64_t t = static_cast<int64_t>(b) * a.s + key;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (some) {
-    for (int h = 0; h < group; ++h) {
-      const float4 x = reinterpret_cast<const float4*>(p + h * head_step)[c * 128 + row];
-      sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
-    }
+  for (int k = 0; k < a.parts; ++k) {
+    if (steps < a.parts && part_begin(steps, k, a.parts) == part_begin(steps, k + 1, a.parts)) continue;  // nothing walked
+    const float4 x = reinterpret_cast<const float4*>(p + k * part_size)[c * 128 + row];
+    sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
   }
   const bool is_k = c < HD / 4;
   const float m = is_k ? a.score.scale : 1.f;
@@ -850,7 +873,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     if (lane == 0) {
       const int items = n_t * n_hb;
       auto take = [&](int lin) -> Item {
-        Item it{-1, 0, 0, {0, 0, 0, 0}};
+        Item it{-1, 0, 0, 0, 0, {0, 0, 0, 0}};
         if (lin < items) {
           const Where w = where(lin);
           it.lin = lin;
@@ -1156,34 +1179,42 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
   if (e != cudaSuccess) return e;
   const int sms = gemm_num_sms();
   const int64_t q_items = static_cast<int64_t>(n_t) * g.nh * g.B;
-  const int64_t k_items = static_cast<int64_t>(n_t) * (a.partial ? g.nh : g.nkv) * g.B;
+  const int64_t k_items = static_cast<int64_t>(n_t) * g.nkv * a.parts * g.B;
   e = launch_following(dq, dim3(static_cast<unsigned>(q_items < sms ? q_items : sms)), Roles<kQWarps>::kThreads,
                        SmemQ<HD>::BYTES, st, mq, mk, mv, md, mdq, a);
   if (e != cudaSuccess) return e;
-  auto* dkdv = a.partial ? &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, true>
+  auto* dkdv = a.parts > 1 ? &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, true>
                          : &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, false>;
-  e = allow_smem(dkdv, SmemKV<HD>::BYTES, dkdv_ready[a.partial != nullptr]);
+  e = allow_smem(dkdv, SmemKV<HD>::BYTES, dkdv_ready[a.parts > 1]);
   if (e != cudaSuccess) return e;
   e = launch_following(dkdv, dim3(static_cast<unsigned>(k_items < sms ? k_items : sms)), Roles<kKWarps>::kThreads,
                        SmemKV<HD>::BYTES, st, mq, mk, mv, md, mdk, mdv, a);
-  if (e != cudaSuccess || !a.partial) return e;
+  if (e != cudaSuccess || a.parts == 1) return e;
   return launch_following(span_join_kernel<HD>, dim3(static_cast<unsigned>(n_t) * g.nkv * g.B, HD / 4), 256, 0, st, a, n_t);
 }
 
 }  // namespace
 
-// With few key tiles the groups' heads are walked by different blocks, whose fp32 sums another kernel
-// adds: where the tiles would leave half of the 152 SMs idle. (B 2, s 333, 4 query heads on one key
-// head: dK/dV 37 us in 6 blocks of up to 12 tiles each, 14 + 4 us in 24 blocks.) With more tiles the
-// sums' traffic, 1 KB a key and query head, costs more than the even load saves.
-static bool split_heads(int B, int s, int nh, int nkv) {
-  return nh > nkv && static_cast<int64_t>(pad128(s) / 128) * nkv * B <= 152 / 2;
+// Parts that the walk of a key tile, its group's heads one after another, is cut into; each part is an
+// item and leaves fp32 sums, which another kernel adds. With few key tiles the longest walk is the
+// kernel's time: below one an SM they are cut into about 512 items (B 2, s 333, 4/1 heads: dK/dV 37 us
+// in 6 blocks, 14 + 4 us in 24; 4096 tokens, 32/4 heads: the whole backward 578 us in 128 items, 386 in 512),
+// with up to two an SM if they are long enough to pay for the sums, 1 KB a key and part written and
+// read (256 items cut into 512: 16384 tokens, 8/2 heads, up to 512 steps each, 1376 -> 1329 us; 4096 tokens,
+// 40/8 heads, up to 160, 462 -> 482).
+static int walk_parts(int B, int s, int nh, int nkv) {
+  const int group = nh / nkv;
+  const int64_t n_t = pad128(s) / 128, items = n_t * nkv * B, longest = n_t * group;
+  if (items > 152 / 2 && longest < (items > 152 ? 512 : 64)) return 1;
+  const int64_t parts = (kMaxParts + items / 2) / items;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(group, parts)));
 }
 
 uint64_t attn_span_bwd_scratch(int B, int s, int nh, int nkv, int hd) {
   const uint64_t sp = static_cast<uint64_t>(pad128(s));
   const uint64_t lists = static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * (sizeof(Hull) + sizeof(int2))) + 16;
-  const uint64_t sums = split_heads(B, s, nh, nkv) ? static_cast<uint64_t>(B) * nh * sp * 2 * hd * sizeof(float) : 0;
+  const int parts = walk_parts(B, s, nh, nkv);
+  const uint64_t sums = parts > 1 ? static_cast<uint64_t>(B) * nkv * parts * sp * 2 * hd * sizeof(float) : 0;
   return (lists + 15) / 16 * 16 + sums;
 }
 
@@ -1221,10 +1252,10 @@ cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, con
   const int64_t tiles = static_cast<int64_t>(g.B) * (pad128(g.s) / 128);
   int2* q_ranges = reinterpret_cast<int2*>(hulls + tiles);
   const uint64_t all = attn_span_bwd_scratch(g.B, g.s, g.nh, g.nkv, g.hd);
-  const uint64_t sums = static_cast<uint64_t>(g.B) * g.nh * pad128(g.s) * 2 * g.hd * sizeof(float);
-  float* partial = split_heads(g.B, g.s, g.nh, g.nkv)
-                       ? reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + (all - sums)) : nullptr;
-  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_ranges, reinterpret_cast<int*>(q_ranges + tiles), partial, dq,
+  const int parts = walk_parts(g.B, g.s, g.nh, g.nkv);
+  const uint64_t sums = static_cast<uint64_t>(g.B) * g.nkv * parts * pad128(g.s) * 2 * g.hd * sizeof(float);
+  float* partial = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + (all - sums)) : nullptr;
+  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_ranges, reinterpret_cast<int*>(q_ranges + tiles), parts, partial, dq,
                   dk, dv, lddq, lddk, lddv, g.B, g.s, g.nh, g.nkv, score_args(g), err};
   return dispatch(g, [&](auto hd, auto cap, auto bias) {
     return launch<decltype(hd)::value, decltype(cap)::value, decltype(bias)::value>(g, o, ldo, lse, dout, lddo, a, lsd,

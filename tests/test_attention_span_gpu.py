@@ -175,6 +175,27 @@ def test_backward(K, B, s, nh, nkv, hd, kind, cap, bias):
     assert int(kw["err"].item()) == 0
 
 
+@pytest.mark.parametrize("s,nh,nkv,kind,cap", [(1100, 144, 9, "causal", 0.0), (1030, 120, 10, "docs_padded", 20.0),
+                                               (3500, 152, 8, "prefix", 0.0)])
+def test_long_walks_of_few_key_tiles(K, s, nh, nkv, kind, cap):
+    """Many query heads on a key head: dK and dV from parts of the walk over them, key heads sampled."""
+    B, hd, G = 1, 64, nh // nkv
+    rng, qkv, x, vis, slopes, kw = _case(K, B, s, nh, nkv, hd, kind, cap, False, s)
+    o, lse = K.attn_span_fwd(*qkv, B, s, nh, nkv, hd, **kw)
+    do, dot = _bf16(rng, (s, nh * hd))
+    got = [_np(t).reshape(B, s, -1, hd) for t in K.attn_span_bwd(*qkv, o, lse, dot, B, s, nh, nkv, hd, **kw)]
+    assert int(kw["err"].item()) == 0
+    on, do = _np(o).reshape(B, s, nh, hd), do.reshape(B, s, nh, hd)
+    for g in (0, nkv - 1):
+        h = slice(g * G, (g + 1) * G)
+        k = slice(g, g + 1)
+        _check_backward([got[0][:, :, h], got[1][:, :, k], got[2][:, :, k]], (x[0][:, :, h], x[1][:, :, k], x[2][:, :, k]),
+                        on[:, :, h], lse[:, h], do[:, :, h], vis, hd ** -0.5, cap, np.zeros(G), B, s, G, 1, hd)
+    again = K.attn_span_bwd(*qkv, o, lse, dot, B, s, nh, nkv, hd, **kw)
+    for a, b in zip(again, got):
+        assert np.array_equal(_np(a).reshape(b.shape), b)
+
+
 @pytest.mark.parametrize("cap", [30.0, 50.0, 60.0])
 @pytest.mark.parametrize("size", [2.0 ** -30, 1.0, 2.0 ** 30])
 def test_scores_at_the_cap(K, cap, size):
