@@ -164,11 +164,6 @@ struct ItemRing {
 };
 constexpr int kTakeAhead = 2;     // the next item is taken with the last this many loads of an item
 
-__device__ __forceinline__ Hull load_l2(const Hull* h) {
-  const int4 v = __ldcg(reinterpret_cast<const int4*>(h));
-  return {v.x, v.y, v.z, v.w};
-}
-
 // Publish item number n (one thread).
 __device__ __forceinline__ bool put_item(const ItemRing& r, int n, const Item& it) {
   if (!mbar_wait(&r.empty[n & 1], ((n >> 1) & 1) ^ 1u, r.err, kErrTimeoutAttn)) return false;
@@ -213,7 +208,7 @@ __global__ void __launch_bounds__(256)
                       const float* __restrict__ lse, Spans spans, float2* __restrict__ lsd, Hull* __restrict__ hulls,
                       int* __restrict__ taken, int s, int nh, int n_t) {
   constexpr int kLanes = HD / 8;  // lanes per row
-  let_next_start();
+  let_next_start();  // (dQ and dK/dV do not: the next one's blocks among theirs cost 17 us of 362 at 7B)
   if (blockIdx.x == 0 && threadIdx.x < 2) taken[threadIdx.x] = 0;  // items taken by dQ and by dK/dV
   __shared__ Hull parts[4];
   const int tile = blockIdx.x % n_t;
@@ -260,7 +255,7 @@ struct BwdArgs {
   const float* slopes;
   const float2* lsd;
   const Hull* hulls;   // [B][tiles] of the query tiles
-  int* q_tiles;        // [B][tiles] query tiles of a key tile's walk, where it has parts
+  int2* q_ranges;      // [B][tiles] first and last query tile that meets a key tile (last -1: none)
   int* taken;          // [2] items taken: dQ, dK/dV
   int parts;           // parts of a key tile's walk
   float* partial;      // with more than one, their sums: [B][nkv][parts][tiles][2][HD/4][128][4]
@@ -271,7 +266,9 @@ struct BwdArgs {
   int* err;
 };
 
-// Where part `k` of `parts` of a walk of `steps` steps begins.
+// Query tiles of a key tile's walk (per query head of the group), and where part `k` of `parts` of `steps`
+// steps begins.
+__device__ __forceinline__ int walk_tiles(int2 range) { return range.y < 0 ? 0 : range.y - range.x + 1; }
 __device__ __forceinline__ int part_begin(int steps, int k, int parts) {
   return static_cast<uint32_t>(steps * k) / static_cast<uint32_t>(parts);  // steps <= 2^19, parts <= kMaxParts
 }
@@ -392,7 +389,6 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     tmem_relinquish();
   }
   wait_for_previous();
-  let_next_start();  // dQ's blocks take over the SMs as this kernel's last ones leave them
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -407,61 +403,43 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     // few tiles before its end: taken with the item itself, the items no longer go to the blocks that
     // are done first (14B heads, 256 unequal items: 385 -> 470 us); taken any later, the next item's
     // first loads come late
-    const int items = n_t * n_hb;
-    auto take = [&](int lin) -> Item {  // by the whole warp
-      Item it{-1, 0, 0, 0, 0, {0, 0, 0, 0}};
-      if (lin < items) {
-        const Where w = where(lin);
-        // the query tiles from the first to the last whose hull meets the key tile
-        const Hull* hulls = a.hulls + static_cast<int64_t>(w.b) * n_t;
-        int first = INT_MAX, last = -1;
-        for (int q = lane; q < n_t; q += 32) {
-          const Hull h = hulls[q];
-          if (h.min_lo < w.kt * 128 + 128 && h.max_hi > w.kt * 128) {
-            first = min(first, q);
-            last = q;
-          }
+    if (lane == 0) {
+      const int items = n_t * n_hb;
+      auto take = [&](int lin) -> Item {
+        Item it{-1, 0, 0, 0, 0, {0, 0, 0, 0}};
+        if (lin < items) {
+          const Where w = where(lin);
+          const int2 r = a.q_ranges[static_cast<int64_t>(w.b) * n_t + w.kt];
+          it.lin = lin;
+          it.first = r.x;
+          it.count = walk_tiles(r);
+          it.begin = part_begin(group * it.count, w.part, parts);
+          it.steps = part_begin(group * it.count, w.part + 1, parts) - it.begin;
         }
-        it.lin = lin;
-        it.first = __reduce_min_sync(0xffffffffu, first);
-        last = __reduce_max_sync(0xffffffffu, last);
-        it.count = last < 0 ? 0 : last - it.first + 1;
-        it.begin = part_begin(group * it.count, w.part, parts);
-        it.steps = part_begin(group * it.count, w.part + 1, parts) - it.begin;
-        if (PARTIAL && lane == 0 && w.part == 0) a.q_tiles[static_cast<int64_t>(w.b) * n_t + w.kt] = it.count;
-      }
-      return it;
-    };
-    auto put = [&](int m, const Item& it) {
-      bool ok = true;
-      if (lane == 0) ok = put_item(ring, m, it);
-      return __all_sync(0xffffffffu, ok);
-    };
-    Item cur = take(blockIdx.x);
-    bool ok = put(0, cur);
-    for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
-      const Where w = where(cur.lin);
-      const int total = cur.steps, early = max(total - kTakeAhead, 0);
-      Item next;
-      auto hand_on = [&] {
-        int taken = 0;
-        if (lane == 0) taken = atomicAdd(a.taken + 1, 1);
-        next = take(gridDim.x + __shfl_sync(0xffffffffu, taken, 0));
-        return put(m, next);
+        return it;
       };
-      if (total == 0 && !(ok = hand_on())) break;
-      for (int i = 0; i < total; ++i, ++g) {
-        if (i == early && !(ok = hand_on())) break;
-        const int st = g % QS;
-        if (!(ok = mbar_wait_warp(&q_empty[st], ((g / QS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
-        if (lane == 0) {
+      Item cur = take(blockIdx.x);
+      bool ok = put_item(ring, 0, cur);
+      for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
+        const Where w = where(cur.lin);
+        const int total = cur.steps, early = max(total - kTakeAhead, 0);
+        Item next;
+        auto hand_on = [&] {
+          next = take(gridDim.x + atomicAdd(a.taken + 1, 1));
+          return put_item(ring, m, next);
+        };
+        if (total == 0 && !(ok = hand_on())) break;
+        for (int i = 0; i < total; ++i, ++g) {
+          if (i == early && !(ok = hand_on())) break;
+          const int st = g % QS;
+          if (!(ok = mbar_wait(&q_empty[st], ((g / QS) & 1) ^ 1u, err, kErrTimeoutAttn))) break;
           mbar_arrive_expect_tx(&q_full[st], L::TILE);
           const int x = (PARTIAL ? cur.begin : 0) + i;
           tma_load_4d(sm + L::Q + st * L::TILE, &map_q, &q_full[st], 0, (cur.first + x % cur.count) * 128,
                       (w.kvh * group + x / cur.count) * (HD / 64), w.b);
         }
+        cur = next;
       }
-      cur = next;
     }
   } else if (warp == R::kRingWarp) {
     // the dO ring with the (-lse2, -delta) pairs
@@ -773,7 +751,7 @@ __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ 
   const int kvh = hb % a.nkv, b = hb / a.nkv, group = a.nh / a.nkv;
   const int row = threadIdx.x & 127, key = kt * 128 + row;
   if (key >= a.s) return;
-  const int steps = group * a.q_tiles[static_cast<int64_t>(b) * n_t + kt];
+  const int steps = group * walk_tiles(a.q_ranges[static_cast<int64_t>(b) * n_t + kt]);
   const int64_t part_size = static_cast<int64_t>(n_t) * (2 * 128 * HD);
   const float* p = a.partial + (static_cast<int64_t>(b) * a.nkv + kvh) * a.parts * part_size + kt * static_cast<int64_t>(2 * 128 * HD);
   const int64_t t = static_cast<int64_t>(b) * a.s + key;
@@ -881,6 +859,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -898,20 +877,20 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         if (lin < items) {
           const Where w = where(lin);
           it.lin = lin;
-          it.hull = load_l2(a.hulls + static_cast<int64_t>(w.b) * n_t + w.qt);
+          it.hull = a.hulls[static_cast<int64_t>(w.b) * n_t + w.qt];
           it.first = it.hull.min_lo / 128;
           it.count = it.hull.max_hi > 0 ? (it.hull.max_hi + 127) / 128 - it.first : 0;
         }
         return it;
       };
-      Item cur = take(atomicAdd(a.taken, 1));  // not blockIdx.x: blocks start as dK/dV's end
+      Item cur = take(blockIdx.x);
       bool ok = put_item(ring, 0, cur);
       for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
         const Where w = where(cur.lin);
         const int early = max(cur.count - kTakeAhead, 0);
         Item next;
         auto hand_on = [&] {
-          next = take(atomicAdd(a.taken, 1));
+          next = take(gridDim.x + atomicAdd(a.taken, 1));
           return put_item(ring, m, next);
         };
         if (cur.count == 0 && !(ok = hand_on())) break;
@@ -943,7 +922,22 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     }
   } else if (warp == R::kItemWarp) {
     // Q and dO, once per item, and the gradient of the item before, from the K stage of its last tile,
-    // which is released when it has been read
+    // which is released when it has been read; first this block's share of the query ranges that dK/dV walks
+    for (int64_t i = blockIdx.x; i < static_cast<int64_t>(a.B) * n_t; i += gridDim.x) {
+      const Hull* hulls = a.hulls + i / n_t * n_t;
+      const int k0 = static_cast<int>(i % n_t) * 128;
+      int first = INT_MAX, last = -1;
+      for (int q = lane; q < n_t; q += 32) {
+        const Hull h = hulls[q];
+        if (h.min_lo < k0 + 128 && h.max_hi > k0) {
+          first = min(first, q);
+          last = q;
+        }
+      }
+      first = __reduce_min_sync(0xffffffffu, first);
+      last = __reduce_max_sync(0xffffffffu, last);
+      if (lane == 0) a.q_ranges[i] = make_int2(first, last);
+    }
     if (lane == 0) {
       Item it;
       Where out{0, 0, 0};
@@ -1056,7 +1050,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     auto look = [&](const Where& w) -> Ahead {
       const int q = w.qt * 128 + row;
       return {fetch_span(a.spans, w.b, q, s),
-              __ldcg(a.lsd + (static_cast<int64_t>(w.b) * nh + w.head) * pad128(s) + q)};  // padded: q is inside
+              a.lsd[(static_cast<int64_t>(w.b) * nh + w.head) * pad128(s) + q]};  // padded: q is inside
     };
     Item it, next_it;
     Where next_w{0, 0, 0};
@@ -1156,7 +1150,6 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tbase, 512);
-  wait_for_previous();  // what follows this kernel follows dK/dV too
 }
 
 template <int HD, bool CAP, bool BIAS>
@@ -1187,15 +1180,15 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
   const int sms = gemm_num_sms();
   const int64_t q_items = static_cast<int64_t>(n_t) * g.nh * g.B;
   const int64_t k_items = static_cast<int64_t>(n_t) * g.nkv * a.parts * g.B;
+  e = launch_following(dq, dim3(static_cast<unsigned>(q_items < sms ? q_items : sms)), Roles<kQWarps>::kThreads,
+                       SmemQ<HD>::BYTES, st, mq, mk, mv, md, mdq, a);
+  if (e != cudaSuccess) return e;
   auto* dkdv = a.parts > 1 ? &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, true>
                          : &attn_span_dkdv_kernel<HD, CAP, BIAS, kKWarps, false>;
   e = allow_smem(dkdv, SmemKV<HD>::BYTES, dkdv_ready[a.parts > 1]);
   if (e != cudaSuccess) return e;
   e = launch_following(dkdv, dim3(static_cast<unsigned>(k_items < sms ? k_items : sms)), Roles<kKWarps>::kThreads,
                        SmemKV<HD>::BYTES, st, mq, mk, mv, md, mdk, mdv, a);
-  if (e != cudaSuccess) return e;
-  e = launch_following(dq, dim3(static_cast<unsigned>(q_items < sms ? q_items : sms)), Roles<kQWarps>::kThreads,
-                       SmemQ<HD>::BYTES, st, mq, mk, mv, md, mdq, a);
   if (e != cudaSuccess || a.parts == 1) return e;
   return launch_following(span_join_kernel<HD>, dim3(static_cast<unsigned>(n_t) * g.nkv * g.B, HD / 4), 256, 0, st, a, n_t);
 }
@@ -1219,7 +1212,7 @@ static int walk_parts(int B, int s, int nh, int nkv) {
 
 uint64_t attn_span_bwd_scratch(int B, int s, int nh, int nkv, int hd) {
   const uint64_t sp = static_cast<uint64_t>(pad128(s));
-  const uint64_t lists = static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * (sizeof(Hull) + sizeof(int))) + 16;
+  const uint64_t lists = static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * (sizeof(Hull) + sizeof(int2))) + 16;
   const int parts = walk_parts(B, s, nh, nkv);
   const uint64_t sums = parts > 1 ? static_cast<uint64_t>(B) * nkv * parts * sp * 2 * hd * sizeof(float) : 0;
   return (lists + 15) / 16 * 16 + sums;
@@ -1257,12 +1250,12 @@ cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, con
   float2* lsd = static_cast<float2*>(scratch);
   Hull* hulls = reinterpret_cast<Hull*>(lsd + static_cast<int64_t>(g.B) * g.nh * pad128(g.s));
   const int64_t tiles = static_cast<int64_t>(g.B) * (pad128(g.s) / 128);
-  int* q_tiles = reinterpret_cast<int*>(hulls + tiles);
+  int2* q_ranges = reinterpret_cast<int2*>(hulls + tiles);
   const uint64_t all = attn_span_bwd_scratch(g.B, g.s, g.nh, g.nkv, g.hd);
   const int parts = walk_parts(g.B, g.s, g.nh, g.nkv);
   const uint64_t sums = static_cast<uint64_t>(g.B) * g.nkv * parts * pad128(g.s) * 2 * g.hd * sizeof(float);
   float* partial = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + (all - sums)) : nullptr;
-  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_tiles, q_tiles + tiles, parts, partial, dq,
+  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_ranges, reinterpret_cast<int*>(q_ranges + tiles), parts, partial, dq,
                   dk, dv, lddq, lddk, lddv, g.B, g.s, g.nh, g.nkv, score_args(g), err};
   return dispatch(g, [&](auto hd, auto cap, auto bias) {
     return launch<decltype(hd)::value, decltype(cap)::value, decltype(bias)::value>(g, o, ldo, lse, dout, lddo, a, lsd,
