@@ -26,11 +26,11 @@
 //
 // Measured (head size 128): two 4096-token sequences of 32 heads, packed documents of 700 tokens on
 // average, 343 us (delta 27, dQ 123, dK/dV 188), 7 products over 1.35 times the visible scores; 4096
-// tokens, 40/8 heads, capped, 633 us (18, 239, 378). The delta kernel is bound by HBM; the others keep the
-// tensor cores 51 % (dQ) and 46 % (dK/dV) busy and wait for one another's halves in turn. A tile of dK/dV
-// moves 192 KB of operands, 64 KB of TMA writes and 845 wavefronts of ordinary accesses (most of them the
-// pairs' broadcasts) through shared memory; smaller products that start earlier (S^T by halves) move
-// more and end later: 349 us.
+// tokens, 40/8 heads, capped, 634 us (18, 239, 378; the longest walk is 1.15 times the mean load of an SM). The
+// delta kernel is bound by HBM; the others keep the tensor cores 51 % (dQ) and 46 % (dK/dV) busy and wait for
+// one another's halves in turn. A tile of dK/dV moves 192 KB of operands, 64 KB of TMA writes and 845
+// wavefronts of ordinary accesses (most of them the pairs' broadcasts) through shared memory; smaller
+// products that start earlier (S^T by halves) move more and end later: 349 us.
 #include <algorithm>
 #include <cstdint>
 
@@ -58,7 +58,7 @@ struct Roles {
   static constexpr int kThreads = EW * 32 + 128;
   static constexpr int kItemReaders = EW + 3;  // lane 0 of every warp but the one that takes items
 };
-constexpr int kMaxParts = 512;        // of a key tile's walk
+constexpr int kPartItems = 512;       // items that few key tiles' walks are cut into
 constexpr int kSlice128 = 128 * 128;  // bytes of a [128 rows][64 bf16] swizzle-atom-wide slice
 
 __host__ __device__ __forceinline__ int pad128(int s) { return (s + 127) & ~127; }
@@ -270,7 +270,7 @@ struct BwdArgs {
 // steps begins.
 __device__ __forceinline__ int walk_tiles(int2 range) { return range.y < 0 ? 0 : range.y - range.x + 1; }
 __device__ __forceinline__ int part_begin(int steps, int k, int parts) {
-  return static_cast<uint32_t>(steps * k) / static_cast<uint32_t>(parts);  // steps <= 2^19, parts <= kMaxParts
+  return static_cast<uint32_t>(steps * k) / static_cast<uint32_t>(parts);  // steps <= 2^19, parts <= kPartItems
 }
 
 // P and dS of one pair of columns: scores (capped: their tanh) and dP in, P and dS out. nl = -lse2,
@@ -1197,17 +1197,17 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
 
 // Parts that the walk of a key tile, its group's heads one after another, is cut into; each part is an
 // item and leaves fp32 sums, which another kernel adds. With few key tiles the longest walk is the
-// kernel's time: below one an SM they are cut into about 512 items (B 2, s 333, 4/1 heads: dK/dV 37 us
-// in 6 blocks, 14 + 4 us in 24; 4096 tokens, 32/4 heads: the whole backward 578 us in 128 items, 386 in 512),
-// with up to two an SM if they are long enough to pay for the sums, 1 KB a key and part written and
-// read (256 items cut into 512: 16384 tokens, 8/2 heads, up to 512 steps each, 1376 -> 1329 us; 4096 tokens,
-// 40/8 heads, up to 160, 462 -> 482).
+// kernel's time: up to one an SM they are cut into about 512 (B 2, s 333, 4/1 heads: dK/dV 37 us in 6 blocks,
+// 14 + 4 us in 24; 4096 tokens, 32/4 heads: the whole backward 578 us in 128 items, 388 in 256, 385 in 512;
+// 8192, 16/2: 1104, 710, 691), unless the walks are too short to pay for the sums, 1 KB a key and part
+// written and read. Up to two an SM are cut in two if they are very long (256 items: 16384 tokens, 8/2
+// heads, up to 512 steps each, 1376 -> 1342 us; 4096 tokens, 40/8 heads, up to 160, 462 -> 482).
 static int walk_parts(int B, int s, int nh, int nkv) {
   const int group = nh / nkv;
   const int64_t n_t = pad128(s) / 128, items = n_t * nkv * B, longest = n_t * group;
-  if (items > 152 / 2 && longest < (items > 152 ? 512 : 64)) return 1;
-  const int64_t parts = (kMaxParts + items / 2) / items;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(group, parts)));
+  if (items > 152) return items <= 304 && longest >= 512 && group > 1 ? 2 : 1;
+  if (items > 152 / 2 && longest < 64) return 1;
+  return static_cast<int>(std::min<int64_t>(group, (kPartItems + items / 2) / items));
 }
 
 uint64_t attn_span_bwd_scratch(int B, int s, int nh, int nkv, int hd) {
