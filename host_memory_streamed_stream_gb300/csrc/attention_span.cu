@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
       const uint64_t vd = smem_desc_sw128(smem_addr(sm + L::V + vs * L::TILE), kSlice64, 1024);
 #pragma unroll
       for (int kk = 0; kk < kKeys / 16; ++kk)  // A = P_j from TMEM: 16 keys = 8 columns per step
-        umma_bf16_tmem_a_warp(tO, tS0 + st * kKeys + (16 * kk / kCols) * kCols + 16 * kk % kCols / 2, desc_advance(vd, kk * 2048), idesc_o,
-                              (j > 0 || kk > 0) ? 1u : 0u);
+        umma_bf16_tmem_a_warp(tO, tS0 + st * kKeys + (16 * kk / kCols) * kCols + 16 * kk % kCols / 2,
+                              desc_advance(vd, kk * 2048), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
       umma_commit_warp(&v_empty[vs]);
       umma_commit_warp(pv_done);
       if (j == n_kv - 1) umma_commit_warp(o_done);
@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
       const float inv = 1.f / l;
       // the warp's 32 rows and this part's columns, up to 64 at a time
       constexpr int kOut = BOUNDED ? HD / 2 : HD, kStep = kOut < 64 ? kOut : 64;
-      bf16* o0 = a.o + (static_cast<int64_t>(b) * s + q0 + sub * 32) * a.ldo + static_cast<int64_t>(head) * HD + part * kOut;
+      bf16* o0 = a.o + (static_cast<int64_t>(b) * s + q0 + sub * 32) * a.ldo + static_cast<int64_t>(head) * HD +
+                 part * kOut;
 #pragma unroll
       for (int c = 0; c < kOut; c += kStep) {
         uint4 out[kStep / 8];
@@ -380,9 +381,9 @@ cudaError_t launch(const AttnSpanArgs& g, bf16* o, int64_t ldo, float* lse, int*
   // pair of them, 144, 147, 134 us, capped 223, 221, 195; two sequences of 32 heads, 2 MB a pair, 214, 212,
   // 217, as packed documents 110, 109, 108.)
   constexpr int64_t kGroupBytes = 64 << 20;
-  const int64_t pairs = std::min<int64_t>(kGroupBytes / (s * HD * 4) * (g.nh / g.nkv), static_cast<int64_t>(g.nh) * g.B);
-  const FwdArgs a{{g.lo, g.hi}, g.slopes, o, ldo, lse, g.s, g.nh, g.nkv, static_cast<int>(std::max<int64_t>(pairs, kHeadGroup)),
-                  score_args(g), err};
+  const int64_t fit = kGroupBytes / (s * HD * 4) * (g.nh / g.nkv), pairs = static_cast<int64_t>(g.nh) * g.B;
+  const int head_group = static_cast<int>(std::max<int64_t>(std::min(fit, pairs), kHeadGroup));
+  const FwdArgs a{{g.lo, g.hi}, g.slopes, o, ldo, lse, g.s, g.nh, g.nkv, head_group, score_args(g), err};
   auto run = [&](auto bounded) {
     auto* kernel = &attn_span_fwd_kernel<HD, CAP, BIAS, decltype(bounded)::value>;
     static std::atomic<uint64_t> ready{0};

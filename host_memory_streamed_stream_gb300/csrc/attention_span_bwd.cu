@@ -93,9 +93,9 @@ __device__ __forceinline__ void tmem_ld_pair(uint32_t ta, uint32_t tb, float (&a
 }
 
 // An item's gradients leave through shared memory: each thread converts its share of a row (W columns
-// from col0) of the accumulator and writes it to the ring stage that the item's last tile
-// was read from, in the swizzled layout of a TMA store, which the warp that loads the items' own operands issues. (Each lane storing
-// its own row to global memory touches 32 lines an instruction: 7500 cycles for the two 128 x 128
+// from col0) of the accumulator and writes it to the ring stage that the item's last tile was read
+// from, in the swizzled layout of a TMA store, which the warp that loads the items' own operands
+// issues. (Each lane storing its own row to global memory touches 32 lines an instruction: 7500 cycles for the two 128 x 128
 // gradients of a key tile, two tiles' work. Rows transposed through the warp first: 4700.)
 template <int W>
 __device__ __forceinline__ void stage_cols(uint32_t taddr, int col0, float scale, uint8_t* tile, int row) {
@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(256)
     if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = h;
   }
   __syncthreads();
-  if (threadIdx.x == 0) hulls[static_cast<int64_t>(b) * n_t + tile] = join(join(parts[0], parts[1]), join(parts[2], parts[3]));
+  if (threadIdx.x == 0)
+    hulls[static_cast<int64_t>(b) * n_t + tile] = join(join(parts[0], parts[1]), join(parts[2], parts[3]));
 }
 
 struct BwdArgs {
@@ -630,7 +631,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         uint32_t vis[2] = {~0u, ~0u};  // visible query columns of this thread's key, per half
         if (!all) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) vis[h] = warp_transpose(span_bits(clamp_span(ahead.seen[h], s), k0 + sub * 32), lane);
+          for (int h = 0; h < 2; ++h)
+            vis[h] = warp_transpose(span_bits(clamp_span(ahead.seen[h], s), k0 + sub * 32), lane);
         }
         const float slope2 = BIAS ? __ldg(a.slopes + hq) * kLog2e : 0.f;
         if (++qt == it.first + it.count) {  // the walk of the group's next head
@@ -715,7 +717,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       if (!(ok = mbar_wait_warp(acc_full, n & 1, err, kErrTimeoutAttn))) break;
       tc_fence_after();
       if constexpr (PARTIAL) {
-        float* p = a.partial + (((static_cast<int64_t>(w.b) * nkv + w.kvh) * parts + w.part) * n_t + w.kt) * (2 * 128 * HD);
+        const int64_t slot = ((static_cast<int64_t>(w.b) * nkv + w.kvh) * parts + w.part) * n_t + w.kt;
+        float* p = a.partial + slot * (2 * 128 * HD);
         partial_cols<HD * 4 / EW>(tdK + tl, part * (HD * 4 / EW), p, row);
         partial_cols<HD * 4 / EW>(tdV + tl, part * (HD * 4 / EW), p + 128 * HD, row);
         tc_fence_before();
@@ -753,11 +756,12 @@ __global__ void __launch_bounds__(256) span_join_kernel(const __grid_constant__ 
   if (key >= a.s) return;
   const int steps = group * walk_tiles(a.q_ranges[static_cast<int64_t>(b) * n_t + kt]);
   const int64_t part_size = static_cast<int64_t>(n_t) * (2 * 128 * HD);
-  const float* p = a.partial + (static_cast<int64_t>(b) * a.nkv + kvh) * a.parts * part_size + kt * static_cast<int64_t>(2 * 128 * HD);
+  const float* p = a.partial + (static_cast<int64_t>(b) * a.nkv + kvh) * a.parts * part_size +
+                   kt * static_cast<int64_t>(2 * 128 * HD);
   const int64_t t = static_cast<int64_t>(b) * a.s + key;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = 0; k < a.parts; ++k) {
-    if (steps < a.parts && part_begin(steps, k, a.parts) == part_begin(steps, k + 1, a.parts)) continue;  // nothing walked
+    if (steps < a.parts && part_begin(steps, k, a.parts) == part_begin(steps, k + 1, a.parts)) continue;  // no step
     const float4 x = reinterpret_cast<const float4*>(p + k * part_size)[c * 128 + row];
     sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
   }
@@ -1190,7 +1194,8 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
   e = launch_following(dkdv, dim3(static_cast<unsigned>(k_items < sms ? k_items : sms)), Roles<kKWarps>::kThreads,
                        SmemKV<HD>::BYTES, st, mq, mk, mv, md, mdk, mdv, a);
   if (e != cudaSuccess || a.parts == 1) return e;
-  return launch_following(span_join_kernel<HD>, dim3(static_cast<unsigned>(n_t) * g.nkv * g.B, HD / 4), 256, 0, st, a, n_t);
+  const dim3 join_grid(static_cast<unsigned>(n_t) * g.nkv * g.B, HD / 4);
+  return launch_following(span_join_kernel<HD>, join_grid, 256, 0, st, a, n_t);
 }
 
 }  // namespace
@@ -1212,7 +1217,8 @@ static int walk_parts(int B, int s, int nh, int nkv) {
 
 uint64_t attn_span_bwd_scratch(int B, int s, int nh, int nkv, int hd) {
   const uint64_t sp = static_cast<uint64_t>(pad128(s));
-  const uint64_t lists = static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * (sizeof(Hull) + sizeof(int2))) + 16;
+  const uint64_t tile = sizeof(Hull) + sizeof(int2);
+  const uint64_t lists = static_cast<uint64_t>(B) * (nh * sp * sizeof(float2) + sp / 128 * tile) + 16;
   const int parts = walk_parts(B, s, nh, nkv);
   const uint64_t sums = parts > 1 ? static_cast<uint64_t>(B) * nkv * parts * sp * 2 * hd * sizeof(float) : 0;
   return (lists + 15) / 16 * 16 + sums;
@@ -1255,8 +1261,9 @@ cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, con
   const int parts = walk_parts(g.B, g.s, g.nh, g.nkv);
   const uint64_t sums = static_cast<uint64_t>(g.B) * g.nkv * parts * pad128(g.s) * 2 * g.hd * sizeof(float);
   float* partial = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + (all - sums)) : nullptr;
-  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_ranges, reinterpret_cast<int*>(q_ranges + tiles), parts, partial, dq,
-                  dk, dv, lddq, lddk, lddv, g.B, g.s, g.nh, g.nkv, score_args(g), err};
+  int* taken = reinterpret_cast<int*>(q_ranges + tiles);
+  const BwdArgs a{{g.lo, g.hi}, g.slopes, lsd, hulls, q_ranges, taken, parts, partial, dq, dk, dv, lddq,
+                  lddk, lddv, g.B, g.s, g.nh, g.nkv, score_args(g), err};
   return dispatch(g, [&](auto hd, auto cap, auto bias) {
     return launch<decltype(hd)::value, decltype(cap)::value, decltype(bias)::value>(g, o, ldo, lse, dout, lddo, a, lsd,
                                                                                     hulls, st);

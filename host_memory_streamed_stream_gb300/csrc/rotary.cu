@@ -10,8 +10,8 @@
 // read neighbouring vectors in both accesses (with 16 adjacent columns per thread instead, every
 // access covers half of each 32-byte sector: 53 us instead of 51 for 8192 x 64 interleaved heads).
 // Measured (head size 128; a plain copy reaches 6.77 TB/s): rotation of 8192 x 64 heads 43.1 us, 6.3
-// TB/s; norm forward of 4096 x 48 heads 24.6 us (21 us of it on the device, half of it in start and tail), its backward of
-// 8192 x 64 heads 74.7 us, 5.4 TB/s. A single token takes 3 us on the device and is bound by the call.
+// TB/s; norm forward of 4096 x 48 heads 24.6 us (21 us of it on the device, where its start and tail
+// show), its backward of 8192 x 64 heads 74.7 us, 5.4 TB/s. A single token takes 3 us on the device and is bound by the call.
 #include <cmath>
 #include <cstdint>
 
@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(kRotThreads, 4) row_kernel(const __grid_consta
 
 template <int HD>
 cudaError_t launch_rows(const RowArgs& a, bool interleaved, bool inverse, cudaStream_t s) {
-  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.T) + a.split.token_slots - 1) / a.split.token_slots);
+  const int64_t slots = a.split.token_slots;
+  const unsigned blocks = static_cast<unsigned>((a.T + slots - 1) / slots);
   auto* kernel = interleaved ? (inverse ? row_kernel<HD, true, HD == 0> : row_kernel<HD, true, false>)
                              : (inverse ? row_kernel<HD, false, HD == 0> : row_kernel<HD, false, false>);
   kernel<<<blocks, (a.split.units * a.split.rows() + 31) / 32 * 32, 0, s>>>(a);
@@ -639,8 +640,8 @@ cudaError_t qk_norm_rope_bwd(const bf16* dy, int64_t lddy, const bf16* x, int64_
   kernel<<<sp.q.blocks + sp.k.blocks, kRotThreads, 0, s>>>(a, sp);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_following(hd == 64 ? qk_gain_reduce_kernel<64> : qk_gain_reduce_kernel<128>, dim3(2), 1024, 0, s, partial,
-                          sp.q.blocks, sp.k.blocks, dgq, dgk);
+  return launch_following(hd == 64 ? qk_gain_reduce_kernel<64> : qk_gain_reduce_kernel<128>, dim3(2), 1024, 0, s,
+                          partial, sp.q.blocks, sp.k.blocks, dgq, dgk);
 }
 
 }  // namespace mt

@@ -231,7 +231,8 @@ def qk_norm_rope_bwd(dy, x, gq, gk, rstd, n_heads, n_kv_heads, head_dim, cos_sin
     if out is None:
         out = torch.empty((T, cols), dtype=torch.bfloat16, device=x.device)
     lib = _lib.load()
-    partial = torch.empty((lib.mtk_qk_norm_rope_bwd_parts(T, n_heads, n_kv_heads, head_dim), head_dim), dtype=torch.float32, device=x.device)
+    parts = lib.mtk_qk_norm_rope_bwd_parts(T, n_heads, n_kv_heads, head_dim)
+    partial = torch.empty((parts, head_dim), dtype=torch.float32, device=x.device)
     dgq, dgk = torch.empty_like(gq), torch.empty_like(gk)
     pos = None if positions is None else _vec(positions, T, torch.int32, "positions", dev)
     err = _err(err, x.device)

@@ -155,13 +155,14 @@ int mtk_rotary(const void* x, int64_t ldx, void* y, int64_t ldy, int T, int head
  * with the rotation R of mtk_rotary (rot_dim = 0: no rotation; cos_sin, positions and err_flag may
  * then be NULL). x, y bf16 with row strides ldx, ldy (columns past the key heads, such as v, are
  * neither read nor written); gq, gk bf16 [head_dim]; rstd f32 [T][n_heads + n_kv_heads], or NULL.
- * y may be x (then ldy = ldx), else they must not overlap. head_dim 64 or 128, rot_dim a multiple of 16, at most 65536 heads.
+ * y may be x (then ldy = ldx), else they must not overlap. head_dim 64 or 128, rot_dim a multiple of
+ * 16, at most 65536 heads.
  *
  * mtk_qk_norm_rope_bwd: from dy (row stride lddy), the forward's x and its rstd, with u = R^T dy and
  * n = x_h * rstd: dx_h = rstd (u g - n mean(u g n)), dgq and dgk bf16 [head_dim] = the sums of u n
  * over tokens and query (key) heads, added in a fixed order through `partial`, f32
- * [mtk_qk_norm_rope_bwd_parts(...)][head_dim]. dx may be dy or x (with the same row stride), else it overlaps neither. A
- * bad position counts as no rotation, with *err_flag set to 8.
+ * [mtk_qk_norm_rope_bwd_parts(...)][head_dim]. dx may be dy or x (with the same row stride), else it
+ * overlaps neither. A bad position counts as no rotation, with *err_flag set to 8.
  */
 int mtk_qk_norm_rope(const void* x, int64_t ldx, const void* gq, const void* gk, void* y, int64_t ldy, void* rstd,
                      int T, int n_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved, float eps,
