@@ -5,6 +5,7 @@ to one C entry point and raises on a nonzero status.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 
 import numpy as np
@@ -161,6 +162,14 @@ def _table(cos_sin, dev):
     return _vec(cos_sin, cos_sin.numel(), torch.float32, "cos_sin", dev), shape[0], 2 * shape[1]
 
 
+def _host(a):
+    """Address of a contiguous numpy array (ndarray.ctypes costs 2 us more after a launch)."""
+    try:
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))
+    except (TypeError, ValueError):  # read-only or empty
+        return a.ctypes.data
+
+
 def rotary_inv_freq(rot_dim, theta=10000.0, scaling="plain", factor=1.0, original_positions=0, low=1.0, high=32.0):
     """rot_dim/2 rotation frequencies (numpy float64, radians per position); see mtk_rotary_inv_freq
     for the scalings "plain", "linear", "base" and "bands"."""
@@ -168,7 +177,7 @@ def rotary_inv_freq(rot_dim, theta=10000.0, scaling="plain", factor=1.0, origina
         raise MTError(-1, f"scaling: one of {sorted(ROTARY_SCALINGS)}")
     out = np.empty(max(int(rot_dim) // 2, 1), dtype=np.float64)
     _ok(_lib.load().mtk_rotary_inv_freq(rot_dim, theta, ROTARY_SCALINGS[scaling], factor, original_positions, low, high,
-                                        out.ctypes.data), "rotary_inv_freq")
+                                        _host(out)), "rotary_inv_freq")
     return out
 
 
@@ -180,7 +189,7 @@ def rotary_table(inv_freq, n_pos, amplitude=1.0, out=None):
         out = torch.empty((n_pos, f.size, 2), dtype=torch.float32, device="cuda")
     _need(out.shape == (n_pos, f.size, 2), "out: fp32 [n_pos, rot_dim/2, 2]")
     dev = _device(out)
-    _ok(_lib.load().mtk_rotary_table(f.ctypes.data, 2 * f.size, n_pos, amplitude,
+    _ok(_lib.load().mtk_rotary_table(_host(f), 2 * f.size, n_pos, amplitude,
                                      _vec(out, out.numel(), torch.float32, "out", dev), _stream(dev)), "rotary_table")
     return out
 
@@ -360,14 +369,13 @@ def _span_scratch(B, s, nh, nkv, hd):
 
 def attn_span_bwd(q, k, v, o, lse, dout, B, s, nh, nkv, hd, lo=None, hi=None, scale=None, cap=0.0, slopes=None,
                   out=None, err=None):
-    """(dq, dk, dv) of attn_span_fwd; out: three tensors to write, None: the column ranges of one new
-    [B*s, (nh+2*nkv)*hd] tensor, the layout of a fused projection's gradient."""
+    """(dq, dk, dv) of attn_span_fwd; out: three tensors to write, such as the column ranges of a fused
+    projection's gradient; None: new ones."""
     dev = _device(q)
     *ptrs, sl = _span_args(q, k, v, B, s, nh, nkv, hd, lo, hi, slopes, dev)
     T = B * s
     if out is None:
-        out = torch.empty((T, (nh + 2 * nkv) * hd), dtype=torch.bfloat16, device=q.device)
-        out = out.split((nh * hd, nkv * hd, nkv * hd), 1)
+        out = [torch.empty((T, n * hd), dtype=torch.bfloat16, device=q.device) for n in (nh, nkv, nkv)]
     dq, dk, dv = out
     lib = _lib.load()
     scratch = torch.empty(_span_scratch(B, s, nh, nkv, hd), dtype=torch.uint8, device=q.device)
