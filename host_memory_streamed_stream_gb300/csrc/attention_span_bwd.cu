@@ -164,6 +164,16 @@ struct ItemRing {
 };
 constexpr int kTakeAhead = 2;     // the next item is taken with the last this many loads of an item
 
+// Waits test a phase's parity, so one that is two phases behind never ends. Everyone who waits for a phase
+// of a barrier is therefore needed for the phase after it on the same barrier. The accumulators' release
+// (acc_empty) is waited for by the MMA warp and by the warp that stores the item's gradients, and the latter
+// has by then loaded what the next item needs: an item of one or two tiles can end before it looks.
+// Its barriers are used in turn, item n arrives at number n % kAccTurns, and item n + 2 needs
+// operands that the storing warp loads after its wait for item n.
+constexpr int kAccTurns = 2;
+__device__ __forceinline__ uint64_t* acc_turn(uint64_t* acc_empty, int n) { return acc_empty + n % kAccTurns; }
+__device__ __forceinline__ uint32_t acc_parity(int n) { return n / kAccTurns & 1; }
+
 // Publish item number n (one thread).
 __device__ __forceinline__ bool put_item(const ItemRing& r, int n, const Item& it) {
   if (!mbar_wait(&r.empty[n & 1], ((n >> 1) & 1) ^ 1u, r.err, kErrTimeoutAttn)) return false;
@@ -336,9 +346,10 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   uint64_t* dp_free = bar + 14;          // every warp holds its dP^T columns in registers
   uint64_t* p_half = bar + 15;           // [2]: every warp has written P^T/dS^T of that half
   uint64_t* acc_full = bar + 17;         // the item's accumulating MMAs have completed
-  uint64_t* acc_empty = bar + 18;        // every warp has read its part of dK and dV and staged it
-  const ItemRing ring{bar + 19, bar + 21, reinterpret_cast<Item*>(bar + 24), err};
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 23);
+  uint64_t* acc_empty = bar + 18;        // [kAccTurns]: every warp has read its part of dK and dV and staged it
+  const ItemRing ring{bar + 20, bar + 22, reinterpret_cast<Item*>(bar + 25), err};
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 24);
+  static_assert(25 * 8 + 2 * sizeof(Item) <= 320, "barriers and item slots past their shared memory");
 
   const int s = a.s, nh = a.nh, nkv = a.nkv;
   const int group = nh / nkv;
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     mbar_init(&p_half[0], EW);
     mbar_init(&p_half[1], EW);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, EW);
+    for (int i = 0; i < kAccTurns; ++i) mbar_init(&acc_empty[i], EW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ring.full[i], 1);
       mbar_init(&ring.empty[i], R::kItemReaders);
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       Where out{0, 0, 0, 0};
       bool ok = true;
       auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
-        if (!mbar_wait(acc_empty, n & 1, err, kErrTimeoutAttn)) return false;
+        if (!mbar_wait(acc_turn(acc_empty, n), acc_parity(n), err, kErrTimeoutAttn)) return false;
         if constexpr (!PARTIAL) {
           tma_store_4d(&map_dk, sm + L::Q + (g % QS) * L::TILE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
           tma_store_4d(&map_dv, sm + L::DO + (g % DS) * L::DSTAGE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
@@ -563,7 +574,9 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
           }
           if (!(ok = mbar_wait_warp(&p_half[h], g & 1, err, kErrTimeoutAttn))) break;
           // the first product of an item overwrites the accumulators: the last item's have been read
-          if (h == 0 && i == 0 && n > 0 && !(ok = mbar_wait_warp(acc_empty, (n - 1) & 1, err, kErrTimeoutAttn))) break;
+          if (h == 0 && i == 0 && n > 0 &&
+              !(ok = mbar_wait_warp(acc_turn(acc_empty, n - 1), acc_parity(n - 1), err, kErrTimeoutAttn)))
+            break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {  // 16 queries per step; A (P^T, dS^T) from TMEM
@@ -723,7 +736,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         partial_cols<HD * 4 / EW>(tdV + tl, part * (HD * 4 / EW), p + 128 * HD, row);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
+        if (lane == 0) mbar_arrive(acc_turn(acc_empty, n));
         ++n;
         continue;
       }
@@ -734,7 +747,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
+      if (lane == 0) mbar_arrive(acc_turn(acc_empty, n));
       ++n;
     }
   }
@@ -815,9 +828,9 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   uint64_t* dp_free = bar + 13;          // every warp holds its dP columns in registers
   uint64_t* ds_half = bar + 14;          // [2]
   uint64_t* acc_full = bar + 16;         // the item's dQ MMAs have completed
-  uint64_t* acc_empty = bar + 17;        // every warp has read its part of dQ and staged it
-  const ItemRing ring{bar + 18, bar + 20, reinterpret_cast<Item*>(bar + 23), err};
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 22);
+  uint64_t* acc_empty = bar + 17;        // [kAccTurns]: every warp has read its part of dQ and staged it
+  const ItemRing ring{bar + 19, bar + 21, reinterpret_cast<Item*>(bar + 24), err};
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 23);
 
   const int s = a.s, nh = a.nh;
   const int n_t = (s + 127) / 128, n_hb = nh * a.B;
@@ -848,7 +861,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     mbar_init(&ds_half[0], EW);
     mbar_init(&ds_half[1], EW);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, EW);
+    for (int i = 0; i < kAccTurns; ++i) mbar_init(&acc_empty[i], EW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ring.full[i], 1);
       mbar_init(&ring.empty[i], R::kItemReaders);
@@ -947,7 +960,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       Where out{0, 0, 0};
       bool ok = true;
       auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
-        if (!mbar_wait(acc_empty, n & 1, err, kErrTimeoutAttn)) return false;
+        if (!mbar_wait(acc_turn(acc_empty, n), acc_parity(n), err, kErrTimeoutAttn)) return false;
         tma_store_4d(&map_dq, sm + L::K + (g % KS) * L::TILE, 0, out.qt * 128, out.head * (HD / 64), out.b);
         bulk_commit();
         bulk_wait_read();
@@ -1026,7 +1039,9 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
           }
           if (!(ok = mbar_wait_warp(&ds_half[h], g & 1, err, kErrTimeoutAttn))) break;
           // the first product of an item overwrites the accumulator: the last item's has been read
-          if (h == 0 && j == 0 && n > 0 && !(ok = mbar_wait_warp(acc_empty, (n - 1) & 1, err, kErrTimeoutAttn))) break;
+          if (h == 0 && j == 0 && n > 0 &&
+              !(ok = mbar_wait_warp(acc_turn(acc_empty, n - 1), acc_parity(n - 1), err, kErrTimeoutAttn)))
+            break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 4 * h; kk < 4 * h + 4; ++kk)  // 16 keys per step; A (dS) from TMEM
@@ -1145,7 +1160,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
+      if (lane == 0) mbar_arrive(acc_turn(acc_empty, n));
       ++n;
     }
   }
