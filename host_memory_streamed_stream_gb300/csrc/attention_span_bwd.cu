@@ -164,15 +164,15 @@ struct ItemRing {
 };
 constexpr int kTakeAhead = 2;     // the next item is taken with the last this many loads of an item
 
-// Waits test a phase's parity, so one that is two phases behind never ends. Everyone who waits for a phase
-// of a barrier is therefore needed for the phase after it on the same barrier. The accumulators' release
-// (acc_empty) is waited for by the MMA warp and by the warp that stores the item's gradients, and the latter
-// has by then loaded what the next item needs: an item of one or two tiles can end before it looks.
-// Its barriers are used in turn, item n arrives at number n % kAccTurns, and item n + 2 needs
-// operands that the storing warp loads after its wait for item n.
+// Barriers used in turn (turn_bar), as their waits are not needed for the very next phase; of the others, every
+// waiter is.
+// acc_empty, by items: the accumulators' release is waited for by the MMA warp and by the warp that stores
+// the item's gradients, which has by then loaded what the next item needs. An item of one or two tiles
+// can end before it looks; item n + 2 needs operands that it loads after its wait for item n.
 constexpr int kAccTurns = 2;
-__device__ __forceinline__ uint64_t* acc_turn(uint64_t* acc_empty, int n) { return acc_empty + n % kAccTurns; }
-__device__ __forceinline__ uint32_t acc_parity(int n) { return n / kAccTurns & 1; }
+// dQ's second half of dS, by tiles: the MMA warp has issued the next tile's scores when it waits for it, which
+// is all that the elementwise warps need to finish that tile too; the scores of tile g + 2 come after.
+constexpr int kLastHalfTurns = 2;
 
 // Publish item number n (one thread).
 __device__ __forceinline__ bool put_item(const ItemRing& r, int n, const Item& it) {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       Where out{0, 0, 0, 0};
       bool ok = true;
       auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
-        if (!mbar_wait(acc_turn(acc_empty, n), acc_parity(n), err, kErrTimeoutAttn)) return false;
+        if (!mbar_wait(turn_bar<kAccTurns>(acc_empty, n), turn_parity<kAccTurns>(n), err, kErrTimeoutAttn)) return false;
         if constexpr (!PARTIAL) {
           tma_store_4d(&map_dk, sm + L::Q + (g % QS) * L::TILE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
           tma_store_4d(&map_dv, sm + L::DO + (g % DS) * L::DSTAGE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
           if (!(ok = mbar_wait_warp(&p_half[h], g & 1, err, kErrTimeoutAttn))) break;
           // the first product of an item overwrites the accumulators: the last item's have been read
           if (h == 0 && i == 0 && n > 0 &&
-              !(ok = mbar_wait_warp(acc_turn(acc_empty, n - 1), acc_parity(n - 1), err, kErrTimeoutAttn)))
+              !(ok = mbar_wait_warp(turn_bar<kAccTurns>(acc_empty, n - 1), turn_parity<kAccTurns>(n - 1), err, kErrTimeoutAttn)))
             break;
           tc_fence_after();
 #pragma unroll
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         partial_cols<HD * 4 / EW>(tdV + tl, part * (HD * 4 / EW), p + 128 * HD, row);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_turn(acc_empty, n));
+        if (lane == 0) mbar_arrive(turn_bar<kAccTurns>(acc_empty, n));
         ++n;
         continue;
       }
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_turn(acc_empty, n));
+      if (lane == 0) mbar_arrive(turn_bar<kAccTurns>(acc_empty, n));
       ++n;
     }
   }
@@ -826,11 +826,12 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   uint64_t* v_empty = bar + 10;          // [VS]
   uint64_t* sdp_full = bar + 12;         // the tile's S and dP are complete
   uint64_t* dp_free = bar + 13;          // every warp holds its dP columns in registers
-  uint64_t* ds_half = bar + 14;          // [2]
-  uint64_t* acc_full = bar + 16;         // the item's dQ MMAs have completed
-  uint64_t* acc_empty = bar + 17;        // [kAccTurns]: every warp has read its part of dQ and staged it
-  const ItemRing ring{bar + 19, bar + 21, reinterpret_cast<Item*>(bar + 24), err};
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 23);
+  uint64_t* ds_first = bar + 14;         // every warp has written its first half of the tile's dS
+  uint64_t* ds_last = bar + 15;          // [kLastHalfTurns]: and its second
+  uint64_t* acc_full = bar + 17;         // the item's dQ MMAs have completed
+  uint64_t* acc_empty = bar + 18;        // [kAccTurns]: every warp has read its part of dQ and staged it
+  const ItemRing ring{bar + 20, bar + 22, reinterpret_cast<Item*>(bar + 25), err};
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 24);
 
   const int s = a.s, nh = a.nh;
   const int n_t = (s + 127) / 128, n_hb = nh * a.B;
@@ -858,8 +859,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     }
     mbar_init(sdp_full, 1);
     mbar_init(dp_free, EW);
-    mbar_init(&ds_half[0], EW);
-    mbar_init(&ds_half[1], EW);
+    mbar_init(ds_first, EW);
+    for (int i = 0; i < kLastHalfTurns; ++i) mbar_init(&ds_last[i], EW);
     mbar_init(acc_full, 1);
     for (int i = 0; i < kAccTurns; ++i) mbar_init(&acc_empty[i], EW);
     for (int i = 0; i < 2; ++i) {
@@ -960,7 +961,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       Where out{0, 0, 0};
       bool ok = true;
       auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
-        if (!mbar_wait(acc_turn(acc_empty, n), acc_parity(n), err, kErrTimeoutAttn)) return false;
+        if (!mbar_wait(turn_bar<kAccTurns>(acc_empty, n), turn_parity<kAccTurns>(n), err, kErrTimeoutAttn)) return false;
         tma_store_4d(&map_dq, sm + L::K + (g % KS) * L::TILE, 0, out.qt * 128, out.head * (HD / 64), out.b);
         bulk_commit();
         bulk_wait_read();
@@ -1037,10 +1038,12 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
             umma_commit_warp(sdp_full);
             if (j + 2 == total) umma_commit_warp(q_empty);
           }
-          if (!(ok = mbar_wait_warp(&ds_half[h], g & 1, err, kErrTimeoutAttn))) break;
+          if (!(ok = mbar_wait_warp(h ? turn_bar<kLastHalfTurns>(ds_last, g) : ds_first,
+                                    h ? turn_parity<kLastHalfTurns>(g) : g & 1, err, kErrTimeoutAttn)))
+            break;
           // the first product of an item overwrites the accumulator: the last item's has been read
           if (h == 0 && j == 0 && n > 0 &&
-              !(ok = mbar_wait_warp(acc_turn(acc_empty, n - 1), acc_parity(n - 1), err, kErrTimeoutAttn)))
+              !(ok = mbar_wait_warp(turn_bar<kAccTurns>(acc_empty, n - 1), turn_parity<kAccTurns>(n - 1), err, kErrTimeoutAttn)))
             break;
           tc_fence_after();
 #pragma unroll
@@ -1139,7 +1142,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ds_half[h]);
+          if (lane == 0) mbar_arrive(h ? turn_bar<kLastHalfTurns>(ds_last, g) : ds_first);
         }
       }
       if (!ok) break;
@@ -1160,7 +1163,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_turn(acc_empty, n));
+      if (lane == 0) mbar_arrive(turn_bar<kAccTurns>(acc_empty, n));
       ++n;
     }
   }

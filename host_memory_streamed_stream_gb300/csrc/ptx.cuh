@@ -77,6 +77,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
   return mbar_wait_limit(bar, parity, err, code, kWaitLimitNs);
 }
 
+// A wait tests a phase's parity, so one that comes two phases late never ends. Whoever waits for a phase has to
+// be needed for the next phase of the same barrier. Where it is needed one later only, the phases are dealt
+// in turn to several barriers: the barrier of phase n, and its parity there.
+template <int TURNS>
+__device__ __forceinline__ uint64_t* turn_bar(uint64_t* bars, int n) {
+  return bars + static_cast<uint32_t>(n) % TURNS;
+}
+template <int TURNS>
+__device__ __forceinline__ uint32_t turn_parity(int n) {
+  return static_cast<uint32_t>(n) / TURNS & 1u;
+}
+
 // Warp-uniform wait for threads that go on to warp-collective instructions (tcgen05.ld/st,
 // shuffles): every lane waits, then all lanes agree on success, so a timeout on one lane can
 // never leave the others inside a collective without it.

@@ -234,9 +234,9 @@ class DkDv(Block):
 
 
 class Dq(Block):
-    def __init__(self, walks, acc_turns):
+    def __init__(self, walks, acc_turns, last_half_turns):
         super().__init__(walks, acc_turns)
-        self.sdp, self.half = Turns(1, 1), [Turns(1, self.ELEM), Turns(1, self.ELEM)]
+        self.sdp, self.half = Turns(1, 1), [Turns(1, self.ELEM), Turns(last_half_turns, self.ELEM)]
         self.held = (self.ring1,)
 
     def walk(self, n, g0, tiles):
@@ -278,12 +278,16 @@ def _stuck(kind, lo, hi, seeds=150, **turns):
     return [s for s in range(seeds) if kind([random.Random(s).randint(lo, hi) for _ in range(12)], **turns).stuck(s)]
 
 
-@pytest.mark.parametrize("kind,lo,hi", [(DkDv, 1, 1), (DkDv, 1, 2), (DkDv, 3, 3), (DkDv, 0, 6), (Dq, 1, 1), (Dq, 0, 1)])
-def test_every_schedule_ends(kind, lo, hi):
-    assert _stuck(kind, lo, hi, acc_turns=_turns("kAccTurns")) == []
-
-
+@pytest.mark.parametrize("lo,hi", [(1, 1), (1, 2), (2, 2), (3, 3), (0, 6), (20, 30)])
 @pytest.mark.parametrize("kind", [DkDv, Dq])
-def test_one_barrier_for_the_accumulators_loses_a_phase(kind):
-    """What the turns are for: with one barrier, items of one tile get stuck under some schedules."""
-    assert _stuck(kind, 1, 1, acc_turns=1)
+def test_every_schedule_ends(kind, lo, hi):
+    turns = {"last_half_turns": _turns("kLastHalfTurns")} if kind is Dq else {}
+    assert _stuck(kind, lo, hi, 150 if hi < 20 else 30, acc_turns=_turns("kAccTurns"), **turns) == []
+
+
+@pytest.mark.parametrize("kind,lo,hi,turns", [(DkDv, 1, 1, dict(acc_turns=1)),
+                                              (Dq, 1, 1, dict(acc_turns=1, last_half_turns=2)),
+                                              (Dq, 3, 3, dict(acc_turns=2, last_half_turns=1))])
+def test_one_barrier_loses_a_phase(kind, lo, hi, turns):
+    """What the turns are for: with one barrier some schedules get stuck."""
+    assert _stuck(kind, lo, hi, **turns)
