@@ -470,6 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // warp holds this tile's dP columns in registers. dS is written as bf16 pairs over its S columns.
 // K and V come in separate rings: K three tiles deep (read by S and by dQ, and the next tile's S
 // starts early), V two deep (read only by dP, released as soon as dP has run).
+// Barriers of dS's second half, used in turn (turn_bar): when the MMA warp waits for it, it has issued the next
+// tile's scores, which is all that the elementwise warps need to finish that tile too.
+constexpr int kLastHalfTurns = 2;
 template <int HD>
 struct SmemQ {
   static constexpr int NSL = HD / 64;
@@ -506,9 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_empty = bar + 9;           // [VS]
   uint64_t* sdp_full = bar + 11;         // the tile's S and dP are complete
   uint64_t* dp_free = bar + 12;          // every warp holds its dP columns in registers
-  uint64_t* ds_half = bar + 13;          // [2]
-  uint64_t* dq_done = bar + 15;          // the last tile's dQ MMAs have completed
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 16);
+  uint64_t* ds_first = bar + 13;         // every warp has written its first half of the tile's dS
+  uint64_t* ds_last = bar + 14;          // [kLastHalfTurns]: and its second
+  uint64_t* dq_done = bar + 16;          // the last tile's dQ MMAs have completed
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 17);
 
   const int n_t = (s + 127) / 128;
   const TileSlot slot = heavy_first_slot(static_cast<int>(blockIdx.x), n_t, static_cast<int>(gridDim.x) / n_t);
@@ -531,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(sdp_full, 1);
     mbar_init(dp_free, kElemWarps);
-    mbar_init(&ds_half[0], kElemWarps);
-    mbar_init(&ds_half[1], kElemWarps);
+    mbar_init(ds_first, kElemWarps);
+    for (int i = 0; i < kLastHalfTurns; ++i) mbar_init(&ds_last[i], kElemWarps);
     mbar_init(dq_done, 1);
     fence_mbar_init();
     tma_prefetch_map(&map_q);
@@ -609,7 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = scores(j + 1, true, tdP))) break;
           umma_commit_warp(sdp_full);
         }
-        if (!(ok = mbar_wait_warp(&ds_half[h], j & 1, err, kErrTimeoutAttn))) break;
+        if (!(ok = mbar_wait_warp(h ? turn_bar<kLastHalfTurns>(ds_last, j) : ds_first,
+                                  h ? turn_parity<kLastHalfTurns>(j) : j & 1, err, kErrTimeoutAttn)))
+          break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 4 * h; kk < 4 * h + 4; ++kk)  // 16 keys per step; A (dS) from TMEM
@@ -662,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ds_half[h]);
+        if (lane == 0) mbar_arrive(h ? turn_bar<kLastHalfTurns>(ds_last, j) : ds_first);
       }
     }
     float4 rot[4 / kParts][HD / 16];

@@ -285,6 +285,12 @@ def test_every_schedule_ends(kind, lo, hi):
     assert _stuck(kind, lo, hi, 150 if hi < 20 else 30, acc_turns=_turns("kAccTurns"), **turns) == []
 
 
+def test_every_schedule_of_the_causal_dq_ends():
+    """The layer template's dQ kernel: the same roles, one item a block."""
+    turns = _turns("kLastHalfTurns", "attention_bwd_tc.cu")
+    assert not any(Dq([40], acc_turns=1, last_half_turns=turns).stuck(s) for s in range(300))
+
+
 @pytest.mark.parametrize("kind,lo,hi,turns", [(DkDv, 1, 1, dict(acc_turns=1)),
                                               (Dq, 1, 1, dict(acc_turns=1, last_half_turns=2)),
                                               (Dq, 3, 3, dict(acc_turns=2, last_half_turns=1))])
