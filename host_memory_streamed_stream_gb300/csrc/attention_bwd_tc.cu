@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   if (smem_addr(sm) & 1023) {  // the swizzled layouts need a 1024-byte aligned base
-    if (threadIdx.x == 0) atomicCAS(err, 0, kErrTimeoutAttn);
+    if (threadIdx.x == 0) record_give_up(err, kErrTimeoutAttn);
     return;
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   if (smem_addr(sm) & 1023) {  // the swizzled layouts need a 1024-byte aligned base
-    if (threadIdx.x == 0) atomicCAS(err, 0, kErrTimeoutAttn);
+    if (threadIdx.x == 0) record_give_up(err, kErrTimeoutAttn);
     return;
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);

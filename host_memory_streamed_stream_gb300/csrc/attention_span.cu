@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
   uint8_t* sm = smem_raw;
   int* err = a.err;
   if (smem_addr(sm) & 1023) {  // the swizzled layouts need a 1024-byte aligned base
-    if (threadIdx.x == 0) atomicCAS(err, 0, kErrTimeoutAttn);
+    if (threadIdx.x == 0) record_give_up(err, kErrTimeoutAttn);
     return;
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);

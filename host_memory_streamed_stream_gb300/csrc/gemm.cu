@@ -148,9 +148,9 @@ __device__ __forceinline__ void split_sources(const Params& p, int tile, int num
       __nanosleep(64);
       if (ld_acquire_u32(f) == p.epoch) break;
       if ((it & 63u) == 0) {
-        if (*reinterpret_cast<volatile int*>(p.err) != 0) break;
+        if (gave_up(p.err)) break;
         if (global_ns() - t0 > kWaitLimitNs) {
-          atomicCAS(p.err, 0, kErrTimeoutSplit);
+          record_give_up(p.err, kErrTimeoutSplit);
           break;
         }
       }

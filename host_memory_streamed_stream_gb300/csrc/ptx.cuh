@@ -8,7 +8,8 @@
 
 namespace mt {
 
-// Error codes a kernel may leave in the device error flag.
+// Error codes a kernel may leave in the device error flag. A wait's code tells the grid's other threads to give up
+// too; a bad position is a data error that stops no kernel, also not those that share the flag.
 constexpr int kErrTimeoutTmaFull = 1;    // MMA issuer waited too long for a TMA tile
 constexpr int kErrTimeoutSmemFree = 2;   // TMA producer waited too long for a free stage
 constexpr int kErrTimeoutAccFull = 3;    // epilogue waited too long for an accumulator
@@ -27,6 +28,16 @@ __device__ __forceinline__ unsigned long long global_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
+}
+
+// Whether some thread has given up a wait.
+__device__ __forceinline__ bool gave_up(const int* err) {
+  const int code = *reinterpret_cast<const volatile int*>(err);
+  return code != 0 && code != kErrBadPosition;
+}
+// Record that a wait gave up, unless another one did before.
+__device__ __forceinline__ void record_give_up(int* err, int code) {
+  if (atomicCAS(err, 0, code) == kErrBadPosition) atomicCAS(err, kErrBadPosition, code);
 }
 
 // ---------------------------------------------------------------- mbarrier
@@ -65,9 +76,9 @@ __device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, 
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 255u) == 0) {
-      if (*reinterpret_cast<volatile int*>(err) != 0) return false;
+      if (gave_up(err)) return false;
       if (global_ns() - t0 > limit_ns) {
-        atomicCAS(err, 0, code);
+        record_give_up(err, code);
         return false;
       }
     }

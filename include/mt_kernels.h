@@ -20,8 +20,11 @@
  *  - the call only enqueues work; it returns MT_OK (0), MT_EINVAL for bad
  *    sizes or alignment (nothing enqueued), or MT_ECUDA for a launch error;
  *  - `err_flag` (device int, may be NULL where unused) receives a nonzero
- *    code if a kernel's bounded internal wait gave up; it is never cleared
- *    by the library.
+ *    code if a kernel's bounded internal wait gave up (1 to 7) or a position
+ *    lay outside a rotation table (8); it is never cleared by the library.
+ *    While it holds the code of a wait, the waits of every kernel that is
+ *    given it give up early and outputs may stay unwritten. Code 8 stops
+ *    nothing, and the code of a wait replaces it.
  */
 #ifndef MT_KERNELS_H
 #define MT_KERNELS_H
@@ -291,8 +294,8 @@ int mtk_attn_block_slot(int lin, int n_tiles, int n_hb, int* rank, int* hb);
 /*
  * Self-check of the kernels' bounded waits: one thread waits, through the same wait routine the
  * GEMM and attention pipelines use, on an mbarrier phase that never completes. After limit_ns
- * (0 .. 4e9, the pipelines' own limit) it gives up, stores code 6 in *err_flag (unless a code is
- * already there), writes *gave_up = 1 and returns; no copy or MMA is in flight. This is how a
+ * (0 .. 4e9, the pipelines' own limit) it gives up, stores code 6 in *err_flag (unless a wait's code
+ * is already there), writes *gave_up = 1 and returns; no copy or MMA is in flight. This is how a
  * stalled pipeline ends instead of hanging the GPU: the host reads the flag after the step
  * (mt_train_step returns MT_EKERNEL) and the context stays usable. err_flag and gave_up are
  * device ints; the call only enqueues.

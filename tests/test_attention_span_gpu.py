@@ -403,3 +403,38 @@ def test_attention_block_of_packed_documents(K, cap, bias):
     for got, ref in ((_np(o).reshape(B, s, nh, hd), ro), (_np(dx).reshape(d.shape), d), (_np(dgq), rg[:nh].sum(0)),
                      (_np(dgk), rg[nh:].sum(0))):
         assert np.linalg.norm(got - ref) <= bound * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True)])
+def test_a_bad_position_in_the_flag_stops_no_kernel(K, cap, bias):
+    """A flag that already holds a data error (code 8): the same bits as with a clean one, the code still there."""
+    B, s, nh, nkv, hd = 2, 700, 8, 2, 128
+    rng, qkv, _, _, _, kw = _case(K, B, s, nh, nkv, hd, "docs", cap, bias, 11)
+    _, dot = _bf16(rng, (B * s, nh * hd))
+    _, w = _bf16(rng, (1000, nh * hd))
+    _, fused = _bf16(rng, (B * s, (nh + 2 * nkv) * hd))
+
+    def step(code):
+        err = torch.full((1,), code, dtype=torch.int32, device="cuda")
+        args = dict(kw, err=err)
+        o, lse = K.attn_span_fwd(*qkv, B, s, nh, nkv, hd, **args)
+        out = [o, lse, *K.attn_span_bwd(*qkv, o, lse, dot, B, s, nh, nkv, hd, **args)]
+        out.append(K.gemm(o, False, w, False, B * s, 1000, nh * hd, err=err))
+        o, lse = K.attn_fwd(fused, B, s, nh, nkv, hd, err=err)
+        out += [o, lse, K.attn_bwd(fused, o, lse, dot, B, s, nh, nkv, hd, err=err)]
+        assert int(err.item()) == code
+        return out
+
+    want = step(0)
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(step(8), want))
+
+
+def test_a_wait_that_gives_up_is_recorded_over_a_bad_position(K):
+    from host_memory_streamed_stream_gb300 import _lib
+
+    err = torch.full((1,), 8, dtype=torch.int32, device="cuda")
+    gone = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert _lib.load().mtk_bounded_wait_check(err.data_ptr(), gone.data_ptr(), 1_000_000, None) == 0
+    torch.cuda.synchronize()
+    assert int(err.item()) == 6 and int(gone.item()) == 1
