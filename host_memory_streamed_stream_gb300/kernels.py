@@ -1,7 +1,8 @@
 """Per-kernel binding (``include/mt_kernels.h``) over torch CUDA tensors: marshalling only.
 
 Each function passes the tensors' device pointers and the current torch stream
-to one C entry point and raises on a nonzero status.
+to one C entry point and raises on a nonzero status. What only the device sees goes into the flag `err`
+that a call may be given; check(err) reads it.
 """
 from __future__ import annotations
 
@@ -62,6 +63,17 @@ def gemm_use_workspace(device=None):
 
 def _err(err, dev):
     return torch.zeros(1, dtype=torch.int32, device=dev) if err is None else err
+
+
+def check(err):
+    """Wait for the calls that were given `err` (a zeroed int32 device tensor of one element) and raise
+    MTError if one of them left a code there: a wait that gave up (outputs are then invalid), or a
+    position outside its rotation table (that token is unrotated). Calls without `err` report neither.
+    """
+    code = int(err.item())
+    if code != 0:
+        raise MTError(-7, "a position outside the rotation table" if code == 8 else
+                      f"a kernel's bounded wait gave up (code {code})")
 
 
 def gemm_qkv_rope(a, w, cos_sin, seq, n_heads, n_kv_heads, head_dim, err=None):
@@ -196,7 +208,8 @@ def rotary_table(inv_freq, n_pos, amplitude=1.0, out=None):
 
 def rotary(x, heads, head_dim, cos_sin, positions=None, interleaved=False, inverse=False, out=None, err=None):
     """x [T, heads*head_dim] with the first rot_dim (the table's) columns of every head rotated at
-    `positions` (int32 [T]; None: t % n_pos). out: a new tensor, another one, or x itself (in place)."""
+    `positions` (int32 [T]; None: t % n_pos). out: a new tensor, another one, or x itself (in place).
+    A position outside the table leaves its token unrotated and a code in `err` (see check)."""
     T, cols, dev = x.shape[0], heads * head_dim, _device(x)
     ldx = _rows(x, T, cols, "x", dev)
     tab, n_pos, rot = _table(cos_sin, dev)
