@@ -281,7 +281,7 @@ struct BwdArgs {
 // steps begins.
 __device__ __forceinline__ int walk_tiles(int2 range) { return range.y < 0 ? 0 : range.y - range.x + 1; }
 __device__ __forceinline__ int part_begin(int steps, int k, int parts) {
-  return static_cast<uint32_t>(steps * k) / static_cast<uint32_t>(parts);  // steps <= 2^19, parts <= kPartItems
+  return static_cast<uint32_t>(steps * k) / static_cast<uint32_t>(parts);  // steps <= kSpanMaxWalk / 128, parts <= kPartItems
 }
 
 // P and dS of one pair of columns: scores (capped: their tanh) and dP in, P and dS out. nl = -lse2,
@@ -1256,9 +1256,9 @@ cudaError_t attn_span_bwd(const AttnSpanArgs& g, const bf16* o, int64_t ldo, con
       static_cast<double>(g.s) * 2 * lddk >= 1e12 || static_cast<double>(g.s) * 2 * lddv >= 1e12 ||
       ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(err)) & 3))
     return cudaErrorInvalidValue;
-  // the walk of one key tile, up to s/128 tiles for each of its query heads at 2 to 3 us, stays well below
-  // the limit of the waits for its end
-  if (static_cast<int64_t>(g.s) * (g.nh / g.nkv) > kSpanMaxWalk) return cudaErrorInvalidValue;
+  // the walk of one key tile, up to ceil(s/128) tiles for each of its query heads at 2 to 3 us, stays well
+  // below the limit of the waits for its end, and its steps below 2^19 (part_begin)
+  if ((static_cast<int64_t>(g.s) + 127) / 128 * 128 * (g.nh / g.nkv) > kSpanMaxWalk) return cudaErrorInvalidValue;
   struct Columns {
     const bf16* p;
     int64_t ld, cols;

@@ -161,7 +161,7 @@ cudaError_t attn_bwd(const bf16* qkv, const bf16* o, const float* lse, const bf1
 // z = scale q.k, cap > 0: z = cap tanh(z / cap), slopes: z -= slopes[head] |i - j|. q, k, v are
 // separate [B*s] row matrices with their own row strides (multiples of 8).
 constexpr int kSpanMaxSeq = 1 << 22;
-constexpr int64_t kSpanMaxWalk = int64_t{1} << 26;  // s * query heads per key head, backward
+constexpr int64_t kSpanMaxWalk = int64_t{1} << 26;  // padded s * query heads per key head, backward
 struct AttnSpanArgs {
   const bf16 *q, *k, *v;
   int64_t ldq, ldk, ldv;

@@ -269,7 +269,7 @@ int mtk_attn_bwd_rope(const void* qkv, const void* o, const void* lse, const voi
  * mtk_attn_span_bwd: dq bf16 [B*s, nh*hd], dk, dv bf16 [B*s, nkv*hd] (row strides lddq, lddk, lddv;
  *   every row is written) from dout, o and lse, deterministic, no atomics. scratch: device memory of
  *   mtk_attn_span_bwd_scratch_bytes() bytes, 16-byte aligned, not shared by calls that may run at the same
- *   time. s * (nh / nkv) <= 2^26. Gradients of slopes are not computed.
+ *   time. (s rounded up to a multiple of 128) * (nh / nkv) <= 2^26. Gradients of slopes are not computed.
  */
 int mtk_doc_spans(const int32_t* bounds, int n_docs, const int32_t* prefix, int B, int s, int32_t* lo, int32_t* hi,
                   int32_t* positions);

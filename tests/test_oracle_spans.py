@@ -140,3 +140,13 @@ def test_attn_span_refusals(lib):
     assert lib.mtk_attn_span_bwd_scratch_bytes(0, 1, 1, 1, 64) == 0
     assert lib.mtk_attn_span_bwd_scratch_bytes(1, 4194305, 1, 1, 64) == 0
     assert lib.mtk_attn_span_bwd_scratch_bytes(2, 129, 4, 2, 64) >= 2 * 4 * 256 * 8
+
+
+def test_attn_span_backward_refuses_walks_of_too_many_steps(lib):
+    """The limit on a key tile's walk counts whole tiles: one token, 2^24 query heads on one key head."""
+    at = [(i + 1) << 32 for i in range(8)]  # aligned addresses that nothing reads, no two rows overlap
+    nh, hd = 1 << 24, 64
+    q = nh * hd
+    scratch, lse, err = 1 << 40, 1 << 36, 1 << 21
+    assert lib.mtk_attn_span_bwd(at[0], q, at[1], hd, at[2], hd, None, None, at[3], q, lse, at[4], q, at[5], q, at[6], hd,
+                                 at[7], hd, scratch, 1, 1, nh, 1, hd, 0.1, 0.0, None, err, None) == -1
