@@ -41,8 +41,7 @@ def gemm(A, a_mn, B, b_mn, M, N, K, epi=EPI_STORE_BF16, R=None, err=None, out=No
     """C[M,N] = A * B (see mtk_gemm_bf16 for the operand storage orders)."""
     if out is None:
         out = torch.empty(M, N, dtype=torch.bfloat16 if epi == EPI_STORE_BF16 else torch.float32, device=A.device)
-    if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=A.device)
+    err = _err(err, A.device)
     _ok(_lib.load().mtk_gemm_bf16(A.data_ptr(), A.stride(0), int(a_mn), B.data_ptr(), B.stride(0), int(b_mn),
                                   out.data_ptr(), out.stride(0), _p(R), R.stride(0) if R is not None else 0, M, N, K,
                                   epi, err.data_ptr(), _s()), "gemm")
@@ -62,7 +61,12 @@ def gemm_use_workspace(device=None):
 
 
 def _err(err, dev):
-    return torch.zeros(1, dtype=torch.int32, device=dev) if err is None else err
+    """The flag's tensor: the caller's, or a new one that nobody reads."""
+    if err is None:
+        return torch.zeros(1, dtype=torch.int32, device=dev)
+    if err.dtype is not torch.int32 or err.numel() < 1 or err.device != dev:
+        raise MTError(-1, f"err: an int32 tensor on {dev}")
+    return err
 
 
 def check(err):
@@ -311,8 +315,7 @@ def cross_entropy(logits, labels):
 def attn_fwd(qkv, B, s, nh, nkv, hd, err=None):
     o = torch.empty(B * s, nh * hd, dtype=torch.bfloat16, device=qkv.device)
     lse = torch.empty(B, nh, s, dtype=torch.float32, device=qkv.device)
-    if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=qkv.device)
+    err = _err(err, qkv.device)
     _ok(_lib.load().mtk_attn_fwd(qkv.data_ptr(), o.data_ptr(), lse.data_ptr(), B, s, nh, nkv, hd, err.data_ptr(),
                                  _s()), "attn_fwd")
     return o, lse
@@ -322,8 +325,7 @@ def attn_bwd(qkv, o, lse, dout, B, s, nh, nkv, hd, err=None, cos_sin=None):
     """dqkv; with cos_sin (fp32 [s][hd/2][2]) dq and dk get the transpose RoPE rotation."""
     dqkv = torch.empty_like(qkv)
     delta = torch.empty(B, nh, (s + 127) // 128 * 128, 2, dtype=torch.float32, device=qkv.device)
-    if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=qkv.device)
+    err = _err(err, qkv.device)
     lib = _lib.load()
     if cos_sin is None:
         _ok(lib.mtk_attn_bwd(qkv.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(), dqkv.data_ptr(),

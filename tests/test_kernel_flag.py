@@ -28,6 +28,44 @@ def test_check(K):
             K.check(torch.tensor([code], dtype=torch.int32))
 
 
+BAD_FLAGS = [dict(dtype=torch.int64), dict(dtype=torch.float32), dict(dtype=torch.int32, device="cpu"),
+             dict(dtype=torch.int32, n=0)]
+
+
+@pytest.mark.parametrize("bad", BAD_FLAGS)
+def test_flag_refusals_on_the_host(K, bad):
+    """The kernels write to the flag through its address, so its type and device are checked before a launch."""
+    from host_memory_streamed_stream_gb300 import MTError
+
+    dev = torch.device("meta")
+    with pytest.raises(MTError, match="err"):
+        K._err(torch.zeros(bad.get("n", 1), dtype=bad["dtype"], device=bad.get("device", dev)), dev)
+    good = torch.zeros(1, dtype=torch.int32, device=dev)
+    assert K._err(good, dev) is good
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", BAD_FLAGS)
+def test_flag_refusals(K, bad):
+    from host_memory_streamed_stream_gb300 import MTError
+
+    err = torch.zeros(bad.get("n", 1), dtype=bad["dtype"], device=bad.get("device", "cuda"))
+    x = torch.zeros(8, 6 * 64, dtype=torch.bfloat16, device="cuda")
+    g = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    tab = K.rotary_table(K.rotary_inv_freq(64), 8)
+    q, k, v = x[:, :256], x[:, 256:320], x[:, 320:]
+    o, lse = K.attn_span_fwd(q, k, v, 1, 8, 4, 1, 64)
+    _, rstd = K.qk_norm_rope(x, g, g, 4, 1, 64, tab)
+    for call in (lambda: K.rotary(x, 5, 64, tab, err=err), lambda: K.qk_norm_rope(x, g, g, 4, 1, 64, tab, err=err),
+                 lambda: K.qk_norm_rope_bwd(x, x, g, g, rstd, 4, 1, 64, tab, err=err),
+                 lambda: K.attn_span_fwd(q, k, v, 1, 8, 4, 1, 64, err=err),
+                 lambda: K.attn_span_bwd(q, k, v, o, lse, o, 1, 8, 4, 1, 64, err=err),
+                 lambda: K.attn_fwd(x, 1, 8, 4, 1, 64, err=err),
+                 lambda: K.gemm(x, False, x, False, 8, 8, 384, err=err)):
+        with pytest.raises(MTError, match="err"):
+            call()
+
+
 def _example():
     """The README's attention block of packed documents."""
     with open(README) as f:
