@@ -337,13 +337,20 @@ def attn_bwd(qkv, o, lse, dout, B, s, nh, nkv, hd, err=None, cos_sin=None):
     return dqkv
 
 
+def _int32(a, what):
+    """A contiguous int32 array of the same whole numbers."""
+    a = np.asarray(a)
+    _need(a.size == 0 or (a.dtype.kind in "iu" and a.min() >= -2 ** 31 and a.max() < 2 ** 31), f"{what}: 32-bit integers")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
 def doc_spans(bounds, B, s, prefix=None):
     """(lo, hi, positions) numpy int32 [B*s] of packed documents: document d holds the tokens
     bounds[d] <= t < bounds[d+1]; prefix: how many of its first tokens all of it sees (None: causal)."""
-    bounds = np.ascontiguousarray(bounds, dtype=np.int32)
+    bounds = _int32(bounds, "bounds")
     _need(bounds.ndim == 1 and bounds.size >= 1, "bounds: n_docs + 1 token indices")
     if prefix is not None:
-        prefix = np.ascontiguousarray(prefix, dtype=np.int32)
+        prefix = _int32(prefix, "prefix")
         _need(prefix.shape == (bounds.size - 1,), "prefix: one length for each document")
     _need(B > 0 and s > 0, "B and s: positive")
     out = np.empty((3, B * s), dtype=np.int32)

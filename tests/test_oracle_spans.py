@@ -150,3 +150,19 @@ def test_attn_span_backward_refuses_walks_of_too_many_steps(lib):
     scratch, lse, err = 1 << 40, 1 << 36, 1 << 21
     assert lib.mtk_attn_span_bwd(at[0], q, at[1], hd, at[2], hd, None, None, at[3], q, lse, at[4], q, at[5], q, at[6], hd,
                                  at[7], hd, scratch, 1, 1, nh, 1, hd, 0.1, 0.0, None, err, None) == -1
+
+
+def test_doc_spans_takes_whole_numbers_of_32_bits(lib):
+    """Boundaries that a conversion to int32 would change are refused, not wrapped or cut."""
+    from host_memory_streamed_stream_gb300 import MTError, kernels as K
+
+    for bounds, prefix in ((np.array([0, 2 ** 32 + 4]), None), (np.array([0, 4], dtype=np.uint64) + 2 ** 32, None),
+                           ([0.0, 4.7], None), ([0, 4], np.array([2 ** 32 + 1])), ([0, 4], [1.5]), ([0, 2 ** 31], None),
+                           ([False, True], None)):
+        with pytest.raises(MTError):
+            K.doc_spans(bounds, 1, 8, prefix)
+    want = K.doc_spans(np.array([0, 4, 8], dtype=np.int32), 1, 8, np.array([2, 0], dtype=np.int32))
+    for dtype in (np.uint8, np.int16, np.int64):
+        got = K.doc_spans(np.array([0, 4, 8], dtype=dtype), 1, 8, [2, 0])
+        assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    assert not any(a.any() for a in K.doc_spans([3], 1, 8, []))  # no documents
