@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 17);
   Hull* hulls = reinterpret_cast<Hull*>(bar + 18);               // [4] of the softmax warps
   uint32_t* empty_rows = reinterpret_cast<uint32_t*>(bar + 26);  // [4] bit r: the warp's row r is padding
+  uint64_t* drained = bar + 28;  // the MMA warp's last products have completed
 
   const int s = a.s, nh = a.nh;
   const int n_qt = (s + 127) / 128;
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
     }
     mbar_init(pv_done, 1);
     mbar_init(o_done, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
@@ -165,19 +167,24 @@ __global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
     if (lane == 0 && n_kv > 0) {
       mbar_arrive_expect_tx(q_full, L::NSL * kSlice128);
       tma_load_4d(sm + L::Q, &map_q, q_full, 0, q0, head * (HD / 64), b);  // all head_dim slices at once
-      for (int j = 0; j < n_kv; ++j) {
+      int j = 0;
+      for (; j < n_kv; ++j) {
         const int st = j % kKStages;
         if (!mbar_wait(&k_empty[st], ((j / kKStages) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
         mbar_arrive_expect_tx(&k_full[st], L::TILE);
         tma_load_4d(sm + L::K + st * L::TILE, &map_k, &k_full[st], 0, (j0 + j) * kKeys, kvh * (HD / 64), b);
       }
+      mbar_drain(q_full, 0);
+      ring_drain<kKStages>(k_full, j);
     } else if (lane == 1) {
-      for (int j = 0; j < n_kv; ++j) {
+      int j = 0;
+      for (; j < n_kv; ++j) {
         const int st = j % kVStages;
         if (!mbar_wait(&v_empty[st], ((j / kVStages) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
         mbar_arrive_expect_tx(&v_full[st], L::TILE);
         tma_load_4d(sm + L::V + st * L::TILE, &map_v, &v_full[st], 0, (j0 + j) * kKeys, kvh * (HD / 64), b);
       }
+      ring_drain<kVStages>(v_full, j);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -218,6 +225,7 @@ __global__ void __launch_bounds__(BOUNDED ? 320 : 192, 2)
       umma_commit_warp(pv_done);
       if (j == n_kv - 1) umma_commit_warp(o_done);
     }
+    mma_drain(drained);
   } else {
     // ------------------------------------------------------------ softmax (warps 2..5, or 2..9)
     const uint32_t tl = static_cast<uint32_t>(sub * 32) << 16;

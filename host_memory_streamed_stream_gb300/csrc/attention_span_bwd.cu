@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   uint64_t* acc_empty = bar + 18;        // [kAccTurns]: every warp has read its part of dK and dV and staged it
   const ItemRing ring{bar + 20, bar + 22, reinterpret_cast<Item*>(bar + 25), err};
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 24);
-  static_assert(25 * 8 + 2 * sizeof(Item) <= 320, "barriers and item slots past their shared memory");
+  uint64_t* drained = bar + 34;          // the MMA warp's last products have completed
+  static_assert(25 * 8 + 2 * sizeof(Item) <= 34 * 8, "item slots past their shared memory");
 
   const int s = a.s, nh = a.nh, nkv = a.nkv;
   const int group = nh / nkv;
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     mbar_init(&p_half[0], EW);
     mbar_init(&p_half[1], EW);
     mbar_init(acc_full, 1);
+    mbar_init(drained, 1);
     for (int i = 0; i < kAccTurns; ++i) mbar_init(&acc_empty[i], EW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ring.full[i], 1);
@@ -432,7 +434,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       };
       Item cur = take(blockIdx.x);
       bool ok = put_item(ring, 0, cur);
-      for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
+      int g = 0;
+      for (int m = 1; ok && cur.lin >= 0; ++m) {
         const Where w = where(cur.lin);
         const int total = cur.steps, early = max(total - kTakeAhead, 0);
         Item next;
@@ -452,13 +455,15 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         }
         cur = next;
       }
+      ring_drain<QS>(q_full, g);
     }
   } else if (warp == R::kRingWarp) {
     // the dO ring with the (-lse2, -delta) pairs
     if (lane == 0) {
       Item it;
       bool ok = true;
-      for (int m = 0, g = 0; ok && get_item(ring, m, it); ++m) {
+      int g = 0;
+      for (int m = 0; ok && get_item(ring, m, it); ++m) {
         const Where w = where(it.lin);
         const int begin = PARTIAL ? it.begin : 0;
         for (int i = begin; i < begin + it.steps; ++i, ++g) {
@@ -471,6 +476,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
           bulk_load_1d(base + L::TILE, a.lsd + (static_cast<int64_t>(w.b) * nh + hq) * sp + q0, 1024, &d_full[st]);
         }
       }
+      ring_drain<DS>(d_full, g);
     }
   } else if (warp == R::kItemWarp) {
     // K and V, once per item; and the gradients of the item before, from the stages of its last tile,
@@ -509,6 +515,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         }
       }
       if (ok && stored < n) store(stored, g - 1);
+      if (n > 0) mbar_drain(kv_full, (n - 1) & 1);
       bulk_wait();
     }
   } else if (warp == 1) {
@@ -599,6 +606,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       }
       ++n;
     }
+    mma_drain(drained);
   } else {
     const int sub = warp & 3;
     const int part = (warp - 2) >> 2;  // which kCols of each 64 query columns this warp takes
@@ -832,6 +840,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
   uint64_t* acc_empty = bar + 18;        // [kAccTurns]: every warp has read its part of dQ and staged it
   const ItemRing ring{bar + 20, bar + 22, reinterpret_cast<Item*>(bar + 25), err};
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 24);
+  uint64_t* drained = bar + 34;          // the MMA warp's last products have completed
 
   const int s = a.s, nh = a.nh;
   const int n_t = (s + 127) / 128, n_hb = nh * a.B;
@@ -862,6 +871,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
     mbar_init(ds_first, EW);
     for (int i = 0; i < kLastHalfTurns; ++i) mbar_init(&ds_last[i], EW);
     mbar_init(acc_full, 1);
+    mbar_init(drained, 1);
     for (int i = 0; i < kAccTurns; ++i) mbar_init(&acc_empty[i], EW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ring.full[i], 1);
@@ -903,7 +913,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       };
       Item cur = take(blockIdx.x);
       bool ok = put_item(ring, 0, cur);
-      for (int m = 1, g = 0; ok && cur.lin >= 0; ++m) {
+      int g = 0;
+      for (int m = 1; ok && cur.lin >= 0; ++m) {
         const Where w = where(cur.lin);
         const int early = max(cur.count - kTakeAhead, 0);
         Item next;
@@ -922,12 +933,14 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         }
         cur = next;
       }
+      ring_drain<KS>(k_full, g);
     }
   } else if (warp == R::kRingWarp) {
     if (lane == 0) {  // the V ring
       Item it;
       bool ok = true;
-      for (int m = 0, g = 0; ok && get_item(ring, m, it); ++m) {
+      int g = 0;
+      for (int m = 0; ok && get_item(ring, m, it); ++m) {
         const Where w = where(it.lin);
         for (int j = 0; j < it.count; ++j, ++g) {
           const int st = g % VS;
@@ -937,6 +950,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
                       w.head / group * (HD / 64), w.b);
         }
       }
+      ring_drain<VS>(v_full, g);
     }
   } else if (warp == R::kItemWarp) {
     // Q and dO, once per item, and the gradient of the item before, from the K stage of its last tile,
@@ -986,6 +1000,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
         }
       }
       if (ok && stored < n) store(stored, g - 1);
+      if (n > 0) mbar_drain(q_full, (n - 1) & 1);
       bulk_wait();
     }
   } else if (warp == 1) {
@@ -1058,6 +1073,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       }
       ++n;
     }
+    mma_drain(drained);
   } else {
     const int sub = warp & 3;
     const int part = (warp - 2) >> 2;  // which kCols of each 64 key columns this warp takes

@@ -108,6 +108,20 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, i
   return __all_sync(0xffffffffu, ok);
 }
 
+// The end of a block whose waits may have given up: what is still in flight would land in shared or tensor memory
+// that is another block's by then. Until a phase has completed, whatever the flag holds, for 0.2 s at most.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity) && global_ns() - t0 < 200000000ull) {
+  }
+}
+// The last loads of a ring of STAGES stages, of which `issued` have been started (by the thread that starts them).
+template <int STAGES>
+__device__ __forceinline__ void ring_drain(uint64_t* full, int issued) {
+  for (int k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k) mbar_drain(&full[k % STAGES], k / STAGES & 1);
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -197,6 +211,11 @@ __device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
       " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar))
       : "memory");
+}
+// Until every MMA issued by this warp has completed (see mbar_drain); `bar` has no other use.
+__device__ __forceinline__ void mma_drain(uint64_t* bar) {
+  umma_commit_warp(bar);
+  mbar_drain(bar, 0);
 }
 // Arrive once on `bar` when every MMA issued so far by this thread has completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
