@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_half = bar + 14;           // [2]: every warp has written P^T/dS^T of that half
   uint64_t* acc_done = bar + 16;         // the last tile's accumulating MMAs have completed
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 17);
+  uint64_t* drained = bar + 18;          // the MMA warp's last products have completed
 
   const int n_t = (s + 127) / 128;
   const TileSlot slot = heavy_first_slot(static_cast<int>(blockIdx.x), n_t, static_cast<int>(gridDim.x) / n_t);
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&p_half[0], kElemWarps);
     mbar_init(&p_half[1], kElemWarps);
     mbar_init(acc_done, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
     tma_prefetch_map(&map_kv);
     tma_prefetch_map(&map_q);
@@ -286,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
       tma_load_4d(sm + L::K, &map_kv, kv_full, 0, k0, (nh + kvh) * (HD / 64), b);
       tma_load_4d(sm + L::V, &map_kv, kv_full, 0, k0, (nh + nkv + kvh) * (HD / 64), b);
-      for (int i = 0; i < total; ++i) {
+      int i = 0;
+      for (; i < total; ++i) {
         const int st = i % QS;
         const int hq = kvh * group + i / per_head;
         const int q0 = (kt + i % per_head) * 128;
@@ -294,8 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&q_full[st], L::TILE);
         tma_load_4d(sm + L::Q + st * L::TILE, &map_q, &q_full[st], 0, q0, hq * (HD / 64), b);
       }
+      mbar_drain(kv_full, 0);
+      ring_drain<QS>(q_full, i);
     } else if (lane == 1) {
-      for (int i = 0; i < total; ++i) {
+      int i = 0;
+      for (; i < total; ++i) {
         const int st = i % DS;
         const int hq = kvh * group + i / per_head;
         const int q0 = (kt + i % per_head) * 128;
@@ -305,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d(base, &map_do, &d_full[st], 0, q0, hq * (HD / 64), b);
         bulk_load_1d(base + L::TILE, lsd + (static_cast<int64_t>(b) * nh + hq) * sp + q0, 1024, &d_full[st]);
       }
+      ring_drain<DS>(d_full, i);
     }
   } else if (warp == 1) {
     // the whole warp runs the issuing loop; elect.sync picks the lane that issues each MMA
@@ -381,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit_warp(acc_done);
       }
     }
+    mma_drain(drained);
   } else {
     const int sub = warp & 3;
     const int part = (warp - 2) >> 2;  // which 32 of each 64 query columns this warp takes
@@ -513,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* ds_last = bar + 14;          // [kLastHalfTurns]: and its second
   uint64_t* dq_done = bar + 16;          // the last tile's dQ MMAs have completed
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 17);
+  uint64_t* drained = bar + 18;          // the MMA warp's last products have completed
 
   const int n_t = (s + 127) / 128;
   const TileSlot slot = heavy_first_slot(static_cast<int>(blockIdx.x), n_t, static_cast<int>(gridDim.x) / n_t);
@@ -538,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(ds_first, kElemWarps);
     for (int i = 0; i < kLastHalfTurns; ++i) mbar_init(&ds_last[i], kElemWarps);
     mbar_init(dq_done, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_do);
@@ -560,19 +570,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(q_full, 2 * L::TILE);
       tma_load_4d(sm + L::Q, &map_q, q_full, 0, q0, head * (HD / 64), b);
       tma_load_4d(sm + L::DO, &map_do, q_full, 0, q0, head * (HD / 64), b);
-      for (int j = 0; j < n_kv; ++j) {
+      int j = 0;
+      for (; j < n_kv; ++j) {
         const int st = j % KS;
         if (!mbar_wait(&k_empty[st], ((j / KS) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
         mbar_arrive_expect_tx(&k_full[st], L::TILE);
         tma_load_4d(sm + L::K + st * L::TILE, &map_kv, &k_full[st], 0, j * 128, (nh + kvh) * (HD / 64), b);
       }
+      mbar_drain(q_full, 0);
+      ring_drain<KS>(k_full, j);
     } else if (lane == 1) {
-      for (int j = 0; j < n_kv; ++j) {
+      int j = 0;
+      for (; j < n_kv; ++j) {
         const int st = j % VS;
         if (!mbar_wait(&v_empty[st], ((j / VS) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
         mbar_arrive_expect_tx(&v_full[st], L::TILE);
         tma_load_4d(sm + L::V + st * L::TILE, &map_kv, &v_full[st], 0, j * 128, (nh + nkv + kvh) * (HD / 64), b);
       }
+      ring_drain<VS>(v_full, j);
     }
   } else if (warp == 1) {
     // the whole warp runs the issuing loop; elect.sync picks the lane that issues each MMA
@@ -626,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit_warp(&k_empty[j % KS]);
       if (j == n_kv - 1) umma_commit_warp(dq_done);
     }
+    mma_drain(drained);
   } else {
     const int sub = warp & 3;
     const int part = (warp - 2) >> 2;  // which 32 of each 64 key columns this warp takes

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* pv_done = bar + 15;  // one phase per O += P_j V_j (the lazy rescale waits on it)
   uint64_t* o_done = bar + 16;   // once: every O += P_j V_j of the tile has completed
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 17);
+  uint64_t* drained = bar + 18;  // the MMA warp's last products have completed
 
   const int n_qt = (s + 127) / 128;
   const TileSlot slot = heavy_first_slot(static_cast<int>(blockIdx.x), n_qt, static_cast<int>(gridDim.x) / n_qt);
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     mbar_init(pv_done, 1);
     mbar_init(o_done, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_kv);
@@ -137,19 +139,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       mbar_arrive_expect_tx(q_full, L::NSL * kSlice128);
       tma_load_4d(sm + L::Q, &map_q, q_full, 0, q0, head * (HD / 64), b);  // all head_dim slices at once
-      for (int j = 0; j < n_kv; ++j) {
+      int j = 0;
+      for (; j < n_kv; ++j) {
         const int st = j % kKStages;
         if (!mbar_wait(&k_empty[st], ((j / kKStages) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
         mbar_arrive_expect_tx(&k_full[st], L::TILE);
         tma_load_4d(sm + L::K + st * L::TILE, &map_kv, &k_full[st], 0, j * kKeys, (nh + kvh) * (HD / 64), b);
       }
+      mbar_drain(q_full, 0);
+      ring_drain<kKStages>(k_full, j);
     } else if (lane == 1) {
-      for (int j = 0; j < n_kv; ++j) {
+      int j = 0;
+      for (; j < n_kv; ++j) {
         const int st = j % kVStages;
         if (!mbar_wait(&v_empty[st], ((j / kVStages) & 1) ^ 1u, err, kErrTimeoutAttn)) break;
         mbar_arrive_expect_tx(&v_full[st], L::TILE);
         tma_load_4d(sm + L::V + st * L::TILE, &map_kv, &v_full[st], 0, j * kKeys, (nh + nkv + kvh) * (HD / 64), b);
       }
+      ring_drain<kVStages>(v_full, j);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -191,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       umma_commit_warp(pv_done);
       if (j == n_kv - 1) umma_commit_warp(o_done);
     }
+    mma_drain(drained);
   } else {
     // ------------------------------------------------------------ softmax (warps 2..5)
     const int sub = warp & 3;

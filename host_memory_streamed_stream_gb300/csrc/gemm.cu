@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t* acc_full = bars + 2 * STAGES;   // [2]   MMA -> epilogue
   uint64_t* acc_empty = bars + 2 * STAGES + 2;  // [2] epilogue -> MMA
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+  uint64_t* drained = bars + 2 * STAGES + 5;  // the MMA warp's last products have completed
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -518,6 +519,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], EPI_WARPS);
     }
+    mbar_init(drained, 1);
     fence_mbar_init();
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int stage = 0;
+      int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
@@ -566,12 +568,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           } else {
             tma_load_2d(sb, &map_b, &full[stage], k0, n0);
           }
+          ++issued;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
+      ring_drain<STAGES>(full, issued);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -618,6 +622,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (ok) umma_commit_warp(&acc_full[acc]);
       }
+      mma_drain(drained);
     }
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9)
