@@ -30,15 +30,14 @@ __device__ __forceinline__ unsigned long long global_ns() {
   return t;
 }
 
-// Whether some thread has given up a wait.
+// Whether some thread has given up a wait: codes 1 to 7.
 __device__ __forceinline__ bool gave_up(const int* err) {
-  const int code = *reinterpret_cast<const volatile int*>(err);
-  return code != 0 && code != kErrBadPosition;
+  static_assert(kErrBadPosition == 8, "a data error is not among the waits' codes");
+  return (*reinterpret_cast<const volatile int*>(err) & 7) != 0;
 }
-// Record that a wait gave up, unless another one did before.
-__device__ __forceinline__ void record_give_up(int* err, int code) {
-  if (atomicCAS(err, 0, code) == kErrBadPosition) atomicCAS(err, kErrBadPosition, code);
-}
+// Record that a wait gave up where none did before (if several do at once, one of their codes stays). A plain
+// store: this stands in every wait, and what the attention kernels' loops hold in code costs them time.
+__device__ __forceinline__ void record_give_up(int* err, int code) { *reinterpret_cast<volatile int*>(err) = code; }
 
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
