@@ -18,8 +18,8 @@
 // Measured (head size 128): two 4096-token sequences of 32 heads, packed documents of 700 tokens on
 // average, 108 us (1.28 times the visible scores are computed in the tiles, at 890 TFLOP/s: blocks are
 // eleven tiles long, two of five tiles take the masked path, and the longest blocks end last); the same
-// sequences causal 209 us, 1310 TFLOP/s; 16384 tokens, 8/2 heads, causal 345 us, 1590 TFLOP/s, capped with
-// a prefix 600 us, 980 TFLOP/s, bound by the elementwise warps' instructions. Blocks that go on to further
+// sequences causal 209 us, 1310 TFLOP/s; 16384 tokens, 8/2 heads, causal 352 us, 1560 TFLOP/s, capped with
+// a prefix 598 us, 980 TFLOP/s, bound by the elementwise warps' instructions. Blocks that go on to further
 // items (taken over from the grid) instead of ending came out slower, 135 us for the packed documents:
 // the look-ahead costs the tile loop more than the second CTA of an SM leaves uncovered.
 #include <algorithm>

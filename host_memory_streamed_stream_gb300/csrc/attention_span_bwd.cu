@@ -25,8 +25,8 @@
 //    memory before the products that sum over them, as 0 x NaN is NaN: padding may hold anything.
 //
 // Measured (head size 128): two 4096-token sequences of 32 heads, packed documents of 700 tokens on
-// average, 343 us (delta 27, dQ 123, dK/dV 188), 7 products over 1.35 times the visible scores; 4096
-// tokens, 40/8 heads, capped, 634 us (18, 239, 378; the longest walk is 1.15 times the mean load of an SM). The
+// average, 343 to 349 us (delta 27, dQ 123, dK/dV 188), 7 products over 1.35 times the visible scores; 4096
+// tokens, 40/8 heads, capped, 635 us (18, 239, 378; the longest walk is 1.15 times the mean load of an SM). The
 // delta kernel is bound by HBM; the others keep the tensor cores 51 % (dQ) and 46 % (dK/dV) busy and wait for
 // one another's halves in turn. A tile of dK/dV moves 192 KB of operands, 64 KB of TMA writes and 845
 // wavefronts of ordinary accesses (most of them the pairs' broadcasts) through shared memory; smaller
@@ -701,8 +701,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
               dv[c] = keep ? dv[c] : 0.f;
             }
           }
-          // P^T pairs then dS^T pairs over this warp's own 16 S^T columns: the A operands of
-          // K-step cb / 16 of the accumulating MMAs
+          // P^T pairs then dS^T pairs over this warp's own kCols S^T columns, 16 at a time: the A operands of
+          // K-steps cb / 16 and on of the accumulating MMAs
 #pragma unroll
           for (int o = 0; o < kCols; o += 16) {
             store_pairs16<kCols>(ts + cb + o, sv, o);
@@ -1142,7 +1142,7 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kCols; ++c) dv[c] = vis >> c & 1u ? dv[c] : 0.f;
           }
-          // dS goes back into TMEM over this warp's S columns (A operand of K-step cb / 16)
+          // dS goes back into TMEM over this warp's S columns (A operands of K-steps cb / 16 and on)
 #pragma unroll
           for (int o = 0; o < kCols; o += 16) store_pairs16<kCols>(ts + cb + o, dv, o);
           tmem_st_wait();
@@ -1238,14 +1238,17 @@ cudaError_t launch(const AttnSpanArgs& g, const bf16* o, int64_t ldo, const floa
 // item and leaves fp32 sums, which another kernel adds. With few key tiles the longest walk is the
 // kernel's time: up to one an SM they are cut into about 512 (B 2, s 333, 4/1 heads: dK/dV 37 us in 6 blocks,
 // 14 + 4 us in 24; 4096 tokens, 32/4 heads: the whole backward 578 us in 128 items, 388 in 256, 385 in 512;
-// 8192, 16/2: 1104, 710, 691), unless the walks are too short to pay for the sums, 1 KB a key and part
-// written and read. Up to two an SM are cut in two if they are very long (256 items: 16384 tokens, 8/2
-// heads, up to 512 steps each, 1376 -> 1342 us; 4096 tokens, 40/8 heads, up to 160, 462 -> 482).
+// 8192, 16/2: 1104, 710, 691), unless more than one for two SMs are too short to pay for the sums, 1 KB a key and
+// part written and read (whole backward, 128 items of up to 16 steps 75 us, in two 86, in four 91; 32 steps 107,
+// 99, 109; 96 of up to 60 steps 162, 123, 121; 112 of up to 64, cut: 171, 132, 136). Up to two an SM are cut in
+// two if they are very long (256 items, causal: of up to 160 steps 472 us, in two 479; 256 steps 705, 696; 384
+// 1045, 1021; 512 1393 and 1359, 1353 and 1303 with 8/2 heads of 16384 tokens; 1024 2672, 2585). Both limits are
+// above where the times cross, between 16 and 32 and between 160 and 256 steps.
 static int walk_parts(int B, int s, int nh, int nkv) {
   const int group = nh / nkv;
   const int64_t n_t = pad128(s) / 128, items = n_t * nkv * B, longest = n_t * group;
-  if (items > 152) return items <= 304 && longest >= 512 && group > 1 ? 2 : 1;
-  if (items > 152 / 2 && longest < 64) return 1;
+  if (items > kSms) return items <= 2 * kSms && longest >= 512 && group > 1 ? 2 : 1;
+  if (items > kSms / 2 && longest < 64) return 1;
   return static_cast<int>(std::min<int64_t>(group, (kPartItems + items / 2) / items));
 }
 

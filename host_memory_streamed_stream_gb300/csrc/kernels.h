@@ -10,6 +10,8 @@ namespace mt {
 
 using bf16 = __nv_bfloat16;
 
+constexpr int kSms = 152;  // of a GB300, for the rules that split work by items or rows an SM
+
 // ------------------------------------------------------------------ GEMM
 // C[M,N] = A[M,K] * B[K,N] with bf16 operands and fp32 accumulation on tcgen05.
 //   a_mn = false: A stored as [M rows][K] (K contiguous, row stride lda)
@@ -136,7 +138,7 @@ cudaError_t qk_norm_rope(const bf16* x, int64_t ldx, const bf16* gq, const bf16*
                          int T, int nh, int nkv, int hd, int rot, bool interleaved, float eps,
                          const int32_t* positions, const float* cs, int n_pos, int* err, cudaStream_t s);
 // Its backward: dx (may be dy or x) and the gain gradients, through `partial` fp32 [parts][hd].
-constexpr int kQkNormParts = 304;  // blocks of the backward: two on each SM
+constexpr int kQkNormParts = 2 * kSms;  // blocks of the backward: two on each SM
 int qk_norm_rope_bwd_parts(int T, int nh, int nkv, int hd);
 cudaError_t qk_norm_rope_bwd(const bf16* dy, int64_t lddy, const bf16* x, int64_t ldx, const bf16* gq, const bf16* gk,
                              const float* rstd, bf16* dx, int64_t lddx, float* partial, bf16* dgq, bf16* dgk, int T,

@@ -152,13 +152,14 @@ struct RowSplit {
   __host__ __device__ int rows() const { return head_slots * token_slots; }
 };
 // The split that leaves the fewest threads idle over the turns; among equals the one with the most
-// turns, up to most_turns, for angles loaded once a token (two turns, for few tokens, to spread
-// them). 8192 x 64 heads rotated in 4 turns 43.1 us, in 8 44.8, in 2 45.4; 4096 x 48 heads normed in up
-// to 8 turns 24.6 us, in up to 4 28.6.
+// turns, up to most_turns, for angles loaded once a token. 8192 x 64 heads rotated in 4 turns 43.1 us, in
+// 8 44.8, in 2 45.4; 4096 x 48 heads normed in up to 8 turns 24.6 us, in up to 4 28.6. Below 16 tokens an SM
+// two turns at most, to spread them (40/8 heads, norm forward, backward: 64 tokens 10.8, 14.8 us in up to 8
+// turns, 8.7, 10.8 in two; 608 tokens 12.8, 18.9 and 10.7, 18.9; 2048 the same; 4096 27.5, 44.3 and 30, 49.7).
 RowSplit row_split(int T, int heads, int hd, int most_turns) {
   RowSplit s{hd / 16, 1, 1};
   const int slots = kRotThreads / s.units;
-  if (T < 152 * 16) most_turns = 2;
+  if (T < kSms * 16) most_turns = 2;
   double best = -1.0;
   for (int hs = heads < slots ? heads : slots; hs >= 1; --hs) {
     const int turns = (heads + hs - 1) / hs;
@@ -479,7 +480,8 @@ __global__ void __launch_bounds__(1024)
 // for every p up to the rounding of F itself (2^-53 of the frequency), where p f in fp32 would lose
 // all of it for far positions and fp64 arithmetic is slow on this part. The top 32 bits, less the
 // nearest quarter turn, convert to fp32 with an error below 2^-26 turns. The kernel is bound by
-// instructions: 131072 x 64 angles take 14 us, 4.8 TB/s, below the 20 us of the host's calls.
+// instructions (two scalar series an angle): 131072 x 64 angles take 14 us, 4.8 TB/s, below the 20 us of the
+// host's calls.
 struct TurnTable {
   uint64_t turns[kRotaryMaxPairs];
 };
@@ -576,7 +578,7 @@ cudaError_t rotary_table(const double* inv_freq, int rot, int n_pos, double amp,
   const int pairs = rot / 2;
   const dim3 threads((pairs + 1) / 2, kRotThreads / ((pairs + 1) / 2));
   const unsigned groups = (static_cast<unsigned>(n_pos) + threads.y - 1) / threads.y;
-  rotary_table_kernel<<<groups < 152 * 8 ? groups : 152 * 8, threads, 0, s>>>(f, reinterpret_cast<float2*>(out), n_pos,
+  rotary_table_kernel<<<groups < kSms * 8 ? groups : kSms * 8, threads, 0, s>>>(f, reinterpret_cast<float2*>(out), n_pos,
                                                                              pairs, static_cast<float>(amp));
   return cudaGetLastError();
 }

@@ -371,7 +371,7 @@ def attn_span_fwd(q, k, v, B, s, nh, nkv, hd, lo=None, hi=None, scale=None, cap=
     """(o, lse) of attention in which row i sees the keys lo[i] <= j < hi[i] (int32 [B*s], see
     doc_spans; None: causal). scale: 1/sqrt(hd) if None; cap: tanh cap of the scores (0: none);
     slopes: fp32 [nh], lowers the scores by slopes[h] |i - j|. q, k, v may be column ranges of
-    wider tensors."""
+    wider tensors. With a cap up to 50.5 and no slopes, v has to lie between 2^-40 and 2^40 in size, or be 0."""
     dev = _device(q)
     *ptrs, sl = _span_args(q, k, v, B, s, nh, nkv, hd, lo, hi, slopes, dev)
     if out is None:

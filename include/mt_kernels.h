@@ -127,6 +127,9 @@ int mtk_rope(void* qkv, int64_t ld, int T, int seq, int n_heads, int n_kv_heads,
  *     MTK_ROTARY_BANDS   f_i (w + (1-w)/factor), w = (n_i - low)/(high - low) clamped to [0,1],
  *                        n_i = original_positions * f_i / (2 pi) the turns over the trained
  *                        context: high frequencies kept, low ones interpolated, a ramp between
+ *                        that is linear in n_i (rules whose ramp is linear in the index i between
+ *                        the same ends give other frequencies there; pass those to
+ *                        mtk_rotary_table as they are)
  *   MT_EINVAL unless rot_dim is even, 2..256, theta > 0 and, where they are used, factor > 0,
  *   original_positions > 0 and high > low, all finite.
  * mtk_rotary_table: cos_sin f32 [n_pos][rot_dim/2][2] = amplitude * (cos, sin)(p * inv_freq[i]) for
@@ -165,7 +168,7 @@ int mtk_rotary(const void* x, int64_t ldx, void* y, int64_t ldy, int T, int head
  * n = x_h * rstd: dx_h = rstd (u g - n mean(u g n)), dgq and dgk bf16 [head_dim] = the sums of u n
  * over tokens and query (key) heads, added in a fixed order through `partial`, f32
  * [mtk_qk_norm_rope_bwd_parts(...)][head_dim]. dx may be dy or x (with the same row stride), else it
- * overlaps neither. A bad position counts as no rotation, with *err_flag set to 8.
+ * overlaps neither (these are checked; rstd, partial, dgq and dgk have to lie apart from all else). A bad position counts as no rotation, with *err_flag set to 8.
  */
 int mtk_qk_norm_rope(const void* x, int64_t ldx, const void* gq, const void* gk, void* y, int64_t ldy, void* rstd,
                      int T, int n_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved, float eps,
@@ -262,8 +265,10 @@ int mtk_attn_bwd_rope(const void* qkv, const void* o, const void* lse, const voi
  *   at t0 gets lo = t0, hi = max(t + 1, t0 + prefix[d]) up to the part's end, both inside the
  *   sequence, and position t - t0. prefix int32 [n_docs] >= 0 or NULL (0: causal; the document's
  *   length: two-sided). lo, hi int32 [B*s], positions int32 [B*s] or NULL; B*s < 2^31.
- * Outputs may be column ranges of one buffer with the inputs or each other but share no element with them
- * (MT_EINVAL).
+ * The row matrices written (o; dq, dk, dv) may be column ranges of one buffer with the ones read or each other
+ * but share no element with them: MT_EINVAL, also where they only might, their strides being different and the
+ * memory from first to last element the same. lse, lo, hi, slopes, scratch and err_flag lie apart from all that
+ * is written, which is not checked.
  * mtk_attn_span_fwd: o bf16 [B*s, nh*hd] (row stride ldo), lse f32 [B, nh, s] in mtk_attn_fwd's
  *   units (log2). err_flag: device int, required, as for all attention entries.
  * mtk_attn_span_bwd: dq bf16 [B*s, nh*hd], dk, dv bf16 [B*s, nkv*hd] (row strides lddq, lddk, lddv;

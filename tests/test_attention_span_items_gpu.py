@@ -80,3 +80,32 @@ def test_many_short_walks(K, hd, nkv, kind, cap, bias):
         _check_forward(heads[4][:, :, h], lse[:, h].contiguous(), x, *args)
         _check_backward([heads[5][:, :, h], heads[6][:, :, j], heads[7][:, :, j]], x, heads[4][:, :, h],
                         lse[:, h].contiguous(), heads[3][:, :, h], *args)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_two_streams_at_once(K, hd):
+    """Calls that overlap on the device: the blocks of one wait for the other's tensor memory, results unchanged."""
+    rng = np.random.default_rng(hd)
+    b, s, nh = 2, 1000, 24
+    streams, calls, want = [torch.cuda.Stream() for _ in range(2)], [], []
+    for cap in (0.0, 20.0):
+        q, k, v, d = (_bf16(rng, (b * s, nh * hd))[1] for _ in range(4))
+        lo, hi, _ = K.doc_spans(np.unique(np.append(rng.integers(0, b * s, 15), [0, b * s])), b, s)
+        kw = dict(lo=_i32(lo), hi=_i32(hi), cap=cap, err=torch.zeros(1, dtype=torch.int32, device="cuda"))
+
+        def call(q=q, k=k, v=v, d=d, kw=kw):
+            o, lse = K.attn_span_fwd(q, k, v, b, s, nh, nh, hd, **kw)
+            return (o, lse, *K.attn_span_bwd(q, k, v, o, lse, d, b, s, nh, nh, hd, **kw))
+
+        calls.append((call, kw["err"]))
+        want.append(call())
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for n in range(2):
+            with torch.cuda.stream(streams[n]):
+                got[n].append(calls[n][0]())
+    torch.cuda.synchronize()
+    for n in range(2):
+        K.check(calls[n][1])
+        assert all(torch.equal(a, w) for g in got[n] for a, w in zip(g, want[n]))
