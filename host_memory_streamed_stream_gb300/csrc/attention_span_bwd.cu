@@ -281,7 +281,8 @@ struct BwdArgs {
 // steps begins.
 __device__ __forceinline__ int walk_tiles(int2 range) { return range.y < 0 ? 0 : range.y - range.x + 1; }
 __device__ __forceinline__ int part_begin(int steps, int k, int parts) {
-  return static_cast<uint32_t>(steps * k) / static_cast<uint32_t>(parts);  // steps <= kSpanMaxWalk / 128, parts <= kPartItems
+  // steps <= kSpanMaxWalk / 128, k <= parts <= kPartItems
+  return static_cast<uint32_t>(steps * k) / static_cast<uint32_t>(parts);
 }
 
 // P and dS of one pair of columns: scores (capped: their tanh) and dP in, P and dS out. nl = -lse2,
@@ -486,7 +487,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       Where out{0, 0, 0, 0};
       bool ok = true;
       auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
-        if (!mbar_wait(turn_bar<kAccTurns>(acc_empty, n), turn_parity<kAccTurns>(n), err, kErrTimeoutAttn)) return false;
+        if (!mbar_wait(turn_bar<kAccTurns>(acc_empty, n), turn_parity<kAccTurns>(n), err, kErrTimeoutAttn))
+          return false;
         if constexpr (!PARTIAL) {
           tma_store_4d(&map_dk, sm + L::Q + (g % QS) * L::TILE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
           tma_store_4d(&map_dv, sm + L::DO + (g % DS) * L::DSTAGE, 0, out.kt * 128, out.kvh * (HD / 64), out.b);
@@ -582,7 +584,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
           if (!(ok = mbar_wait_warp(&p_half[h], g & 1, err, kErrTimeoutAttn))) break;
           // the first product of an item overwrites the accumulators: the last item's have been read
           if (h == 0 && i == 0 && n > 0 &&
-              !(ok = mbar_wait_warp(turn_bar<kAccTurns>(acc_empty, n - 1), turn_parity<kAccTurns>(n - 1), err, kErrTimeoutAttn)))
+              !(ok = mbar_wait_warp(turn_bar<kAccTurns>(acc_empty, n - 1), turn_parity<kAccTurns>(n - 1), err,
+                                    kErrTimeoutAttn)))
             break;
           tc_fence_after();
 #pragma unroll
@@ -975,7 +978,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
       Where out{0, 0, 0};
       bool ok = true;
       auto store = [&](int n, int g) -> bool {  // item n, which ended with tile g
-        if (!mbar_wait(turn_bar<kAccTurns>(acc_empty, n), turn_parity<kAccTurns>(n), err, kErrTimeoutAttn)) return false;
+        if (!mbar_wait(turn_bar<kAccTurns>(acc_empty, n), turn_parity<kAccTurns>(n), err, kErrTimeoutAttn))
+          return false;
         tma_store_4d(&map_dq, sm + L::K + (g % KS) * L::TILE, 0, out.qt * 128, out.head * (HD / 64), out.b);
         bulk_commit();
         bulk_wait_read();
@@ -1058,7 +1062,8 @@ __global__ void __launch_bounds__(Roles<EW>::kThreads, 1)
             break;
           // the first product of an item overwrites the accumulator: the last item's has been read
           if (h == 0 && j == 0 && n > 0 &&
-              !(ok = mbar_wait_warp(turn_bar<kAccTurns>(acc_empty, n - 1), turn_parity<kAccTurns>(n - 1), err, kErrTimeoutAttn)))
+              !(ok = mbar_wait_warp(turn_bar<kAccTurns>(acc_empty, n - 1), turn_parity<kAccTurns>(n - 1), err,
+                                    kErrTimeoutAttn)))
             break;
           tc_fence_after();
 #pragma unroll

@@ -578,8 +578,8 @@ cudaError_t rotary_table(const double* inv_freq, int rot, int n_pos, double amp,
   const int pairs = rot / 2;
   const dim3 threads((pairs + 1) / 2, kRotThreads / ((pairs + 1) / 2));
   const unsigned groups = (static_cast<unsigned>(n_pos) + threads.y - 1) / threads.y;
-  rotary_table_kernel<<<groups < kSms * 8 ? groups : kSms * 8, threads, 0, s>>>(f, reinterpret_cast<float2*>(out), n_pos,
-                                                                             pairs, static_cast<float>(amp));
+  rotary_table_kernel<<<groups < kSms * 8 ? groups : kSms * 8, threads, 0, s>>>(
+      f, reinterpret_cast<float2*>(out), n_pos, pairs, static_cast<float>(amp));
   return cudaGetLastError();
 }
 

@@ -340,7 +340,8 @@ def attn_bwd(qkv, o, lse, dout, B, s, nh, nkv, hd, err=None, cos_sin=None):
 def _int32(a, what):
     """A contiguous int32 array of the same whole numbers."""
     a = np.asarray(a)
-    _need(a.size == 0 or (a.dtype.kind in "iu" and a.min() >= -2 ** 31 and a.max() < 2 ** 31), f"{what}: 32-bit integers")
+    _need(a.size == 0 or (a.dtype.kind in "iu" and a.min() >= -2 ** 31 and a.max() < 2 ** 31),
+          f"{what}: 32-bit integers")
     return np.ascontiguousarray(a, dtype=np.int32)
 
 

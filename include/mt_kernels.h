@@ -168,7 +168,8 @@ int mtk_rotary(const void* x, int64_t ldx, void* y, int64_t ldy, int T, int head
  * n = x_h * rstd: dx_h = rstd (u g - n mean(u g n)), dgq and dgk bf16 [head_dim] = the sums of u n
  * over tokens and query (key) heads, added in a fixed order through `partial`, f32
  * [mtk_qk_norm_rope_bwd_parts(...)][head_dim]. dx may be dy or x (with the same row stride), else it
- * overlaps neither (these are checked; rstd, partial, dgq and dgk have to lie apart from all else). A bad position counts as no rotation, with *err_flag set to 8.
+ * overlaps neither (these are checked; rstd, partial, dgq and dgk have to lie apart from all else).
+ * A bad position counts as no rotation, with *err_flag set to 8.
  */
 int mtk_qk_norm_rope(const void* x, int64_t ldx, const void* gq, const void* gk, void* y, int64_t ldy, void* rstd,
                      int T, int n_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved, float eps,

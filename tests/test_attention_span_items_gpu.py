@@ -18,7 +18,8 @@ B, S, NH, CHUNK = 4, 700, 32, 4  # 768 query tiles; 4 key heads: 96 key tiles, o
 def _bounds(kind, rng):
     """Documents of the B * S tokens; those of a sequence that end before it leave padding."""
     if kind == "tiles":  # every walk is one tile, the last tile's of 60 rows
-        return np.unique(np.concatenate([np.append(np.arange(b * S, (b + 1) * S, 128), (b + 1) * S) for b in range(B)])), []
+        starts = [np.arange(b * S, (b + 1) * S, 128) for b in range(B)]
+        return np.unique(np.concatenate([*starts, [B * S]])), []
     out, dead = [], []
     for b in range(B):
         at, end = b * S, (b + 1) * S
