@@ -121,6 +121,19 @@ SIGNATURES = {
     "mtk_embed_fwd": (c_int, [c_vp, c_vp, c_vp, c_int, c_int, c_vp]),
     "mtk_embed_bwd": (c_int, [c_vp, c_vp, c_vp, c_vp, c_int, c_int, c_vp]),
     "mtk_cross_entropy": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_int, c_vp]),
+    "mtk_token_logprobs": (c_int, [c_vp, c_int, c_i64, c_vp, c_vp, c_vp, c_int, c_int, c_f32, c_vp, c_vp]),
+    "mtk_token_logprobs_bwd": (c_int, [c_vp, c_int, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_int, c_int, c_f32, c_vp]),
+    "mtk_policy_loss": (c_int, [c_vp, c_int, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_f32, c_f32, c_f32, c_f32, c_vp,
+                                c_i64, c_vp, c_vp, c_vp, c_int, c_int, c_vp, c_vp]),
+    "mtk_preference_loss": (c_int, [c_vp, c_vp, c_vp, c_vp, c_int, c_int, c_int, c_f32, c_f32, c_f32, c_int, c_vp,
+                                    c_vp, c_vp, c_vp, c_vp]),
+    "mtk_layernorm_fwd": (c_int, [c_vp, c_int, c_i64, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_int, c_int, c_f32, c_vp]),
+    "mtk_layernorm_bwd_parts": (c_int, [c_int, c_int]),
+    "mtk_layernorm_bwd": (c_int, [c_vp, c_int, c_i64, c_vp, c_int, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp,
+                                  c_vp, c_vp, c_vp, c_int, c_int, c_vp]),
+    "mtk_embed_lookup": (c_int, [c_vp, c_vp, c_vp, c_int, c_int, c_int, c_int, c_f32, c_vp, c_vp]),
+    "mtk_embed_lookup_bwd_scratch_bytes": (c_u64, [c_int, c_int]),
+    "mtk_embed_lookup_bwd": (c_int, [c_vp, c_vp, c_int, c_vp, c_vp, c_int, c_int, c_int, c_f32, c_int, c_vp, c_vp]),
     "mtk_attn_fwd": (c_int, [c_vp, c_vp, c_vp, c_int, c_int, c_int, c_int, c_int, c_vp, c_vp]),
     "mtk_attn_bwd": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_int, c_int, c_int, c_int, c_vp, c_vp]),
     "mtk_attn_bwd_rope": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_int, c_int, c_int, c_int, c_vp,

@@ -235,6 +235,75 @@ int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, voi
   return rc(mt::mean_reduce(static_cast<const float*>(row_loss), T, static_cast<float*>(loss), S(stream)));
 }
 
+int mtk_token_logprobs(const void* logits, int type, int64_t ld, const void* labels, void* logp, void* lse, int T,
+                       int V, float scale, int* err_flag, void* stream) {
+  return rc(mt::token_logprobs(logits, type, ld, static_cast<const int32_t*>(labels), static_cast<float*>(logp),
+                               static_cast<float*>(lse), T, V, scale, err_flag, S(stream)));
+}
+
+int mtk_token_logprobs_bwd(const void* logits, int type, int64_t ld, const void* labels, const void* lse,
+                           const void* dlogp, void* dlogits, int64_t ldd, int T, int V, float scale, void* stream) {
+  return rc(mt::token_logprobs_bwd(logits, type, ld, static_cast<const int32_t*>(labels),
+                                   static_cast<const float*>(lse), static_cast<const float*>(dlogp),
+                                   static_cast<bf16*>(dlogits), ldd, T, V, scale, S(stream)));
+}
+
+int mtk_policy_loss(const void* logits, int type, int64_t ld, const void* labels, const void* old_logp,
+                    const void* advantages, const void* ref_logp, const void* weights, float clip_low, float clip_high,
+                    float kl, float scale, void* dlogits, int64_t ldd, void* logp, void* row_loss, void* loss, int T,
+                    int V, int* err_flag, void* stream) {
+  return rc(mt::policy_loss(logits, type, ld, static_cast<const int32_t*>(labels),
+                            static_cast<const float*>(old_logp), static_cast<const float*>(advantages),
+                            static_cast<const float*>(ref_logp), static_cast<const float*>(weights), clip_low,
+                            clip_high, kl, scale, static_cast<bf16*>(dlogits), ldd, static_cast<float*>(logp),
+                            static_cast<float*>(row_loss), static_cast<float*>(loss), T, V, err_flag, S(stream)));
+}
+
+int mtk_preference_loss(const void* logp, const void* ref_logp, const void* labels, const void* bounds, int pairs,
+                        int T, int kind, float beta, float margin, float smoothing, int average, void* pair_loss,
+                        void* loss, void* rewards, void* dlogp, void* stream) {
+  return rc(mt::preference_loss(static_cast<const float*>(logp), static_cast<const float*>(ref_logp),
+                                static_cast<const int32_t*>(labels), static_cast<const int32_t*>(bounds), pairs, T,
+                                kind, beta, margin, smoothing, average != 0, static_cast<float*>(pair_loss),
+                                static_cast<float*>(loss), static_cast<float*>(rewards), static_cast<float*>(dlogp),
+                                S(stream)));
+}
+
+int mtk_layernorm_fwd(const void* x, int type, int64_t ldx, const void* gamma, const void* beta, void* y, int64_t ldy,
+                      void* mean, void* rstd, int T, int h, float eps, void* stream) {
+  return rc(mt::layernorm_fwd(x, type, ldx, static_cast<const bf16*>(gamma), static_cast<const bf16*>(beta),
+                              static_cast<bf16*>(y), ldy, static_cast<float*>(mean), static_cast<float*>(rstd), T, h,
+                              eps, S(stream)));
+}
+
+int mtk_layernorm_bwd_parts(int T, int h) { return mt::layernorm_bwd_parts(T, h); }
+
+int mtk_layernorm_bwd(const void* dy, int dy_type, int64_t lddy, const void* x, int type, int64_t ldx,
+                      const void* gamma, const void* mean, const void* rstd, const void* dres, int64_t lddres,
+                      void* dx, void* dx_bf16, void* partial, void* dgamma, void* dbeta, int T, int h, void* stream) {
+  return rc(mt::layernorm_bwd(dy, dy_type, lddy, x, type, ldx, static_cast<const bf16*>(gamma),
+                              static_cast<const float*>(mean), static_cast<const float*>(rstd), dres, lddres, dx,
+                              static_cast<bf16*>(dx_bf16), static_cast<float*>(partial), static_cast<bf16*>(dgamma),
+                              static_cast<bf16*>(dbeta), T, h, S(stream)));
+}
+
+int mtk_embed_lookup(const void* tok, const void* E, void* x, int type, int T, int h, int V, float scale,
+                     int* err_flag, void* stream) {
+  return rc(mt::embed_lookup(static_cast<const int32_t*>(tok), static_cast<const bf16*>(E), x, type, T, h, V, scale,
+                             err_flag, S(stream)));
+}
+
+uint64_t mtk_embed_lookup_bwd_scratch_bytes(int T, int h) {
+  if (T <= 0 || T > mt::kEmbedMaxTokens || h <= 0 || h > mt::kEmbedMaxWidth) return 0;
+  return mt::embed_lookup_bwd_scratch(T, h);
+}
+
+int mtk_embed_lookup_bwd(const void* tok, const void* dx, int type, void* dE, void* scratch, int T, int h, int V,
+                         float scale, int accumulate, int* err_flag, void* stream) {
+  return rc(mt::embed_lookup_bwd(static_cast<const int32_t*>(tok), dx, type, static_cast<bf16*>(dE), scratch, T, h, V,
+                                 scale, accumulate != 0, err_flag, S(stream)));
+}
+
 int mtk_attn_fwd(const void* qkv, void* o, void* lse, int B, int s, int nh, int nkv, int head_dim, int* err_flag,
                  void* stream) {
   if (!qkv || !o || !lse || !err_flag || B <= 0 || s <= 0) return MT_EINVAL;

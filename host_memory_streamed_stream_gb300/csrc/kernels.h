@@ -145,6 +145,42 @@ cudaError_t qk_norm_rope_bwd(const bf16* dy, int64_t lddy, const bf16* x, int64_
                              int nh, int nkv, int hd, int rot, bool interleaved, const int32_t* positions,
                              const float* cs, int n_pos, int* err, cudaStream_t s);
 
+// ------------------------------------------------------------------ losses on given tokens
+// Rules, checks and formulas: mtk_token_logprobs, mtk_policy_loss and mtk_preference_loss. type: MTK_F32 or
+// MTK_BF16 logits, ld and ldd multiples of 8.
+cudaError_t token_logprobs(const void* logits, int type, int64_t ld, const int32_t* labels, float* logp, float* lse,
+                           int T, int V, float scale, int* err, cudaStream_t s);
+cudaError_t token_logprobs_bwd(const void* logits, int type, int64_t ld, const int32_t* labels, const float* lse,
+                               const float* dlogp, bf16* dlogits, int64_t ldd, int T, int V, float scale,
+                               cudaStream_t s);
+cudaError_t policy_loss(const void* logits, int type, int64_t ld, const int32_t* labels, const float* old_logp,
+                        const float* adv, const float* ref, const float* weights, float clip_low, float clip_high,
+                        float kl, float scale, bf16* dlogits, int64_t ldd, float* logp, float* row_loss, float* loss,
+                        int T, int V, int* err, cudaStream_t s);
+constexpr int kPreferenceMaxPairs = 1 << 20;
+cudaError_t preference_loss(const float* logp, const float* ref, const int32_t* labels, const int32_t* bounds,
+                            int pairs, int T, int kind, float beta, float margin, float smoothing, bool average,
+                            float* pair_loss, float* loss, float* rewards, float* dlogp, cudaStream_t s);
+
+// ------------------------------------------------------------------ layer norm
+// Rows of type x_type (dres and dx too) and dy_type; partial fp32 [layernorm_bwd_parts()][2][h].
+constexpr int kLayerNormMaxWidth = 16384;
+cudaError_t layernorm_fwd(const void* x, int type, int64_t ldx, const bf16* gamma, const bf16* beta, bf16* y,
+                          int64_t ldy, float* mean, float* rstd, int T, int h, float eps, cudaStream_t s);
+int layernorm_bwd_parts(int T, int h);
+cudaError_t layernorm_bwd(const void* dy, int dy_type, int64_t lddy, const void* x, int type, int64_t ldx,
+                          const bf16* gamma, const float* mean, const float* rstd, const void* dres, int64_t lddres,
+                          void* dx, bf16* dx_bf16, float* partial, bf16* dgamma, bf16* dbeta, int T, int h,
+                          cudaStream_t s);
+
+// ------------------------------------------------------------------ embedding with scale, gradient by sorted tokens
+constexpr int kEmbedMaxTokens = 1 << 26, kEmbedMaxVocab = 1 << 24, kEmbedMaxWidth = 65536;
+cudaError_t embed_lookup(const int32_t* tok, const bf16* E, void* x, int type, int T, int h, int V, float scale,
+                         int* err, cudaStream_t s);
+uint64_t embed_lookup_bwd_scratch(int T, int h);
+cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16* dE, void* scratch, int T, int h,
+                             int V, float scale, bool add, int* err, cudaStream_t s);
+
 // ------------------------------------------------------------------ attention
 // Causal grouped-query flash attention over qkv [B*s, (nh + 2 nkv) hd] (q | k | v columns,
 // RoPE already applied). o bf16 [B*s, nh*hd]; lse fp32 [B, nh, s] in base-2 units of the

@@ -9,7 +9,7 @@
 namespace mt {
 
 // Error codes a kernel may leave in the device error flag. A wait's code tells the grid's other threads to give up
-// too; a bad position is a data error that stops no kernel, also not those that share the flag.
+// too; a bad position or token is a data error that stops no kernel, also not those that share the flag.
 constexpr int kErrTimeoutTmaFull = 1;    // MMA issuer waited too long for a TMA tile
 constexpr int kErrTimeoutSmemFree = 2;   // TMA producer waited too long for a free stage
 constexpr int kErrTimeoutAccFull = 3;    // epilogue waited too long for an accumulator
@@ -18,6 +18,7 @@ constexpr int kErrTimeoutAttn = 5;       // an attention pipeline wait gave up
 constexpr int kErrTimeoutProbe = 6;      // the wait-expiry self-check gave up (as it is meant to)
 constexpr int kErrTimeoutSplit = 7;      // a GEMM tile's owner waited too long for a partial sum
 constexpr int kErrBadPosition = 8;       // a token's position lies outside the rotation table
+constexpr int kErrBadToken = 16;         // a token id or label lies outside the vocabulary
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;  // 4 s: far above any legal wait
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -32,7 +33,7 @@ __device__ __forceinline__ unsigned long long global_ns() {
 
 // Whether some thread has given up a wait: codes 1 to 7.
 __device__ __forceinline__ bool gave_up(const int* err) {
-  static_assert(kErrBadPosition == 8, "a data error is not among the waits' codes");
+  static_assert(kErrBadPosition == 8 && kErrBadToken == 16, "a data error is not among the waits' codes");
   return (*reinterpret_cast<const volatile int*>(err) & 7) != 0;
 }
 // Record that a wait gave up where none did before (if several do at once, one of their codes stays). A plain

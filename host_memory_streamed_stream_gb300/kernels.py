@@ -15,6 +15,8 @@ import torch
 from . import MTError, _lib
 
 EPI_STORE_BF16, EPI_STORE_F32, EPI_ADD_F32 = 0, 1, 2
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "square": 2}
+ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 
 
@@ -71,13 +73,14 @@ def _err(err, dev):
 
 def check(err):
     """Wait for the calls that were given `err` (a zeroed int32 device tensor of one element) and raise
-    MTError if one of them left a code there: a wait that gave up (outputs are then invalid), or a
-    position outside its rotation table (that token is unrotated). Calls without `err` report neither.
+    MTError if one of them left a code there: a wait that gave up (outputs are then invalid), a
+    position outside its rotation table (that token is unrotated), or a token id or label outside the
+    vocabulary (that row counts as padding). Calls without `err` report none of them.
     """
     code = int(err.item())
     if code != 0:
-        raise MTError(-7, "a position outside the rotation table" if code == 8 else
-                      f"a kernel's bounded wait gave up (code {code})")
+        raise MTError(-7, {8: "a position outside the rotation table", 16: "a token id outside the vocabulary"}.get(
+            code, f"a kernel's bounded wait gave up (code {code})"))
 
 
 def gemm_qkv_rope(a, w, cos_sin, seq, n_heads, n_kv_heads, head_dim, err=None):
@@ -310,6 +313,187 @@ def cross_entropy(logits, labels):
     _ok(_lib.load().mtk_cross_entropy(logits.data_ptr(), labels.data_ptr(), dl.data_ptr(), rl.data_ptr(),
                                       loss.data_ptr(), T, V, _s()), "cross_entropy")
     return loss, rl, dl
+
+
+def _typed_rows(t, n, cols, what, dev):
+    """(pointer, type, row stride) of an fp32 or bf16 [n, cols] tensor with unit column stride."""
+    shape, stride = t.shape, t.stride()
+    kind = ROW_TYPES.get(t.dtype)
+    if (kind is None or len(shape) != 2 or shape[0] != n or shape[1] != cols or stride[1] != 1 and cols > 1
+            or t.get_device() != dev):
+        raise MTError(-1, f"{what}: an fp32 or bf16 [{n}, {cols}] tensor with unit column stride on cuda:{dev}")
+    return t.data_ptr(), kind, stride[0] if n > 1 else (cols + 7) // 8 * 8
+
+
+def _opt(t, n, dtype, what, dev):
+    return None if t is None else _vec(t, n, dtype, what, dev)
+
+
+def _flag(err, dev):
+    """Address of the caller's flag (None: nothing is reported)."""
+    if err is None:
+        return None
+    if err.dtype is not torch.int32 or err.numel() < 1 or err.get_device() != dev:
+        raise MTError(-1, f"err: an int32 tensor on cuda:{dev}")
+    return err.data_ptr()
+
+
+def _logits(logits, labels):
+    """(device, T, V, pointer, type, row stride, labels' pointer)"""
+    _need(logits.dim() == 2, "logits: [T, V]")
+    dev = _device(logits)
+    T, V = logits.shape
+    return (dev, T, V, *_typed_rows(logits, T, V, "logits", dev), _vec(labels, T, torch.int32, "labels", dev))
+
+
+def _grad_rows(out, T, V, dev):
+    """dlogits and its row stride: the caller's, or new rows a multiple of 8 columns apart."""
+    if out is None:
+        ld = (V + 7) // 8 * 8
+        out = torch.empty((T, ld), dtype=torch.bfloat16, device=torch.device("cuda", dev))
+        return (out if ld == V else out[:, :V]), ld
+    ptr, kind, ld = _typed_rows(out, T, V, "out", dev)
+    _need(kind == 1, "out: bf16")
+    return out, ld
+
+
+def token_logprobs(logits, labels, scale=1.0, err=None):
+    """(logp, lse) f32 [T]: the log-probability of each row's label (int32; < 0: not trained, 0) under
+    softmax(scale * logits), logits f32 or bf16 [T, V] with a row stride that is a multiple of 8, and the
+    log of the softmax's sum. A label >= V leaves a code in `err` (see check)."""
+    dev, T, V, z, kind, ld, lab = _logits(logits, labels)
+    logp, lse = (torch.empty(T, dtype=torch.float32, device=logits.device) for _ in range(2))
+    _ok(_lib.load().mtk_token_logprobs(z, kind, ld, lab, logp.data_ptr(), lse.data_ptr(), T, V, scale,
+                                       _flag(err, dev), _stream(dev)), "token_logprobs")
+    return logp, lse
+
+
+def token_logprobs_bwd(logits, labels, lse, dlogp, scale=1.0, out=None):
+    """dlogits bf16 [T, V] of token_logprobs from dlogp f32 [T]; out: another tensor, or bf16 logits themselves."""
+    dev, T, V, z, kind, ld, lab = _logits(logits, labels)
+    out, ldd = _grad_rows(out, T, V, dev)
+    _ok(_lib.load().mtk_token_logprobs_bwd(z, kind, ld, lab, _vec(lse, T, torch.float32, "lse", dev),
+                                           _vec(dlogp, T, torch.float32, "dlogp", dev), out.data_ptr(), ldd, T, V,
+                                           scale, _stream(dev)), "token_logprobs_bwd")
+    return out
+
+
+def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, weights=None, clip_low=0.2, clip_high=0.2,
+                kl=0.0, scale=1.0, out=None, err=None):
+    """(loss [1], row_loss [T], logp [T], dlogits bf16 [T, V]) of the clipped policy loss with a KL term (see
+    mtk_policy_loss): row_loss = w (-min(r A, clip(r) A) + kl (exp(ref - logp) - (ref - logp) - 1)), r = exp(logp -
+    old_logp), w = weights (None: 1/T). logits, labels, scale as for token_logprobs; out as for its backward."""
+    dev, T, V, z, kind, ld, lab = _logits(logits, labels)
+    out, ldd = _grad_rows(out, T, V, dev)
+    logp, row_loss = (torch.empty(T, dtype=torch.float32, device=logits.device) for _ in range(2))
+    loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+    f32 = torch.float32
+    _ok(_lib.load().mtk_policy_loss(z, kind, ld, lab, _vec(old_logp, T, f32, "old_logp", dev),
+                                    _vec(advantages, T, f32, "advantages", dev), _opt(ref_logp, T, f32, "ref_logp", dev),
+                                    _opt(weights, T, f32, "weights", dev), clip_low, clip_high, kl, scale,
+                                    out.data_ptr(), ldd, logp.data_ptr(), row_loss.data_ptr(), loss.data_ptr(), T, V,
+                                    _flag(err, dev), _stream(dev)), "policy_loss")
+    return loss, row_loss, logp, out
+
+
+def preference_loss(logp, bounds, labels=None, ref_logp=None, kind="sigmoid", beta=0.1, margin=0.0, smoothing=0.0,
+                    average=False):
+    """(loss [1], rewards [2 pairs], dlogp [T]) of pairs of sequences (2i preferred over 2i + 1), sequence j the rows
+    bounds[j] <= t < bounds[j+1] (device int32 [2 pairs + 1]) with labels >= 0. kind: "sigmoid", "hinge" or "square" of
+    h = beta (s_2i - s_2i+1) - margin, s the sums (average: means) of logp - ref_logp; see mtk_preference_loss."""
+    if kind not in PREFERENCE_KINDS:
+        raise MTError(-1, f"kind: one of {sorted(PREFERENCE_KINDS)}")
+    dev, f32 = _device(logp), torch.float32
+    T, n = logp.numel(), bounds.numel() - 1
+    _need(n > 0 and n % 2 == 0, "bounds: 2 pairs + 1 row indices")
+    pair_loss, rewards, dlogp = (torch.empty(k, dtype=f32, device=logp.device) for k in (n // 2 + 1, n, T))
+    loss = pair_loss[n // 2:]
+    _ok(_lib.load().mtk_preference_loss(_vec(logp, T, f32, "logp", dev), _opt(ref_logp, T, f32, "ref_logp", dev),
+                                        _opt(labels, T, torch.int32, "labels", dev),
+                                        _vec(bounds, n + 1, torch.int32, "bounds", dev), n // 2, T,
+                                        PREFERENCE_KINDS[kind], beta, margin, smoothing, int(average),
+                                        pair_loss.data_ptr(), loss.data_ptr(), rewards.data_ptr(), dlogp.data_ptr(),
+                                        _stream(dev)), "preference_loss")
+    return loss, rewards, dlogp
+
+
+def layernorm_fwd(x, gamma, beta=None, eps=1e-5, out=None):
+    """(y bf16 [T, h], mean [T], rstd [T]) of the layer norm of x, f32 or bf16 [T, h] with a row stride that is a
+    multiple of 8; gamma and beta (None: 0) bf16 [h]. out: another tensor for y."""
+    _need(x.dim() == 2, "x: [T, h]")
+    dev = _device(x)
+    T, h = x.shape
+    px, kind, ldx = _typed_rows(x, T, h, "x", dev)
+    if out is None:
+        out = torch.empty((T, h), dtype=torch.bfloat16, device=x.device)
+    py, ykind, ldy = _typed_rows(out, T, h, "out", dev)
+    _need(ykind == 1, "out: bf16")
+    mean, rstd = (torch.empty(T, dtype=torch.float32, device=x.device) for _ in range(2))
+    _ok(_lib.load().mtk_layernorm_fwd(px, kind, ldx, _vec(gamma, h, torch.bfloat16, "gamma", dev),
+                                      _opt(beta, h, torch.bfloat16, "beta", dev), py, ldy, mean.data_ptr(),
+                                      rstd.data_ptr(), T, h, eps, _stream(dev)), "layernorm_fwd")
+    return out, mean, rstd
+
+
+def layernorm_bwd(dy, x, gamma, mean, rstd, dres=None, bias=True):
+    """(dx, dx_bf16, dgamma, dbeta) of layernorm_fwd: dx of x's type, with dres (of x's type, or None) added; dx_bf16
+    the same rounded (None for bf16 rows); dbeta None without `bias`. dy f32 or bf16."""
+    _need(x.dim() == 2, "x: [T, h]")
+    dev = _device(x)
+    T, h = x.shape
+    px, kind, ldx = _typed_rows(x, T, h, "x", dev)
+    pdy, dy_kind, lddy = _typed_rows(dy, T, h, "dy", dev)
+    pres, res_kind, ldres = (None, kind, 0) if dres is None else _typed_rows(dres, T, h, "dres", dev)
+    _need(res_kind == kind, "dres: of x's type")
+    lib = _lib.load()
+    dx = torch.empty((T, h), dtype=x.dtype, device=x.device)
+    dxb = torch.empty((T, h), dtype=torch.bfloat16, device=x.device) if kind == 0 else None
+    partial = torch.empty(2 * h * lib.mtk_layernorm_bwd_parts(T, h), dtype=torch.float32, device=x.device)
+    dg = torch.empty(h, dtype=torch.bfloat16, device=x.device)
+    db = torch.empty(h, dtype=torch.bfloat16, device=x.device) if bias else None
+    _ok(lib.mtk_layernorm_bwd(pdy, dy_kind, lddy, px, kind, ldx, _vec(gamma, h, torch.bfloat16, "gamma", dev),
+                              _vec(mean, T, torch.float32, "mean", dev), _vec(rstd, T, torch.float32, "rstd", dev),
+                              pres, ldres, dx.data_ptr(), _p(dxb), partial.data_ptr(), dg.data_ptr(), _p(db), T, h,
+                              _stream(dev)), "layernorm_bwd")
+    return dx, dxb, dg, db
+
+
+def _table_rows(t, what, dev, types=ROW_TYPES):
+    """(rows, columns, type) of a contiguous matrix."""
+    _need(t.dim() == 2 and t.dtype in types and t.is_contiguous() and t.get_device() == dev,
+          f"{what}: a contiguous matrix on cuda:{dev} of {' or '.join(str(d) for d in types)}")
+    return t.shape[0], t.shape[1], ROW_TYPES[t.dtype]
+
+
+def embed_lookup(tok, E, scale=1.0, dtype=torch.float32, err=None):
+    """x [T, h] of `dtype` (f32 or bf16) = scale * E[tok], E bf16 [V, h], tok int32 [T]: < 0 is padding (a row of
+    zeros); an id >= V counts as padding and leaves a code in `err` (see check)."""
+    dev, T = _device(E), tok.numel()
+    V, h, _ = _table_rows(E, "E", dev, (torch.bfloat16,))
+    _need(dtype in ROW_TYPES, "dtype: f32 or bf16")
+    x = torch.empty((T, h), dtype=dtype, device=E.device)
+    _ok(_lib.load().mtk_embed_lookup(_vec(tok, T, torch.int32, "tok", dev), E.data_ptr(), x.data_ptr(),
+                                     ROW_TYPES[dtype], T, h, V, scale, _flag(err, dev), _stream(dev)), "embed_lookup")
+    return x
+
+
+def embed_lookup_bwd(tok, dx, V, scale=1.0, accumulate=None, err=None):
+    """dE bf16 [V, h] of embed_lookup from dx f32 or bf16 [T, h], the same from run to run. accumulate: a dE to add to (its
+    rows of no token stay), such as the gradient of a head that shares the table."""
+    dev, T = _device(dx), tok.numel()
+    rows, h, kind = _table_rows(dx, "dx", dev)
+    _need(rows == T, "dx: one row for each token")
+    dE = accumulate
+    if dE is None:
+        dE = torch.empty((V, h), dtype=torch.bfloat16, device=dx.device)
+    else:
+        _need(_table_rows(dE, "accumulate", dev, (torch.bfloat16,))[:2] == (V, h), "accumulate: [V, h]")
+    lib = _lib.load()
+    scratch = torch.empty(lib.mtk_embed_lookup_bwd_scratch_bytes(T, h), dtype=torch.uint8, device=dx.device)
+    _ok(lib.mtk_embed_lookup_bwd(_vec(tok, T, torch.int32, "tok", dev), dx.data_ptr(), kind, dE.data_ptr(),
+                                 scratch.data_ptr(), T, h, V, scale, int(accumulate is not None), _flag(err, dev),
+                                 _stream(dev)), "embed_lookup_bwd")
+    return dE
 
 
 def attn_fwd(qkv, B, s, nh, nkv, hd, err=None):

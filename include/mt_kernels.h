@@ -20,11 +20,12 @@
  *  - the call only enqueues work; it returns MT_OK (0), MT_EINVAL for bad
  *    sizes or alignment (nothing enqueued), or MT_ECUDA for a launch error;
  *  - `err_flag` (device int, may be NULL where unused) receives a nonzero
- *    code if a kernel's bounded internal wait gave up (1 to 7) or a position
- *    lay outside a rotation table (8); it is never cleared by the library.
+ *    code if a kernel's bounded internal wait gave up (1 to 7), a position
+ *    lay outside a rotation table (8) or a token id outside the vocabulary
+ *    (16); it is never cleared by the library.
  *    While it holds the code of a wait, the waits of every kernel that is
- *    given it give up early and outputs may stay unwritten. Code 8 stops
- *    nothing, and the code of a wait replaces it.
+ *    given it give up early and outputs may stay unwritten. Codes 8 and 16
+ *    stop nothing, and the code of a wait replaces them.
  */
 #ifndef MT_KERNELS_H
 #define MT_KERNELS_H
@@ -219,6 +220,90 @@ int mtk_embed_bwd(const void* order, const void* offsets, const void* dx, void* 
  */
 int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, void* row_loss, void* loss, int T, int V,
                       void* stream);
+
+/* Element types of the entries below that take more than one. */
+#define MTK_F32 0
+#define MTK_BF16 1
+
+/*
+ * Log-probabilities of given tokens and the losses of fine-tuning on them, beside the cross-entropy. (The pages name no
+ * such objective.) logits [T, V] of `type` with row stride ld (a multiple of 8; V may be any size: columns
+ * past V are neither read nor written), labels int32 [T], scale a > 0 (one over the temperature):
+ *   lse_t = log sum_v exp(a z_tv),  logp_t = a z_t,label - lse_t,  p_tv = exp(a z_tv - lse_t).
+ * A label < 0 marks a row that is not trained (a prompt, padding): nothing of its logits is read, its outputs
+ * are 0. A label >= V counts as one and sets *err_flag (device int or NULL) to 16. Logits may be -inf; a row
+ * with NaN, +inf or nothing but -inf gives NaN, as does a label whose logit is -inf (logp = -inf, and NaN where a
+ * loss takes differences of it).
+ *
+ * mtk_token_logprobs: logp f32 [T] and lse f32 [T].
+ * mtk_token_logprobs_bwd: dlogits bf16 [T, V] (row stride ldd) = a dlogp_t ([v = label] - p_tv) from dlogp f32 [T]
+ *   and the forward's lse. dlogits may be the bf16 logits themselves (the same address and stride), else they
+ *   must not overlap (MT_EINVAL).
+ * mtk_policy_loss: the clipped policy loss with a KL term, loss and gradient in one call. With
+ *   r = exp(logp - old_logp), A = advantages, w = weights (f32 [T]; NULL: 1/T for every row):
+ *     l_t = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(ref - logp) - (ref - logp) - 1)
+ *     loss = sum_t w l,  dlogits = w l' a ([v = label] - p),  l' = -(r A where r A is the smaller) + kl (1 - exp(ref - logp)).
+ *   old_logp, advantages, ref_logp f32 [T] (ref_logp may be NULL where kl = 0); 0 <= clip_low <= 1,
+ *   clip_high >= 0, kl >= 0. Writes logp f32 [T], row_loss f32 [T] = w l, loss f32 [1] and dlogits (as above).
+ *   The sum runs in a fixed order.
+ * mtk_preference_loss: on pairs of sequences, 2i the preferred and 2i + 1 the other one. Sequence j holds the rows
+ *   bounds[j] <= t < bounds[j+1] (DEVICE int32 [2 pairs + 1], not decreasing, clamped to [0, T]); its score s_j is the sum of
+ *   logp - ref_logp over its rows with labels >= 0 (labels NULL: all; ref_logp NULL: 0; average != 0: their
+ *   mean, 0 of no rows). With h = beta (s_2i - s_2i+1) - margin the pair's loss is
+ *     MTK_PREF_SIGMOID  (1 - smoothing) softplus(-h) + smoothing softplus(h)
+ *     MTK_PREF_HINGE    max(0, 1 - h)
+ *     MTK_PREF_SQUARE   ((h - 1/2) / beta)^2
+ *   loss f32 [1] is the mean over pairs, pair_loss f32 [pairs], rewards f32 [2 pairs] = beta s_j and dlogp f32 [T] the
+ *   loss's gradient (0 for rows of no sequence). beta > 0, 0 <= smoothing <= 1/2 (sigmoid only), 1 <= pairs <= 2^20.
+ */
+#define MTK_PREF_SIGMOID 0
+#define MTK_PREF_HINGE 1
+#define MTK_PREF_SQUARE 2
+int mtk_token_logprobs(const void* logits, int type, int64_t ld, const void* labels, void* logp, void* lse, int T,
+                       int V, float scale, int* err_flag, void* stream);
+int mtk_token_logprobs_bwd(const void* logits, int type, int64_t ld, const void* labels, const void* lse,
+                           const void* dlogp, void* dlogits, int64_t ldd, int T, int V, float scale, void* stream);
+int mtk_policy_loss(const void* logits, int type, int64_t ld, const void* labels, const void* old_logp,
+                    const void* advantages, const void* ref_logp, const void* weights, float clip_low, float clip_high,
+                    float kl, float scale, void* dlogits, int64_t ldd, void* logp, void* row_loss, void* loss, int T,
+                    int V, int* err_flag, void* stream);
+int mtk_preference_loss(const void* logp, const void* ref_logp, const void* labels, const void* bounds, int pairs,
+                        int T, int kind, float beta, float margin, float smoothing, int average, void* pair_loss,
+                        void* loss, void* rewards, void* dlogp, void* stream);
+
+/*
+ * Layer norm beside the RMSNorm: y bf16 = n gamma + beta, n = (x - mean) rstd, mean f32 [T] the row's mean and
+ * rstd f32 [T] = 1/sqrt(mean((x - mean)^2) + eps). x [T, h] of `type` with row stride ldx, y with row stride
+ * ldy; gamma, beta bf16 [h], 16-byte aligned (beta may be NULL). h a multiple of 8, at most 16384. y must not overlap x.
+ *
+ * mtk_layernorm_bwd: with u = dy gamma: dx = dres + rstd (u - mean(u) - n mean(u n)) over the h columns, from dy [T, h]
+ * of dy_type (row stride lddy), the forward's x, mean and rstd and dres of x's type (row stride lddres, or
+ * NULL: 0). dx of x's type, contiguous; dx_bf16 (NULL, or for f32 rows) receives dx rounded to bf16. dgamma bf16 [h] =
+ * sum_t dy n and dbeta bf16 [h] (or NULL) = sum_t dy, added in a fixed order through `partial`, f32
+ * [mtk_layernorm_bwd_parts(T, h)][2][h]. dx may be dres (with stride h); it overlaps no other input.
+ */
+int mtk_layernorm_fwd(const void* x, int type, int64_t ldx, const void* gamma, const void* beta, void* y, int64_t ldy,
+                      void* mean, void* rstd, int T, int h, float eps, void* stream);
+int mtk_layernorm_bwd_parts(int T, int h);
+int mtk_layernorm_bwd(const void* dy, int dy_type, int64_t lddy, const void* x, int type, int64_t ldx,
+                      const void* gamma, const void* mean, const void* rstd, const void* dres, int64_t lddres,
+                      void* dx, void* dx_bf16, void* partial, void* dgamma, void* dbeta, int T, int h, void* stream);
+
+/*
+ * Embedding with a scale, and its gradient by sorted tokens: no order or offsets from the host, padding, fp32 or bf16 rows.
+ * mtk_embed_lookup: x [T, h] of `type` = scale E[tok_t], E bf16 [V, h]; tok int32 [T]. A token < 0 is
+ *   padding (a row of zeros); one >= V counts as padding and sets *err_flag (device int or NULL) to 16.
+ * mtk_embed_lookup_bwd: dE bf16 [V, h] = scale * the sum of the rows dx_t (of `type`, contiguous) with tok_t = v, in
+ *   fp32 and an order that depends on T only; rows of no token become 0. accumulate != 0: the sum is added to
+ *   dE's rows instead (as for a table that is also the LM head's), rows of no token stay as they are. scratch: device memory
+ *   of mtk_embed_lookup_bwd_scratch_bytes(T, h) bytes, not shared by calls that may run at the same time.
+ * T <= 2^26, V <= 2^24, h a multiple of 8, at most 65536. x, dE and scratch overlap nothing else.
+ */
+int mtk_embed_lookup(const void* tok, const void* E, void* x, int type, int T, int h, int V, float scale,
+                     int* err_flag, void* stream);
+uint64_t mtk_embed_lookup_bwd_scratch_bytes(int T, int h);
+int mtk_embed_lookup_bwd(const void* tok, const void* dx, int type, void* dE, void* scratch, int T, int h, int V,
+                         float scale, int accumulate, int* err_flag, void* stream);
 
 /*
  * Causal grouped-query flash attention on qkv bf16 [B*s, (nh+2*nkv)*hd] (q | k | v), on the
