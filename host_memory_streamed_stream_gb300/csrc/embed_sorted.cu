@@ -8,6 +8,7 @@
 // kernel adds in order. No floating-point atomics: the result does not change from run to run.
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "follow.cuh"
 #include "kernels.h"
@@ -18,25 +19,26 @@ namespace mt {
 namespace {
 
 // ------------------------------------------------------------------ lookup
-// A thread takes eight columns of a token; consecutive threads consecutive columns.
+// W columns a thread at a time, 16 bytes of x: blockDim.x threads a row, blockDim.y rows a block.
 template <class X>
 __global__ void __launch_bounds__(256) lookup_kernel(const int32_t* tok, const bf16* E, X* x, int T, int h, int V,
                                                      float scale, int* err) {
-  const int units = h / 8;
-  const int64_t total = static_cast<int64_t>(T) * units, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-    const int64_t t = i / units;
-    const int c = static_cast<int>(i - t * units) * 8;
-    const int v = tok[t];
-    float a[8] = {};
-    if (v >= 0 && v < V) {
-      unpack8(load8(E + static_cast<int64_t>(v) * h + c), a);
+  constexpr int W = 16 / sizeof(X);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (t >= T) return;
+  const int v = tok[t];
+  const bool on = v >= 0 && v < V;
+  if (v >= V && threadIdx.x == 0) record_bad_token(err);
+  const bf16* row = E + static_cast<int64_t>(on ? v : 0) * h;
+#pragma unroll 4
+  for (int c = threadIdx.x * W; c < h; c += blockDim.x * W) {
+    float a[W] = {};
+    if (on) {
+      read_cols<bf16, W>(row + c, a);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] *= scale;
-    } else if (v >= V && c == 0) {
-      record_bad_token(err);
+      for (int j = 0; j < W; ++j) a[j] *= scale;
     }
-    store8(x + t * h + c, a);
+    write_cols<X, W>(x + t * h + c, a);
   }
 }
 
@@ -44,13 +46,14 @@ __global__ void __launch_bounds__(256) lookup_kernel(const int32_t* tok, const b
 constexpr int kSortBlocks = 8;     // one cluster, the largest that is portable
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortBits = 9;       // of a digit at most: 16 x 512 counters a block
+constexpr int kSortBits = 9;       // of a digit at most
 constexpr int kSortBins = 1 << kSortBits;
+constexpr int kSortAhead = 8;      // loads a thread has in flight
+constexpr int kSortSmem = kSortWarps * kSortBins * 4;  // counters; of the other blocks: a bit a row, and zeros
+constexpr int kZeroBlocks = 240;   // with the sorting ones, two on an SM at most
+constexpr int kZeroBytes = kSortSmem / 2;
+constexpr int kZeroRows = (kSortSmem - kZeroBytes) * 8;
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // *p of block `rank` of this cluster.
 __device__ __forceinline__ int cluster_load(const int* p, int rank) {
   uint32_t a;
@@ -63,52 +66,65 @@ __device__ __forceinline__ int cluster_load(const int* p, int rank) {
 struct SortArgs {
   const int32_t* tok;
   int2 *a, *b;  // pairs (token or V, row): the passes go from one to the other
+  int* number;  // of a pair among the equal digits of its warp
   int T, V, passes, bits;
   bf16* dE;
   int64_t h;
-  bool zero;
   int* err;
 };
 
-// Least significant digit first. Each warp of the cluster owns T / 128 consecutive pairs and counts their digits;
-// the place of a digit's first pair of a warp is the sum of what comes before it in (digit, block, warp) order, which
-// keeps equal digits in order.
-__device__ void sort_pairs(const SortArgs& g, int (*count)[kSortBins], int* total, int* base, int* warp_sum) {
+// Least significant digit first. Each warp of the cluster owns T / 128 consecutive pairs, counts their digits and
+// numbers equal ones; the place of a digit's first pair of a warp is the sum of what comes before it in (digit, block,
+// warp) order, which keeps equal digits in order.
+__device__ void sort_pairs(const SortArgs& g, int* count, int* total, int* base, int* warp_sum) {
   const int rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bins = 1 << g.bits;
   const int each = (g.T + kSortBlocks * kSortWarps - 1) / (kSortBlocks * kSortWarps);
   const int64_t first = static_cast<int64_t>(rank * kSortWarps + warp) * each;
   const int lo = static_cast<int>(first < g.T ? first : g.T), hi = min(g.T, lo + each);
+  int* mine = count + warp * bins;
   for (int pass = 0; pass < g.passes; ++pass) {
     const int2* src = pass & 1 ? g.a : g.b;
     int2* dst = pass & 1 ? g.b : g.a;
     const int shift = pass * g.bits;
-    auto pair = [&](int i) {
-      if (pass > 0) return __ldcg(src + i);
-      int v = g.tok[i];
+    auto key = [&](int i) {
+      if (pass > 0) return __ldcg(&src[i].x);
+      const int v = g.tok[i];
       if (v >= g.V) record_bad_token(g.err);
-      return make_int2(v < 0 || v >= g.V ? g.V : v, i);
+      return v < 0 || v >= g.V ? g.V : v;
     };
-    for (int i = threadIdx.x; i < kSortWarps * kSortBins; i += kSortThreads) count[0][i] = 0;
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) count[i] = 0;
     __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const int i = i0 + lane;
-      const unsigned active = __ballot_sync(0xffffffffu, i < hi);
-      if (i < hi) {
-        const int d = pair(i).x >> shift & (bins - 1);
-        const unsigned same = __match_any_sync(active, d);
-        if (lane == __ffs(same) - 1) count[warp][d] += __popc(same);
+    for (int i0 = lo; i0 < hi; i0 += 32 * kSortAhead) {
+      int k[kSortAhead];
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j) {
+        const int i = i0 + 32 * j + lane;
+        k[j] = i < hi ? key(i) : 0;
       }
-      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j) {
+        const int i = i0 + 32 * j + lane;
+        const unsigned active = __ballot_sync(0xffffffffu, i < hi);
+        if (i < hi) {
+          const int d = k[j] >> shift & (bins - 1);
+          const unsigned same = __match_any_sync(active, d);
+          const int n = mine[d], below = __popc(same & ((1u << lane) - 1));
+          g.number[i] = n + below;
+          __syncwarp(active);
+          if (below == 0) mine[d] = n + __popc(same);
+        }
+        __syncwarp();
+      }
     }
     __syncthreads();
     // per digit: exclusive sums over the block's warps, and the block's total
     for (int d = threadIdx.x; d < bins; d += kSortThreads) {
       int s = 0;
-#pragma unroll
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
-        const int c = count[w][d];
-        count[w][d] = s;
+        const int c = count[w * bins + d];
+        count[w * bins + d] = s;
         s += c;
       }
       total[d] = s;
@@ -117,13 +133,14 @@ __device__ void sort_pairs(const SortArgs& g, int (*count)[kSortBins], int* tota
     // what comes before this block's pairs of a digit: those of smaller digits, and of lower blocks
     const int d = threadIdx.x;  // bins <= kSortThreads
     int below = 0, all = 0;
-    if (d < bins)
+    if (d < bins) {
 #pragma unroll
       for (int r = 0; r < kSortBlocks; ++r) {
         const int c = cluster_load(total + d, r);
         below += r < rank ? c : 0;
         all += c;
       }
+    }
     int s = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -136,59 +153,74 @@ __device__ void sort_pairs(const SortArgs& g, int (*count)[kSortBins], int* tota
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
     if (d < bins) base[d] = before + s - all + below;
     __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const int i = i0 + lane;
-      const unsigned active = __ballot_sync(0xffffffffu, i < hi);
-      if (i < hi) {
-        const int2 p = pair(i);
-        const int k = p.x >> shift & (bins - 1);
-        const unsigned same = __match_any_sync(active, k);
-        const int at = base[k] + count[warp][k] + __popc(same & ((1u << lane) - 1));
-        dst[at] = p;
-        __syncwarp(active);
-        if (lane == __ffs(same) - 1) count[warp][k] += __popc(same);
+    for (int i0 = lo; i0 < hi; i0 += 32 * kSortAhead) {
+      int2 p[kSortAhead];
+      int n[kSortAhead];
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j) {
+        const int i = i0 + 32 * j + lane;
+        if (i >= hi) continue;
+        if (pass > 0) p[j] = __ldcg(src + i);
+        else p[j] = make_int2(key(i), i);
+        n[j] = g.number[i];
       }
-      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j) {
+        if (i0 + 32 * j + lane >= hi) continue;
+        const int k = p[j].x >> shift & (bins - 1);
+        dst[base[k] + mine[k] + n[j]] = p[j];
+      }
     }
     cluster_sync();  // pairs written, totals read
   }
 }
 
 __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortArgs g) {
-  __shared__ int count[kSortWarps][kSortBins];
+  extern __shared__ __align__(128) char sort_smem[];
   __shared__ int total[kSortBins], base[kSortBins], warp_sum[kSortWarps];
   wait_for_previous();
   let_next_start();
   if (blockIdx.x < kSortBlocks) {
-    sort_pairs(g, count, total, base, warp_sum);
+    sort_pairs(g, reinterpret_cast<int*>(sort_smem), total, base, warp_sum);
     return;
   }
-  // the other clusters: zeros in the rows of this block's share of the table that no token uses
+  // the other clusters: zeros in the rows of this block's share of the table that no token uses, by bulk copies
   const int blocks = gridDim.x - kSortBlocks, b = blockIdx.x - kSortBlocks;
   const int v0 = static_cast<int>(static_cast<int64_t>(g.V) * b / blocks);
   const int v1 = static_cast<int>(static_cast<int64_t>(g.V) * (b + 1) / blocks);
-  unsigned* used = reinterpret_cast<unsigned*>(count);  // a bit for each row: 2^18 of them
-  const int units = static_cast<int>(g.h / 8);
-  for (int r0 = v0; r0 < v1; r0 += 32 * kSortWarps * kSortBins) {
-    const int r1 = min(v1, r0 + 32 * kSortWarps * kSortBins);
+  uint4* zeros = reinterpret_cast<uint4*>(sort_smem);
+  unsigned* used = reinterpret_cast<unsigned*>(sort_smem + kZeroBytes);
+  const int row_bytes = static_cast<int>(g.h) * 2;
+  for (int i = threadIdx.x; i * 16 < min(kZeroBytes, row_bytes); i += kSortThreads) zeros[i] = make_uint4(0, 0, 0, 0);
+  for (int r0 = v0; r0 < v1; r0 += kZeroRows) {
+    const int r1 = min(v1, r0 + kZeroRows);
     __syncthreads();
     for (int i = threadIdx.x; i < (r1 - r0 + 31) / 32; i += kSortThreads) used[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < g.T; i += kSortThreads) {
-      const int v = g.tok[i];
-      if (v >= r0 && v < r1) atomicOr(used + (v - r0) / 32, 1u << ((v - r0) & 31));
+    for (int i0 = threadIdx.x; i0 < g.T; i0 += kSortThreads * kSortAhead) {
+      int v[kSortAhead];
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j) v[j] = i0 + j * kSortThreads < g.T ? g.tok[i0 + j * kSortThreads] : -1;
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j)
+        if (v[j] >= r0 && v[j] < r1) atomicOr(used + (v[j] - r0) / 32, 1u << ((v[j] - r0) & 31));
     }
+    fence_async_shared();
     __syncthreads();
-    for (int r = r0 + (threadIdx.x >> 5); r < r1; r += kSortWarps) {
+    for (int r = r0 + threadIdx.x; r < r1; r += kSortThreads) {
       if (used[(r - r0) / 32] >> ((r - r0) & 31) & 1) continue;
-      uint4* row = reinterpret_cast<uint4*>(g.dE + r * g.h);
-      for (int i = threadIdx.x & 31; i < units; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+      char* row = reinterpret_cast<char*>(g.dE + r * g.h);
+      for (int i = 0; i < row_bytes; i += kZeroBytes) bulk_store(row + i, zeros, min(kZeroBytes, row_bytes - i));
     }
+    bulk_store_end_group();
   }
+  bulk_store_wait_read();
 }
 
 // ------------------------------------------------------------------ sums of runs
-constexpr int kSumThreads = 128;  // of eight columns each: 1024 columns a block
+constexpr int kSumThreads = 256;  // of 16 bytes of a row each
+constexpr int kSumAhead = 8;      // rows a thread has in flight
+constexpr int kSumChunk = 128;    // sorted rows a block sums, at most
 
 struct SumArgs {
   const int2* pairs;
@@ -199,68 +231,99 @@ struct SumArgs {
   float scale;
   bool add;
 };
+template <int W>
 __device__ __forceinline__ void write_row(const SumArgs& g, int v, int c, const float* acc) {
   bf16* p = g.dE + static_cast<int64_t>(v) * g.h + c;
-  float out[8], old[8] = {};
-  if (g.add) unpack8(load8(p), old);
+  float out[W], old[W] = {};
+  if (g.add) read_cols<bf16, W>(p, old);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) out[j] = fmaf(acc[j], g.scale, old[j]);
-  store8(p, out);
+  for (int j = 0; j < W; ++j) out[j] = fmaf(acc[j], g.scale, old[j]);
+  write_cols<bf16, W>(p, out);
+}
+template <int W>
+__device__ __forceinline__ void write_partial(const SumArgs& g, int chunk, int which, int c, const float* acc) {
+  float* p = g.partial + (static_cast<int64_t>(chunk) * 2 + which) * g.h + c;
+#pragma unroll
+  for (int j = 0; j < W; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
 }
 
 template <class X>
 __global__ void __launch_bounds__(kSumThreads) run_sum_kernel(const SumArgs g) {
+  constexpr int W = 16 / sizeof(X);
+  __shared__ int2 pairs[kSumChunk];
+  __shared__ int ends[2];  // the tokens before and behind the chunk
   wait_for_previous();
   let_next_start();
-  const int c = (blockIdx.y * kSumThreads + threadIdx.x) * 8;
+  const int p0 = blockIdx.x * g.chunk, n = min(g.T - p0, g.chunk);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) pairs[i] = __ldcg(g.pairs + p0 + i);
+  if (threadIdx.x == 0) ends[0] = p0 > 0 ? __ldcg(&g.pairs[p0 - 1].x) : -1;
+  if (threadIdx.x == 0) ends[1] = p0 + n < g.T ? __ldcg(&g.pairs[p0 + n].x) : -1;
+  __syncthreads();
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
   if (c >= g.h) return;
-  const int p0 = blockIdx.x * g.chunk, p1 = min(g.T, p0 + g.chunk);
-  const X* dx = static_cast<const X*>(g.dx);
-  float acc[8] = {}, a[8];
-  int cur = __ldcg(&g.pairs[p0].x);
-  if (cur == g.V) return;
-  bool from_before = p0 > 0 && __ldcg(&g.pairs[p0 - 1].x) == cur;
-  for (int p = p0; p < p1; ++p) {
-    const int2 q = __ldcg(g.pairs + p);
-    if (q.x != cur) {
-      if (from_before) store8(g.partial + static_cast<int64_t>(blockIdx.x) * 2 * g.h + c, acc);
-      else write_row(g, cur, c, acc);
-      from_before = false;
-      cur = q.x;
-      if (cur == g.V) return;
+  const X* dx = static_cast<const X*>(g.dx) + c;
+  float acc[W] = {};
+  int cur = pairs[0].x;
+  bool from_before = ends[0] == cur;
+  for (int i0 = 0; i0 < n; i0 += kSumAhead) {
+    uint4 raw[kSumAhead];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    for (int j = 0; j < kSumAhead; ++j)
+      if (i0 + j < n && pairs[i0 + j].x != g.V)
+        raw[j] = *reinterpret_cast<const uint4*>(dx + static_cast<int64_t>(pairs[i0 + j].y) * g.h);
+#pragma unroll
+    for (int j = 0; j < kSumAhead; ++j) {
+      if (i0 + j >= n) break;
+      const int v = pairs[i0 + j].x;
+      if (v != cur) {
+        if (from_before) write_partial<W>(g, blockIdx.x, 0, c, acc);
+        else write_row<W>(g, cur, c, acc);
+        from_before = false;
+        cur = v;
+#pragma unroll
+        for (int k = 0; k < W; ++k) acc[k] = 0.f;
+      }
+      if (cur == g.V) return;  // padding, at the end
+      float a[W];
+      read_cols<X, W>(reinterpret_cast<const X*>(&raw[j]), a);
+#pragma unroll
+      for (int k = 0; k < W; ++k) acc[k] += a[k];
     }
-    unpack8(load8(dx + static_cast<int64_t>(q.y) * g.h + c), a);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] += a[j];
   }
-  const bool goes_on = p1 < g.T && __ldcg(&g.pairs[p1].x) == cur;
-  if (from_before) store8(g.partial + static_cast<int64_t>(blockIdx.x) * 2 * g.h + c, acc);
-  else if (goes_on) store8(g.partial + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * g.h + c, acc);
-  else write_row(g, cur, c, acc);
+  if (from_before) write_partial<W>(g, blockIdx.x, 0, c, acc);
+  else if (ends[1] == cur) write_partial<W>(g, blockIdx.x, 1, c, acc);
+  else write_row<W>(g, cur, c, acc);
 }
 
-// The runs that cross a border: one block for each chunk in which such a run begins.
+// The runs that cross a border: one block for each chunk in which such a run begins, 4 columns a thread.
 __global__ void __launch_bounds__(kSumThreads) run_join_kernel(const SumArgs g) {
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
+  const int p0 = blockIdx.x * g.chunk, chunks = (g.T + g.chunk - 1) / g.chunk;
   wait_for_previous();
-  const int c = (blockIdx.y * kSumThreads + threadIdx.x) * 8;
-  if (c >= g.h) return;
-  const int p0 = blockIdx.x * g.chunk;
-  int64_t end = static_cast<int64_t>(p0) + g.chunk;
+  const int64_t end = static_cast<int64_t>(p0) + g.chunk;
   if (end >= g.T) return;
-  const int cur = __ldcg(&g.pairs[end - 1].x);
-  if (cur == g.V || __ldcg(&g.pairs[end].x) != cur) return;           // no run goes on
-  if (p0 > 0 && __ldcg(&g.pairs[p0 - 1].x) == cur) return;            // it began in an earlier chunk
-  const float* part = g.partial + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * g.h + c;
-  float acc[8], a[8];
-  unpack8(load8(part), acc);
-  for (int k = blockIdx.x + 1; end < g.T && __ldcg(&g.pairs[end].x) == cur; ++k, end += g.chunk) {
-    unpack8(load8(g.partial + static_cast<int64_t>(k) * 2 * g.h + c), a);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] += a[j];
+  const int before = p0 > 0 ? __ldcg(&g.pairs[p0 - 1].x) : -1;
+  const int cur = __ldcg(&g.pairs[end - 1].x), next = __ldcg(&g.pairs[end].x);
+  if (cur == g.V || next != cur || before == cur) return;  // no run goes on, or it began in an earlier chunk
+  // the chunks that it goes on into
+  int last = blockIdx.x + 1;
+  for (int k0 = last;; k0 += blockDim.x) {
+    const int k = k0 + threadIdx.x;
+    const int n = __syncthreads_count(k < chunks && __ldcg(&g.pairs[static_cast<int64_t>(k) * g.chunk].x) == cur);
+    last = k0 + n;
+    if (n < static_cast<int>(blockDim.x)) break;
   }
-  write_row(g, cur, c, acc);
+  if (c >= g.h) return;
+  const float* part = g.partial + static_cast<int64_t>(blockIdx.x) * 2 * g.h + c;
+  const float4 q = *reinterpret_cast<const float4*>(part + g.h);
+  float acc[4] = {q.x, q.y, q.z, q.w};
+  part += 2 * g.h;
+#pragma unroll 8
+  for (int k = blockIdx.x + 1; k < last; ++k, part += 2 * g.h) {
+    const float4 a = *reinterpret_cast<const float4*>(part);
+    acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
+  }
+  write_row<4>(g, cur, c, acc);
 }
 
 bool embed_shape_ok(int T, int V, int h) {
@@ -268,7 +331,12 @@ bool embed_shape_ok(int T, int V, int h) {
 }
 uint64_t table_bytes(int V, int h) { return static_cast<uint64_t>(V) * h * sizeof(bf16); }
 // Sorted rows a block sums.
-int sum_chunk(int T) { return T <= 4096 ? 16 : T <= 32768 ? 32 : 128; }
+int sum_chunk(int T) { return T <= 4096 ? 16 : T <= 32768 ? 32 : kSumChunk; }
+// Threads that go over `units` in the fewest turns of at most `most`, and then as evenly as whole warps can.
+int threads_of(int units, int most) {
+  const int turns = (units + most - 1) / most;
+  return ((units + turns - 1) / turns + 31) / 32 * 32;
+}
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -279,19 +347,19 @@ cudaError_t embed_lookup(const int32_t* tok, const bf16* E, void* x, int type, i
       (err && !vec_ok(err, 4)) || !std::isfinite(scale) ||
       ranges_overlap(E, table_bytes(V, h), x, static_cast<uint64_t>(T) * h * row_type_bytes(type)))
     return cudaErrorInvalidValue;
-  const int64_t blocks = (static_cast<int64_t>(T) * (h / 8) + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, kSms * 16));
+  const int threads = threads_of(h * row_type_bytes(type) / 16, 256);
+  const dim3 block(threads, 256 / threads), grid((T + block.y - 1) / block.y);
   if (type == kRowF32)
-    lookup_kernel<float><<<grid, 256, 0, s>>>(tok, E, static_cast<float*>(x), T, h, V, scale, err);
+    lookup_kernel<float><<<grid, block, 0, s>>>(tok, E, static_cast<float*>(x), T, h, V, scale, err);
   else
-    lookup_kernel<bf16><<<grid, 256, 0, s>>>(tok, E, static_cast<bf16*>(x), T, h, V, scale, err);
+    lookup_kernel<bf16><<<grid, block, 0, s>>>(tok, E, static_cast<bf16*>(x), T, h, V, scale, err);
   return cudaGetLastError();
 }
 
 uint64_t embed_lookup_bwd_scratch(int T, int h) {
   const int chunk = sum_chunk(T);
-  const size_t chunks = (T + chunk - 1) / chunk;
-  return 2 * round256(static_cast<size_t>(T) * sizeof(int2)) + chunks * 2 * h * sizeof(float);
+  const size_t n = T, chunks = (n + chunk - 1) / chunk;
+  return 2 * round256(n * sizeof(int2)) + round256(n * sizeof(int)) + chunks * 2 * h * sizeof(float);
 }
 
 cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16* dE, void* scratch, int T, int h,
@@ -307,19 +375,28 @@ cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16*
   while ((V >> bits) > 0) ++bits;  // of the keys 0 .. V
   const int passes = (bits + kSortBits - 1) / kSortBits;
   char* at = static_cast<char*>(scratch);
-  int2* a = reinterpret_cast<int2*>(at);
-  int2* b = reinterpret_cast<int2*>(at + round256(static_cast<size_t>(T) * sizeof(int2)));
-  float* partial = reinterpret_cast<float*>(at + 2 * round256(static_cast<size_t>(T) * sizeof(int2)));
-  const SortArgs g{tok, a, b, T, V, passes, (bits + passes - 1) / passes, dE, h, !add, err};
-  const unsigned blocks = add ? kSortBlocks : kSortBlocks + 2 * kSms / kSortBlocks * kSortBlocks;
-  cudaError_t e = launch_following(sort_kernel, dim3(blocks), kSortThreads, 0, s, g);
+  auto take = [&at](size_t bytes) { return std::exchange(at, at + round256(bytes)); };
+  int2* a = reinterpret_cast<int2*>(take(static_cast<size_t>(T) * sizeof(int2)));
+  int2* b = reinterpret_cast<int2*>(take(static_cast<size_t>(T) * sizeof(int2)));
+  int* number = reinterpret_cast<int*>(take(static_cast<size_t>(T) * sizeof(int)));
+  const SortArgs g{tok, a, b, number, T, V, passes, (bits + passes - 1) / passes, dE, h, err};
+  const unsigned blocks = add ? kSortBlocks : kSortBlocks + kZeroBlocks;
+  cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
   if (e != cudaSuccess) return e;
-  const int chunk = sum_chunk(T);
-  const SumArgs r{passes & 1 ? a : b, dx, dE, partial, T, V, h, chunk, scale, add};
-  const dim3 grid((T + chunk - 1) / chunk, (h / 8 + kSumThreads - 1) / kSumThreads);
-  e = launch_following(type == kRowF32 ? run_sum_kernel<float> : run_sum_kernel<bf16>, grid, kSumThreads, 0, s, r);
+  e = launch_following(sort_kernel, dim3(blocks), kSortThreads, kSortSmem, s, g);
   if (e != cudaSuccess) return e;
-  return launch_following(run_join_kernel, grid, kSumThreads, 0, s, r);
+  const int chunk = sum_chunk(T), chunks = (T + chunk - 1) / chunk;
+  const SumArgs r{passes & 1 ? a : b, dx, dE, reinterpret_cast<float*>(at), T, V, h, chunk, scale, add};
+  auto grid = [&](int units, unsigned& threads) {
+    threads = threads_of(units, kSumThreads);
+    return dim3(chunks, (units + threads - 1) / threads);
+  };
+  unsigned threads;
+  dim3 blocks_xy = grid(h * row_type_bytes(type) / 16, threads);
+  e = launch_following(type == kRowF32 ? run_sum_kernel<float> : run_sum_kernel<bf16>, blocks_xy, threads, 0, s, r);
+  if (e != cudaSuccess || chunks == 1) return e;
+  blocks_xy = grid(h / 4, threads);
+  return launch_following(run_join_kernel, blocks_xy, threads, 0, s, r);
 }
 
 }  // namespace mt

@@ -58,6 +58,82 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(bf16 x) { return __bfloat162float(x); }
 
+// W neighbouring columns, in 8 or 16 bytes.
+__device__ __forceinline__ void unpack2(uint32_t x, float* v) {
+  v[0] = __uint_as_float(x << 16);
+  v[1] = __uint_as_float(x & 0xffff0000u);
+}
+template <class T, int W>
+__device__ __forceinline__ void read_cols(const T* p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    static_assert(W == 4, "16 bytes");
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else if constexpr (W == 4) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    unpack2(q.x, v);
+    unpack2(q.y, v + 2);
+  } else {
+    unpack8(*reinterpret_cast<const uint4*>(p), v);
+  }
+}
+template <class T, int W>
+__device__ __forceinline__ void write_cols(T* p, const float* v) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else if constexpr (W == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  else store8(p, v);
+}
+
+// cp.async: 16 bytes (or 8) of global memory to shared memory, of which the first `bytes` are read and the rest is
+// zero. A thread waits for its own copies by groups.
+__device__ __forceinline__ void cp_async_chunk(void* dst, const void* src, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_half(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most n of this thread's groups are in flight, n <= 24.
+__device__ __forceinline__ void cp_async_wait_groups(int n) {
+#define MT_WAIT(N) \
+  case N: asm volatile("cp.async.wait_group " #N ";" ::: "memory"); break;
+  switch (n) {
+    MT_WAIT(1) MT_WAIT(2) MT_WAIT(3) MT_WAIT(4) MT_WAIT(5) MT_WAIT(6) MT_WAIT(7) MT_WAIT(8) MT_WAIT(9) MT_WAIT(10)
+    MT_WAIT(11) MT_WAIT(12) MT_WAIT(13) MT_WAIT(14) MT_WAIT(15) MT_WAIT(16) MT_WAIT(17) MT_WAIT(18) MT_WAIT(19)
+    MT_WAIT(20) MT_WAIT(21) MT_WAIT(22) MT_WAIT(23) MT_WAIT(24)
+    default: asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+#undef MT_WAIT
+}
+
+// Bulk copies of shared memory to global memory: both 16-byte aligned, a multiple of 16 bytes. What was written to
+// shared memory before is fenced first; the source stays as it is until the copies have read it.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_end_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// The blocks of a cluster.
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_blocks() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // A token id outside the vocabulary: a data error, which does not replace another code.
 __device__ __forceinline__ void record_bad_token(int* err) {
   if (err) atomicCAS(err, 0, kErrBadToken);

@@ -7,6 +7,7 @@
 // subtracted before the product with c, which keeps masks of the type's lowest value in range. The label's
 // logit, the maximum and the logarithm meet in 64 bits: a ratio of policies is exp of a small difference of
 // numbers of size 10, of which fp32 would lose 2^-21.
+#include <algorithm>
 #include <cmath>
 
 #include "follow.cuh"
@@ -18,42 +19,94 @@ namespace mt {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kLn2 = 0.6931471805599453;
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);
+constexpr float kLn2 = 0.6931471805599453f, kLn2Low = 0.6931471805599453 - static_cast<double>(kLn2);
 
 __device__ __forceinline__ float pow2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Running maximum and sum of 2^(c (z - max)). max = -inf: nothing but -inf so far, sum 0.
+// c = a log2 e as the sum of two floats: one alone is off by up to 2^-25, which moves a row's logp by that times the
+// label's distance from the mean, always the same way (1e-7 a token, which a sequence of 1000 tokens adds up).
+struct Factor {
+  float hi, lo;
+};
+__device__ __forceinline__ Factor factor(float scale) {
+  const float hi = scale * kLog2e;
+  // scale times log2 e's own rounded-off part, and the product's
+  return {hi, fmaf(scale, kLog2e, -hi) + scale * kLog2eLow};
+}
+__device__ __forceinline__ float times(float d, const Factor& c) { return fmaf(d, c.hi, d * c.lo); }
+__device__ __forceinline__ float2 times(float2 d, const Factor& c) {
+  return __ffma2_rn(d, make_float2(c.hi, c.hi), __fmul2_rn(d, make_float2(c.lo, c.lo)));
+}
+
+// Sum of 2^(c (z - m)) for an m that is not far below the maximum: it is raised only where a term would pass 2^8, which
+// after the first few terms of a row is hardly ever. m = -inf: nothing but -inf so far, sum 0.
 struct MaxSum {
   float m, s;
 };
-__device__ __forceinline__ MaxSum merge(const MaxSum& a, const MaxSum& b, float c) {
+__device__ __forceinline__ MaxSum merge(const MaxSum& a, const MaxSum& b, const Factor& c) {
   const float m = fmaxf(a.m, b.m);
   const float mm = m == -INFINITY ? 0.f : m;
-  return {m, a.s * pow2((a.m - mm) * c) + b.s * pow2((b.m - mm) * c)};
+  return {m, a.s * pow2(times(a.m - mm, c)) + b.s * pow2(times(b.m - mm, c))};
+}
+__device__ __forceinline__ MaxSum merge_warp(MaxSum r, const Factor& c) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    r = merge(r, {__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o)}, c);
+  return r;
+}
+__device__ __forceinline__ void raise_max(MaxSum& r, float top, const Factor& c) {
+  if ((top - r.m) * c.hi > 8.f || r.m == -INFINITY) {
+    if (r.s != 0.f) r.s *= pow2(times(r.m - top, c));
+    r.m = top;
+  }
 }
 template <int N>
-__device__ __forceinline__ void add_terms(MaxSum& r, const float* z, float c) {
+__device__ __forceinline__ void add_terms(MaxSum& r, const float* z, const Factor& c) {
   float top = z[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) top = fmaxf(top, z[i]);
-  if (top > r.m) {
-    r.s *= pow2((r.m - top) * c);
-    r.m = top;
-  }
+  raise_max(r, top, c);
   const float m = r.m == -INFINITY ? 0.f : r.m;
+  if constexpr (N == 1) {
+    r.s += pow2(times(z[0] - m, c));
+  } else {
+    float2 sum = make_float2(r.s, 0.f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) r.s += pow2((z[i] - m) * c);
+    for (int i = 0; i < N; i += 2) {
+      const float2 x = times(__fadd2_rn(make_float2(z[i], z[i + 1]), make_float2(-m, -m)), c);
+      sum = __fadd2_rn(sum, make_float2(pow2(x.x), pow2(x.y)));
+    }
+    r.s = sum.x + sum.y;
+  }
 }
 
-// log2 of a sum of exponentials, to 2^-24 of its fraction rather than of its size.
-__device__ __forceinline__ double log2_split(float s) {
+// A number held as two floats, the second what the first has lost: a few instructions of 4 cycles where 64-bit
+// arithmetic takes 40 cycles each, in the one thread that a whole row waits for.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair add(const Pair& a, const Pair& b) {
+  const float s = a.hi + b.hi, x = s - a.hi;
+  return {s, (a.hi - (s - x)) + (b.hi - x) + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Pair product(const Pair& a, float b) {
+  const float p = a.hi * b;
+  return {p, fmaf(a.hi, b, -p) + a.lo * b};
+}
+__device__ __forceinline__ Pair negative(const Pair& a) { return {-a.hi, -a.lo}; }
+// With an infinity or NaN among the parts the second float may be NaN where the sum is not.
+__device__ __forceinline__ float value(const Pair& a) { return isfinite(a.hi) ? a.hi + a.lo : a.hi; }
+// The logarithm, to 2^-24 of its fraction rather than of its size.
+__device__ __forceinline__ Pair log_pair(float s) {
   int e;
-  const float f = frexpf(s, &e);
-  return static_cast<double>(e) + static_cast<double>(log2f(f));
+  float f = frexpf(s, &e);
+  if (f < 0.70710678f) f *= 2.f, e -= 1;
+  if (!(s > 0.f && s < INFINITY)) return {logf(s), 0.f};
+  return add(product({kLn2, kLn2Low}, static_cast<float>(e)), {logf(f), 0.f});
 }
 
 struct TokenRows {
@@ -73,140 +126,317 @@ struct TokenRows {
   int* err;
 };
 
-// What one row's label gives: its log-probability, and for the policy loss the row's loss and d loss / d logp.
-template <bool POLICY>
-__device__ __forceinline__ float finish_row(const TokenRows& g, int t, float z_label, const MaxSum& r) {
-  const float c = g.scale * kLog2e;
-  const double log2_sum = log2_split(r.s);
-  const double logp = ((static_cast<double>(z_label) - r.m) * c - log2_sum) * kLn2;
-  g.logp[t] = static_cast<float>(logp);
+// A row's numbers besides its logits, loaded ahead of where they are used (and converted there: the thread goes on).
+template <class Z>
+struct RowInputs {
+  Z z_label;
+  float old_logp, adv, ref, weight;
+  __device__ __forceinline__ float label() const { return to_f32(z_label); }
+};
+template <class Z, bool POLICY>
+__device__ __forceinline__ RowInputs<Z> row_inputs(const TokenRows& g, int64_t t, int label) {
+  RowInputs<Z> r{};
+  r.z_label = static_cast<const Z*>(g.logits)[t * g.ld + label];
+  if constexpr (POLICY) {
+    r.old_logp = g.old_logp[t];
+    r.adv = g.adv[t];
+    r.ref = g.kl != 0.f ? g.ref[t] : 0.f;
+    r.weight = g.weights ? g.weights[t] : 1.f / static_cast<float>(g.T);
+  }
+  return r;
+}
+// What the second look at a row needs: dlogits_v = kp 2^(c (z_v - m)) + k [v = label].
+struct RowGrad {
+  float m, k, kp;
+};
+// The row's log-probability, and for the policy loss its loss and d loss / d logp. `write`: of several callers, one.
+template <bool POLICY, class Z>
+__device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, const RowInputs<Z>& in, const MaxSum& r,
+                                              bool write) {
+  const Pair log_sum = log_pair(r.s);
+  const float z = in.label();
+  Pair logp = add(product(add({z, 0.f}, {-r.m, 0.f}), g.scale), negative(log_sum));
+  if (logp.hi > 0.f) logp = {0.f, 0.f};  // by rounding, where the label has all of the probability
+  if (write) g.logp[t] = value(logp);
   if constexpr (!POLICY) {
-    g.lse[t] = static_cast<float>((static_cast<double>(r.m) * c + log2_sum) * kLn2);
-    return 0.f;
+    if (write) g.lse[t] = value(add(product({r.m, 0.f}, g.scale), log_sum));
+    return {};
   } else {
-    const float w = g.weights ? g.weights[t] : 1.f / static_cast<float>(g.T);
-    const float adv = g.adv[t];
-    const float ratio = expf(static_cast<float>(logp - static_cast<double>(g.old_logp[t])));
+    const float ratio = expf(value(add(logp, {-in.old_logp, 0.f})));
     const float lo = 1.f - g.clip_low, hi = 1.f + g.clip_high;
     // comparisons rather than fminf, which would drop a NaN
     const float cut = ratio < lo ? lo : ratio > hi ? hi : ratio;
-    const bool held = ratio * adv > cut * adv;
-    float loss = held ? -cut * adv : -ratio * adv;
-    float d = held ? 0.f : -ratio * adv;
+    const bool held = ratio * in.adv > cut * in.adv;
+    float loss = held ? -cut * in.adv : -ratio * in.adv;
+    float d = held ? 0.f : -ratio * in.adv;
     if (g.kl != 0.f) {
-      const float far = static_cast<float>(static_cast<double>(g.ref[t]) - logp);
+      const float far = value(add({in.ref, 0.f}, negative(logp)));
       const float em1 = expm1f(far);
       loss += g.kl * (em1 - far);
       d -= g.kl * em1;
     }
-    g.row_loss[t] = w * loss;
-    return w * d;
+    if (write) g.row_loss[t] = in.weight * loss;
+    const float k = in.weight * d * g.scale;
+    return {r.m == -INFINITY ? 0.f : r.m, k, -k / r.s};
   }
 }
 
-// One block a row: maximum and sum over the row, then, for the policy loss, the row once more (from the L2)
-// for its gradient.
+// ------------------------------------------------------------------ rows in registers and in shared memory
+// Both kernels read the logits from memory once and keep the row on the SM until its gradient is written, in
+// chunks of 16 bytes: the thread that loaded a chunk is the only one that reads it.
+template <class Z>
+constexpr int kChunk = 16 / static_cast<int>(sizeof(Z));  // columns of a chunk
+
+template <class Z>
+__device__ __forceinline__ void unpack_chunk(const uint4& u, float* v) {
+  if constexpr (sizeof(Z) == 2) {
+    unpack8(u, v);
+  } else {
+    v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
+  }
+}
+// A chunk's gradient, which nothing here reads again.
+template <class Z>
+__device__ __forceinline__ void write_chunk(bf16* d, float* v, const RowGrad& q, const Factor& c, int to_label) {
+  constexpr int N = kChunk<Z>;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 x = __fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), make_float2(-q.m, -q.m)),
+                                make_float2(c.hi, c.hi));
+    const float2 p = __fmul2_rn(make_float2(pow2(x.x), pow2(x.y)), make_float2(q.kp, q.kp));
+    v[i] = p.x, v[i + 1] = p.y;
+  }
+  if (static_cast<unsigned>(to_label) < N) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += i == to_label ? q.k : 0.f;
+  }
+  if constexpr (N == 8) __stcs(reinterpret_cast<uint4*>(d), pack8(v));
+  else __stcs(reinterpret_cast<uint2*>(d), make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])));
+}
+// Zeros in the columns [0, n) of a row, by `threads` threads.
+__device__ __forceinline__ void zero_row(bf16* d, int n, int at, int threads) {
+  for (int i = at * 8; i < (n & ~7); i += threads * 8) *reinterpret_cast<uint4*>(d + i) = make_uint4(0, 0, 0, 0);
+  for (int i = (n & ~7) + at; i < n; i += threads) d[i] = __float2bfloat16_rn(0.f);
+}
+template <bool POLICY>
+__device__ __forceinline__ void masked_row(const TokenRows& g, int64_t t, int label) {
+  if (label >= g.V) record_bad_token(g.err);
+  g.logp[t] = 0.f;
+  if (POLICY) g.row_loss[t] = 0.f;
+  else g.lse[t] = 0.f;
+}
+
+// Short rows, up to 32 x kWarpChunks chunks: a warp a row, in registers.
+constexpr int kWarpChunks = 8;
 template <class Z, bool POLICY>
-__global__ void __launch_bounds__(512) token_rows_kernel(const TokenRows g) {
-  __shared__ MaxSum part[16];
-  __shared__ float shared_k, shared_m, shared_inv;
-  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  constexpr int N = kChunk<Z>;
+  if constexpr (POLICY) let_next_start();
+  if (t >= g.T) return;
   const Z* z = static_cast<const Z*>(g.logits) + t * g.ld;
   bf16* d = POLICY ? g.dlogits + t * g.ldd : nullptr;
-  const int label = g.labels[t], whole = g.V & ~7;
-  if (label < 0 || label >= g.V) {  // nothing of the row is read
-    if (threadIdx.x == 0) {
-      if (label >= g.V) record_bad_token(g.err);
-      g.logp[t] = 0.f;
-      if (POLICY) g.row_loss[t] = 0.f;
-      else g.lse[t] = 0.f;
-    }
-    if constexpr (POLICY) {
-      for (int i = threadIdx.x * 8; i < whole; i += blockDim.x * 8)
-        *reinterpret_cast<uint4*>(d + i) = make_uint4(0, 0, 0, 0);
-      for (int i = whole + threadIdx.x; i < g.V; i += blockDim.x) d[i] = __float2bfloat16_rn(0.f);
-    }
+  const int label = g.labels[t];
+  if (label < 0 || label >= g.V) {
+    if (lane == 0) masked_row<POLICY>(g, t, label);
+    if (POLICY) zero_row(d, g.V, lane, 32);
     return;
   }
-  const float c = g.scale * kLog2e;
-  MaxSum r{-INFINITY, 0.f};
-  float v[8];
-  for (int i = threadIdx.x * 8; i < whole; i += blockDim.x * 8) {
-    unpack8(load8(z + i), v);
-    add_terms<8>(r, v, c);
-  }
-  for (int i = whole + threadIdx.x; i < g.V; i += blockDim.x) {
-    v[0] = to_f32(z[i]);
-    add_terms<1>(r, v, c);
-  }
+  RowInputs<Z> in{};
+  if (lane == 0) in = row_inputs<Z, POLICY>(g, t, label);
+  uint4 raw[kWarpChunks];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    r = merge(r, {__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o)}, c);
+  for (int j = 0; j < kWarpChunks; ++j) {
+    const int col = (j * 32 + lane) * N;
+    if (col + N <= g.V) raw[j] = *reinterpret_cast<const uint4*>(z + col);
+  }
+  const Factor c = factor(g.scale);
+  MaxSum r{-INFINITY, 0.f};
+  float v[N];
+#pragma unroll
+  for (int j = 0; j < kWarpChunks; ++j) {
+    const int col = (j * 32 + lane) * N;
+    if (col + N <= g.V) {
+      unpack_chunk<Z>(raw[j], v);
+      add_terms<N>(r, v, c);
+    } else {
+      for (int i = col; i < g.V; ++i) {
+        v[0] = to_f32(z[i]);
+        add_terms<1>(r, v, c);
+      }
+    }
+  }
+  r = merge_warp(r, c);
+  RowGrad q{};
+  if (lane == 0) q = finish_row<POLICY>(g, t, in, r, true);
+  if constexpr (POLICY) {
+    q.m = __shfl_sync(0xffffffffu, q.m, 0);
+    q.k = __shfl_sync(0xffffffffu, q.k, 0);
+    q.kp = __shfl_sync(0xffffffffu, q.kp, 0);
+#pragma unroll
+    for (int j = 0; j < kWarpChunks; ++j) {
+      const int col = (j * 32 + lane) * N;
+      if (col + N <= g.V) {
+        unpack_chunk<Z>(raw[j], v);
+        write_chunk<Z>(d + col, v, q, c, label - col);
+      } else {
+        for (int i = col; i < g.V; ++i)
+          d[i] = __float2bfloat16_rn(q.kp * pow2((to_f32(z[i]) - q.m) * c.hi) + (i == label ? q.k : 0.f));
+      }
+    }
+  }
+}
+
+// Longer rows: a block a row, or, for very wide and for few rows, a cluster of blocks that split it by columns. The policy
+// loss reads the row a second time, from the L2, for its gradient.
+// *p of block `rank` of the cluster = v.
+__device__ __forceinline__ void cluster_store(MaxSum* p, unsigned rank, const MaxSum& v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.m), "f"(v.s) : "memory");
+}
+
+template <class Z, bool POLICY, int NT>
+__global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRows g, int share) {
+  constexpr int N = kChunk<Z>, WARPS = NT / 32;
+  __shared__ MaxSum part[WARPS], others[8];
+  __shared__ RowGrad shared;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned rank = cluster_rank(), blocks = cluster_blocks();
+  const int64_t t = blockIdx.x / blocks;
+  const int c0 = static_cast<int>(rank) * share, cols = min(share, g.V - c0), whole = cols / N * N;
+  const int label = g.labels[t];
+  if constexpr (POLICY) let_next_start();
+  if (label < 0 || label >= g.V) {  // the same for all blocks of the cluster
+    if (rank == 0 && threadIdx.x == 0) masked_row<POLICY>(g, t, label);
+    if (POLICY) zero_row(g.dlogits + t * g.ldd + c0, cols, threadIdx.x, NT);
+    return;
+  }
+  const Z* z = static_cast<const Z*>(g.logits) + t * g.ld + c0;
+  RowInputs<Z> in{};
+  if (threadIdx.x == 0) in = row_inputs<Z, POLICY>(g, t, label);
+  const Factor c = factor(g.scale);
+  MaxSum r{-INFINITY, 0.f};
+  int i = threadIdx.x * N;
+  for (; i + NT * N < whole; i += 2 * NT * N) {
+    const uint4 x = *reinterpret_cast<const uint4*>(z + i), y = *reinterpret_cast<const uint4*>(z + i + NT * N);
+    float v[2 * N];
+    unpack_chunk<Z>(x, v);
+    unpack_chunk<Z>(y, v + N);
+    add_terms<2 * N>(r, v, c);
+  }
+  if (i < whole) {
+    float v[N];
+    unpack_chunk<Z>(*reinterpret_cast<const uint4*>(z + i), v);
+    add_terms<N>(r, v, c);
+  }
+  if (whole + static_cast<int>(threadIdx.x) < cols) {
+    const float v = to_f32(z[whole + threadIdx.x]);
+    add_terms<1>(r, &v, c);
+  }
+  r = merge_warp(r, c);
   if (lane == 0) part[warp] = r;
   __syncthreads();
   if (warp == 0) {
-    r = lane < warps ? part[lane] : MaxSum{-INFINITY, 0.f};
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-      r = merge(r, {__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o)}, c);
-    if (lane == 0) {
-      shared_k = finish_row<POLICY>(g, t, to_f32(z[label]), r) * g.scale;
-      shared_m = r.m == -INFINITY ? 0.f : r.m;
-      shared_inv = 1.f / r.s;
+    r = merge_warp(lane < WARPS ? part[lane] : MaxSum{-INFINITY, 0.f}, c);
+    if (blocks > 1 && lane < static_cast<int>(blocks)) cluster_store(&others[rank], lane, r);
+  }
+  if (blocks > 1) {
+    cluster_sync();
+    if (threadIdx.x == 0) {
+      r = others[0];
+      for (unsigned k = 1; k < blocks; ++k) r = merge(r, others[k], c);
     }
   }
+  if (threadIdx.x == 0) shared = finish_row<POLICY>(g, t, in, r, rank == 0);
   if constexpr (POLICY) {
     __syncthreads();
-    const float k = shared_k, m = shared_m, kp = -k * shared_inv;
-    for (int i = threadIdx.x * 8; i < whole; i += blockDim.x * 8) {
-      unpack8(load8(z + i), v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = kp * pow2((v[j] - m) * c) + (i + j == label ? k : 0.f);
-      store8(d + i, v);
+    const RowGrad q = shared;
+    bf16* d = g.dlogits + t * g.ldd + c0;
+    const int at = label - c0;
+    i = threadIdx.x * N;
+    for (; i + NT * N < whole; i += 2 * NT * N) {
+      const uint4 x = __ldcs(reinterpret_cast<const uint4*>(z + i));
+      const uint4 y = __ldcs(reinterpret_cast<const uint4*>(z + i + NT * N));
+      float v[N];
+      unpack_chunk<Z>(x, v);
+      write_chunk<Z>(d + i, v, q, c, at - i);
+      unpack_chunk<Z>(y, v);
+      write_chunk<Z>(d + i + NT * N, v, q, c, at - i - NT * N);
     }
-    for (int i = whole + threadIdx.x; i < g.V; i += blockDim.x)
-      d[i] = __float2bfloat16_rn(kp * pow2((to_f32(z[i]) - m) * c) + (i == label ? k : 0.f));
+    if (i < whole) {
+      float v[N];
+      unpack_chunk<Z>(__ldcs(reinterpret_cast<const uint4*>(z + i)), v);
+      write_chunk<Z>(d + i, v, q, c, at - i);
+    }
+    i = whole + threadIdx.x;
+    if (i < cols) d[i] = __float2bfloat16_rn(q.kp * pow2((to_f32(z[i]) - q.m) * c.hi) + (i == at ? q.k : 0.f));
   }
 }
 
-// dlogits of given dlogp and lse: a pass over the logits.
+// dlogits of given dlogp and lse: a pass over the logits, from the last row to the first, since the L2 still holds some
+// of the last rows that token_logprobs read.
+constexpr int kGradChunks = 4;  // of a thread
 template <class Z>
 __global__ void __launch_bounds__(256) token_grad_kernel(const TokenRows g, const float* dlogp) {
-  const int t = blockIdx.y;
+  constexpr int N = kChunk<Z>;
+  const int64_t t = gridDim.y - 1 - blockIdx.y;
   const Z* z = static_cast<const Z*>(g.logits) + t * g.ld;
   bf16* d = g.dlogits + t * g.ldd;
-  const int label = g.labels[t], whole = g.V & ~7;
-  const bool on = label >= 0 && label < g.V;
-  const float k = on ? dlogp[t] * g.scale : 0.f;
-  const float lse = on ? g.lse[t] : 0.f;
-  const int stride = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
-  for (int i = first * 8; i < whole; i += stride * 8) {
-    float v[8] = {};
-    if (on) {
-      unpack8(load8(z + i), v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = -k * pow2(fmaf(v[j], g.scale, -lse) * kLog2e) + (i + j == label ? k : 0.f);
-    }
-    store8(d + i, v);
+  const int label = g.labels[t], whole = g.V / N * N, first = (blockIdx.x * 256 * kGradChunks + threadIdx.x) * N;
+  if (label < 0 || label >= g.V) {
+    const int c0 = blockIdx.x * 256 * kGradChunks * N;
+    zero_row(d + c0, min(256 * kGradChunks * N, g.V - c0), threadIdx.x, 256);
+    return;
   }
-  for (int i = whole + first; i < g.V; i += stride)
-    d[i] = __float2bfloat16_rn(on ? -k * pow2(fmaf(to_f32(z[i]), g.scale, -lse) * kLog2e) + (i == label ? k : 0.f) : 0.f);
+  uint4 raw[kGradChunks];
+#pragma unroll
+  for (int j = 0; j < kGradChunks; ++j)
+    if (first + j * 256 * N < whole) raw[j] = __ldcs(reinterpret_cast<const uint4*>(z + first + j * 256 * N));
+  const float k = dlogp[t] * g.scale;
+  const RowGrad q{g.lse[t] / g.scale, k, -k};
+  const Factor c = factor(g.scale);
+#pragma unroll
+  for (int j = 0; j < kGradChunks; ++j) {
+    const int i = first + j * 256 * N;
+    if (i < whole) {
+      float v[N];
+      unpack_chunk<Z>(raw[j], v);
+      write_chunk<Z>(d + i, v, q, c, label - i);
+    } else {
+      for (int n = i; n < min(i + N, g.V); ++n)
+        d[n] = __float2bfloat16_rn(q.kp * pow2((to_f32(z[n]) - q.m) * c.hi) + (n == label ? k : 0.f));
+    }
+  }
 }
 
-// out = sum of v[0..n) times f, in 64 bits and a fixed order.
-__global__ void __launch_bounds__(1024) sum_kernel(const float* v, int n, double f, float* out) {
-  __shared__ double red[32];
+// out = sum of v[0..n) times f in a fixed order.
+__global__ void __launch_bounds__(1024) sum_kernel(const float* v, int n, float f, float* out) {
+  __shared__ Pair red[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_previous();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) s += static_cast<double>(v[i]);
+  Pair s{0.f, 0.f};
+  for (int i = threadIdx.x; i < n; i += 8 * blockDim.x) {
+    float x[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    for (int j = 0; j < 8; ++j) x[j] = i + j * static_cast<int>(blockDim.x) < n ? v[i + j * blockDim.x] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = add(s, {x[j], 0.f});
+  }
+  auto warp_sum = [&] {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      s = add(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+  };
+  warp_sum();
+  if (lane == 0) red[warp] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.0;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i];
-    *out = static_cast<float>(s * f);
+  if (warp == 0) {
+    s = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : Pair{0.f, 0.f};
+    warp_sum();
+    if (lane == 0) *out = (s.hi + s.lo) * f;
   }
 }
 
@@ -299,8 +529,42 @@ bool grad_ok(const TokenRows& g, int type) {
   if (type == kRowBf16 && g.dlogits == g.logits) return g.ldd == g.ld;
   return !spans_overlap(g.logits, g.ld, row_type_bytes(type), g.dlogits, g.ldd, 2, g.T, g.V);
 }
-unsigned row_threads(int V) { return V <= 1024 ? 128 : V <= 8192 ? 256 : 512; }
+// Blocks of a row: as many as keep the rows that are being worked on, two on an SM, in two thirds of the L2, and, where
+// there are few rows, as have 2048 columns each to do, up to two on an SM.
+constexpr int kShareBytes = 160 << 10;
+int row_blocks(int T, int V, int esz, bool policy) {
+  int n = 1;
+  while (policy && n < 8 && static_cast<int64_t>(V) * esz > static_cast<int64_t>(n) * kShareBytes) n *= 2;
+  while (n < 8 && static_cast<int64_t>(T) * n <= kSms && V / (2 * n) >= 2048) n *= 2;
+  return n;
+}
 
+template <class Z, bool POLICY, int NT>
+cudaError_t launch_blocks(const TokenRows& g, int blocks, cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {static_cast<unsigned>(blocks), 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(g.T) * blocks);
+  cfg.blockDim = dim3(NT);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = blocks > 1 ? 1 : 0;
+  const int share = ((g.V + blocks - 1) / blocks + 7) / 8 * 8;
+  return cudaLaunchKernelEx(&cfg, token_rows_kernel<Z, POLICY, NT>, g, share);
+}
+template <class Z, bool POLICY>
+cudaError_t launch_rows(const TokenRows& g, cudaStream_t s) {
+  if (g.V <= 32 * kWarpChunks * kChunk<Z>) {
+    token_warp_kernel<Z, POLICY><<<(g.T + 3) / 4, 128, 0, s>>>(g);
+    return cudaGetLastError();
+  }
+  const int blocks = row_blocks(g.T, g.V, sizeof(Z), POLICY);
+  const int bytes = g.V / blocks * static_cast<int>(sizeof(Z));
+  if (bytes <= 16 << 10) return launch_blocks<Z, POLICY, 256>(g, blocks, s);
+  if (!POLICY || bytes <= 48 << 10) return launch_blocks<Z, POLICY, 512>(g, blocks, s);
+  return launch_blocks<Z, POLICY, 1024>(g, blocks, s);
+}
 }  // namespace
 
 cudaError_t token_logprobs(const void* logits, int type, int64_t ld, const int32_t* labels, float* logp, float* lse,
@@ -309,9 +573,7 @@ cudaError_t token_logprobs(const void* logits, int type, int64_t ld, const int32
   g.logits = logits, g.ld = ld, g.labels = labels, g.T = T, g.V = V, g.scale = scale, g.logp = logp, g.lse = lse;
   g.err = err;
   if (!rows_args_ok(g, type) || !vec_ok(logp, 4) || !vec_ok(lse, 4)) return cudaErrorInvalidValue;
-  auto* k = type == kRowF32 ? token_rows_kernel<float, false> : token_rows_kernel<bf16, false>;
-  k<<<T, row_threads(V), 0, s>>>(g);
-  return cudaGetLastError();
+  return type == kRowF32 ? launch_rows<float, false>(g, s) : launch_rows<bf16, false>(g, s);
 }
 
 cudaError_t token_logprobs_bwd(const void* logits, int type, int64_t ld, const int32_t* labels, const float* lse,
@@ -322,14 +584,15 @@ cudaError_t token_logprobs_bwd(const void* logits, int type, int64_t ld, const i
   g.lse = const_cast<float*>(lse), g.dlogits = dlogits, g.ldd = ldd;
   if (!rows_args_ok(g, type) || !vec_ok(lse, 4) || !vec_ok(dlogp, 4) || !grad_ok(g, type)) return cudaErrorInvalidValue;
   auto* k = type == kRowF32 ? token_grad_kernel<float> : token_grad_kernel<bf16>;
-  for (int t = 0; t < T; t += 65535) {
+  const int columns = 256 * kGradChunks * (16 / row_type_bytes(type));
+  for (int end = T; end > 0; end -= 65535) {
     TokenRows a = g;
-    const int n = T - t < 65535 ? T - t : 65535;
+    const int n = std::min(end, 65535), t = end - n;
     a.logits = static_cast<const char*>(logits) + t * ld * row_type_bytes(type);
     a.dlogits = dlogits + t * ldd;
     a.labels += t;
     a.lse += t;
-    k<<<dim3((V + 4095) / 4096, n), 256, 0, s>>>(a, dlogp + t);
+    k<<<dim3((V + columns - 1) / columns, n), 256, 0, s>>>(a, dlogp + t);
   }
   return cudaGetLastError();
 }
@@ -346,11 +609,9 @@ cudaError_t policy_loss(const void* logits, int type, int64_t ld, const int32_t*
   if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f) || !std::isfinite(clip_high) || !(kl >= 0.f) ||
       !std::isfinite(kl) || (kl > 0.f && !ref))
     return cudaErrorInvalidValue;
-  auto* k = type == kRowF32 ? token_rows_kernel<float, true> : token_rows_kernel<bf16, true>;
-  k<<<T, row_threads(V), 0, s>>>(g);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = type == kRowF32 ? launch_rows<float, true>(g, s) : launch_rows<bf16, true>(g, s);
   if (e != cudaSuccess) return e;
-  return launch_following(sum_kernel, dim3(1), 1024, 0, s, row_loss, T, 1.0, loss);
+  return launch_following(sum_kernel, dim3(1), 1024, 0, s, row_loss, T, 1.f, loss);
 }
 
 cudaError_t preference_loss(const float* logp, const float* ref, const int32_t* labels, const int32_t* bounds,
@@ -366,7 +627,7 @@ cudaError_t preference_loss(const float* logp, const float* ref, const int32_t* 
                      dlogp};
   const cudaError_t e = launch_following(preference_kernel, dim3(pairs + 1), 512, 0, s, g);
   if (e != cudaSuccess) return e;
-  return launch_following(sum_kernel, dim3(1), 1024, 0, s, pair_loss, pairs, 1.0 / pairs, loss);
+  return launch_following(sum_kernel, dim3(1), 1024, 0, s, pair_loss, pairs, 1.f / static_cast<float>(pairs), loss);
 }
 
 }  // namespace mt
