@@ -52,6 +52,7 @@ constexpr int kSortAhead = 8;      // loads a thread has in flight
 constexpr int kSortSmem = kSortWarps * kSortBins * 4;  // counters; of the other blocks: a bit a row, and zeros
 constexpr int kZeroBlocks = 240;   // with the sorting ones, two on an SM at most
 constexpr int kZeroBytes = kSortSmem / 2;
+constexpr int kClusterTokens = 32768;
 constexpr int kZeroRows = (kSortSmem - kZeroBytes) * 8;
 
 // *p of block `rank` of this cluster.
@@ -66,74 +67,128 @@ __device__ __forceinline__ int cluster_load(const int* p, int rank) {
 struct SortArgs {
   const int32_t* tok;
   int2 *a, *b;  // pairs (token or V, row): the passes go from one to the other
-  int* number;  // of a pair among the equal digits of its warp
+  int* number;  // of a pair among the equal digits of its block
+  int* counts;  // [blocks][bins] of a pass, where the blocks are not a cluster
   int T, V, passes, bits;
   bf16* dE;
   int64_t h;
   int* err;
 };
 
-// Least significant digit first. Each warp of the cluster owns T / 128 consecutive pairs, counts their digits and
-// numbers equal ones; the place of a digit's first pair of a warp is the sum of what comes before it in (digit, block,
-// warp) order, which keeps equal digits in order.
-__device__ void sort_pairs(const SortArgs& g, int* count, int* total, int* base, int* warp_sum) {
-  const int rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int bins = 1 << g.bits;
-  const int each = (g.T + kSortBlocks * kSortWarps - 1) / (kSortBlocks * kSortWarps);
-  const int64_t first = static_cast<int64_t>(rank * kSortWarps + warp) * each;
-  const int lo = static_cast<int>(first < g.T ? first : g.T), hi = min(g.T, lo + each);
-  int* mine = count + warp * bins;
-  for (int pass = 0; pass < g.passes; ++pass) {
-    const int2* src = pass & 1 ? g.a : g.b;
-    int2* dst = pass & 1 ? g.b : g.a;
-    const int shift = pass * g.bits;
-    auto key = [&](int i) {
-      if (pass > 0) return __ldcg(&src[i].x);
-      const int v = g.tok[i];
-      if (v >= g.V) record_bad_token(g.err);
-      return v < 0 || v >= g.V ? g.V : v;
-    };
-    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) count[i] = 0;
-    __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += 32 * kSortAhead) {
-      int k[kSortAhead];
+// Least significant digit first. The blocks own consecutive pairs, and so do a block's warps: each counts the digits
+// of its pairs and numbers equal ones; the place of a digit's first pair of a warp is the sum of what comes before
+// it in (digit, block, warp) order, which keeps equal digits in order.
+struct PassView {
+  const SortArgs& g;
+  const int2* src;
+  int2* dst;
+  int shift, bins, lo, hi;  // this warp's pairs
+  bool first;
+  __device__ PassView(const SortArgs& a, int pass, int block, int blocks)
+      : g(a), src(pass & 1 ? a.a : a.b), dst(pass & 1 ? a.b : a.a), shift(pass * a.bits), bins(1 << a.bits),
+        first(pass == 0) {
+    const int each = (a.T + blocks * kSortWarps - 1) / (blocks * kSortWarps);
+    const int64_t begin = static_cast<int64_t>(block * kSortWarps + (threadIdx.x >> 5)) * each;
+    lo = static_cast<int>(begin < a.T ? begin : a.T);
+    hi = min(a.T, lo + each);
+  }
+  __device__ __forceinline__ int key(int i) const {
+    if (!first) return __ldcg(&src[i].x);
+    const int v = g.tok[i];
+    if (v >= g.V) record_bad_token(g.err);
+    return v < 0 || v >= g.V ? g.V : v;
+  }
+  __device__ __forceinline__ int digit(int k) const { return k >> shift & (bins - 1); }
+};
+// count[warp][digit] = pairs of this digit in the block's warps before; total[digit] of the block; numbers of the pairs
+// within their warp.
+__device__ void count_digits(const PassView& p, int* count, int* total) {
+  const int lane = threadIdx.x & 31;
+  int* mine = count + (threadIdx.x >> 5) * p.bins;
+  for (int i = threadIdx.x; i < kSortWarps * p.bins; i += kSortThreads) count[i] = 0;
+  __syncthreads();
+  for (int i0 = p.lo; i0 < p.hi; i0 += 32 * kSortAhead) {
+    int k[kSortAhead];
 #pragma unroll
-      for (int j = 0; j < kSortAhead; ++j) {
-        const int i = i0 + 32 * j + lane;
-        k[j] = i < hi ? key(i) : 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kSortAhead; ++j) {
-        const int i = i0 + 32 * j + lane;
-        const unsigned active = __ballot_sync(0xffffffffu, i < hi);
-        if (i < hi) {
-          const int d = k[j] >> shift & (bins - 1);
-          const unsigned same = __match_any_sync(active, d);
-          const int n = mine[d], below = __popc(same & ((1u << lane) - 1));
-          g.number[i] = n + below;
-          __syncwarp(active);
-          if (below == 0) mine[d] = n + __popc(same);
-        }
-        __syncwarp();
-      }
+    for (int j = 0; j < kSortAhead; ++j) {
+      const int i = i0 + 32 * j + lane;
+      k[j] = i < p.hi ? p.key(i) : 0;
     }
-    __syncthreads();
-    // per digit: exclusive sums over the block's warps, and the block's total
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) {
-      int s = 0;
+#pragma unroll
+    for (int j = 0; j < kSortAhead; ++j) {
+      const int i = i0 + 32 * j + lane;
+      const unsigned active = __ballot_sync(0xffffffffu, i < p.hi);
+      if (i < p.hi) {
+        const int d = p.digit(k[j]);
+        const unsigned same = __match_any_sync(active, d);
+        const int n = mine[d], below = __popc(same & ((1u << lane) - 1));
+        p.g.number[i] = n + below;
+        __syncwarp(active);
+        if (below == 0) mine[d] = n + __popc(same);
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < p.bins; d += kSortThreads) {
+    int s = 0;
 #pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = count[w * bins + d];
-        count[w * bins + d] = s;
-        s += c;
-      }
-      total[d] = s;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int c = count[w * p.bins + d];
+      count[w * p.bins + d] = s;
+      s += c;
     }
+    total[d] = s;
+  }
+}
+// Where the block's pairs of each digit begin, from digit threadIdx.x's pairs in all blocks and in those before this one.
+__device__ void digit_bases(const PassView& p, int all, int below, int* base, int* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = threadIdx.x;  // bins <= kSortThreads
+  int s = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += v;
+  }
+  if (lane == 31) warp_sum[warp] = s;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  if (d < p.bins) base[d] = before + s - all + below;
+  __syncthreads();
+}
+__device__ void place_pairs(const PassView& p, const int* count, const int* base) {
+  const int lane = threadIdx.x & 31;
+  const int* mine = count ? count + (threadIdx.x >> 5) * p.bins : nullptr;
+  for (int i0 = p.lo; i0 < p.hi; i0 += 32 * kSortAhead) {
+    int2 q[kSortAhead];
+    int n[kSortAhead];
+#pragma unroll
+    for (int j = 0; j < kSortAhead; ++j) {
+      const int i = i0 + 32 * j + lane;
+      if (i >= p.hi) continue;
+      if (p.first) q[j] = make_int2(p.key(i), i);
+      else q[j] = __ldcg(p.src + i);
+      n[j] = __ldcg(p.g.number + i);
+    }
+#pragma unroll
+    for (int j = 0; j < kSortAhead; ++j) {
+      if (i0 + 32 * j + lane >= p.hi) continue;
+      const int d = p.digit(q[j].x);
+      p.dst[base[d] + (mine ? mine[d] : 0) + n[j]] = q[j];
+    }
+  }
+}
+
+// Up to kClusterTokens one cluster does all passes, and its blocks read each other's totals.
+__device__ void sort_pairs(const SortArgs& g, int* count, int* total, int* base, int* warp_sum) {
+  const int rank = blockIdx.x, d = threadIdx.x;
+  for (int pass = 0; pass < g.passes; ++pass) {
+    const PassView p(g, pass, rank, kSortBlocks);
+    count_digits(p, count, total);
     cluster_sync();
-    // what comes before this block's pairs of a digit: those of smaller digits, and of lower blocks
-    const int d = threadIdx.x;  // bins <= kSortThreads
     int below = 0, all = 0;
-    if (d < bins) {
+    if (d < p.bins) {
 #pragma unroll
       for (int r = 0; r < kSortBlocks; ++r) {
         const int c = cluster_load(total + d, r);
@@ -141,38 +196,43 @@ __device__ void sort_pairs(const SortArgs& g, int* count, int* total, int* base,
         all += c;
       }
     }
-    int s = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += v;
-    }
-    if (lane == 31) warp_sum[warp] = s;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    if (d < bins) base[d] = before + s - all + below;
-    __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += 32 * kSortAhead) {
-      int2 p[kSortAhead];
-      int n[kSortAhead];
-#pragma unroll
-      for (int j = 0; j < kSortAhead; ++j) {
-        const int i = i0 + 32 * j + lane;
-        if (i >= hi) continue;
-        if (pass > 0) p[j] = __ldcg(src + i);
-        else p[j] = make_int2(key(i), i);
-        n[j] = g.number[i];
-      }
-#pragma unroll
-      for (int j = 0; j < kSortAhead; ++j) {
-        if (i0 + 32 * j + lane >= hi) continue;
-        const int k = p[j].x >> shift & (bins - 1);
-        dst[base[k] + mine[k] + n[j]] = p[j];
-      }
-    }
+    digit_bases(p, all, below, base, warp_sum);
+    place_pairs(p, count, base);
     cluster_sync();  // pairs written, totals read
   }
+}
+
+// More tokens: a launch that counts and one that places for each pass, over up to kManyBlocks blocks.
+constexpr int kManyBlocks = 128;
+__global__ void __launch_bounds__(kSortThreads) digit_count_kernel(const SortArgs g, int pass) {
+  extern __shared__ __align__(128) char sort_smem[];
+  wait_for_previous();
+  let_next_start();
+  const PassView p(g, pass, blockIdx.x, gridDim.x);
+  int* count = reinterpret_cast<int*>(sort_smem);
+  count_digits(p, count, g.counts + blockIdx.x * p.bins);
+  __syncthreads();
+  // numbers within the block, which the next launch needs alone
+  const int* mine = count + (threadIdx.x >> 5) * p.bins;
+  for (int i = p.lo + (threadIdx.x & 31); i < p.hi; i += 32) g.number[i] += mine[p.digit(p.key(i))];
+}
+__global__ void __launch_bounds__(kSortThreads) digit_place_kernel(const SortArgs g, int pass) {
+  __shared__ int base[kSortBins], warp_sum[kSortWarps];
+  wait_for_previous();
+  let_next_start();
+  const PassView p(g, pass, blockIdx.x, gridDim.x);
+  const int d = threadIdx.x, rank = blockIdx.x;
+  int below = 0, all = 0;
+  if (d < p.bins) {
+#pragma unroll 16
+    for (int r = 0; r < static_cast<int>(gridDim.x); ++r) {
+      const int c = __ldcg(g.counts + r * p.bins + d);
+      below += r < rank ? c : 0;
+      all += c;
+    }
+  }
+  digit_bases(p, all, below, base, warp_sum);
+  place_pairs(p, nullptr, base);
 }
 
 __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortArgs g) {
@@ -227,10 +287,39 @@ struct SumArgs {
   const void* dx;
   bf16* dE;
   float* partial;  // [chunks][2][h]: a run from the chunk before (0), one that goes on into the next (1)
-  int T, V, h, chunk;
+  int T, V, h, chunk, chunks;
   float scale;
   bool add;
 };
+// Zeros in the rows of no token, with the tokens sorted: part `b` of `parts` of the table, columns from c on.
+constexpr int kGapRows = 4096;
+__device__ void zero_gaps(const SumArgs& g, unsigned* used, int b, int parts) {
+  const int v0 = static_cast<int>(static_cast<int64_t>(g.V) * b / parts);
+  const int v1 = static_cast<int>(static_cast<int64_t>(g.V) * (b + 1) / parts);
+  for (int r0 = v0; r0 < v1; r0 += kGapRows) {
+    const int r1 = min(v1, r0 + kGapRows);
+    int lo = 0, hi = g.T;  // the first pair of a token from r0 on
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      if (__ldcg(&g.pairs[mid].x) < r0) lo = mid + 1;
+      else hi = mid;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kGapRows / 32; i += blockDim.x) used[i] = 0;
+    __syncthreads();
+    for (int i = lo + threadIdx.x; i < g.T; i += blockDim.x) {
+      const int v = __ldcg(&g.pairs[i].x);
+      if (v >= r1) break;
+      atomicOr(used + (v - r0) / 32, 1u << ((v - r0) & 31));
+    }
+    __syncthreads();
+    for (int r = r0; r < r1; ++r) {
+      if (used[(r - r0) / 32] >> ((r - r0) & 31) & 1) continue;
+      uint4* row = reinterpret_cast<uint4*>(g.dE + static_cast<int64_t>(r) * g.h);
+      for (int i = threadIdx.x; i < g.h / 8; i += blockDim.x) row[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
 template <int W>
 __device__ __forceinline__ void write_row(const SumArgs& g, int v, int c, const float* acc) {
   bf16* p = g.dE + static_cast<int64_t>(v) * g.h + c;
@@ -254,6 +343,12 @@ __global__ void __launch_bounds__(kSumThreads) run_sum_kernel(const SumArgs g) {
   __shared__ int ends[2];  // the tokens before and behind the chunk
   wait_for_previous();
   let_next_start();
+  if (static_cast<int>(blockIdx.x) >= g.chunks) {
+    static_assert(sizeof(pairs) >= kGapRows / 8, "a bit a row");
+    zero_gaps(g, reinterpret_cast<unsigned*>(pairs), (blockIdx.x - g.chunks) * gridDim.y + blockIdx.y,
+              (gridDim.x - g.chunks) * gridDim.y);
+    return;
+  }
   const int p0 = blockIdx.x * g.chunk, n = min(g.T - p0, g.chunk);
   for (int i = threadIdx.x; i < n; i += blockDim.x) pairs[i] = __ldcg(g.pairs + p0 + i);
   if (threadIdx.x == 0) ends[0] = p0 > 0 ? __ldcg(&g.pairs[p0 - 1].x) : -1;
@@ -298,7 +393,7 @@ __global__ void __launch_bounds__(kSumThreads) run_sum_kernel(const SumArgs g) {
 // The runs that cross a border: one block for each chunk in which such a run begins, 4 columns a thread.
 __global__ void __launch_bounds__(kSumThreads) run_join_kernel(const SumArgs g) {
   const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
-  const int p0 = blockIdx.x * g.chunk, chunks = (g.T + g.chunk - 1) / g.chunk;
+  const int p0 = blockIdx.x * g.chunk;
   wait_for_previous();
   const int64_t end = static_cast<int64_t>(p0) + g.chunk;
   if (end >= g.T) return;
@@ -309,7 +404,7 @@ __global__ void __launch_bounds__(kSumThreads) run_join_kernel(const SumArgs g) 
   int last = blockIdx.x + 1;
   for (int k0 = last;; k0 += blockDim.x) {
     const int k = k0 + threadIdx.x;
-    const int n = __syncthreads_count(k < chunks && __ldcg(&g.pairs[static_cast<int64_t>(k) * g.chunk].x) == cur);
+    const int n = __syncthreads_count(k < g.chunks && __ldcg(&g.pairs[static_cast<int64_t>(k) * g.chunk].x) == cur);
     last = k0 + n;
     if (n < static_cast<int>(blockDim.x)) break;
   }
@@ -359,7 +454,8 @@ cudaError_t embed_lookup(const int32_t* tok, const bf16* E, void* x, int type, i
 uint64_t embed_lookup_bwd_scratch(int T, int h) {
   const int chunk = sum_chunk(T);
   const size_t n = T, chunks = (n + chunk - 1) / chunk;
-  return 2 * round256(n * sizeof(int2)) + round256(n * sizeof(int)) + chunks * 2 * h * sizeof(float);
+  return 2 * round256(n * sizeof(int2)) + round256(n * sizeof(int)) +
+         (T > kClusterTokens ? kManyBlocks * kSortBins * sizeof(int) : 0) + chunks * 2 * h * sizeof(float);
 }
 
 cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16* dE, void* scratch, int T, int h,
@@ -379,20 +475,33 @@ cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16*
   int2* a = reinterpret_cast<int2*>(take(static_cast<size_t>(T) * sizeof(int2)));
   int2* b = reinterpret_cast<int2*>(take(static_cast<size_t>(T) * sizeof(int2)));
   int* number = reinterpret_cast<int*>(take(static_cast<size_t>(T) * sizeof(int)));
-  const SortArgs g{tok, a, b, number, T, V, passes, (bits + passes - 1) / passes, dE, h, err};
-  const unsigned blocks = add ? kSortBlocks : kSortBlocks + kZeroBlocks;
-  cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-  if (e != cudaSuccess) return e;
-  e = launch_following(sort_kernel, dim3(blocks), kSortThreads, kSortSmem, s, g);
-  if (e != cudaSuccess) return e;
+  const bool many = T > kClusterTokens;
+  int* counts = reinterpret_cast<int*>(take(many ? kManyBlocks * kSortBins * sizeof(int) : 0));
+  const SortArgs g{tok, a, b, number, counts, T, V, passes, (bits + passes - 1) / passes, dE, h, err};
+  cudaError_t e;
+  if (many) {
+    for (int pass = 0; pass < passes; ++pass) {
+      const int smem = kSortWarps * (1 << g.bits) * 4;
+      e = launch_following(digit_count_kernel, dim3(kManyBlocks), kSortThreads, smem, s, g, pass);
+      if (e == cudaSuccess) e = launch_following(digit_place_kernel, dim3(kManyBlocks), kSortThreads, 0, s, g, pass);
+      if (e != cudaSuccess) return e;
+    }
+  } else {
+    const unsigned blocks = add ? kSortBlocks : kSortBlocks + kZeroBlocks;
+    e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_following(sort_kernel, dim3(blocks), kSortThreads, kSortSmem, s, g);
+    if (e != cudaSuccess) return e;
+  }
   const int chunk = sum_chunk(T), chunks = (T + chunk - 1) / chunk;
-  const SumArgs r{passes & 1 ? a : b, dx, dE, reinterpret_cast<float*>(at), T, V, h, chunk, scale, add};
+  const SumArgs r{passes & 1 ? a : b, dx, dE, reinterpret_cast<float*>(at), T, V, h, chunk, chunks, scale, add};
   auto grid = [&](int units, unsigned& threads) {
     threads = threads_of(units, kSumThreads);
     return dim3(chunks, (units + threads - 1) / threads);
   };
   unsigned threads;
   dim3 blocks_xy = grid(h * row_type_bytes(type) / 16, threads);
+  if (many && !add) blocks_xy.x += (kZeroBlocks + blocks_xy.y - 1) / blocks_xy.y;
   e = launch_following(type == kRowF32 ? run_sum_kernel<float> : run_sum_kernel<bf16>, blocks_xy, threads, 0, s, r);
   if (e != cudaSuccess || chunks == 1) return e;
   blocks_xy = grid(h / 4, threads);

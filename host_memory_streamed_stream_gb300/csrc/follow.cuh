@@ -11,6 +11,24 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 // Until the kernel before has completed and its writes are visible.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// As below, in clusters of `cluster` blocks.
+template <class... P, class... A>
+cudaError_t launch_cluster_following(void (*kernel)(P...), dim3 grid, unsigned threads, unsigned cluster, size_t smem,
+                                     cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {cluster, 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 // Launch `kernel`, which calls wait_for_previous() before it touches what the kernel before it on the
 // stream reads or writes.
 template <class... P, class... A>

@@ -16,15 +16,27 @@ namespace mt {
 
 namespace {
 
-constexpr int kNormCols = 16;      // columns a thread holds of a row
-constexpr int kNormThreads = 256;  // at least so many threads a block, in groups of whole warps that share a row
+// Threads hold 32 columns of a row each in the forward and 16 in the backward (whose gains' sums take as many registers
+// again); an SM holds 512 of them, with 128 registers each. Rows share a block in groups of whole warps. Arithmetic is in
+// packed pairs: with scalar instructions these kernels are bound by issuing them.
+constexpr int kFwdCols = 32, kBwdCols = 16;
+constexpr int kFwdThreads = 128, kBwdThreads = 256;  // of a block, at least
+constexpr int kSmThreads = 512;
+constexpr int kNormRing = 192 << 10;  // bytes of the rings on an SM
 
 struct NormShape {
-  int group, groups;  // threads a row, rows a block at a time
+  int group, groups, blocks;  // threads a row, rows a block at a time, blocks on an SM
 };
-NormShape norm_shape(int cols) {
-  const int group = ((cols + kNormCols - 1) / kNormCols + 31) / 32 * 32;
-  return {group, std::max(1, kNormThreads / group)};
+NormShape norm_shape(int cols, int each, int least) {
+  NormShape n;
+  n.group = ((cols + each - 1) / each + 31) / 32 * 32;
+  n.groups = std::max(1, least / n.group);
+  n.blocks = std::max(1, kSmThreads / (n.group * n.groups));
+  return n;
+}
+// Rows that a block's ring holds.
+int ring_stages(const NormShape& n, int row_bytes) {
+  return std::max(1, std::min(4, kNormRing / n.blocks / row_bytes));
 }
 
 // A copy of W neighbouring columns, 8 or 16 bytes, into shared memory.
@@ -33,32 +45,39 @@ __device__ __forceinline__ void copy_cols(void* dst, const T* src) {
   if constexpr (W * sizeof(T) == 16) cp_async_chunk(dst, src);
   else cp_async_half(dst, src);
 }
+// W columns as pairs.
+template <class T, int W>
+__device__ __forceinline__ void read_pairs(const T* p, float2* v) {
+  float a[W];
+  read_cols<T, W>(p, a);
+#pragma unroll
+  for (int j = 0; j < W / 2; ++j) v[j] = make_float2(a[2 * j], a[2 * j + 1]);
+}
+template <class T, int W>
+__device__ __forceinline__ void write_pairs(T* p, const float2* v) {
+  float a[W];
+#pragma unroll
+  for (int j = 0; j < W / 2; ++j) a[2 * j] = v[j].x, a[2 * j + 1] = v[j].y;
+  write_cols<T, W>(p, a);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 unpacked(uint32_t p) {
+  return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+}
 
-// Sums over the threads of a row, N values at a time: shuffles and, where the row has several warps, shared memory
-// (two copies in turn, so that one barrier a sum is enough). Every thread adds the warps' sums in the same order.
 template <int N>
-struct RowSum {
-  float red[2][32][N];
-};
-template <int N>
-__device__ __forceinline__ void row_sum(float* v, RowSum<N>& s, int& turn, int group, int id) {
+__device__ __forceinline__ void lane_sums(float* v, int lanes) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (group == 32) return;
-  const int warps = group >> 5, first = id * warps;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s.red[turn][threadIdx.x >> 5][i] = v[i];
-  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int w = first; w < first + warps; ++w)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += s.red[turn][w][i];
-  turn ^= 1;
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
+// The threads of a group meet; `id` of its block.
+__device__ __forceinline__ void group_sync(int id, int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
+}
+__device__ __forceinline__ int lanes_for(int warps) { return warps > 16 ? 32 : warps > 8 ? 16 : warps > 4 ? 8 : warps > 2 ? 4 : warps; }
 
 struct LnFwd {
   const void* x;
@@ -67,65 +86,106 @@ struct LnFwd {
   bf16* y;
   int64_t ldy;
   float *mean, *rstd;
-  int T, h, group;
+  int T, h, group, stages;
   float eps;
 };
 
-// A group a row, with its columns in registers. MAX threads a block at most; the smaller kind leaves room for six blocks
-// on an SM, whose rows overlap.
-template <class X, int MAX>
-__global__ void __launch_bounds__(MAX, MAX == kNormThreads ? 6 : 1) ln_fwd_kernel(const LnFwd g) {
-  constexpr int W = 16 / sizeof(X), K = kNormCols / W;
-  __shared__ RowSum<1> sums;
-  const int id = threadIdx.x / g.group, at = threadIdx.x - id * g.group;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / g.group) + id;
-  if (t >= g.T) return;  // a whole group
-  const X* x = static_cast<const X*>(g.x) + t * g.ldx;
-  const float inv_h = 1.f / static_cast<float>(g.h);
-  int turn = 0;
-  uint4 raw[K];
+// Persistent blocks whose groups take rows in turn; each thread copies its columns of the rows ahead into its own part
+// of a ring in shared memory, so that the loads go on through a row's sums. Mean and squares meet at one barrier: each
+// warp sums the squares about its own mean, and what that leaves out is the warps' means about the row's.
+template <class X>
+__global__ void __launch_bounds__(kSmThreads) ln_fwd_kernel(const LnFwd g) {
+  constexpr int W = 16 / sizeof(X), K = kFwdCols / W;
+  extern __shared__ uint4 ring[];  // [stages][K][threads]
+  __shared__ float4 meet[2][32];   // a warp's columns, mean and squares; two in turn
+  const int id = threadIdx.x / g.group, at = threadIdx.x - id * g.group, groups = blockDim.x / g.group;
+  const int lane = threadIdx.x & 31, warps = g.group >> 5, lanes = lanes_for(warps);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + id, ahead = t;
+  wait_for_previous();
+  let_next_start();
+  auto slot = [&](int st, int k) { return ring + (st * K + k) * blockDim.x + threadIdx.x; };
+  auto load = [&](int st) {
+    if (ahead < g.T) {
+      const X* x = static_cast<const X*>(g.x) + ahead * g.ldx;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (at + k * g.group) * W;
-    if (c < g.h) raw[k] = *reinterpret_cast<const uint4*>(x + c);
-  }
-  float v[K][W], s = 0.f;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if ((at + k * g.group) * W >= g.h) break;
-    read_cols<X, W>(reinterpret_cast<const X*>(&raw[k]), v[k]);
-#pragma unroll
-    for (int j = 0; j < W; ++j) s += v[k][j];
-  }
-  row_sum<1>(&s, sums, turn, g.group, id);
-  const float mean = s * inv_h;
-  s = 0.f;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if ((at + k * g.group) * W >= g.h) break;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      v[k][j] -= mean;
-      s += v[k][j] * v[k][j];
+      for (int k = 0; k < K; ++k) {
+        const int c = (at + k * g.group) * W;
+        if (c < g.h) cp_async_chunk(slot(st, k), x + c);
+      }
+      ahead += step;
     }
-  }
-  row_sum<1>(&s, sums, turn, g.group, id);
-  const float r = rsqrtf(s * inv_h + g.eps);
-  if (at == 0) {
-    g.mean[t] = mean;
-    g.rstd[t] = r;
-  }
-  bf16* y = g.y + t * g.ldy;
+    cp_async_end_group();
+  };
+  for (int i = 0; i < g.stages; ++i) load(i);
+  float2 gain[K][W / 2], bias[K][W / 2] = {};
+  int mine = 0;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (at + k * g.group) * W;
     if (c >= g.h) break;
-    float a[W], b[W] = {};
-    read_cols<bf16, W>(g.gamma + c, a);
-    if (g.beta) read_cols<bf16, W>(g.beta + c, b);
+    mine += W;
+    read_pairs<bf16, W>(g.gamma + c, gain[k]);
+    if (g.beta) read_pairs<bf16, W>(g.beta + c, bias[k]);
+  }
+  const float count = static_cast<float>(__reduce_add_sync(0xffffffffu, mine));
+  const float inv_count = count > 0.f ? 1.f / count : 0.f, inv_h = 1.f / static_cast<float>(g.h);
+  int turn = 0, stage = 0;
+  for (; t < g.T; t += step) {
+    cp_async_wait_groups(g.stages - 1);
+    float2 v[K][W / 2], part[2] = {};
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[k][j] = v[k][j] * r * a[j] + b[j];
-    write_cols<bf16, W>(y + c, v[k]);
+    for (int k = 0; k < K; ++k) {
+      if (k * W >= mine) break;
+      read_pairs<X, W>(reinterpret_cast<const X*>(slot(stage, k)), v[k]);
+#pragma unroll
+      for (int j = 0; j < W / 2; ++j) part[j & 1] = __fadd2_rn(part[j & 1], v[k][j]);
+    }
+    load(stage);
+    stage = stage + 1 == g.stages ? 0 : stage + 1;
+    float mean = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+    lane_sums<1>(&mean, 32);
+    mean *= inv_count;
+    part[0] = part[1] = both(0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * W >= mine) break;
+#pragma unroll
+      for (int j = 0; j < W / 2; ++j) {
+        const float2 d = __fadd2_rn(v[k][j], both(-mean));
+        part[j & 1] = __ffma2_rn(d, d, part[j & 1]);
+      }
+    }
+    float squares = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+    lane_sums<1>(&squares, 32);
+    if (warps > 1) {
+      if (lane == 0) meet[turn][threadIdx.x >> 5] = make_float4(count, mean, squares, 0.f);
+      group_sync(id, g.group);
+      const int w = lane & (lanes - 1);
+      const float4 q = w < warps ? meet[turn][id * warps + w] : make_float4(0.f, 0.f, 0.f, 0.f);
+      mean = q.x * q.y;
+      lane_sums<1>(&mean, lanes);
+      mean *= inv_h;
+      squares = q.z + q.x * (q.y - mean) * (q.y - mean);
+      lane_sums<1>(&squares, lanes);
+      turn ^= 1;
+    }
+    const float r = rsqrtf(squares * inv_h + g.eps);
+    if (at == 0) {
+      g.mean[t] = mean;
+      g.rstd[t] = r;
+    }
+    bf16* y = g.y + t * g.ldy;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * W >= mine) break;
+#pragma unroll
+      for (int j = 0; j < W / 2; ++j) {
+        const float2 n = __fmul2_rn(__fadd2_rn(v[k][j], both(-mean)), both(r));
+        v[k][j] = __ffma2_rn(n, gain[k][j], bias[k][j]);
+      }
+      write_pairs<bf16, W>(y + (at + k * g.group) * W, v[k]);
+    }
   }
 }
 
@@ -144,17 +204,17 @@ struct LnBwd {
   int T, h, group, stages, stage_bytes, share;
 };
 
-// Persistent blocks whose groups take rows in turn; each thread copies its columns of the rows ahead into its own part
-// of a ring in shared memory, so that the loads go on through a row's sums. dy n and dy add up in registers. Rows wider than 512 threads hold are shared by two blocks of a cluster (CL = 2), by columns.
+// The same with dy, x and dres of a row in the ring; dy n and dy add up in registers over a block's rows. Rows wider than
+// 512 threads hold are shared by two blocks of a cluster (CL = 2), by columns.
 template <class X, class D, int CL>
-__global__ void __launch_bounds__(512) ln_bwd_kernel(const LnBwd g) {
-  constexpr int W = sizeof(X) == 4 || sizeof(D) == 4 ? 4 : 8, K = kNormCols / W;
+__global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
+  constexpr int W = sizeof(X) == 4 || sizeof(D) == 4 ? 4 : 8, K = kBwdCols / W;
   constexpr int BX = W * sizeof(X), BD = W * sizeof(D);
   extern __shared__ __align__(16) char bwd_ring[];  // [stages][dy, x, dres][K][threads]; at the end [groups - 1][2][h]
-  __shared__ RowSum<2> sums;
-  __shared__ float2 halves[2][2];
+  __shared__ float2 meet[2][32], halves[2][2];
   const unsigned rank = CL > 1 ? cluster_rank() : 0;
   const int groups = blockDim.x / g.group, id = threadIdx.x / g.group, at = threadIdx.x - id * g.group;
+  const int lane = threadIdx.x & 31, warps = g.group >> 5, lanes = lanes_for(warps);
   const int c0 = static_cast<int>(rank) * g.share, cols = CL > 1 ? min(g.share, g.h - c0) : g.h;
   const int64_t step = static_cast<int64_t>(gridDim.x / CL) * groups;
   const float inv_h = 1.f / static_cast<float>(g.h);
@@ -163,27 +223,41 @@ __global__ void __launch_bounds__(512) ln_bwd_kernel(const LnBwd g) {
   const X* res = g.dres ? static_cast<const X*>(g.dres) + c0 : nullptr;
   int turn = 0, stage = 0, half_turn = 0;
   int64_t t = static_cast<int64_t>(blockIdx.x / CL) * groups + id, ahead = t;
+  wait_for_previous();
+  let_next_start();
   auto slot = [&](int st, int bytes_before, int bytes, int k) {
     return bwd_ring + st * g.stage_bytes + (bytes_before * K) * blockDim.x + (k * blockDim.x + threadIdx.x) * bytes;
   };
-  auto load = [&](int st) {
-    if (ahead < g.T) {
+  auto load = [&](int st) {  // dy and x of the row ahead, whose slots are read first
+    if (ahead >= g.T) return;
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = (at + k * g.group) * W;
-        if (c < cols) {
-          copy_cols<D, W>(slot(st, 0, BD, k), dy + ahead * g.lddy + c);
-          copy_cols<X, W>(slot(st, BD, BX, k), x + ahead * g.ldx + c);
-          if (res) copy_cols<X, W>(slot(st, BD + BX, BX, k), res + ahead * g.lddres + c);
+    for (int k = 0; k < K; ++k) {
+      const int c = (at + k * g.group) * W;
+      if (c < cols) {
+        copy_cols<D, W>(slot(st, 0, BD, k), dy + ahead * g.lddy + c);
+        copy_cols<X, W>(slot(st, BD, BX, k), x + ahead * g.ldx + c);
+      }
+    }
+  };
+  auto load_rest = [&](int st) {
+    if (ahead < g.T) {
+      if (res) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int c = (at + k * g.group) * W;
+          if (c < cols) copy_cols<X, W>(slot(st, BD + BX, BX, k), res + ahead * g.lddres + c);
         }
       }
       ahead += step;
     }
     cp_async_end_group();
   };
-  for (int i = 0; i < g.stages; ++i) load(i);
+  for (int i = 0; i < g.stages; ++i) {
+    load(i);
+    load_rest(i);
+  }
   uint32_t gain[K][W / 2];
-  float dg[K][W] = {}, db[K][W] = {};
+  float2 dg[K][W / 2] = {}, db[K][W / 2] = {};
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (at + k * g.group) * W;
@@ -195,35 +269,40 @@ __global__ void __launch_bounds__(512) ln_bwd_kernel(const LnBwd g) {
   if (t < g.T) r = g.rstd[t], mean = g.mean[t];
   for (; t < g.T; t += step) {
     cp_async_wait_groups(g.stages - 1);
-    float n[K][W], u[K][W], d[K][W], s[2] = {0.f, 0.f};
+    float2 n[K][W / 2], u[K][W / 2], sum[2] = {};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if ((at + k * g.group) * W >= cols) break;
-      read_cols<D, W>(reinterpret_cast<const D*>(slot(stage, 0, BD, k)), u[k]);
-      read_cols<X, W>(reinterpret_cast<const X*>(slot(stage, BD, BX, k)), n[k]);
-      if (res) read_cols<X, W>(reinterpret_cast<const X*>(slot(stage, BD + BX, BX, k)), d[k]);
+      read_pairs<D, W>(reinterpret_cast<const D*>(slot(stage, 0, BD, k)), u[k]);
+      read_pairs<X, W>(reinterpret_cast<const X*>(slot(stage, BD, BX, k)), n[k]);
     }
     load(stage);
-    stage = stage + 1 == g.stages ? 0 : stage + 1;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if ((at + k * g.group) * W >= cols) break;
-      float gk[W];
 #pragma unroll
-      for (int j = 0; j < W / 2; ++j) unpack2(gain[k][j], gk + 2 * j);
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        n[k][j] = (n[k][j] - mean) * r;
-        dg[k][j] += u[k][j] * n[k][j];
-        db[k][j] += u[k][j];
-        u[k][j] *= gk[j];
-        s[0] += u[k][j];
-        s[1] += u[k][j] * n[k][j];
+      for (int j = 0; j < W / 2; ++j) {
+        n[k][j] = __fmul2_rn(__fadd2_rn(n[k][j], both(-mean)), both(r));
+        dg[k][j] = __ffma2_rn(u[k][j], n[k][j], dg[k][j]);
+        db[k][j] = __fadd2_rn(db[k][j], u[k][j]);
+        u[k][j] = __fmul2_rn(u[k][j], unpacked(gain[k][j]));
+        sum[0] = __fadd2_rn(sum[0], u[k][j]);
+        sum[1] = __ffma2_rn(u[k][j], n[k][j], sum[1]);
       }
     }
+    float s[2] = {sum[0].x + sum[0].y, sum[1].x + sum[1].y};
     const float rt = r;
     if (t + step < g.T) r = g.rstd[t + step], mean = g.mean[t + step];
-    row_sum<2>(s, sums, turn, g.group, id);
+    lane_sums<2>(s, 32);
+    if (warps > 1) {
+      if (lane == 0) meet[turn][threadIdx.x >> 5] = make_float2(s[0], s[1]);
+      group_sync(id, g.group);
+      const int w = lane & (lanes - 1);
+      const float2 q = w < warps ? meet[turn][id * warps + w] : make_float2(0.f, 0.f);
+      s[0] = q.x, s[1] = q.y;
+      lane_sums<2>(s, lanes);
+      turn ^= 1;
+    }
     if constexpr (CL > 1) {
       if (threadIdx.x < CL) {
         uint32_t a;
@@ -235,35 +314,39 @@ __global__ void __launch_bounds__(512) ln_bwd_kernel(const LnBwd g) {
       s[1] = halves[half_turn][0].y + halves[half_turn][1].y;
       half_turn ^= 1;
     }
-    const float a0 = s[0] * inv_h, a1 = s[1] * inv_h;
+    const float2 a0 = both(-s[0] * inv_h), a1 = both(-s[1] * inv_h);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (at + k * g.group) * W;
       if (c >= cols) break;
+      float2 d[W / 2];
+      if (res) read_pairs<X, W>(reinterpret_cast<const X*>(slot(stage, BD + BX, BX, k)), d);
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        u[k][j] = rt * (u[k][j] - a0 - n[k][j] * a1);
-        if (res) u[k][j] += d[k][j];
+      for (int j = 0; j < W / 2; ++j) {
+        u[k][j] = __ffma2_rn(n[k][j], a1, __fadd2_rn(u[k][j], a0));
+        u[k][j] = res ? __ffma2_rn(u[k][j], both(rt), d[j]) : __fmul2_rn(u[k][j], both(rt));
       }
-      write_cols<X, W>(static_cast<X*>(g.dx) + t * g.h + c0 + c, u[k]);
-      if (g.dx_bf16) write_cols<bf16, W>(g.dx_bf16 + t * g.h + c0 + c, u[k]);
+      write_pairs<X, W>(static_cast<X*>(g.dx) + t * g.h + c0 + c, u[k]);
+      if (g.dx_bf16) write_pairs<bf16, W>(g.dx_bf16 + t * g.h + c0 + c, u[k]);
     }
+    load_rest(stage);
+    stage = stage + 1 == g.stages ? 0 : stage + 1;
   }
   if constexpr (CL > 1) cluster_sync();  // no block ends while the other may write its half here
   float* out = g.partial + static_cast<int64_t>(blockIdx.x / CL) * 2 * g.h + c0;
+  float2* other = reinterpret_cast<float2*>(bwd_ring);  // [groups - 1][2][h / 2]
   if (groups > 1) {
     cp_async_wait_groups(0);
     __syncthreads();  // the ring is free
-    float* other = reinterpret_cast<float*>(bwd_ring);
     if (id > 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = (at + k * g.group) * W;
         if (c >= cols) break;
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          other[2 * (id - 1) * g.h + c + j] = dg[k][j];
-          other[(2 * id - 1) * g.h + c + j] = db[k][j];
+        for (int j = 0; j < W / 2; ++j) {
+          other[(id - 1) * g.h + c / 2 + j] = dg[k][j];
+          other[(id - 1) * g.h + (g.h + c) / 2 + j] = db[k][j];
         }
       }
     }
@@ -274,70 +357,83 @@ __global__ void __launch_bounds__(512) ln_bwd_kernel(const LnBwd g) {
   for (int k = 0; k < K; ++k) {
     const int c = (at + k * g.group) * W;
     if (c >= cols) break;
-    if (groups > 1) {
-      const float* other = reinterpret_cast<const float*>(bwd_ring);
-      for (int o = 0; o < groups - 1; ++o)
+    for (int o = 0; o < groups - 1; ++o)
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          dg[k][j] += other[2 * o * g.h + c + j];
-          db[k][j] += other[(2 * o + 1) * g.h + c + j];
-        }
-    }
+      for (int j = 0; j < W / 2; ++j) {
+        dg[k][j] = __fadd2_rn(dg[k][j], other[o * g.h + c / 2 + j]);
+        db[k][j] = __fadd2_rn(db[k][j], other[o * g.h + (g.h + c) / 2 + j]);
+      }
 #pragma unroll
-    for (int j = 0; j < W; j += 4) {
-      *reinterpret_cast<float4*>(out + c + j) = make_float4(dg[k][j], dg[k][j + 1], dg[k][j + 2], dg[k][j + 3]);
-      *reinterpret_cast<float4*>(out + g.h + c + j) = make_float4(db[k][j], db[k][j + 1], db[k][j + 2], db[k][j + 3]);
+    for (int j = 0; j < W / 2; j += 2) {
+      *reinterpret_cast<float4*>(out + c + 2 * j) = make_float4(dg[k][j].x, dg[k][j].y, dg[k][j + 1].x, dg[k][j + 1].y);
+      *reinterpret_cast<float4*>(out + g.h + c + 2 * j) =
+          make_float4(db[k][j].x, db[k][j].y, db[k][j + 1].x, db[k][j + 1].y);
     }
   }
 }
 
-// dgamma and dbeta: the blocks' sums added in a fixed order, 32 columns a block.
-__global__ void __launch_bounds__(512) ln_gain_kernel(const float* partial, int parts, int h, bf16* dgamma,
-                                                      bf16* dbeta) {
-  __shared__ float acc[16][33];
+// dgamma and dbeta: the blocks' sums added in a fixed order, 128 columns a block, each warp a part of the sums.
+constexpr int kGainWarps = 16;
+__global__ void __launch_bounds__(32 * kGainWarps) ln_gain_kernel(const float* partial, int parts, int h, bf16* dgamma,
+                                                                  bf16* dbeta) {
+  __shared__ float acc[kGainWarps][128];
   wait_for_previous();
-  const int c = threadIdx.x & 31, w = threadIdx.x >> 5, j = blockIdx.x * 32 + c;
-  float s = 0.f;
-  if (j < 2 * h)
-    for (int p = w; p < parts; p += 16) s += partial[static_cast<int64_t>(p) * 2 * h + j];
-  acc[w][c] = s;
+  let_next_start();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = blockIdx.x * 128 + lane * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (j < 2 * h) {
+#pragma unroll 10
+    for (int p = w; p < parts; p += kGainWarps) {
+      const float4 q = *reinterpret_cast<const float4*>(partial + static_cast<int64_t>(p) * 2 * h + j);
+      s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+    }
+  }
+  *reinterpret_cast<float4*>(&acc[w][lane * 4]) = s;
   __syncthreads();
-  if (w == 0 && j < 2 * h) {
-    s = 0.f;
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (threadIdx.x < 128 && c < 2 * h) {
+    float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s += acc[k][c];
-    bf16* out = j < h ? dgamma + j : dbeta ? dbeta + j - h : nullptr;
-    if (out) *out = __float2bfloat16_rn(s);
+    for (int k = 0; k < kGainWarps; ++k) sum += acc[k][threadIdx.x];
+    bf16* out = c < h ? dgamma + c : dbeta ? dbeta + c - h : nullptr;
+    if (out) *out = __float2bfloat16_rn(sum);
   }
 }
 
-constexpr int kNormRing = 192 << 10;  // bytes of the rings on an SM
+template <class X>
+cudaError_t launch_fwd(LnFwd g, cudaStream_t s) {
+  const NormShape n = norm_shape(g.h, kFwdCols, kFwdThreads);
+  const int threads = n.group * n.groups, row = threads * kFwdCols * static_cast<int>(sizeof(X));
+  g.group = n.group;
+  g.stages = ring_stages(n, row);
+  const cudaError_t e =
+      cudaFuncSetAttribute(ln_fwd_kernel<X>, cudaFuncAttributeMaxDynamicSharedMemorySize, g.stages * row);
+  if (e != cudaSuccess) return e;
+  return launch_following(ln_fwd_kernel<X>, dim3(std::min((g.T + n.groups - 1) / n.groups, kSms * n.blocks)), threads,
+                          g.stages * row, s, g);
+}
 
 struct BwdShape {
-  int group, groups, cluster, blocks, share;  // blocks on an SM; columns of a block of the cluster
+  NormShape n;
+  int cluster, share;  // blocks of a row, and columns of each
 };
 BwdShape bwd_shape(int h) {
-  const int cluster = h > 512 * kNormCols ? 2 : 1;
+  const int cluster = h > kSmThreads * kBwdCols ? 2 : 1;
   const int share = cluster > 1 ? (h / 2 + 7) / 8 * 8 : h;
-  const NormShape n = norm_shape(share);
-  return {n.group, n.groups, cluster, n.group * n.groups > kNormThreads ? 1 : 2, share};
+  return {norm_shape(share, kBwdCols, kBwdThreads), cluster, share};
 }
 template <class X, class D>
-cudaError_t launch_bwd(const LnBwd& g, const BwdShape& n, int parts, int threads, int smem, cudaStream_t s) {
-  auto* k = n.cluster > 1 ? ln_bwd_kernel<X, D, 2> : ln_bwd_kernel<X, D, 1>;
+cudaError_t launch_bwd(LnBwd g, const BwdShape& b, int parts, cudaStream_t s) {
+  const int threads = b.n.group * b.n.groups;
+  const int row = threads * kBwdCols * static_cast<int>(sizeof(D) + sizeof(X) * (g.dres ? 2 : 1));
+  g.stages = ring_stages(b.n, row);
+  g.stage_bytes = row;
+  // at the end the ring holds the sums of all groups but one
+  const int smem = std::max(g.stages * row, (b.n.groups - 1) * 2 * g.h * 4);
+  auto* k = b.cluster > 1 ? ln_bwd_kernel<X, D, 2> : ln_bwd_kernel<X, D, 1>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {static_cast<unsigned>(n.cluster), 1, 1};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(parts * n.cluster);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = n.cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k, g);
+  return launch_cluster_following(k, dim3(parts * b.cluster), threads, b.cluster, smem, s, g);
 }
 
 bool ln_shape_ok(int T, int h) { return T > 0 && h > 0 && h % 8 == 0 && h <= kLayerNormMaxWidth; }
@@ -350,19 +446,14 @@ cudaError_t layernorm_fwd(const void* x, int type, int64_t ldx, const bf16* gamm
       (beta && !vec_ok(beta, 16)) || !vec_ok(mean, 4) || !vec_ok(rstd, 4) || !(eps >= 0.f) || std::isinf(eps) ||
       spans_overlap(x, ldx, row_type_bytes(type), y, ldy, 2, T, h))
     return cudaErrorInvalidValue;
-  const NormShape n = norm_shape(h);
-  const int threads = n.group * n.groups;
-  const LnFwd g{x, ldx, gamma, beta, y, ldy, mean, rstd, T, h, n.group, eps};
-  auto* k = threads <= kNormThreads ? (type == kRowF32 ? ln_fwd_kernel<float, kNormThreads> : ln_fwd_kernel<bf16, kNormThreads>)
-                                    : (type == kRowF32 ? ln_fwd_kernel<float, 1024> : ln_fwd_kernel<bf16, 1024>);
-  k<<<(T + n.groups - 1) / n.groups, threads, 0, s>>>(g);
-  return cudaGetLastError();
+  return type == kRowF32 ? launch_fwd<float>({x, ldx, gamma, beta, y, ldy, mean, rstd, T, h, 0, 0, eps}, s)
+                         : launch_fwd<bf16>({x, ldx, gamma, beta, y, ldy, mean, rstd, T, h, 0, 0, eps}, s);
 }
 
 int layernorm_bwd_parts(int T, int h) {
   if (!ln_shape_ok(T, h)) return 0;
-  const BwdShape n = bwd_shape(h);
-  return std::min((T + n.groups - 1) / n.groups, kSms * n.blocks / n.cluster);
+  const BwdShape b = bwd_shape(h);
+  return std::min((T + b.n.groups - 1) / b.n.groups, kSms * b.n.blocks / b.cluster);
 }
 
 cudaError_t layernorm_bwd(const void* dy, int dy_type, int64_t lddy, const void* x, int type, int64_t ldx,
@@ -386,23 +477,18 @@ cudaError_t layernorm_bwd(const void* dy, int dy_type, int64_t lddy, const void*
       return cudaErrorInvalidValue;
   }
   if (dx_bf16 && spans_overlap(dx, h, esz, dx_bf16, h, 2, T, h)) return cudaErrorInvalidValue;
-  const BwdShape n = bwd_shape(h);
-  const int threads = n.group * n.groups, parts = layernorm_bwd_parts(T, h);
-  const int row = threads * kNormCols * (row_type_bytes(dy_type) + esz * (dres ? 2 : 1));
-  const int stages = std::max(1, std::min(4, kNormRing / n.blocks / row));
-  // at the end the ring holds the sums of all groups but one
-  const int smem = std::max(stages * row, (n.groups - 1) * 2 * h * 4);
-  const LnBwd g{dy, lddy, x, ldx, gamma, mean, rstd, dres, lddres, dx, dx_bf16, partial, T, h, n.group, stages, row,
-                n.share};
+  const BwdShape b = bwd_shape(h);
+  const int parts = layernorm_bwd_parts(T, h);
+  const LnBwd g{dy, lddy, x, ldx, gamma, mean, rstd, dres, lddres, dx, dx_bf16, partial, T, h, b.n.group, 0, 0, b.share};
   cudaError_t e;
   if (type == kRowF32)
-    e = dy_type == kRowF32 ? launch_bwd<float, float>(g, n, parts, threads, smem, s)
-                           : launch_bwd<float, bf16>(g, n, parts, threads, smem, s);
+    e = dy_type == kRowF32 ? launch_bwd<float, float>(g, b, parts, s)
+                           : launch_bwd<float, bf16>(g, b, parts, s);
   else
-    e = dy_type == kRowF32 ? launch_bwd<bf16, float>(g, n, parts, threads, smem, s)
-                           : launch_bwd<bf16, bf16>(g, n, parts, threads, smem, s);
+    e = dy_type == kRowF32 ? launch_bwd<bf16, float>(g, b, parts, s)
+                           : launch_bwd<bf16, bf16>(g, b, parts, s);
   if (e != cudaSuccess) return e;
-  return launch_following(ln_gain_kernel, dim3((2 * h + 31) / 32), 512, 0, s, partial, parts, h, dgamma, dbeta);
+  return launch_following(ln_gain_kernel, dim3((2 * h + 127) / 128), 32 * kGainWarps, 0, s, partial, parts, h, dgamma, dbeta);
 }
 
 }  // namespace mt

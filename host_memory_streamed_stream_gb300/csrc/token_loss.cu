@@ -93,6 +93,12 @@ __device__ __forceinline__ Pair add(const Pair& a, const Pair& b) {
   const float s = a.hi + b.hi, x = s - a.hi;
   return {s, (a.hi - (s - x)) + (b.hi - x) + (a.lo + b.lo)};
 }
+__device__ __forceinline__ Pair add_warp(Pair a) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    a = add(a, {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
+  return a;
+}
 __device__ __forceinline__ Pair product(const Pair& a, float b) {
   const float p = a.hi * b;
   return {p, fmaf(a.hi, b, -p) + a.lo * b};
@@ -234,7 +240,8 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   constexpr int N = kChunk<Z>;
-  if constexpr (POLICY) let_next_start();
+  wait_for_previous();
+  let_next_start();
   if (t >= g.T) return;
   const Z* z = static_cast<const Z*>(g.logits) + t * g.ld;
   bf16* d = POLICY ? g.dlogits + t * g.ldd : nullptr;
@@ -307,8 +314,9 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
   const unsigned rank = cluster_rank(), blocks = cluster_blocks();
   const int64_t t = blockIdx.x / blocks;
   const int c0 = static_cast<int>(rank) * share, cols = min(share, g.V - c0), whole = cols / N * N;
+  wait_for_previous();
+  let_next_start();
   const int label = g.labels[t];
-  if constexpr (POLICY) let_next_start();
   if (label < 0 || label >= g.V) {  // the same for all blocks of the cluster
     if (rank == 0 && threadIdx.x == 0) masked_row<POLICY>(g, t, label);
     if (POLICY) zero_row(g.dlogits + t * g.ldd + c0, cols, threadIdx.x, NT);
@@ -385,6 +393,8 @@ __global__ void __launch_bounds__(256) token_grad_kernel(const TokenRows g, cons
   const int64_t t = gridDim.y - 1 - blockIdx.y;
   const Z* z = static_cast<const Z*>(g.logits) + t * g.ld;
   bf16* d = g.dlogits + t * g.ldd;
+  wait_for_previous();
+  let_next_start();
   const int label = g.labels[t], whole = g.V / N * N, first = (blockIdx.x * 256 * kGradChunks + threadIdx.x) * N;
   if (label < 0 || label >= g.V) {
     const int c0 = blockIdx.x * 256 * kGradChunks * N;
@@ -417,6 +427,7 @@ __global__ void __launch_bounds__(1024) sum_kernel(const float* v, int n, float 
   __shared__ Pair red[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_previous();
+  let_next_start();
   Pair s{0.f, 0.f};
   for (int i = threadIdx.x; i < n; i += 8 * blockDim.x) {
     float x[8];
@@ -425,18 +436,12 @@ __global__ void __launch_bounds__(1024) sum_kernel(const float* v, int n, float 
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = add(s, {x[j], 0.f});
   }
-  auto warp_sum = [&] {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      s = add(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
-  };
-  warp_sum();
+  s = add_warp(s);
   if (lane == 0) red[warp] = s;
   __syncthreads();
   if (warp == 0) {
-    s = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : Pair{0.f, 0.f};
-    warp_sum();
-    if (lane == 0) *out = (s.hi + s.lo) * f;
+    s = add_warp(red[lane]);
+    if (lane == 0) *out = value(s) * f;
   }
 }
 
@@ -460,39 +465,10 @@ struct Preference {
   float *pair_loss, *rewards, *dlogp;
 };
 
-// One block a pair: the sums of its two sequences, its loss, and its rows' dlogp. The last block zeroes the rows
-// of no sequence.
-__global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
-  __shared__ float red[16];
-  wait_for_previous();
-  let_next_start();
-  auto bound = [&](int j) { return min(max(g.bounds[j], 0), g.T); };
-  const int p = blockIdx.x;
-  if (p == g.pairs) {
-    const int first = bound(0), last = max(first, bound(2 * g.pairs));
-    for (int i = threadIdx.x; i < first; i += blockDim.x) g.dlogp[i] = 0.f;
-    for (int i = last + threadIdx.x; i < g.T; i += blockDim.x) g.dlogp[i] = 0.f;
-    return;
-  }
-  float s[2], share[2];
-  int lo[2], hi[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    lo[j] = bound(2 * p + j);
-    hi[j] = bound(2 * p + j + 1);
-    float v = 0.f, n = 0.f;
-    for (int i = lo[j] + threadIdx.x; i < hi[j]; i += blockDim.x) {
-      if (g.labels && g.labels[i] < 0) continue;
-      v += g.ref ? g.logp[i] - g.ref[i] : g.logp[i];
-      n += 1.f;
-    }
-    v = block_total(v, red);
-    n = g.average ? block_total(n, red) : 1.f;
-    share[j] = 1.f / fmaxf(n, 1.f);
-    s[j] = v * share[j];
-  }
-  const float h = g.beta * (s[0] - s[1]) - g.margin;
-  float loss, d;
+// A pair's loss from its two scores, and the derivative by their difference times beta (h).
+__device__ __forceinline__ float pair_loss(const Preference& g, float s0, float s1, float& d) {
+  const float h = g.beta * (s0 - s1) - g.margin;
+  float loss;
   if (g.kind == MTK_PREF_SIGMOID) {
     const float e = expf(-fabsf(h)), l = log1pf(e);  // softplus(-|h|)
     loss = l + (h > 0.f ? g.smoothing * h : (g.smoothing - 1.f) * h);
@@ -505,6 +481,97 @@ __global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
     loss = u * u;
     d = 2.f * u / g.beta;
   }
+  return loss;
+}
+// The row at which sequence j begins, or the one before it ends.
+__device__ __forceinline__ int bound_of(const Preference& g, int j) { return min(max(g.bounds[j], 0), g.T); }
+
+// Few rows: one block does all of it, a warp a sequence at a time.
+constexpr int kFewRows = 4096, kFewPairs = 1024;
+__global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g, float* loss) {
+  __shared__ float score[2 * kFewPairs], share[2 * kFewPairs];
+  __shared__ Pair red[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = 2 * g.pairs;
+  wait_for_previous();
+  let_next_start();
+  for (int j = warp; j < n; j += 32) {
+    const int lo = bound_of(g, j), hi = bound_of(g, j + 1);
+    float v = 0.f, count = 0.f;
+#pragma unroll 8
+    for (int i = lo + lane; i < hi; i += 32) {
+      const bool on = !g.labels || g.labels[i] >= 0;
+      const float a = g.logp[i], b = g.ref ? g.ref[i] : 0.f;
+      v += on ? a - b : 0.f;
+      count += on ? 1.f : 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, o);
+      count += __shfl_xor_sync(0xffffffffu, count, o);
+    }
+    if (lane == 0) {
+      share[j] = g.average ? 1.f / fmaxf(count, 1.f) : 1.f;
+      score[j] = v * share[j];
+      g.rewards[j] = g.beta * score[j];
+    }
+  }
+  __syncthreads();
+  Pair sum{0.f, 0.f};
+  for (int p = threadIdx.x; p < g.pairs; p += 1024) {
+    float d;
+    const float l = pair_loss(g, score[2 * p], score[2 * p + 1], d);
+    g.pair_loss[p] = l;
+    sum = add(sum, {l, 0.f});
+    const float k = g.beta * d / static_cast<float>(g.pairs);
+    score[2 * p] = k * share[2 * p];
+    score[2 * p + 1] = -k * share[2 * p + 1];
+  }
+  sum = add_warp(sum);
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    sum = add_warp(red[lane]);
+    if (lane == 0) *loss = value(sum) / static_cast<float>(g.pairs);
+  }
+  for (int j = warp; j < n; j += 32)
+    for (int i = bound_of(g, j) + lane; i < bound_of(g, j + 1); i += 32)
+      g.dlogp[i] = g.labels && g.labels[i] < 0 ? 0.f : score[j];
+  for (int i = threadIdx.x; i < bound_of(g, 0); i += 1024) g.dlogp[i] = 0.f;
+  for (int i = max(bound_of(g, 0), bound_of(g, n)) + threadIdx.x; i < g.T; i += 1024) g.dlogp[i] = 0.f;
+}
+
+// One block a pair: the sums of its two sequences, its loss, and its rows' dlogp. The last block zeroes the rows
+// of no sequence.
+__global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
+  __shared__ float red[16];
+  wait_for_previous();
+  let_next_start();
+  const int p = blockIdx.x;
+  if (p == g.pairs) {
+    const int first = bound_of(g, 0), last = max(first, bound_of(g, 2 * g.pairs));
+    for (int i = threadIdx.x; i < first; i += blockDim.x) g.dlogp[i] = 0.f;
+    for (int i = last + threadIdx.x; i < g.T; i += blockDim.x) g.dlogp[i] = 0.f;
+    return;
+  }
+  float s[2], share[2];
+  int lo[2], hi[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    lo[j] = bound_of(g, 2 * p + j);
+    hi[j] = bound_of(g, 2 * p + j + 1);
+    float v = 0.f, n = 0.f;
+    for (int i = lo[j] + threadIdx.x; i < hi[j]; i += blockDim.x) {
+      if (g.labels && g.labels[i] < 0) continue;
+      v += g.ref ? g.logp[i] - g.ref[i] : g.logp[i];
+      n += 1.f;
+    }
+    v = block_total(v, red);
+    n = g.average ? block_total(n, red) : 1.f;
+    share[j] = 1.f / fmaxf(n, 1.f);
+    s[j] = v * share[j];
+  }
+  float d;
+  const float loss = pair_loss(g, s[0], s[1], d);
   if (threadIdx.x == 0) {
     g.pair_loss[p] = loss;
     g.rewards[2 * p] = g.beta * s[0];
@@ -541,23 +608,14 @@ int row_blocks(int T, int V, int esz, bool policy) {
 
 template <class Z, bool POLICY, int NT>
 cudaError_t launch_blocks(const TokenRows& g, int blocks, cudaStream_t s) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {static_cast<unsigned>(blocks), 1, 1};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(g.T) * blocks);
-  cfg.blockDim = dim3(NT);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = blocks > 1 ? 1 : 0;
   const int share = ((g.V + blocks - 1) / blocks + 7) / 8 * 8;
-  return cudaLaunchKernelEx(&cfg, token_rows_kernel<Z, POLICY, NT>, g, share);
+  return launch_cluster_following(token_rows_kernel<Z, POLICY, NT>, dim3(static_cast<unsigned>(g.T) * blocks), NT,
+                                  blocks, 0, s, g, share);
 }
 template <class Z, bool POLICY>
 cudaError_t launch_rows(const TokenRows& g, cudaStream_t s) {
   if (g.V <= 32 * kWarpChunks * kChunk<Z>) {
-    token_warp_kernel<Z, POLICY><<<(g.T + 3) / 4, 128, 0, s>>>(g);
-    return cudaGetLastError();
+    return launch_following(token_warp_kernel<Z, POLICY>, dim3((g.T + 3) / 4), 128, 0, s, g);
   }
   const int blocks = row_blocks(g.T, g.V, sizeof(Z), POLICY);
   const int bytes = g.V / blocks * static_cast<int>(sizeof(Z));
@@ -592,9 +650,10 @@ cudaError_t token_logprobs_bwd(const void* logits, int type, int64_t ld, const i
     a.dlogits = dlogits + t * ldd;
     a.labels += t;
     a.lse += t;
-    k<<<dim3((V + columns - 1) / columns, n), 256, 0, s>>>(a, dlogp + t);
+    const cudaError_t e = launch_following(k, dim3((V + columns - 1) / columns, n), 256, 0, s, a, dlogp + t);
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 cudaError_t policy_loss(const void* logits, int type, int64_t ld, const int32_t* labels, const float* old_logp,
@@ -625,6 +684,8 @@ cudaError_t preference_loss(const float* logp, const float* ref, const int32_t* 
     return cudaErrorInvalidValue;
   const Preference g{logp, ref, labels, bounds, pairs, T, kind, beta, margin, smoothing, average, pair_loss, rewards,
                      dlogp};
+  if (T <= kFewRows && pairs <= kFewPairs)
+    return launch_following(preference_few_kernel, dim3(1), 1024, 0, s, g, loss);
   const cudaError_t e = launch_following(preference_kernel, dim3(pairs + 1), 512, 0, s, g);
   if (e != cudaSuccess) return e;
   return launch_following(sum_kernel, dim3(1), 1024, 0, s, pair_loss, pairs, 1.f / static_cast<float>(pairs), loss);
