@@ -25,6 +25,8 @@ __global__ void __launch_bounds__(256) lookup_kernel(const int32_t* tok, const b
                                                      float scale, int* err) {
   constexpr int W = 16 / sizeof(X);
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  wait_for_previous();
+  let_next_start();
   if (t >= T) return;
   const int v = tok[t];
   const bool on = v >= 0 && v < V;
@@ -291,7 +293,7 @@ struct SumArgs {
   float scale;
   bool add;
 };
-// Zeros in the rows of no token, with the tokens sorted: part `b` of `parts` of the table, columns from c on.
+// Zeros in the rows of no token, with the tokens sorted: part `b` of `parts` of the table.
 constexpr int kGapRows = 4096;
 __device__ void zero_gaps(const SumArgs& g, unsigned* used, int b, int parts) {
   const int v0 = static_cast<int>(static_cast<int64_t>(g.V) * b / parts);
@@ -425,7 +427,8 @@ bool embed_shape_ok(int T, int V, int h) {
   return T > 0 && T <= kEmbedMaxTokens && V > 0 && V <= kEmbedMaxVocab && h > 0 && h % 8 == 0 && h <= kEmbedMaxWidth;
 }
 uint64_t table_bytes(int V, int h) { return static_cast<uint64_t>(V) * h * sizeof(bf16); }
-// Sorted rows a block sums.
+// Sorted rows a block sums: few where there are few, so that all SMs have some; many where there are many, which leaves
+// fewer sums at borders (131072 x 4096 bf16: chunks of 128 234 us, of 108, which would make whole waves, 250).
 int sum_chunk(int T) { return T <= 4096 ? 16 : T <= 32768 ? 32 : kSumChunk; }
 // Threads that go over `units` in the fewest turns of at most `most`, and then as evenly as whole warps can.
 int threads_of(int units, int most) {
@@ -445,10 +448,9 @@ cudaError_t embed_lookup(const int32_t* tok, const bf16* E, void* x, int type, i
   const int threads = threads_of(h * row_type_bytes(type) / 16, 256);
   const dim3 block(threads, 256 / threads), grid((T + block.y - 1) / block.y);
   if (type == kRowF32)
-    lookup_kernel<float><<<grid, block, 0, s>>>(tok, E, static_cast<float*>(x), T, h, V, scale, err);
-  else
-    lookup_kernel<bf16><<<grid, block, 0, s>>>(tok, E, static_cast<bf16*>(x), T, h, V, scale, err);
-  return cudaGetLastError();
+    return launch_following(lookup_kernel<float>, grid, block, 0, s, tok, E, static_cast<float*>(x), T, h, V, scale,
+                            err);
+  return launch_following(lookup_kernel<bf16>, grid, block, 0, s, tok, E, static_cast<bf16*>(x), T, h, V, scale, err);
 }
 
 uint64_t embed_lookup_bwd_scratch(int T, int h) {

@@ -32,14 +32,14 @@ cudaError_t launch_cluster_following(void (*kernel)(P...), dim3 grid, unsigned t
 // Launch `kernel`, which calls wait_for_previous() before it touches what the kernel before it on the
 // stream reads or writes.
 template <class... P, class... A>
-cudaError_t launch_following(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+cudaError_t launch_following(void (*kernel)(P...), dim3 grid, dim3 threads, size_t smem, cudaStream_t stream,
                              const A&... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;

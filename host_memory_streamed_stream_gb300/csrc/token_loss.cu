@@ -3,10 +3,11 @@
 //
 //   lse_t = log sum_v exp(a z_tv),  logp_t = a z_t,label - lse_t,  dlogits_tv = a dlogp_t ([v = label] - p_tv)
 //
-// Sums of exponentials run in fp32 against a running maximum, as powers of two (c = a log2 e). The maximum is
-// subtracted before the product with c, which keeps masks of the type's lowest value in range. The label's
-// logit, the maximum and the logarithm meet in 64 bits: a ratio of policies is exp of a small difference of
-// numbers of size 10, of which fp32 would lose 2^-21.
+// Sums of exponentials run in fp32 as powers of two, 2^(c z - m) with c = a log2 e, against a whole number m that
+// is raised where a term would pass 1: rescaling is exact. What an approximation loses always in one direction adds up over the
+// tokens of a sequence, so that c is held as two floats, and the average error of the power is put back. The
+// label's logit, m and the logarithm meet in pairs of floats: a ratio of policies is exp of a small difference
+// of numbers of size 10, of which one float would lose 2^-21.
 #include <algorithm>
 #include <cmath>
 
@@ -19,6 +20,7 @@ namespace mt {
 
 namespace {
 
+constexpr float kMinScale = 0x1p-64f;
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);
 constexpr float kLn2 = 0.6931471805599453f, kLn2Low = 0.6931471805599453 - static_cast<double>(kLn2);
 
@@ -27,61 +29,63 @@ __device__ __forceinline__ float pow2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// c = a log2 e as the sum of two floats: one alone is off by up to 2^-25, which moves a row's logp by that times the
-// label's distance from the mean, always the same way (1e-7 a token, which a sequence of 1000 tokens adds up).
+// The mean relative error of pow2 over any stretch of [-20, 0], measured against 64 bits: -4.9e-8 to -5.1e-8. (Above 0 it is
+// 3.4e-8: exponents are kept at or below 0.)
+constexpr float kPow2Error = -5.0e-8f;
+// c = a log2 e. One float is off by up to 2^-25, which moves a row's logp by that times the label's distance from the
+// mean, always the same way (1e-7 a token, which a sequence of 1000 tokens adds up); hi + lo is not: hi has 12 bits, so
+// that what lo adds to c z is not below its last place, where it would always be lost.
 struct Factor {
-  float hi, lo;
+  float one, hi, lo;
 };
 __device__ __forceinline__ Factor factor(float scale) {
-  const float hi = scale * kLog2e;
-  // scale times log2 e's own rounded-off part, and the product's
-  return {hi, fmaf(scale, kLog2e, -hi) + scale * kLog2eLow};
-}
-__device__ __forceinline__ float times(float d, const Factor& c) { return fmaf(d, c.hi, d * c.lo); }
-__device__ __forceinline__ float2 times(float2 d, const Factor& c) {
-  return __ffma2_rn(d, make_float2(c.hi, c.hi), __fmul2_rn(d, make_float2(c.lo, c.lo)));
+  const float one = scale * kLog2e, hi = __uint_as_float(__float_as_uint(one) & 0xfffff000u);
+  return {one, hi, fmaf(scale, kLog2e, -hi) + scale * kLog2eLow};
 }
 
-// Sum of 2^(c (z - m)) for an m that is not far below the maximum: it is raised only where a term would pass 2^8, which
-// after the first few terms of a row is hardly ever. m = -inf: nothing but -inf so far, sum 0.
+// Sum of 2^(c z - m), m a whole number; -inf: nothing but -inf so far, sum 0. +inf: beyond the range of c z.
 struct MaxSum {
   float m, s;
 };
-__device__ __forceinline__ MaxSum merge(const MaxSum& a, const MaxSum& b, const Factor& c) {
-  const float m = fmaxf(a.m, b.m);
-  const float mm = m == -INFINITY ? 0.f : m;
-  return {m, a.s * pow2(times(a.m - mm, c)) + b.s * pow2(times(b.m - mm, c))};
+// 2^(a - b) for whole a <= b.
+__device__ __forceinline__ float down(float a, float b) {
+  return a == b ? 1.f : __int_as_float((static_cast<int>(fmaxf(a - b, -127.f)) + 127) << 23);
 }
-__device__ __forceinline__ MaxSum merge_warp(MaxSum r, const Factor& c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    r = merge(r, {__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o)}, c);
-  return r;
-}
-__device__ __forceinline__ void raise_max(MaxSum& r, float top, const Factor& c) {
-  if ((top - r.m) * c.hi > 8.f || r.m == -INFINITY) {
-    if (r.s != 0.f) r.s *= pow2(times(r.m - top, c));
-    r.m = top;
-  }
-}
+constexpr float kRoom = 1.f;  // that a raised m leaves: few rows raise it again
 template <int N>
 __device__ __forceinline__ void add_terms(MaxSum& r, const float* z, const Factor& c) {
   float top = z[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) top = fmaxf(top, z[i]);
-  raise_max(r, top, c);
+  top *= c.one;
+  if (top > r.m) {
+    const float m = ceilf(top) + kRoom;
+    r.s *= down(r.m, m);
+    r.m = m;
+  }
   const float m = r.m == -INFINITY ? 0.f : r.m;
   if constexpr (N == 1) {
-    r.s += pow2(times(z[0] - m, c));
+    r.s += pow2(fmaf(z[0], c.lo, fmaf(z[0], c.hi, -m)));
   } else {
-    float2 sum = make_float2(r.s, 0.f);
+    const float2 hi = make_float2(c.hi, c.hi), lo = make_float2(c.lo, c.lo), low = make_float2(-m, -m);
+    // their own sum first: bf16 logits have few values, whose roundings against a long sum would be the same each time
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const float2 x = times(__fadd2_rn(make_float2(z[i], z[i + 1]), make_float2(-m, -m)), c);
+      const float2 q = make_float2(z[i], z[i + 1]), x = __ffma2_rn(q, lo, __ffma2_rn(q, hi, low));
       sum = __fadd2_rn(sum, make_float2(pow2(x.x), pow2(x.y)));
     }
-    r.s = sum.x + sum.y;
+    r.s += sum.x + sum.y;
   }
+}
+// The sum over a warp's lanes, the same in all of them.
+__device__ __forceinline__ MaxSum merge_warp(MaxSum r) {
+  const int i = __float_as_int(r.m), ordered = __reduce_max_sync(0xffffffffu, i ^ (i >> 31 & 0x7fffffff));
+  const float m = __int_as_float(ordered ^ (ordered >> 31 & 0x7fffffff));
+  r.s *= down(r.m, m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
+  return {m, r.s};
 }
 
 // A number held as two floats, the second what the first has lost: a few instructions of 4 cycles where 64-bit
@@ -151,21 +155,23 @@ __device__ __forceinline__ RowInputs<Z> row_inputs(const TokenRows& g, int64_t t
   }
   return r;
 }
-// What the second look at a row needs: dlogits_v = kp 2^(c (z_v - m)) + k [v = label].
+// What the second look at a row needs: dlogits_v = kp 2^(c (z_v - z0) - m) + k [v = label].
 struct RowGrad {
-  float m, k, kp;
+  float z0, m, k, kp;
 };
-// The row's log-probability, and for the policy loss its loss and d loss / d logp. `write`: of several callers, one.
+// The row's log-probability, and for the policy loss its loss and d loss / d logp, from the sum r of 2^(c (z - z0) - m).
+// `write`: of several callers, one.
 template <bool POLICY, class Z>
-__device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, const RowInputs<Z>& in, const MaxSum& r,
-                                              bool write) {
-  const Pair log_sum = log_pair(r.s);
-  const float z = in.label();
-  Pair logp = add(product(add({z, 0.f}, {-r.m, 0.f}), g.scale), negative(log_sum));
+__device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, const RowInputs<Z>& in, float z0,
+                                              const MaxSum& r, bool write) {
+  Pair log_sum = add(product({kLn2, kLn2Low}, r.m), log_pair(r.s));
+  // a power of two is a sum of exact terms
+  if ((__float_as_uint(r.s) & 0x7fffffu) != 0) log_sum = add(log_sum, {-kPow2Error, 0.f});
+  Pair logp = add(product(add({in.label(), 0.f}, {-z0, 0.f}), g.scale), negative(log_sum));
   if (logp.hi > 0.f) logp = {0.f, 0.f};  // by rounding, where the label has all of the probability
   if (write) g.logp[t] = value(logp);
   if constexpr (!POLICY) {
-    if (write) g.lse[t] = value(add(product({r.m, 0.f}, g.scale), log_sum));
+    if (write) g.lse[t] = value(add(product({z0, 0.f}, g.scale), log_sum));
     return {};
   } else {
     const float ratio = expf(value(add(logp, {-in.old_logp, 0.f})));
@@ -183,7 +189,7 @@ __device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, con
     }
     if (write) g.row_loss[t] = in.weight * loss;
     const float k = in.weight * d * g.scale;
-    return {r.m == -INFINITY ? 0.f : r.m, k, -k / r.s};
+    return {z0, r.m == -INFINITY ? 0.f : r.m, k, -k / r.s};
   }
 }
 
@@ -208,8 +214,8 @@ __device__ __forceinline__ void write_chunk(bf16* d, float* v, const RowGrad& q,
   constexpr int N = kChunk<Z>;
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float2 x = __fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), make_float2(-q.m, -q.m)),
-                                make_float2(c.hi, c.hi));
+    const float2 x = __ffma2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), make_float2(-q.z0, -q.z0)),
+                                make_float2(c.one, c.one), make_float2(-q.m, -q.m));
     const float2 p = __fmul2_rn(make_float2(pow2(x.x), pow2(x.y)), make_float2(q.kp, q.kp));
     v[i] = p.x, v[i + 1] = p.y;
   }
@@ -219,6 +225,10 @@ __device__ __forceinline__ void write_chunk(bf16* d, float* v, const RowGrad& q,
   }
   if constexpr (N == 8) __stcs(reinterpret_cast<uint4*>(d), pack8(v));
   else __stcs(reinterpret_cast<uint2*>(d), make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])));
+}
+template <class Z>
+__device__ __forceinline__ bf16 one_grad(Z z, const RowGrad& q, const Factor& c, bool hot) {
+  return __float2bfloat16_rn(q.kp * pow2(fmaf(to_f32(z) - q.z0, c.one, -q.m)) + (hot ? q.k : 0.f));
 }
 // Zeros in the columns [0, n) of a row, by `threads` threads.
 __device__ __forceinline__ void zero_row(bf16* d, int n, int at, int threads) {
@@ -275,10 +285,21 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
       }
     }
   }
-  r = merge_warp(r, c);
+  r = merge_warp(r);
+  float z0 = 0.f;
+  if (r.s == 0.f) {  // beyond the range of c z: with the largest logit subtracted first
+    z0 = -INFINITY;
+    for (int i = lane; i < g.V; i += 32) z0 = fmaxf(z0, to_f32(z[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z0 = fmaxf(z0, __shfl_xor_sync(0xffffffffu, z0, o));
+    r = {0.f, 0.f};
+    for (int i = lane; i < g.V; i += 32) r.s += pow2((to_f32(z[i]) - z0) * c.one);
+    r = merge_warp(r);
+  }
   RowGrad q{};
-  if (lane == 0) q = finish_row<POLICY>(g, t, in, r, true);
+  if (lane == 0) q = finish_row<POLICY>(g, t, in, z0, r, true);
   if constexpr (POLICY) {
+    q.z0 = z0;
     q.m = __shfl_sync(0xffffffffu, q.m, 0);
     q.k = __shfl_sync(0xffffffffu, q.k, 0);
     q.kp = __shfl_sync(0xffffffffu, q.kp, 0);
@@ -290,7 +311,7 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
         write_chunk<Z>(d + col, v, q, c, label - col);
       } else {
         for (int i = col; i < g.V; ++i)
-          d[i] = __float2bfloat16_rn(q.kp * pow2((to_f32(z[i]) - q.m) * c.hi) + (i == label ? q.k : 0.f));
+          d[i] = one_grad(z[i], q, c, i == label);
       }
     }
   }
@@ -308,7 +329,7 @@ __device__ __forceinline__ void cluster_store(MaxSum* p, unsigned rank, const Ma
 template <class Z, bool POLICY, int NT>
 __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRows g, int share) {
   constexpr int N = kChunk<Z>, WARPS = NT / 32;
-  __shared__ MaxSum part[WARPS], others[8];
+  __shared__ MaxSum part[2][WARPS], others[2][8];
   __shared__ RowGrad shared;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned rank = cluster_rank(), blocks = cluster_blocks();
@@ -344,21 +365,31 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
     const float v = to_f32(z[whole + threadIdx.x]);
     add_terms<1>(r, &v, c);
   }
-  r = merge_warp(r, c);
-  if (lane == 0) part[warp] = r;
-  __syncthreads();
-  if (warp == 0) {
-    r = merge_warp(lane < WARPS ? part[lane] : MaxSum{-INFINITY, 0.f}, c);
-    if (blocks > 1 && lane < static_cast<int>(blocks)) cluster_store(&others[rank], lane, r);
-  }
-  if (blocks > 1) {
-    cluster_sync();
-    if (threadIdx.x == 0) {
-      r = others[0];
-      for (unsigned k = 1; k < blocks; ++k) r = merge(r, others[k], c);
+  int turn = 0;
+  auto meet = [&](MaxSum v) {  // over the blocks of the row, in every thread
+    v = merge_warp(v);
+    if (lane == 0) part[turn][warp] = v;
+    __syncthreads();
+    v = merge_warp(lane < WARPS ? part[turn][lane] : MaxSum{-INFINITY, 0.f});
+    if (blocks > 1) {
+      if (warp == 0 && lane < static_cast<int>(blocks)) cluster_store(&others[turn][rank], lane, v);
+      cluster_sync();
+      v = merge_warp(lane < static_cast<int>(blocks) ? others[turn][lane] : MaxSum{-INFINITY, 0.f});
     }
+    turn ^= 1;
+    return v;
+  };
+  r = meet(r);
+  float z0 = 0.f;
+  if (r.s == 0.f) {  // beyond the range of c z: with the largest logit subtracted first
+    r = {-INFINITY, 0.f};
+    for (i = threadIdx.x; i < cols; i += NT) r.m = fmaxf(r.m, to_f32(z[i]));
+    z0 = meet(r).m;
+    r = {0.f, 0.f};
+    for (i = threadIdx.x; i < cols; i += NT) r.s += pow2((to_f32(z[i]) - z0) * c.one);
+    r = meet(r);
   }
-  if (threadIdx.x == 0) shared = finish_row<POLICY>(g, t, in, r, rank == 0);
+  if (threadIdx.x == 0) shared = finish_row<POLICY>(g, t, in, z0, r, rank == 0);
   if constexpr (POLICY) {
     __syncthreads();
     const RowGrad q = shared;
@@ -380,7 +411,7 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
       write_chunk<Z>(d + i, v, q, c, at - i);
     }
     i = whole + threadIdx.x;
-    if (i < cols) d[i] = __float2bfloat16_rn(q.kp * pow2((to_f32(z[i]) - q.m) * c.hi) + (i == at ? q.k : 0.f));
+    if (i < cols) d[i] = one_grad(z[i], q, c, i == at);
   }
 }
 
@@ -406,7 +437,7 @@ __global__ void __launch_bounds__(256) token_grad_kernel(const TokenRows g, cons
   for (int j = 0; j < kGradChunks; ++j)
     if (first + j * 256 * N < whole) raw[j] = __ldcs(reinterpret_cast<const uint4*>(z + first + j * 256 * N));
   const float k = dlogp[t] * g.scale;
-  const RowGrad q{g.lse[t] / g.scale, k, -k};
+  const RowGrad q{g.lse[t] / g.scale, 0.f, k, -k};
   const Factor c = factor(g.scale);
 #pragma unroll
   for (int j = 0; j < kGradChunks; ++j) {
@@ -417,7 +448,7 @@ __global__ void __launch_bounds__(256) token_grad_kernel(const TokenRows g, cons
       write_chunk<Z>(d + i, v, q, c, label - i);
     } else {
       for (int n = i; n < min(i + N, g.V); ++n)
-        d[n] = __float2bfloat16_rn(q.kp * pow2((to_f32(z[n]) - q.m) * c.hi) + (n == label ? k : 0.f));
+        d[n] = one_grad(z[n], q, c, n == label);
     }
   }
 }
@@ -588,7 +619,7 @@ __global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
 
 bool rows_args_ok(const TokenRows& g, int type) {
   return row_type_ok(type) && g.T > 0 && g.V > 0 && rows_ok(g.logits, g.ld, g.V) && vec_ok(g.labels, 4) &&
-         std::isfinite(g.scale) && g.scale > 0.f && (!g.err || vec_ok(g.err, 4));
+         g.scale >= kMinScale && g.scale <= 1.f / kMinScale && (!g.err || vec_ok(g.err, 4));
 }
 // The gradient's rows: apart from the logits', or the bf16 logits themselves.
 bool grad_ok(const TokenRows& g, int type) {

@@ -228,7 +228,7 @@ int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, voi
 /*
  * Log-probabilities of given tokens and the losses of fine-tuning on them, beside the cross-entropy. (The pages name no
  * such objective.) logits [T, V] of `type` with row stride ld (a multiple of 8; V may be any size: columns
- * past V are neither read nor written), labels int32 [T], scale a > 0 (one over the temperature):
+ * past V are neither read nor written), labels int32 [T], scale a (one over the temperature, 2^-64 to 2^64):
  *   lse_t = log sum_v exp(a z_tv),  logp_t = a z_t,label - lse_t,  p_tv = exp(a z_tv - lse_t).
  * A label < 0 marks a row that is not trained (a prompt, padding): nothing of its logits is read, its outputs
  * are 0. A label >= V counts as one and sets *err_flag (device int or NULL) to 16. Logits may be -inf; a row
