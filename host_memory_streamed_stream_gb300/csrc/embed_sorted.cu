@@ -52,7 +52,9 @@ constexpr int kSortBits = 9;       // of a digit at most
 constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortAhead = 8;      // loads a thread has in flight
 constexpr int kSortSmem = kSortWarps * kSortBins * 4;  // counters; of the other blocks: a bit a row, and zeros
-constexpr int kZeroBlocks = 240;   // with the sorting ones, two on an SM at most
+// Blocks that write zeros beside the sort: with its eight, one on an SM (8192 x 4096, 32000 rows: 120 69.6 us, 160, where some
+// SMs have two, 88.8, 240 73.1), or, in the launch of the sums, whatever fits between them (131072: 120 244 us, 240 234).
+constexpr int kZeroBlocks = 120, kGapBlocks = 240;
 constexpr int kZeroBytes = kSortSmem / 2;
 constexpr int kClusterTokens = 32768;
 constexpr int kZeroRows = (kSortSmem - kZeroBytes) * 8;
@@ -282,7 +284,7 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
 // ------------------------------------------------------------------ sums of runs
 constexpr int kSumThreads = 256;  // of 16 bytes of a row each
 constexpr int kSumAhead = 8;      // rows a thread has in flight
-constexpr int kSumChunk = 128;    // sorted rows a block sums, at most
+constexpr int kSumChunk = 256;    // sorted rows a block sums, at most
 
 struct SumArgs {
   const int2* pairs;
@@ -428,8 +430,9 @@ bool embed_shape_ok(int T, int V, int h) {
 }
 uint64_t table_bytes(int V, int h) { return static_cast<uint64_t>(V) * h * sizeof(bf16); }
 // Sorted rows a block sums: few where there are few, so that all SMs have some; many where there are many, which leaves
-// fewer sums at borders (131072 x 4096 bf16: chunks of 128 234 us, of 108, which would make whole waves, 250).
-int sum_chunk(int T) { return T <= 4096 ? 16 : T <= 32768 ? 32 : kSumChunk; }
+// fewer sums at borders. (8192 x 4096 fp32: 32 73.1 us, 64 71.7; 131072 x 4096 bf16: 128 234 us, 256 227, 512 228; 108, which
+// would make whole waves, 250.)
+int sum_chunk(int T) { return T <= 4096 ? 16 : T <= kClusterTokens ? 64 : kSumChunk; }
 // Threads that go over `units` in the fewest turns of at most `most`, and then as evenly as whole warps can.
 int threads_of(int units, int most) {
   const int turns = (units + most - 1) / most;
@@ -503,7 +506,7 @@ cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16*
   };
   unsigned threads;
   dim3 blocks_xy = grid(h * row_type_bytes(type) / 16, threads);
-  if (many && !add) blocks_xy.x += (kZeroBlocks + blocks_xy.y - 1) / blocks_xy.y;
+  if (many && !add) blocks_xy.x += (kGapBlocks + blocks_xy.y - 1) / blocks_xy.y;
   e = launch_following(type == kRowF32 ? run_sum_kernel<float> : run_sum_kernel<bf16>, blocks_xy, threads, 0, s, r);
   if (e != cudaSuccess || chunks == 1) return e;
   blocks_xy = grid(h / 4, threads);
