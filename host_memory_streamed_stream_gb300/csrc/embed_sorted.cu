@@ -19,28 +19,30 @@ namespace mt {
 namespace {
 
 // ------------------------------------------------------------------ lookup
+constexpr int kLookupBlocks = 64;  // on an SM, of which 8 at a time: a block's start costs as much as a short row
 // W columns a thread at a time, 16 bytes of x: blockDim.x threads a row, blockDim.y rows a block.
 template <class X>
 __global__ void __launch_bounds__(256) lookup_kernel(const int32_t* tok, const bf16* E, X* x, int T, int h, int V,
                                                      float scale, int* err) {
   constexpr int W = 16 / sizeof(X);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   wait_for_previous();
   let_next_start();
-  if (t >= T) return;
-  const int v = tok[t];
-  const bool on = v >= 0 && v < V;
-  if (v >= V && threadIdx.x == 0) record_bad_token(err);
-  const bf16* row = E + static_cast<int64_t>(on ? v : 0) * h;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; t < T;
+       t += static_cast<int64_t>(gridDim.x) * blockDim.y) {
+    const int v = tok[t];
+    const bool on = v >= 0 && v < V;
+    if (v >= V && threadIdx.x == 0) record_bad_token(err);
+    const bf16* row = E + static_cast<int64_t>(on ? v : 0) * h;
 #pragma unroll 4
-  for (int c = threadIdx.x * W; c < h; c += blockDim.x * W) {
-    float a[W] = {};
-    if (on) {
-      read_cols<bf16, W>(row + c, a);
+    for (int c = threadIdx.x * W; c < h; c += blockDim.x * W) {
+      float a[W] = {};
+      if (on) {
+        read_cols<bf16, W>(row + c, a);
 #pragma unroll
-      for (int j = 0; j < W; ++j) a[j] *= scale;
+        for (int j = 0; j < W; ++j) a[j] *= scale;
+      }
+      write_cols<X, W>(x + t * h + c, a);
     }
-    write_cols<X, W>(x + t * h + c, a);
   }
 }
 
@@ -225,16 +227,26 @@ __global__ void __launch_bounds__(kSortThreads) digit_place_kernel(const SortArg
   wait_for_previous();
   let_next_start();
   const PassView p(g, pass, blockIdx.x, gridDim.x);
-  const int d = threadIdx.x, rank = blockIdx.x;
+  // the blocks' counts of digit d, in as many shares as there are threads for
+  __shared__ int sums[2][kSortThreads];
+  const int d = threadIdx.x & (p.bins - 1), rank = blockIdx.x, shares = kSortThreads >> g.bits;
   int below = 0, all = 0;
-  if (d < p.bins) {
-#pragma unroll 16
-    for (int r = 0; r < static_cast<int>(gridDim.x); ++r) {
-      const int c = __ldcg(g.counts + r * p.bins + d);
-      below += r < rank ? c : 0;
-      all += c;
-    }
+#pragma unroll 8
+  for (int r = threadIdx.x >> g.bits; r < static_cast<int>(gridDim.x); r += shares) {
+    const int c = __ldcg(g.counts + r * p.bins + d);
+    below += r < rank ? c : 0;
+    all += c;
   }
+  sums[0][threadIdx.x] = below;
+  sums[1][threadIdx.x] = all;
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < p.bins)
+    for (int i = 1; i < shares; ++i) {
+      below += sums[0][threadIdx.x + i * p.bins];
+      all += sums[1][threadIdx.x + i * p.bins];
+    }
+  else
+    below = all = 0;
   digit_bases(p, all, below, base, warp_sum);
   place_pairs(p, nullptr, base);
 }
@@ -449,7 +461,8 @@ cudaError_t embed_lookup(const int32_t* tok, const bf16* E, void* x, int type, i
       ranges_overlap(E, table_bytes(V, h), x, static_cast<uint64_t>(T) * h * row_type_bytes(type)))
     return cudaErrorInvalidValue;
   const int threads = threads_of(h * row_type_bytes(type) / 16, 256);
-  const dim3 block(threads, 256 / threads), grid((T + block.y - 1) / block.y);
+  const dim3 block(threads, 256 / threads);
+  const dim3 grid(std::min<unsigned>((T + block.y - 1) / block.y, kSms * kLookupBlocks));
   if (type == kRowF32)
     return launch_following(lookup_kernel<float>, grid, block, 0, s, tok, E, static_cast<float*>(x), T, h, V, scale,
                             err);

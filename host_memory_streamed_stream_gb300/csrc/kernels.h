@@ -157,7 +157,7 @@ cudaError_t policy_loss(const void* logits, int type, int64_t ld, const int32_t*
                         const float* adv, const float* ref, const float* weights, float clip_low, float clip_high,
                         float kl, float scale, bf16* dlogits, int64_t ldd, float* logp, float* row_loss, float* loss,
                         int T, int V, int* err, cudaStream_t s);
-constexpr int kPreferenceMaxPairs = 1 << 20;
+constexpr int kMaxRows = 1 << 30, kMaxVocab = 1 << 28, kPreferenceMaxPairs = 1 << 20;
 cudaError_t preference_loss(const float* logp, const float* ref, const int32_t* labels, const int32_t* bounds,
                             int pairs, int T, int kind, float beta, float margin, float smoothing, bool average,
                             float* pair_loss, float* loss, float* rewards, float* dlogp, cudaStream_t s);

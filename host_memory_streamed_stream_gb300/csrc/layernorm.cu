@@ -436,7 +436,7 @@ cudaError_t launch_bwd(LnBwd g, const BwdShape& b, int parts, cudaStream_t s) {
   return launch_cluster_following(k, dim3(parts * b.cluster), threads, b.cluster, smem, s, g);
 }
 
-bool ln_shape_ok(int T, int h) { return T > 0 && h > 0 && h % 8 == 0 && h <= kLayerNormMaxWidth; }
+bool ln_shape_ok(int T, int h) { return T > 0 && T <= kMaxRows && h > 0 && h % 8 == 0 && h <= kLayerNormMaxWidth; }
 
 }  // namespace
 

@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
 }
 
 bool rows_args_ok(const TokenRows& g, int type) {
-  return row_type_ok(type) && g.T > 0 && g.V > 0 && rows_ok(g.logits, g.ld, g.V) && vec_ok(g.labels, 4) &&
+  return row_type_ok(type) && g.T > 0 && g.T <= kMaxRows && g.V > 0 && g.V <= kMaxVocab && rows_ok(g.logits, g.ld, g.V) && vec_ok(g.labels, 4) &&
          g.scale >= kMinScale && g.scale <= 1.f / kMinScale && (!g.err || vec_ok(g.err, 4));
 }
 // The gradient's rows: apart from the logits', or the bf16 logits themselves.
@@ -650,8 +650,9 @@ cudaError_t launch_rows(const TokenRows& g, cudaStream_t s) {
   }
   const int blocks = row_blocks(g.T, g.V, sizeof(Z), POLICY);
   const int bytes = g.V / blocks * static_cast<int>(sizeof(Z));
-  if (bytes <= 16 << 10) return launch_blocks<Z, POLICY, 256>(g, blocks, s);
-  if (!POLICY || bytes <= 48 << 10) return launch_blocks<Z, POLICY, 512>(g, blocks, s);
+  if (bytes <= 16 << 10) return launch_blocks<Z, POLICY, 128>(g, blocks, s);
+  if (bytes <= 32 << 10) return launch_blocks<Z, POLICY, 256>(g, blocks, s);
+  if (!POLICY || bytes <= 64 << 10) return launch_blocks<Z, POLICY, 512>(g, blocks, s);
   return launch_blocks<Z, POLICY, 1024>(g, blocks, s);
 }
 }  // namespace
@@ -707,7 +708,7 @@ cudaError_t policy_loss(const void* logits, int type, int64_t ld, const int32_t*
 cudaError_t preference_loss(const float* logp, const float* ref, const int32_t* labels, const int32_t* bounds,
                             int pairs, int T, int kind, float beta, float margin, float smoothing, bool average,
                             float* pair_loss, float* loss, float* rewards, float* dlogp, cudaStream_t s) {
-  if (pairs <= 0 || pairs > kPreferenceMaxPairs || T <= 0 || kind < MTK_PREF_SIGMOID || kind > MTK_PREF_SQUARE ||
+  if (pairs <= 0 || pairs > kPreferenceMaxPairs || T <= 0 || T > kMaxRows || kind < MTK_PREF_SIGMOID || kind > MTK_PREF_SQUARE ||
       !(beta > 0.f) || !std::isfinite(beta) || !std::isfinite(margin) || !(smoothing >= 0.f && smoothing <= 0.5f))
     return cudaErrorInvalidValue;
   if (!vec_ok(logp, 4) || (ref && !vec_ok(ref, 4)) || (labels && !vec_ok(labels, 4)) || !vec_ok(bounds, 4) ||

@@ -362,7 +362,8 @@ def token_logprobs(logits, labels, scale=1.0, err=None):
     softmax(scale * logits), logits f32 or bf16 [T, V] with a row stride that is a multiple of 8, and the
     log of the softmax's sum. A label >= V leaves a code in `err` (see check)."""
     dev, T, V, z, kind, ld, lab = _logits(logits, labels)
-    logp, lse = (torch.empty(T, dtype=torch.float32, device=logits.device) for _ in range(2))
+    logp = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lse = torch.empty_like(logp)
     _ok(_lib.load().mtk_token_logprobs(z, kind, ld, lab, logp.data_ptr(), lse.data_ptr(), T, V, scale,
                                        _flag(err, dev), _stream(dev)), "token_logprobs")
     return logp, lse
@@ -385,9 +386,9 @@ def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, weights=Non
     old_logp), w = weights (None: 1/T). logits, labels, scale as for token_logprobs; out as for its backward."""
     dev, T, V, z, kind, ld, lab = _logits(logits, labels)
     out, ldd = _grad_rows(out, T, V, dev)
-    logp, row_loss = (torch.empty(T, dtype=torch.float32, device=logits.device) for _ in range(2))
-    loss = torch.empty(1, dtype=torch.float32, device=logits.device)
     f32 = torch.float32
+    logp, row_loss = torch.empty_like(labels, dtype=f32), torch.empty_like(labels, dtype=f32)
+    loss = torch.empty(1, dtype=f32, device=logits.device)
     _ok(_lib.load().mtk_policy_loss(z, kind, ld, lab, _vec(old_logp, T, f32, "old_logp", dev),
                                     _vec(advantages, T, f32, "advantages", dev), _opt(ref_logp, T, f32, "ref_logp", dev),
                                     _opt(weights, T, f32, "weights", dev), clip_low, clip_high, kl, scale,
@@ -406,8 +407,9 @@ def preference_loss(logp, bounds, labels=None, ref_logp=None, kind="sigmoid", be
     dev, f32 = _device(logp), torch.float32
     T, n = logp.numel(), bounds.numel() - 1
     _need(n > 0 and n % 2 == 0, "bounds: 2 pairs + 1 row indices")
-    pair_loss, rewards, dlogp = (torch.empty(k, dtype=f32, device=logp.device) for k in (n // 2 + 1, n, T))
-    loss = pair_loss[n // 2:]
+    device = logp.device
+    rewards, dlogp = torch.empty(n, dtype=f32, device=device), torch.empty_like(logp)
+    pair_loss, loss = torch.empty(n // 2, dtype=f32, device=device), torch.empty(1, dtype=f32, device=device)
     _ok(_lib.load().mtk_preference_loss(_vec(logp, T, f32, "logp", dev), _opt(ref_logp, T, f32, "ref_logp", dev),
                                         _opt(labels, T, torch.int32, "labels", dev),
                                         _vec(bounds, n + 1, torch.int32, "bounds", dev), n // 2, T,
@@ -428,7 +430,8 @@ def layernorm_fwd(x, gamma, beta=None, eps=1e-5, out=None):
         out = torch.empty((T, h), dtype=torch.bfloat16, device=x.device)
     py, ykind, ldy = _typed_rows(out, T, h, "out", dev)
     _need(ykind == 1, "out: bf16")
-    mean, rstd = (torch.empty(T, dtype=torch.float32, device=x.device) for _ in range(2))
+    mean = torch.empty(T, dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
     _ok(_lib.load().mtk_layernorm_fwd(px, kind, ldx, _vec(gamma, h, torch.bfloat16, "gamma", dev),
                                       _opt(beta, h, torch.bfloat16, "beta", dev), py, ldy, mean.data_ptr(),
                                       rstd.data_ptr(), T, h, eps, _stream(dev)), "layernorm_fwd")

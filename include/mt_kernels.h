@@ -230,7 +230,7 @@ int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, voi
  * such objective.) logits [T, V] of `type` with row stride ld (a multiple of 8; V may be any size: columns
  * past V are neither read nor written), labels int32 [T], scale a (one over the temperature, 2^-64 to 2^64):
  *   lse_t = log sum_v exp(a z_tv),  logp_t = a z_t,label - lse_t,  p_tv = exp(a z_tv - lse_t).
- * A label < 0 marks a row that is not trained (a prompt, padding): nothing of its logits is read, its outputs
+ * T <= 2^30, V <= 2^28. A label < 0 marks a row that is not trained (a prompt, padding): nothing of its logits is read, its outputs
  * are 0. A label >= V counts as one and sets *err_flag (device int or NULL) to 16. Logits may be -inf; a row
  * with NaN, +inf or nothing but -inf gives NaN, as does a label whose logit is -inf (logp = -inf, and NaN where a
  * loss takes differences of it).
@@ -249,7 +249,7 @@ int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, voi
  * mtk_preference_loss: on pairs of sequences, 2i the preferred and 2i + 1 the other one. Sequence j holds the rows
  *   bounds[j] <= t < bounds[j+1] (DEVICE int32 [2 pairs + 1], not decreasing, clamped to [0, T]); its score s_j is the sum of
  *   logp - ref_logp over its rows with labels >= 0 (labels NULL: all; ref_logp NULL: 0; average != 0: their
- *   mean, 0 of no rows). With h = beta (s_2i - s_2i+1) - margin the pair's loss is
+ *   mean, 0 of no rows; a label >= V counts here, but is reported above). With h = beta (s_2i - s_2i+1) - margin the pair's loss is
  *     MTK_PREF_SIGMOID  (1 - smoothing) softplus(-h) + smoothing softplus(h)
  *     MTK_PREF_HINGE    max(0, 1 - h)
  *     MTK_PREF_SQUARE   ((h - 1/2) / beta)^2
@@ -274,7 +274,8 @@ int mtk_preference_loss(const void* logp, const void* ref_logp, const void* labe
 /*
  * Layer norm beside the RMSNorm: y bf16 = n gamma + beta, n = (x - mean) rstd, mean f32 [T] the row's mean and
  * rstd f32 [T] = 1/sqrt(mean((x - mean)^2) + eps). x [T, h] of `type` with row stride ldx, y with row stride
- * ldy; gamma, beta bf16 [h], 16-byte aligned (beta may be NULL). h a multiple of 8, at most 16384. y must not overlap x.
+ * ldy; gamma, beta bf16 [h], 16-byte aligned (beta may be NULL). T <= 2^30, h a multiple of 8, at most 16384. y must not
+ * overlap x.
  *
  * mtk_layernorm_bwd: with u = dy gamma: dx = dres + rstd (u - mean(u) - n mean(u n)) over the h columns, from dy [T, h]
  * of dy_type (row stride lddy), the forward's x, mean and rstd and dres of x's type (row stride lddres, or
