@@ -4,10 +4,17 @@
 //   lse_t = log sum_v exp(a z_tv),  logp_t = a z_t,label - lse_t,  dlogits_tv = a dlogp_t ([v = label] - p_tv)
 //
 // Sums of exponentials run in fp32 as powers of two, 2^(c z - m) with c = a log2 e, against a whole number m that
-// is raised where a term would pass 1: rescaling is exact. What an approximation loses always in one direction adds up over the
-// tokens of a sequence, so that c is held as two floats, and the average error of the power is put back. The
-// label's logit, m and the logarithm meet in pairs of floats: a ratio of policies is exp of a small difference
-// of numbers of size 10, of which one float would lose 2^-21.
+// is raised where a term would pass 1: rescaling is exact. What an approximation loses always in one direction adds up
+// over the tokens of a sequence, so that c is held as two floats, and the average error of the power is put back: a
+// token's logp is off by 1e-7 and its mean by less than 1e-8 (152064 columns, from 1.9e-7 without). The label's
+// logit, m and the logarithm meet in pairs of floats: a ratio of policies is exp of a small difference of numbers
+// of size 10, of which one float would lose 2^-21.
+//
+// Bound by HBM. Log-probabilities: 6144 rows of 32000 fp32 119 us, 6.6 TB/s, 3072 of 152064 bf16 148 us, 6.3 TB/s
+// (where the exponential unit is 70 % busy). Policy loss, whose second look at a row reads the L2: 202 us, 5.8 TB/s,
+// and 351 us, 5.3 TB/s. Gradient alone: 4048 rows of 152064 bf16, a quarter of them masked, 295 us, 6.7 TB/s with what
+// the L2 still holds. What did not help the policy loss: a ring of shared memory that holds the row, filled by cp.async
+// (370 and 645 us), bulk prefetches of the next row into the L2 (272, 524), persistent blocks (210, 392).
 #include <algorithm>
 #include <cmath>
 
@@ -29,8 +36,8 @@ __device__ __forceinline__ float pow2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The mean relative error of pow2 over any stretch of [-20, 0], measured against 64 bits: -4.9e-8 to -5.1e-8. (Above 0 it is
-// 3.4e-8: exponents are kept at or below 0.)
+// The mean relative error of pow2 over any stretch of [-20, 0], measured against 64 bits: -4.9e-8 to -5.1e-8. (Above 0
+// it is 3.4e-8: exponents are kept at or below 0.)
 constexpr float kPow2Error = -5.0e-8f;
 // c = a log2 e. One float is off by up to 2^-25, which moves a row's logp by that times the label's distance from the
 // mean, always the same way (1e-7 a token, which a sequence of 1000 tokens adds up); hi + lo is not: hi has 12 bits, so
@@ -68,7 +75,7 @@ __device__ __forceinline__ void add_terms(MaxSum& r, const float* z, const Facto
     r.s += pow2(fmaf(z[0], c.lo, fmaf(z[0], c.hi, -m)));
   } else {
     const float2 hi = make_float2(c.hi, c.hi), lo = make_float2(c.lo, c.lo), low = make_float2(-m, -m);
-    // their own sum first: bf16 logits have few values, whose roundings against a long sum would be the same each time
+    // their own sum first: bf16 logits have few values, whose roundings against a long sum are the same each time
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
@@ -78,6 +85,10 @@ __device__ __forceinline__ void add_terms(MaxSum& r, const float* z, const Facto
     r.s += sum.x + sum.y;
   }
 }
+// Beyond this m (logits of 45000 at scale 1) c z is no longer good to 2^-20, and finally out of range: such rows are
+// summed again with the largest logit z0 subtracted before the product, as are rows of nothing but -inf.
+constexpr float kFarthest = 65536.f;
+__device__ __forceinline__ bool too_far(const MaxSum& r) { return !(fabsf(r.m) <= kFarthest); }
 // The sum over a warp's lanes, the same in all of them.
 __device__ __forceinline__ MaxSum merge_warp(MaxSum r) {
   const int i = __float_as_int(r.m), ordered = __reduce_max_sync(0xffffffffu, i ^ (i >> 31 & 0x7fffffff));
@@ -159,8 +170,8 @@ __device__ __forceinline__ RowInputs<Z> row_inputs(const TokenRows& g, int64_t t
 struct RowGrad {
   float z0, m, k, kp;
 };
-// The row's log-probability, and for the policy loss its loss and d loss / d logp, from the sum r of 2^(c (z - z0) - m).
-// `write`: of several callers, one.
+// The row's log-probability, and for the policy loss its loss and d loss / d logp, from the sum r of
+// 2^(c (z - z0) - m). `write`: of several callers, one.
 template <bool POLICY, class Z>
 __device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, const RowInputs<Z>& in, float z0,
                                               const MaxSum& r, bool write) {
@@ -193,9 +204,8 @@ __device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, con
   }
 }
 
-// ------------------------------------------------------------------ rows in registers and in shared memory
-// Both kernels read the logits from memory once and keep the row on the SM until its gradient is written, in
-// chunks of 16 bytes: the thread that loaded a chunk is the only one that reads it.
+// ------------------------------------------------------------------ rows
+// In chunks of 16 bytes; neighbouring threads take neighbouring chunks.
 template <class Z>
 constexpr int kChunk = 16 / static_cast<int>(sizeof(Z));  // columns of a chunk
 
@@ -287,7 +297,7 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
   }
   r = merge_warp(r);
   float z0 = 0.f;
-  if (r.s == 0.f) {  // beyond the range of c z: with the largest logit subtracted first
+  if (too_far(r)) {
     z0 = -INFINITY;
     for (int i = lane; i < g.V; i += 32) z0 = fmaxf(z0, to_f32(z[i]));
 #pragma unroll
@@ -310,15 +320,15 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
         unpack_chunk<Z>(raw[j], v);
         write_chunk<Z>(d + col, v, q, c, label - col);
       } else {
-        for (int i = col; i < g.V; ++i)
-          d[i] = one_grad(z[i], q, c, i == label);
+        for (int i = col; i < g.V; ++i) d[i] = one_grad(z[i], q, c, i == label);
       }
     }
   }
 }
 
-// Longer rows: a block a row, or, for very wide and for few rows, a cluster of blocks that split it by columns. The policy
-// loss reads the row a second time, from the L2, for its gradient.
+// Longer rows: a block a row, or, for very wide and for few rows, a cluster of blocks that split it by columns, with
+// two loads of a thread in flight (one: 240 us for 6144 rows of 32000 fp32, two 204, four at half the threads 266). The
+// policy loss reads the row a second time, from the L2, for its gradient.
 // *p of block `rank` of the cluster = v.
 __device__ __forceinline__ void cluster_store(MaxSum* p, unsigned rank, const MaxSum& v) {
   uint32_t a;
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
   };
   r = meet(r);
   float z0 = 0.f;
-  if (r.s == 0.f) {  // beyond the range of c z: with the largest logit subtracted first
+  if (too_far(r)) {
     r = {-INFINITY, 0.f};
     for (i = threadIdx.x; i < cols; i += NT) r.m = fmaxf(r.m, to_f32(z[i]));
     z0 = meet(r).m;
@@ -447,8 +457,7 @@ __global__ void __launch_bounds__(256) token_grad_kernel(const TokenRows g, cons
       unpack_chunk<Z>(raw[j], v);
       write_chunk<Z>(d + i, v, q, c, label - i);
     } else {
-      for (int n = i; n < min(i + N, g.V); ++n)
-        d[n] = one_grad(z[n], q, c, n == label);
+      for (int n = i; n < min(i + N, g.V); ++n) d[n] = one_grad(z[n], q, c, n == label);
     }
   }
 }
@@ -502,11 +511,12 @@ __device__ __forceinline__ float pair_loss(const Preference& g, float s0, float 
   float loss;
   if (g.kind == MTK_PREF_SIGMOID) {
     const float e = expf(-fabsf(h)), l = log1pf(e);  // softplus(-|h|)
-    loss = l + (h > 0.f ? g.smoothing * h : (g.smoothing - 1.f) * h);
+    // an infinite h times a smoothing of 0 is nothing
+    loss = l + (h <= 0.f ? (g.smoothing - 1.f) * h : g.smoothing > 0.f || h != h ? g.smoothing * h : 0.f);
     d = g.smoothing - (h > 0.f ? e : 1.f) / (1.f + e);
   } else if (g.kind == MTK_PREF_HINGE) {
-    loss = 1.f - h > 0.f ? 1.f - h : 0.f * h;
-    d = h < 1.f ? -1.f : 0.f * h;
+    loss = h >= 1.f ? 0.f : 1.f - h;
+    d = h < 1.f ? -1.f : h >= 1.f ? 0.f : h;  // NaN stays
   } else {
     const float u = (h - 0.5f) / g.beta;
     loss = u * u;
@@ -518,6 +528,7 @@ __device__ __forceinline__ float pair_loss(const Preference& g, float s0, float 
 __device__ __forceinline__ int bound_of(const Preference& g, int j) { return min(max(g.bounds[j], 0), g.T); }
 
 // Few rows: one block does all of it, a warp a sequence at a time.
+// (4048 rows of 8 sequences: 5.3 us, as two launches 6.1 and 2.9.)
 constexpr int kFewRows = 4096, kFewPairs = 1024;
 __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g, float* loss) {
   __shared__ float score[2 * kFewPairs], share[2 * kFewPairs];
@@ -618,8 +629,9 @@ __global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
 }
 
 bool rows_args_ok(const TokenRows& g, int type) {
-  return row_type_ok(type) && g.T > 0 && g.T <= kMaxRows && g.V > 0 && g.V <= kMaxVocab && rows_ok(g.logits, g.ld, g.V) && vec_ok(g.labels, 4) &&
-         g.scale >= kMinScale && g.scale <= 1.f / kMinScale && (!g.err || vec_ok(g.err, 4));
+  return row_type_ok(type) && g.T > 0 && g.T <= kMaxRows && g.V > 0 && g.V <= kMaxVocab &&
+         rows_ok(g.logits, g.ld, g.V) && vec_ok(g.labels, 4) && g.scale >= kMinScale && g.scale <= 1.f / kMinScale &&
+         (!g.err || vec_ok(g.err, 4));
 }
 // The gradient's rows: apart from the logits', or the bf16 logits themselves.
 bool grad_ok(const TokenRows& g, int type) {
@@ -627,8 +639,9 @@ bool grad_ok(const TokenRows& g, int type) {
   if (type == kRowBf16 && g.dlogits == g.logits) return g.ldd == g.ld;
   return !spans_overlap(g.logits, g.ld, row_type_bytes(type), g.dlogits, g.ldd, 2, g.T, g.V);
 }
-// Blocks of a row: as many as keep the rows that are being worked on, two on an SM, in two thirds of the L2, and, where
-// there are few rows, as have 2048 columns each to do, up to two on an SM.
+// Blocks of a row. The policy loss: as many as keep the rows that are being worked on, two on an SM, within what the L2
+// holds of them (3072 rows of 152064 bf16, 304 KB: one block 370 us, two 347, four 437; 128 KB: one 202, two 272). Few
+// rows: as many as have 2048 columns each to do, up to two on an SM.
 constexpr int kShareBytes = 160 << 10;
 int row_blocks(int T, int V, int esz, bool policy) {
   int n = 1;
@@ -645,11 +658,12 @@ cudaError_t launch_blocks(const TokenRows& g, int blocks, cudaStream_t s) {
 }
 template <class Z, bool POLICY>
 cudaError_t launch_rows(const TokenRows& g, cudaStream_t s) {
-  if (g.V <= 32 * kWarpChunks * kChunk<Z>) {
+  if (g.V <= 32 * kWarpChunks * kChunk<Z>)
     return launch_following(token_warp_kernel<Z, POLICY>, dim3((g.T + 3) / 4), 128, 0, s, g);
-  }
   const int blocks = row_blocks(g.T, g.V, sizeof(Z), POLICY);
   const int bytes = g.V / blocks * static_cast<int>(sizeof(Z));
+  // About eight chunks a thread, so that the starts of many rows overlap (4127 rows of 10.5 KB: 256 threads 40 us with
+  // the call, 128 35), and, without a second look, sixteen and more (128 KB rows: 1024 threads 127 us, 512 121).
   if (bytes <= 16 << 10) return launch_blocks<Z, POLICY, 128>(g, blocks, s);
   if (bytes <= 32 << 10) return launch_blocks<Z, POLICY, 256>(g, blocks, s);
   if (!POLICY || bytes <= 64 << 10) return launch_blocks<Z, POLICY, 512>(g, blocks, s);
@@ -708,8 +722,9 @@ cudaError_t policy_loss(const void* logits, int type, int64_t ld, const int32_t*
 cudaError_t preference_loss(const float* logp, const float* ref, const int32_t* labels, const int32_t* bounds,
                             int pairs, int T, int kind, float beta, float margin, float smoothing, bool average,
                             float* pair_loss, float* loss, float* rewards, float* dlogp, cudaStream_t s) {
-  if (pairs <= 0 || pairs > kPreferenceMaxPairs || T <= 0 || T > kMaxRows || kind < MTK_PREF_SIGMOID || kind > MTK_PREF_SQUARE ||
-      !(beta > 0.f) || !std::isfinite(beta) || !std::isfinite(margin) || !(smoothing >= 0.f && smoothing <= 0.5f))
+  if (pairs <= 0 || pairs > kPreferenceMaxPairs || T <= 0 || T > kMaxRows || kind < MTK_PREF_SIGMOID ||
+      kind > MTK_PREF_SQUARE || !(beta > 0.f) || !std::isfinite(beta) || !std::isfinite(margin) ||
+      !(smoothing >= 0.f && smoothing <= 0.5f))
     return cudaErrorInvalidValue;
   if (!vec_ok(logp, 4) || (ref && !vec_ok(ref, 4)) || (labels && !vec_ok(labels, 4)) || !vec_ok(bounds, 4) ||
       !vec_ok(pair_loss, 4) || !vec_ok(loss, 4) || !vec_ok(rewards, 4) || !vec_ok(dlogp, 4))

@@ -390,10 +390,11 @@ def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, weights=Non
     logp, row_loss = torch.empty_like(labels, dtype=f32), torch.empty_like(labels, dtype=f32)
     loss = torch.empty(1, dtype=f32, device=logits.device)
     _ok(_lib.load().mtk_policy_loss(z, kind, ld, lab, _vec(old_logp, T, f32, "old_logp", dev),
-                                    _vec(advantages, T, f32, "advantages", dev), _opt(ref_logp, T, f32, "ref_logp", dev),
-                                    _opt(weights, T, f32, "weights", dev), clip_low, clip_high, kl, scale,
-                                    out.data_ptr(), ldd, logp.data_ptr(), row_loss.data_ptr(), loss.data_ptr(), T, V,
-                                    _flag(err, dev), _stream(dev)), "policy_loss")
+                                    _vec(advantages, T, f32, "advantages", dev),
+                                    _opt(ref_logp, T, f32, "ref_logp", dev), _opt(weights, T, f32, "weights", dev),
+                                    clip_low, clip_high, kl, scale, out.data_ptr(), ldd, logp.data_ptr(),
+                                    row_loss.data_ptr(), loss.data_ptr(), T, V, _flag(err, dev), _stream(dev)),
+        "policy_loss")
     return loss, row_loss, logp, out
 
 
@@ -481,8 +482,8 @@ def embed_lookup(tok, E, scale=1.0, dtype=torch.float32, err=None):
 
 
 def embed_lookup_bwd(tok, dx, V, scale=1.0, accumulate=None, err=None):
-    """dE bf16 [V, h] of embed_lookup from dx f32 or bf16 [T, h], the same from run to run. accumulate: a dE to add to (its
-    rows of no token stay), such as the gradient of a head that shares the table."""
+    """dE bf16 [V, h] of embed_lookup from dx f32 or bf16 [T, h], the same from run to run. accumulate: a dE to add to
+    (its rows of no token stay), such as the gradient of a head that shares the table."""
     dev, T = _device(dx), tok.numel()
     rows, h, kind = _table_rows(dx, "dx", dev)
     _need(rows == T, "dx: one row for each token")

@@ -227,34 +227,36 @@ int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, voi
 
 /*
  * Log-probabilities of given tokens and the losses of fine-tuning on them, beside the cross-entropy. (The pages name no
- * such objective.) logits [T, V] of `type` with row stride ld (a multiple of 8; V may be any size: columns
- * past V are neither read nor written), labels int32 [T], scale a (one over the temperature, 2^-64 to 2^64):
+ * such objective.) logits [T, V] of `type` with row stride ld (a multiple of 8; V may be any size: columns past V are
+ * neither read nor written), labels int32 [T], scale a (one over the temperature, 2^-64 to 2^64), T <= 2^30, V <= 2^28:
  *   lse_t = log sum_v exp(a z_tv),  logp_t = a z_t,label - lse_t,  p_tv = exp(a z_tv - lse_t).
- * T <= 2^30, V <= 2^28. A label < 0 marks a row that is not trained (a prompt, padding): nothing of its logits is read, its outputs
- * are 0. A label >= V counts as one and sets *err_flag (device int or NULL) to 16. Logits may be -inf; a row
- * with NaN, +inf or nothing but -inf gives NaN, as does a label whose logit is -inf (logp = -inf, and NaN where a
- * loss takes differences of it).
+ * A label < 0 marks a row that is not trained (a prompt, padding): nothing of its logits is read, its outputs are 0. A
+ * label >= V counts as one and sets *err_flag (device int or NULL) to 16. Logits may be -inf or of any finite size; a
+ * row with NaN, +inf or nothing but -inf gives NaN, and a label whose logit is -inf the logp -inf.
  *
  * mtk_token_logprobs: logp f32 [T] and lse f32 [T].
- * mtk_token_logprobs_bwd: dlogits bf16 [T, V] (row stride ldd) = a dlogp_t ([v = label] - p_tv) from dlogp f32 [T]
- *   and the forward's lse. dlogits may be the bf16 logits themselves (the same address and stride), else they
- *   must not overlap (MT_EINVAL).
- * mtk_policy_loss: the clipped policy loss with a KL term, loss and gradient in one call. With
- *   r = exp(logp - old_logp), A = advantages, w = weights (f32 [T]; NULL: 1/T for every row):
+ * mtk_token_logprobs_bwd: dlogits bf16 [T, V] (row stride ldd) = a dlogp_t ([v = label] - p_tv) from dlogp f32 [T] and
+ *   the forward's lse (whose rounding p takes on: 2^-24 of lse's size). dlogits may be the bf16 logits themselves (the
+ *   same address and stride), else they must not overlap (MT_EINVAL).
+ * mtk_policy_loss: the clipped policy loss with a KL term, loss and gradient in one call. With r = exp(logp -
+ *   old_logp), A = advantages, w = weights (f32 [T]; NULL: 1/T for every row):
  *     l_t = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(ref - logp) - (ref - logp) - 1)
- *     loss = sum_t w l,  dlogits = w l' a ([v = label] - p),  l' = -(r A where r A is the smaller) + kl (1 - exp(ref - logp)).
- *   old_logp, advantages, ref_logp f32 [T] (ref_logp may be NULL where kl = 0); 0 <= clip_low <= 1,
- *   clip_high >= 0, kl >= 0. Writes logp f32 [T], row_loss f32 [T] = w l, loss f32 [1] and dlogits (as above).
- *   The sum runs in a fixed order.
+ *     loss = sum_t w l,  dlogits = w l' a ([v = label] - p),
+ *     l' = -(r A, where that is the smaller or both are the same) + kl (1 - exp(ref - logp)).
+ *   old_logp, advantages, ref_logp f32 [T] (ref_logp may be NULL where kl = 0); 0 <= clip_low <= 1, clip_high >= 0,
+ *   kl >= 0. Writes logp f32 [T], row_loss f32 [T] = w l, loss f32 [1] and dlogits (as above). The sum runs in a fixed
+ *   order.
  * mtk_preference_loss: on pairs of sequences, 2i the preferred and 2i + 1 the other one. Sequence j holds the rows
- *   bounds[j] <= t < bounds[j+1] (DEVICE int32 [2 pairs + 1], not decreasing, clamped to [0, T]); its score s_j is the sum of
- *   logp - ref_logp over its rows with labels >= 0 (labels NULL: all; ref_logp NULL: 0; average != 0: their
- *   mean, 0 of no rows; a label >= V counts here, but is reported above). With h = beta (s_2i - s_2i+1) - margin the pair's loss is
+ *   bounds[j] <= t < bounds[j+1] (DEVICE int32 [2 pairs + 1], not decreasing, clamped to [0, T]); its score s_j is the
+ *   sum of logp - ref_logp over its rows with labels >= 0 (labels NULL: all; ref_logp NULL: 0; average != 0: their
+ *   mean, 0 of no rows; a label >= V counts here, but is reported above). With h = beta (s_2i - s_2i+1) - margin the
+ *   pair's loss is
  *     MTK_PREF_SIGMOID  (1 - smoothing) softplus(-h) + smoothing softplus(h)
  *     MTK_PREF_HINGE    max(0, 1 - h)
  *     MTK_PREF_SQUARE   ((h - 1/2) / beta)^2
  *   loss f32 [1] is the mean over pairs, pair_loss f32 [pairs], rewards f32 [2 pairs] = beta s_j and dlogp f32 [T] the
- *   loss's gradient (0 for rows of no sequence). beta > 0, 0 <= smoothing <= 1/2 (sigmoid only), 1 <= pairs <= 2^20.
+ *   loss's gradient (0 for rows of no sequence). beta > 0, 0 <= smoothing <= 1/2 (used by sigmoid only), 1 <= pairs <=
+ *   2^20.
  */
 #define MTK_PREF_SIGMOID 0
 #define MTK_PREF_HINGE 1
@@ -274,8 +276,8 @@ int mtk_preference_loss(const void* logp, const void* ref_logp, const void* labe
 /*
  * Layer norm beside the RMSNorm: y bf16 = n gamma + beta, n = (x - mean) rstd, mean f32 [T] the row's mean and
  * rstd f32 [T] = 1/sqrt(mean((x - mean)^2) + eps). x [T, h] of `type` with row stride ldx, y with row stride
- * ldy; gamma, beta bf16 [h], 16-byte aligned (beta may be NULL). T <= 2^30, h a multiple of 8, at most 16384. y must not
- * overlap x.
+ * ldy; gamma, beta bf16 [h], 16-byte aligned (beta may be NULL). T <= 2^30, h a multiple of 8, at most 16384. y must
+ * not overlap x.
  *
  * mtk_layernorm_bwd: with u = dy gamma: dx = dres + rstd (u - mean(u) - n mean(u n)) over the h columns, from dy [T, h]
  * of dy_type (row stride lddy), the forward's x, mean and rstd and dres of x's type (row stride lddres, or
@@ -291,13 +293,14 @@ int mtk_layernorm_bwd(const void* dy, int dy_type, int64_t lddy, const void* x, 
                       void* dx, void* dx_bf16, void* partial, void* dgamma, void* dbeta, int T, int h, void* stream);
 
 /*
- * Embedding with a scale, and its gradient by sorted tokens: no order or offsets from the host, padding, fp32 or bf16 rows.
- * mtk_embed_lookup: x [T, h] of `type` = scale E[tok_t], E bf16 [V, h]; tok int32 [T]. A token < 0 is
- *   padding (a row of zeros); one >= V counts as padding and sets *err_flag (device int or NULL) to 16.
+ * Embedding with a scale, and its gradient by sorted tokens: no order or offsets from the host, padding, fp32 or bf16
+ * rows.
+ * mtk_embed_lookup: x [T, h] of `type` = scale E[tok_t], E bf16 [V, h]; tok int32 [T]. A token < 0 is padding (a row of
+ *   zeros); one >= V counts as padding and sets *err_flag (device int or NULL) to 16.
  * mtk_embed_lookup_bwd: dE bf16 [V, h] = scale * the sum of the rows dx_t (of `type`, contiguous) with tok_t = v, in
- *   fp32 and an order that depends on T only; rows of no token become 0. accumulate != 0: the sum is added to
- *   dE's rows instead (as for a table that is also the LM head's), rows of no token stay as they are. scratch: device memory
- *   of mtk_embed_lookup_bwd_scratch_bytes(T, h) bytes, not shared by calls that may run at the same time.
+ *   fp32 and an order that depends on tok, T and h only; rows of no token become 0. accumulate != 0: the sum is added
+ *   to dE's rows instead (as for a table that is also the LM head's), rows of no token stay as they are. scratch:
+ *   device memory of mtk_embed_lookup_bwd_scratch_bytes(T, h) bytes, not shared by calls that may run at the same time.
  * T <= 2^26, V <= 2^24, h a multiple of 8, at most 65536. x, dE and scratch overlap nothing else.
  */
 int mtk_embed_lookup(const void* tok, const void* E, void* x, int type, int T, int h, int V, float scale,

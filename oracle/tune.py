@@ -9,8 +9,9 @@ def token_logprobs(z, labels, scale=1.0):
     on = labels >= 0
     with np.errstate(invalid="ignore", divide="ignore"):
         m = y.max(1)
-        lse = m + np.log(np.exp(y - m[:, None]).sum(1))
-        logp = y[np.arange(len(y)), np.where(on, labels, 0)] - lse
+        log_sum = np.log(np.exp(y - m[:, None]).sum(1))
+        lse = m + log_sum
+        logp = y[np.arange(len(y)), np.where(on, labels, 0)] - m - log_sum  # exact differences of far logits
     return np.where(on, logp, 0.0), np.where(on, lse, 0.0)
 
 

@@ -1,7 +1,7 @@
 """Embedding lookup with a scale and its gradient by sorted tokens, against float64; the ends of a step together.
 
-Tolerances. The lookup is one product, rounded once to its type (bf16: 2^-8, fp32: 2^-24). A gradient's row is an fp32 sum of n
-rows in some order: n 2^-24 of the sum of sizes, then one rounding to bf16.
+Tolerances. The lookup is one product, rounded once to its type (bf16: 2^-8, fp32: 2^-24). A gradient's row is an fp32
+sum of n rows in some order: n 2^-24 of the sum of sizes, then one rounding to bf16.
 """
 import numpy as np
 import pytest
@@ -123,7 +123,7 @@ def test_ids_outside_the_table(K):
 
 
 def test_at_once_and_captured(K):
-    """Gradients on two streams at the same time, and in two graphs replayed at the same time, give what they give alone."""
+    """Gradients on two streams at the same time, and in two graphs replayed at the same time: what they give alone."""
     rng = np.random.default_rng(4)
     sets = []
     for T, h, V in ((9000, 520, 32000), (3000, 1032, 4000)):
@@ -184,8 +184,8 @@ def _chain(E, G, b, W, tok, lab, old, adv):
 
 
 def test_step_of_them_together(K):
-    """Embedding, layer norm, the GEMMs of the head, the policy loss and all gradients back to the table, twice as used and
-    once replayed from a graph. bf16 holds y, dz and the gradients (2^-8 each), so the results are compared in
+    """Embedding, layer norm, the GEMMs of the head, the policy loss and all gradients back to the table, twice as used
+    and once replayed from a graph. bf16 holds y, dz and the gradients (2^-8 each), so the results are compared in
     norm, with room for the four roundings on the longest way (y, z's sums of y, dz, and the result): 4 * 2^-8."""
     rng = np.random.default_rng(6)
     T, h, V = 256, 128, 512

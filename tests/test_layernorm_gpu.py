@@ -1,8 +1,9 @@
 """Layer norm, forward and backward, against float64.
 
-Tolerances. A sum over a row runs in chains of at most 16 terms a thread, 5 shuffles and 32 warps: 2^-24 * 64 = 2^-18 of the
-sum of sizes bounds it, and what is done with it adds a few steps. With C = 2^-17: mean within C mean|x|; n = (x - mean)
-rstd within C (|n| + mean|x| rstd) (rstd's own error is that of n's sum of squares). bf16 results add half a step, 2^-8.
+Tolerances. A sum over a row runs in chains of at most 32 terms a thread, 5 shuffles and 32 warps: 2^-24 * 128 = 2^-17
+of the sum of sizes bounds it, with what is done with it (a few steps). With C = 2^-17: mean within C mean|x|; n = (x -
+mean) rstd within C (|n| + mean|x| rstd) (rstd's own error is that of n's sum of squares). bf16 results add half a
+step, 2^-8.
 """
 import numpy as np
 import pytest
@@ -65,7 +66,7 @@ def test_forward(K, T, h, kind, bias, pad):
 
 
 def test_forward_far_from_zero(K):
-    """A mean 2^12 times the spread: the squares are of centred values, so it costs 2^-12 of the precision, not 2^-24."""
+    """A mean 2^12 times the spread: the squares are of centred values, which costs 2^-12 of it, not 2^-24."""
     rng = np.random.default_rng(3)
     x = _rows(rng, 5, 4096, "f32", size=0.25, offset=1024.0)
     g = torch.ones(4096, dtype=torch.bfloat16, device="cuda")

@@ -127,7 +127,8 @@ def test_loss_refusals(lib):
                                        d, None)
 
     for kw in (dict(logp=None), dict(ref=P + 2), dict(lab=P + 2), dict(bounds=None), dict(pairs=0),
-               dict(pairs=(1 << 20) + 1), dict(T=0), dict(T=(1 << 30) + 1), dict(kind=3), dict(kind=-1), dict(beta=0.0), dict(beta=inf),
+               dict(pairs=(1 << 20) + 1), dict(T=0), dict(T=(1 << 30) + 1), dict(kind=3), dict(kind=-1), dict(beta=0.0),
+               dict(beta=inf),
                dict(margin=nan), dict(smooth=-0.1), dict(smooth=0.6), dict(smooth=nan), dict(pl=None), dict(loss=None),
                dict(rew=P + 2), dict(d=None)):
         assert pref(**kw) == -1, kw
@@ -138,7 +139,8 @@ def test_norm_and_embedding_refusals(lib):
         return lib.mtk_layernorm_fwd(x, type, ldx, g, b, y, ldy, mean, rstd, T, h, eps, None)
 
     for kw in (dict(x=None), dict(x=P + 8), dict(type=3), dict(ldx=56), dict(ldx=68), dict(g=None), dict(g=P + 8),
-               dict(b=P + 2), dict(y=None), dict(y=Q + 4), dict(ldy=60), dict(mean=None), dict(rstd=P + 2), dict(T=0), dict(T=(1 << 30) + 1),
+               dict(b=P + 2), dict(y=None), dict(y=Q + 4), dict(ldy=60), dict(mean=None), dict(rstd=P + 2), dict(T=0),
+               dict(T=(1 << 30) + 1),
                dict(h=0), dict(h=60), dict(h=16392, ldx=16392, ldy=16392), dict(eps=-1.0), dict(eps=float("nan")),
                dict(y=P), dict(y=P + 512)):
         assert fwd(**kw) == -1, kw
@@ -153,7 +155,8 @@ def test_norm_and_embedding_refusals(lib):
     for kw in (dict(dy=None), dict(dt=2), dict(lddy=60), dict(x=None), dict(type=2), dict(ldx=32), dict(g=P + 4),
                dict(mean=None), dict(rstd=None), dict(res=P, ldr=60), dict(res=P + 4, ldr=64), dict(dx=None),
                dict(dx=R + 8), dict(dxb=R + 16384, type=1), dict(dxb=R + 64), dict(part=None), dict(part=P + 4),
-               dict(dg=None), dict(db=P + 1), dict(T=0), dict(T=(1 << 30) + 1), dict(h=12), dict(dx=Q), dict(dx=P), dict(dx=P + 512),
+               dict(dg=None), dict(db=P + 1), dict(T=0), dict(T=(1 << 30) + 1), dict(h=12), dict(dx=Q), dict(dx=P),
+               dict(dx=P + 512),
                dict(res=R, ldr=72), dict(res=R + 256, ldr=64)):
         assert bwd(**kw) == -1, kw
     assert lib.mtk_layernorm_bwd_parts(0, 64) == 0 and lib.mtk_layernorm_bwd_parts(4, 60) == 0

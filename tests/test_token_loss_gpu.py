@@ -1,9 +1,10 @@
 """Log-probabilities of given tokens and the losses on them, against float64.
 
 Tolerances. A bf16 result is off by half a step at most (2^-8 of its size). A row's lse: each term 2^(c z - max) has a
-rounded factor c and a rounded exponent (2^-24 of |a z - lse| each, 2 R) and the exponential's own error (2^-22), and the
-sum is of at most V / 128 + 16 terms in a chain, 2^-24 each: LSE(V, R) = 2^-24 (2 R + 4 + V / 128 + 16), R the largest
-|a z - lse| that matters, bounded by the largest |a z - lse| of the row. A result adds half a step of its own, 2^-24.
+rounded factor c and a rounded exponent (2^-24 of |a z - lse| each, 2 R) and the exponential's own error (2^-22), and
+the sum is of at most V / 128 + 16 terms in a chain, 2^-24 each: LSE(V, R) = 2^-24 (2 R + 4 + V / 128 + 16), R the
+largest |a z - lse| that matters, bounded by the largest |a z - lse| of the row. A result adds half a step of its own,
+2^-24.
 """
 import numpy as np
 import pytest
@@ -139,8 +140,8 @@ def test_policy(K, T, V, kind, kl, weighted):
     assert np.all(np.abs(_np(row) - R) <= terr + F * np.abs(R))
     assert abs(float(loss) - L) <= np.sum(terr) + F * (np.abs(R).sum() + abs(L))
     kerr = scale * np.abs(wr) * (r * np.abs(adv) * (tol + 8 * F) + kl * (q + 1) * (tol + 8 * F))
-    assert np.all(np.abs(_np(d) - D) <= HALF * np.abs(D) * (1 + HALF) + 2 * kerr[:, None] + np.abs(D) * (tol[:, None] + 8 * F)
-                  + 1e-38)
+    perr = np.abs(D) * (tol[:, None] + 8 * F)
+    assert np.all(np.abs(_np(d) - D) <= HALF * np.abs(D) * (1 + HALF) + 2 * kerr[:, None] + perr + 1e-38)
     assert np.all(_np(d)[~on] == 0) and torch.all(out[:, V:] == 7.0) and int(err.item()) == 0
     if T > 1:  # the fixed order: the same bits again
         again = K.policy_loss(z, *args, **kw)
@@ -174,7 +175,8 @@ def test_many_rows(K):
     assert torch.all(dl[~torch.tensor(on).cuda()] == 0)
     # at ratio 1 neither side of the clip holds: the gradient is that of -A logp / T
     want = tune.token_logprobs_bwd(x, lab, -w.astype(np.float64) / T)
-    assert np.all(np.abs(_np(dl) - want) <= HALF * np.abs(want) + (np.abs(w) / T)[:, None] * (4 * tol + 32 * F)[:, None])
+    room = (np.abs(w) / T * (4 * tol + 32 * F))[:, None]
+    assert np.all(np.abs(_np(dl) - want) <= HALF * np.abs(want) + room)
 
 
 @pytest.mark.parametrize("V", [40, 2000, 33000, 152064])
@@ -207,6 +209,58 @@ def test_values_at_the_ends(K, V):
         assert bool(torch.isnan(row[5])) and bool(torch.isnan(g[5]).all()) and bool(torch.isnan(loss))
         # ratio 0 for the impossible label: nothing to gain, no gradient through it
         assert float(row[1]) == 0.0
+
+
+@pytest.mark.parametrize("V", [72, 5000, 40000, 170000])
+@pytest.mark.parametrize("T", [3, 200])
+def test_far_logits(K, V, T):
+    """Logits far from 0, where c z loses its fraction: rows of nothing but a mask's value, equal huge ones, a mask
+    beside ordinary ones, an offset that leaves the fp32 logits 2^-8. Against float64 of the same fp32 values: with the
+    largest logit subtracted first, what remains is the tolerance of near rows."""
+    rng = np.random.default_rng(V + T)
+    z = torch.tensor(rng.standard_normal((T, V)), dtype=torch.float32).cuda()
+    z[0] = -1.0e9
+    z[1] = 3.0e12
+    z[1, ::3] = 2.9e12
+    z[2, :] += 60000.0
+    if T > 3:
+        z[3, 5:] = -1.0e9
+        z[4] -= 1.0e5
+        z[5] *= 3.0e4
+    lab = (np.arange(T) % 5).astype(np.int32)
+    lab[1] = 1
+    lt = _dev(lab, torch.int32)
+    x = _np(z)
+    rl, rs = tune.token_logprobs(x, lab)
+    logp, lse = K.token_logprobs(z, lt)
+    spread = np.where(np.abs(x - x.max(1, keepdims=True)) < 100, np.abs(x - rs[:, None]), 0).max(1)
+    # a rounded factor on distances up to |z - max| <= 100 (beyond, a term is 0), the row's size in lse itself
+    tol = F * (2 * (spread + 110) + 4 + V / 128 + 16)
+    assert np.all(np.abs(_np(logp) - rl) <= tol + 2 * F * np.abs(rl))
+    assert np.all(np.abs(_np(lse) - rs) <= tol + F * np.abs(rs))
+    adv = rng.standard_normal(T).astype(np.float32)
+    old = _dev(rl + 0.01)
+    loss, row, lp, d = K.policy_loss(z, lt, old, _dev(adv))
+    ref = tune.policy_loss(x, lab, _np(old), adv)[3]
+    k = np.abs(adv / T * np.exp(rl - _np(old)))[:, None]
+    room = k * (2 * tol + 3 * F * np.abs(rl) + 16 * F)[:, None]
+    assert np.all(np.abs(_np(lp) - rl) <= tol + 2 * F * np.abs(rl))  # summed over other blocks than logp
+    assert np.all(np.abs(_np(d) - ref) <= HALF * np.abs(ref) + 2 * room + 1e-38)
+
+
+def test_preference_of_impossible_tokens(K):
+    """A rejected answer with a token of probability 0: nothing left to gain; a preferred one: an infinite loss."""
+    inf = float("inf")
+    b = _dev([0, 2, 4], torch.int32)
+    for pad in (0, 5000):  # both forms of the kernel
+        tail = [0.0] * pad
+        for kind in ("sigmoid", "hinge"):
+            loss, rew, d = K.preference_loss(_dev([-1.0, -2.0, -inf, -1.0] + tail), b, kind=kind)
+            assert float(loss) == 0.0 and float(rew[1]) == -inf and torch.all(d == 0)
+            loss, _, d = K.preference_loss(_dev([-1.0, -inf, -2.0, -1.0] + tail), b, kind=kind, beta=0.5)
+            assert float(loss) == inf and d[:4].tolist() == [-0.5, -0.5, 0.5, 0.5]
+            loss, _, d = K.preference_loss(_dev([-1.0, float("nan"), -2.0, -1.0] + tail), b, kind=kind)
+            assert bool(torch.isnan(loss)) and bool(torch.isnan(d[:4]).all())
 
 
 def test_label_outside_the_vocabulary(K):
