@@ -380,31 +380,28 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
   }
 }
 
-// dgamma and dbeta: the blocks' sums added in a fixed order, 128 columns a block, each warp a part of the sums.
+// dgamma and dbeta: the blocks' sums added in a fixed order, 32 columns a block, each warp a part of the sums (304 x 2 x
+// 4096: 6 us, with 128 columns a block 11).
 constexpr int kGainWarps = 16;
 __global__ void __launch_bounds__(32 * kGainWarps) ln_gain_kernel(const float* partial, int parts, int h, bf16* dgamma,
                                                                   bf16* dbeta) {
-  __shared__ float acc[kGainWarps][128];
+  __shared__ float acc[kGainWarps][33];
   wait_for_previous();
   let_next_start();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = blockIdx.x * 128 + lane * 4;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
+  float s = 0.f;
   if (j < 2 * h) {
 #pragma unroll 10
-    for (int p = w; p < parts; p += kGainWarps) {
-      const float4 q = *reinterpret_cast<const float4*>(partial + static_cast<int64_t>(p) * 2 * h + j);
-      s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
-    }
+    for (int p = w; p < parts; p += kGainWarps) s += partial[static_cast<int64_t>(p) * 2 * h + j];
   }
-  *reinterpret_cast<float4*>(&acc[w][lane * 4]) = s;
+  acc[w][lane] = s;
   __syncthreads();
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (threadIdx.x < 128 && c < 2 * h) {
-    float sum = 0.f;
+  if (w == 0 && j < 2 * h) {
+    s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kGainWarps; ++k) sum += acc[k][threadIdx.x];
-    bf16* out = c < h ? dgamma + c : dbeta ? dbeta + c - h : nullptr;
-    if (out) *out = __float2bfloat16_rn(sum);
+    for (int k = 0; k < kGainWarps; ++k) s += acc[k][lane];
+    bf16* out = j < h ? dgamma + j : dbeta ? dbeta + j - h : nullptr;
+    if (out) *out = __float2bfloat16_rn(s);
   }
 }
 
@@ -497,7 +494,7 @@ cudaError_t layernorm_bwd(const void* dy, int dy_type, int64_t lddy, const void*
     e = dy_type == kRowF32 ? launch_bwd<bf16, float>(g, b, parts, s)
                            : launch_bwd<bf16, bf16>(g, b, parts, s);
   if (e != cudaSuccess) return e;
-  return launch_following(ln_gain_kernel, dim3((2 * h + 127) / 128), 32 * kGainWarps, 0, s, partial, parts, h, dgamma,
+  return launch_following(ln_gain_kernel, dim3((2 * h + 31) / 32), 32 * kGainWarps, 0, s, partial, parts, h, dgamma,
                           dbeta);
 }
 

@@ -527,31 +527,42 @@ __device__ __forceinline__ float pair_loss(const Preference& g, float s0, float 
 // The row at which sequence j begins, or the one before it ends.
 __device__ __forceinline__ int bound_of(const Preference& g, int j) { return min(max(g.bounds[j], 0), g.T); }
 
-// Few rows: one block does all of it, a warp a sequence at a time.
-// (4048 rows of 8 sequences: 5.3 us, as two launches 6.1 and 2.9.)
+// Few rows: one block does all of it; where there are fewer sequences than warps, several warps share one. (322 rows of
+// 4 sequences 5.6 us, 4048 of 8 9.1; as two launches 6.1 and 2.9.)
 constexpr int kFewRows = 4096, kFewPairs = 1024;
 __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g, float* loss) {
   __shared__ float score[2 * kFewPairs], share[2 * kFewPairs];
+  __shared__ float2 part[32];  // a warp's sum and count
   __shared__ Pair red[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = 2 * g.pairs;
+  const int team = n > 16 ? 1 : 32 / n, teams = 32 / team, mate = warp % team;  // team > 1: a team for each sequence
   wait_for_previous();
   let_next_start();
-  for (int j = warp; j < n; j += 32) {
-    const int lo = bound_of(g, j), hi = bound_of(g, j + 1);
+  for (int j0 = 0; j0 < n; j0 += teams) {
+    const int j = j0 + warp / team;
     float v = 0.f, count = 0.f;
+    if (j < n) {
+      const int lo = bound_of(g, j), hi = bound_of(g, j + 1);
 #pragma unroll 8
-    for (int i = lo + lane; i < hi; i += 32) {
-      const bool on = !g.labels || g.labels[i] >= 0;
-      const float a = g.logp[i], b = g.ref ? g.ref[i] : 0.f;
-      v += on ? a - b : 0.f;
-      count += on ? 1.f : 0.f;
+      for (int i = lo + mate * 32 + lane; i < hi; i += team * 32) {
+        const bool on = !g.labels || g.labels[i] >= 0;
+        const float a = g.logp[i], b = g.ref ? g.ref[i] : 0.f;
+        v += on ? a - b : 0.f;
+        count += on ? 1.f : 0.f;
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       v += __shfl_xor_sync(0xffffffffu, v, o);
       count += __shfl_xor_sync(0xffffffffu, count, o);
     }
-    if (lane == 0) {
+    if (team > 1) {
+      if (lane == 0) part[warp] = make_float2(v, count);
+      __syncthreads();
+      v = count = 0.f;
+      for (int k = warp - mate; k < warp - mate + team && k < 32; ++k) v += part[k].x, count += part[k].y;
+    }
+    if (lane == 0 && mate == 0 && j < n) {
       share[j] = g.average ? 1.f / fmaxf(count, 1.f) : 1.f;
       score[j] = v * share[j];
       g.rewards[j] = g.beta * score[j];
@@ -575,11 +586,15 @@ __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g
     sum = add_warp(red[lane]);
     if (lane == 0) *loss = value(sum) / static_cast<float>(g.pairs);
   }
-  for (int j = warp; j < n; j += 32)
-    for (int i = bound_of(g, j) + lane; i < bound_of(g, j + 1); i += 32)
-      g.dlogp[i] = g.labels && g.labels[i] < 0 ? 0.f : score[j];
-  for (int i = threadIdx.x; i < bound_of(g, 0); i += 1024) g.dlogp[i] = 0.f;
-  for (int i = max(bound_of(g, 0), bound_of(g, n)) + threadIdx.x; i < g.T; i += 1024) g.dlogp[i] = 0.f;
+  for (int j = warp / team; j < n; j += teams) {
+    const int lo = bound_of(g, j), hi = bound_of(g, j + 1);
+    const float k = score[j];
+#pragma unroll 4
+    for (int i = lo + mate * 32 + lane; i < hi; i += team * 32) g.dlogp[i] = g.labels && g.labels[i] < 0 ? 0.f : k;
+  }
+  const int first = bound_of(g, 0), last = max(first, bound_of(g, n));
+  for (int i = threadIdx.x; i < first; i += 1024) g.dlogp[i] = 0.f;
+  for (int i = last + threadIdx.x; i < g.T; i += 1024) g.dlogp[i] = 0.f;
 }
 
 // One block a pair: the sums of its two sequences, its loss, and its rows' dlogp. The last block zeroes the rows
