@@ -25,7 +25,8 @@ namespace {
 
 // ------------------------------------------------------------------ lookup
 constexpr int kLookupBlocks = 64;  // on an SM, of which 8 at a time: a block's start costs as much as a short row
-// W columns a thread at a time, 16 bytes of x: blockDim.x threads a row, blockDim.y rows a block.
+// W columns a thread at a time, 16 bytes of x: blockDim.x threads a row, blockDim.y rows a block. (45359 x 640 fp32: 64
+// threads a row 21.6 us, 160, of one load each, 26.2.)
 template <class X>
 __global__ void __launch_bounds__(256) lookup_kernel(const int32_t* tok, const bf16* E, X* x, int T, int h, int V,
                                                      float scale, int* err) {
@@ -467,7 +468,7 @@ cudaError_t embed_lookup(const int32_t* tok, const bf16* E, void* x, int type, i
       (err && !vec_ok(err, 4)) || !std::isfinite(scale) ||
       ranges_overlap(E, table_bytes(V, h), x, static_cast<uint64_t>(T) * h * row_type_bytes(type)))
     return cudaErrorInvalidValue;
-  const int threads = threads_of(h * row_type_bytes(type) / 16, 256);
+  const int threads = std::min(256, (h * row_type_bytes(type) / 16 + 127) / 128 * 32);  // four loads each, or more
   const dim3 block(threads, 256 / threads);
   const dim3 grid(std::min<unsigned>((T + block.y - 1) / block.y, kSms * kLookupBlocks));
   if (type == kRowF32)
