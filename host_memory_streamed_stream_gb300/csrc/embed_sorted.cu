@@ -59,14 +59,13 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 9;       // of a digit at most
 constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortAhead = 8;      // loads a thread has in flight
-constexpr int kSortSmem = kSortWarps * kSortBins * 4;  // counters; of the other blocks: a bit a row, and zeros
-// Blocks that write zeros beside the sort: with its eight, one on an SM (8192 x 4096, 32000 rows: 120 69.6 us, 160,
-// where some SMs have two, 88.8, 240 73.1), or, in the launch of the sums, whatever fits between them (131072: 120 244
-// us, 240 234).
-constexpr int kZeroBlocks = 120, kGapBlocks = 240;
-constexpr int kZeroBytes = kSortSmem / 2;
+constexpr int kSortSmem = kSortWarps * kSortBins * 4;  // counters
 constexpr int kClusterTokens = 32768;
-constexpr int kZeroRows = (kSortSmem - kZeroBytes) * 8;
+// Blocks that write zeros: beside the sort (8192 x 4096, 32000 rows: 120 69.3 us, 144 70.5, 152, of which some share an
+// SM, 87.1, 228 74.3), and in the launch of the sums, where they fill in between (131072 x 4096: 120 244 us, 240 234).
+constexpr int kZeroBlocks = 120, kGapBlocks = 240;
+constexpr int kZeroBytes = 16384;
+constexpr int kZeroRows = 65536;  // a bit each
 
 // *p of block `rank` of this cluster.
 __device__ __forceinline__ int cluster_load(const int* p, int rank) {
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(kSortThreads) digit_place_kernel(const SortArg
   __shared__ int sums[2][kSortThreads];
   const int d = threadIdx.x & (p.bins - 1), rank = blockIdx.x, shares = kSortThreads >> g.bits;
   int below = 0, all = 0;
-#pragma unroll 8
+#pragma unroll 16
   for (int r = threadIdx.x >> g.bits; r < static_cast<int>(gridDim.x); r += shares) {
     const int c = __ldcg(g.counts + r * p.bins + d);
     below += r < rank ? c : 0;
@@ -263,18 +262,20 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
   __shared__ int total[kSortBins], base[kSortBins], warp_sum[kSortWarps];
   wait_for_previous();
   let_next_start();
-  if (blockIdx.x < kSortBlocks) {
-    sort_pairs(g, reinterpret_cast<int*>(sort_smem), total, base, warp_sum);
-    return;
-  }
-  // the other clusters: zeros in the rows of this block's share of the table that no token uses, by bulk copies
-  const int blocks = gridDim.x - kSortBlocks, b = blockIdx.x - kSortBlocks;
-  const int v0 = static_cast<int>(static_cast<int64_t>(g.V) * b / blocks);
-  const int v1 = static_cast<int>(static_cast<int64_t>(g.V) * (b + 1) / blocks);
-  uint4* zeros = reinterpret_cast<uint4*>(sort_smem);
-  unsigned* used = reinterpret_cast<unsigned*>(sort_smem + kZeroBytes);
+  sort_pairs(g, reinterpret_cast<int*>(sort_smem), total, base, warp_sum);
+}
+
+// Zeros in the rows of the table that no token uses, by bulk copies, beside the sort: this kernel starts once the sort's
+// blocks have seen the kernel before them end, needs nothing of theirs, and ends after them. (Blocks of the sort's own
+// launch are placed in clusters, unevenly where the kernel before still holds some SMs: 8192 x 4096 69 to 102 us.)
+__global__ void __launch_bounds__(kSortThreads) zero_kernel(const SortArgs g) {
+  __shared__ __align__(128) uint4 zeros[kZeroBytes / 16];
+  __shared__ unsigned used[kZeroRows / 32];
+  let_next_start();
+  const int v0 = static_cast<int>(static_cast<int64_t>(g.V) * blockIdx.x / gridDim.x);
+  const int v1 = static_cast<int>(static_cast<int64_t>(g.V) * (blockIdx.x + 1) / gridDim.x);
   const int row_bytes = static_cast<int>(g.h) * 2;
-  for (int i = threadIdx.x; i * 16 < min(kZeroBytes, row_bytes); i += kSortThreads) zeros[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < kZeroBytes / 16; i += kSortThreads) zeros[i] = make_uint4(0, 0, 0, 0);
   for (int r0 = v0; r0 < v1; r0 += kZeroRows) {
     const int r1 = min(v1, r0 + kZeroRows);
     __syncthreads();
@@ -298,6 +299,7 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
     bulk_store_end_group();
   }
   bulk_store_wait_read();
+  wait_for_previous();
 }
 
 // ------------------------------------------------------------------ sums of runs
@@ -314,34 +316,29 @@ struct SumArgs {
   float scale;
   bool add;
 };
-// Zeros in the rows of no token, with the tokens sorted: part `b` of `parts` of the table.
-constexpr int kGapRows = 4096;
-__device__ void zero_gaps(const SumArgs& g, unsigned* used, int b, int parts) {
+// Zeros in the rows of no token, with the tokens sorted: part `b` of `parts` of the table, a thread a row, which looks its
+// token up among the pairs.
+constexpr int kGapZeros = 4096;  // bytes
+__device__ void zero_gaps(const SumArgs& g, uint4* zeros, int b, int parts) {
   const int v0 = static_cast<int>(static_cast<int64_t>(g.V) * b / parts);
   const int v1 = static_cast<int>(static_cast<int64_t>(g.V) * (b + 1) / parts);
-  for (int r0 = v0; r0 < v1; r0 += kGapRows) {
-    const int r1 = min(v1, r0 + kGapRows);
-    int lo = 0, hi = g.T;  // the first pair of a token from r0 on
+  for (int i = threadIdx.x; i < kGapZeros / 16; i += blockDim.x) zeros[i] = make_uint4(0, 0, 0, 0);
+  fence_async_shared();
+  __syncthreads();
+  const int row_bytes = g.h * 2;
+  for (int r = v0 + threadIdx.x; r < v1; r += blockDim.x) {
+    int lo = 0, hi = g.T;  // the first pair of a token from r on
     while (lo < hi) {
       const int mid = lo + (hi - lo) / 2;
-      if (__ldcg(&g.pairs[mid].x) < r0) lo = mid + 1;
+      if (__ldcg(&g.pairs[mid].x) < r) lo = mid + 1;
       else hi = mid;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kGapRows / 32; i += blockDim.x) used[i] = 0;
-    __syncthreads();
-    for (int i = lo + threadIdx.x; i < g.T; i += blockDim.x) {
-      const int v = __ldcg(&g.pairs[i].x);
-      if (v >= r1) break;
-      atomicOr(used + (v - r0) / 32, 1u << ((v - r0) & 31));
-    }
-    __syncthreads();
-    for (int r = r0; r < r1; ++r) {
-      if (used[(r - r0) / 32] >> ((r - r0) & 31) & 1) continue;
-      uint4* row = reinterpret_cast<uint4*>(g.dE + static_cast<int64_t>(r) * g.h);
-      for (int i = threadIdx.x; i < g.h / 8; i += blockDim.x) row[i] = make_uint4(0, 0, 0, 0);
-    }
+    if (lo < g.T && __ldcg(&g.pairs[lo].x) == r) continue;
+    char* row = reinterpret_cast<char*>(g.dE + static_cast<int64_t>(r) * g.h);
+    for (int i = 0; i < row_bytes; i += kGapZeros) bulk_store(row + i, zeros, min(kGapZeros, row_bytes - i));
   }
+  bulk_store_end_group();
+  bulk_store_wait_read();
 }
 template <int W>
 __device__ __forceinline__ void write_row(const SumArgs& g, int v, int c, const float* acc) {
@@ -363,14 +360,13 @@ __device__ __forceinline__ void write_partial(const SumArgs& g, int chunk, int w
 template <class X>
 __global__ void __launch_bounds__(kSumThreads) run_sum_kernel(const SumArgs g) {
   constexpr int W = 16 / sizeof(X);
+  __shared__ __align__(128) uint4 zeros[kGapZeros / 16];
   __shared__ int2 pairs[kSumChunk];
   __shared__ int ends[2];  // the tokens before and behind the chunk
   wait_for_previous();
   let_next_start();
   if (static_cast<int>(blockIdx.x) >= g.chunks) {
-    static_assert(sizeof(pairs) >= kGapRows / 8, "a bit a row");
-    zero_gaps(g, reinterpret_cast<unsigned*>(pairs), (blockIdx.x - g.chunks) * gridDim.y + blockIdx.y,
-              (gridDim.x - g.chunks) * gridDim.y);
+    zero_gaps(g, zeros, (blockIdx.x - g.chunks) * gridDim.y + blockIdx.y, (gridDim.x - g.chunks) * gridDim.y);
     return;
   }
   const int p0 = blockIdx.x * g.chunk, n = min(g.T - p0, g.chunk);
@@ -414,10 +410,13 @@ __global__ void __launch_bounds__(kSumThreads) run_sum_kernel(const SumArgs g) {
   else write_row<W>(g, cur, c, acc);
 }
 
-// The runs that cross a border: one block for each chunk in which such a run begins, 4 columns a thread.
-__global__ void __launch_bounds__(kSumThreads) run_join_kernel(const SumArgs g) {
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
-  const int p0 = blockIdx.x * g.chunk;
+// The runs that cross a border: one block for each chunk in which such a run begins. blockDim.x threads of 4 columns, and
+// blockDim.y shares of the chunks that the run goes on into, which meet in shared memory in order.
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) run_join_kernel(const SumArgs g) {
+  __shared__ float4 meet[kJoinThreads];
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4, tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const int threads = blockDim.x * blockDim.y, p0 = blockIdx.x * g.chunk;
   wait_for_previous();
   const int64_t end = static_cast<int64_t>(p0) + g.chunk;
   if (end >= g.T) return;
@@ -425,34 +424,50 @@ __global__ void __launch_bounds__(kSumThreads) run_join_kernel(const SumArgs g) 
   const int cur = __ldcg(&g.pairs[end - 1].x), next = __ldcg(&g.pairs[end].x);
   if (cur == g.V || next != cur || before == cur) return;  // no run goes on, or it began in an earlier chunk
   // the chunks that it goes on into
-  int last = blockIdx.x + 1;
-  for (int k0 = last;; k0 += blockDim.x) {
-    const int k = k0 + threadIdx.x;
+  const int first = blockIdx.x + 1;
+  int last = first;
+  for (int k0 = first;; k0 += threads) {
+    const int k = k0 + tid;
     const int n = __syncthreads_count(k < g.chunks && __ldcg(&g.pairs[static_cast<int64_t>(k) * g.chunk].x) == cur);
     last = k0 + n;
-    if (n < static_cast<int>(blockDim.x)) break;
+    if (n < threads) break;
   }
-  if (c >= g.h) return;
-  const float* part = g.partial + static_cast<int64_t>(blockIdx.x) * 2 * g.h + c;
-  const float4 q = *reinterpret_cast<const float4*>(part + g.h);
-  float acc[4] = {q.x, q.y, q.z, q.w};
-  part += 2 * g.h;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int share = (last - first + blockDim.y - 1) / blockDim.y;
+  const int lo = first + threadIdx.y * share, hi = min(last, lo + share);
+  if (c < g.h) {
+    const float* part = g.partial + static_cast<int64_t>(lo) * 2 * g.h + c;
 #pragma unroll 8
-  for (int k = blockIdx.x + 1; k < last; ++k, part += 2 * g.h) {
-    const float4 a = *reinterpret_cast<const float4*>(part);
-    acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
+    for (int k = lo; k < hi; ++k, part += 2 * g.h) {
+      const float4 a = *reinterpret_cast<const float4*>(part);
+      acc.x += a.x, acc.y += a.y, acc.z += a.z, acc.w += a.w;
+    }
   }
-  write_row<4>(g, cur, c, acc);
+  meet[tid] = acc;
+  __syncthreads();
+  if (threadIdx.y > 0 || c >= g.h) return;
+  const float4 q = *reinterpret_cast<const float4*>(g.partial + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * g.h + c);
+  float sum[4] = {q.x, q.y, q.z, q.w};
+  for (int y = 0; y < static_cast<int>(blockDim.y); ++y) {
+    const float4 a = meet[y * blockDim.x + threadIdx.x];
+    sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
+  }
+  write_row<4>(g, cur, c, sum);
 }
 
 bool embed_shape_ok(int T, int V, int h) {
   return T > 0 && T <= kEmbedMaxTokens && V > 0 && V <= kEmbedMaxVocab && h > 0 && h % 8 == 0 && h <= kEmbedMaxWidth;
 }
 uint64_t table_bytes(int V, int h) { return static_cast<uint64_t>(V) * h * sizeof(bf16); }
-// Sorted rows a block sums: few where there are few, so that all SMs have some; many where there are many, which leaves
-// fewer sums at borders. (8192 x 4096 fp32: 32 73.1 us, 64 71.7; 131072 x 4096 bf16: 128 234 us, 256 227, 512 228; 108,
-// which would make whole waves, 250.)
-int sum_chunk(int T) { return T <= 4096 ? 16 : T <= kClusterTokens ? 64 : kSumChunk; }
+// Sorted rows a block sums: as many as leave the SMs 65536 threads (of eight columns each), which leaves fewer sums at
+// borders. (8192 x 4096 fp32: 32 73.1 us, here 64 71.7; 131072 x 4096 bf16: 128 234 us, here 256 227, 512 228, and 108,
+// which would make whole waves, 250; 77765 x 672 bf16: 256 70 us, here 64 43.)
+int sum_chunk(int T, int h) {
+  const int64_t most = static_cast<int64_t>(T) * (h / 8) / 65536;
+  int chunk = 16;
+  while (chunk < kSumChunk && 2 * chunk <= most) chunk *= 2;
+  return chunk;
+}
 // Threads that go over `units` in the fewest turns of at most `most`, and then as evenly as whole warps can.
 int threads_of(int units, int most) {
   const int turns = (units + most - 1) / most;
@@ -478,7 +493,7 @@ cudaError_t embed_lookup(const int32_t* tok, const bf16* E, void* x, int type, i
 }
 
 uint64_t embed_lookup_bwd_scratch(int T, int h) {
-  const int chunk = sum_chunk(T);
+  const int chunk = sum_chunk(T, h);
   const size_t n = T, chunks = (n + chunk - 1) / chunk;
   return 2 * round256(n * sizeof(int2)) + round256(n * sizeof(int)) +
          (T > kClusterTokens ? kManyBlocks * kSortBins * sizeof(int) : 0) + chunks * 2 * h * sizeof(float);
@@ -513,13 +528,12 @@ cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16*
       if (e != cudaSuccess) return e;
     }
   } else {
-    const unsigned blocks = add ? kSortBlocks : kSortBlocks + kZeroBlocks;
     e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-    if (e != cudaSuccess) return e;
-    e = launch_following(sort_kernel, dim3(blocks), kSortThreads, kSortSmem, s, g);
+    if (e == cudaSuccess) e = launch_following(sort_kernel, dim3(kSortBlocks), kSortThreads, kSortSmem, s, g);
+    if (e == cudaSuccess && !add) e = launch_following(zero_kernel, dim3(kZeroBlocks), kSortThreads, 0, s, g);
     if (e != cudaSuccess) return e;
   }
-  const int chunk = sum_chunk(T), chunks = (T + chunk - 1) / chunk;
+  const int chunk = sum_chunk(T, h), chunks = (T + chunk - 1) / chunk;
   const SumArgs r{passes & 1 ? a : b, dx, dE, reinterpret_cast<float*>(at), T, V, h, chunk, chunks, scale, add};
   auto grid = [&](int units, unsigned& threads) {
     threads = threads_of(units, kSumThreads);
@@ -531,7 +545,7 @@ cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16*
   e = launch_following(type == kRowF32 ? run_sum_kernel<float> : run_sum_kernel<bf16>, blocks_xy, threads, 0, s, r);
   if (e != cudaSuccess || chunks == 1) return e;
   blocks_xy = grid(h / 4, threads);
-  return launch_following(run_join_kernel, blocks_xy, threads, 0, s, r);
+  return launch_following(run_join_kernel, blocks_xy, dim3(threads, kJoinThreads / threads), 0, s, r);
 }
 
 }  // namespace mt
