@@ -8,7 +8,7 @@
 // cluster's, else beside the sums. No floating-point atomics: the result does not change from run to run.
 //
 // Bound by HBM, with a sort of 13 us (8192 tokens) and joins of 6 us that it cannot hide all of. Measured: 8192 tokens
-// x 4096 fp32, 32000 rows 68.6 us (zeros and sort 40, sums 24, joins 6), 5.6 TB/s; 131072 x 4096 bf16 227 us (sort 25,
+// x 4096 fp32, 32000 rows 73 us (zeros and sort 42, sums 24, joins 6), 5.2 TB/s; 131072 x 4096 bf16 227 us (sort 25,
 // sums 190, joins 12), 5.9 TB/s. Lookup of 4096 x 5120 to fp32: 18 us on the device, 20.5 in a row of calls, 5.3 TB/s.
 // Zeroing most rows beside the sums for few tokens too, which would hide the sort, measured 90 us.
 #include <algorithm>
@@ -61,11 +61,7 @@ constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortAhead = 8;      // loads a thread has in flight
 constexpr int kSortSmem = kSortWarps * kSortBins * 4;  // counters
 constexpr int kClusterTokens = 32768;
-// Blocks that write zeros: beside the sort (8192 x 4096, 32000 rows: 120 69.3 us, 144 70.5, 152, of which some share an
-// SM, 87.1, 228 74.3), and in the launch of the sums, where they fill in between (131072 x 4096: 120 244 us, 240 234).
-constexpr int kZeroBlocks = 120, kGapBlocks = 240;
-constexpr int kZeroBytes = 16384;
-constexpr int kZeroRows = 65536;  // a bit each
+constexpr int kGapBlocks = 240;  // that write zeros in the launch of the sums (131072 x 4096: 120 244 us, 240 234)
 
 // *p of block `rank` of this cluster.
 __device__ __forceinline__ int cluster_load(const int* p, int rank) {
@@ -265,41 +261,45 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
   sort_pairs(g, reinterpret_cast<int*>(sort_smem), total, base, warp_sum);
 }
 
-// Zeros in the rows of the table that no token uses, by bulk copies, beside the sort: this kernel starts once the sort's
-// blocks have seen the kernel before them end, needs nothing of theirs, and ends after them. (Blocks of the sort's own
-// launch are placed in clusters, unevenly where the kernel before still holds some SMs: 8192 x 4096 69 to 102 us.)
-__global__ void __launch_bounds__(kSortThreads) zero_kernel(const SortArgs g) {
-  __shared__ __align__(128) uint4 zeros[kZeroBytes / 16];
+// Zeros in the rows of the table that no token uses, beside the sort: this kernel starts once the sort's blocks have
+// seen the kernel before them end, needs nothing of theirs, and ends after them. Many short blocks, which go where
+// there is room: 4096 tokens, 152064 rows of 5120 243 us with 2432 blocks; with one an SM (bulk copies or not) 247 to
+// 277, by the GPU, with blocks that share SMs 365; as blocks of the sort's launch, placed in clusters, up to 439.
+constexpr int kZeroThreads = 256;
+constexpr int kZeroRows = 8192;  // a bit each
+__global__ void __launch_bounds__(kZeroThreads) zero_kernel(const SortArgs g) {
   __shared__ unsigned used[kZeroRows / 32];
   let_next_start();
   const int v0 = static_cast<int>(static_cast<int64_t>(g.V) * blockIdx.x / gridDim.x);
   const int v1 = static_cast<int>(static_cast<int64_t>(g.V) * (blockIdx.x + 1) / gridDim.x);
-  const int row_bytes = static_cast<int>(g.h) * 2;
-  for (int i = threadIdx.x; i < kZeroBytes / 16; i += kSortThreads) zeros[i] = make_uint4(0, 0, 0, 0);
+  const int units = static_cast<int>(g.h) / 8;
   for (int r0 = v0; r0 < v1; r0 += kZeroRows) {
     const int r1 = min(v1, r0 + kZeroRows);
     __syncthreads();
-    for (int i = threadIdx.x; i < (r1 - r0 + 31) / 32; i += kSortThreads) used[i] = 0;
+    for (int i = threadIdx.x; i < (r1 - r0 + 31) / 32; i += kZeroThreads) used[i] = 0;
     __syncthreads();
-    for (int i0 = threadIdx.x; i0 < g.T; i0 += kSortThreads * kSortAhead) {
+    for (int i0 = threadIdx.x; i0 < g.T; i0 += kZeroThreads * kSortAhead) {
       int v[kSortAhead];
 #pragma unroll
-      for (int j = 0; j < kSortAhead; ++j) v[j] = i0 + j * kSortThreads < g.T ? g.tok[i0 + j * kSortThreads] : -1;
+      for (int j = 0; j < kSortAhead; ++j) v[j] = i0 + j * kZeroThreads < g.T ? g.tok[i0 + j * kZeroThreads] : -1;
 #pragma unroll
       for (int j = 0; j < kSortAhead; ++j)
         if (v[j] >= r0 && v[j] < r1) atomicOr(used + (v[j] - r0) / 32, 1u << ((v[j] - r0) & 31));
     }
-    fence_async_shared();
     __syncthreads();
-    for (int r = r0 + threadIdx.x; r < r1; r += kSortThreads) {
+    for (int r = r0 + (threadIdx.x >> 5); r < r1; r += kZeroThreads / 32) {
       if (used[(r - r0) / 32] >> ((r - r0) & 31) & 1) continue;
-      char* row = reinterpret_cast<char*>(g.dE + r * g.h);
-      for (int i = 0; i < row_bytes; i += kZeroBytes) bulk_store(row + i, zeros, min(kZeroBytes, row_bytes - i));
+      uint4* row = reinterpret_cast<uint4*>(g.dE + r * g.h);
+      for (int i = threadIdx.x & 31; i < units; i += 32) row[i] = make_uint4(0, 0, 0, 0);
     }
-    bulk_store_end_group();
   }
-  bulk_store_wait_read();
   wait_for_previous();
+}
+// About 96 KB of the table each, but no more blocks than read the tokens for 20 million in all.
+int zero_blocks(int T, int V, int h) {
+  const int64_t most = std::min<int64_t>(2432, 20000000 / T);
+  const int64_t blocks = (static_cast<int64_t>(V) * h * 2 + 98303) / 98304;
+  return static_cast<int>(std::min(most, blocks));
 }
 
 // ------------------------------------------------------------------ sums of runs
@@ -316,8 +316,8 @@ struct SumArgs {
   float scale;
   bool add;
 };
-// Zeros in the rows of no token, with the tokens sorted: part `b` of `parts` of the table, a thread a row, which looks its
-// token up among the pairs.
+// Zeros in the rows of no token, with the tokens sorted: part `b` of `parts` of the table, a thread a row, which looks
+// its token up among the pairs.
 constexpr int kGapZeros = 4096;  // bytes
 __device__ void zero_gaps(const SumArgs& g, uint4* zeros, int b, int parts) {
   const int v0 = static_cast<int>(static_cast<int64_t>(g.V) * b / parts);
@@ -410,8 +410,8 @@ __global__ void __launch_bounds__(kSumThreads) run_sum_kernel(const SumArgs g) {
   else write_row<W>(g, cur, c, acc);
 }
 
-// The runs that cross a border: one block for each chunk in which such a run begins. blockDim.x threads of 4 columns, and
-// blockDim.y shares of the chunks that the run goes on into, which meet in shared memory in order.
+// The runs that cross a border: one block for each chunk in which such a run begins. blockDim.x threads of 4 columns,
+// and blockDim.y shares of the chunks that the run goes on into, which meet in shared memory in order.
 constexpr int kJoinThreads = 512;
 __global__ void __launch_bounds__(kJoinThreads) run_join_kernel(const SumArgs g) {
   __shared__ float4 meet[kJoinThreads];
@@ -530,7 +530,7 @@ cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16*
   } else {
     e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
     if (e == cudaSuccess) e = launch_following(sort_kernel, dim3(kSortBlocks), kSortThreads, kSortSmem, s, g);
-    if (e == cudaSuccess && !add) e = launch_following(zero_kernel, dim3(kZeroBlocks), kSortThreads, 0, s, g);
+    if (e == cudaSuccess && !add) e = launch_following(zero_kernel, dim3(zero_blocks(T, V, h)), kZeroThreads, 0, s, g);
     if (e != cudaSuccess) return e;
   }
   const int chunk = sum_chunk(T, h), chunks = (T + chunk - 1) / chunk;
