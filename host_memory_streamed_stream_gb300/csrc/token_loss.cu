@@ -10,11 +10,11 @@
 // logit, m and the logarithm meet in pairs of floats: a ratio of policies is exp of a small difference of numbers
 // of size 10, of which one float would lose 2^-21.
 //
-// Bound by HBM. Log-probabilities: 6144 rows of 32000 fp32 119 us, 6.6 TB/s, 3072 of 152064 bf16 148 us, 6.3 TB/s
-// (where the exponential unit is 70 % busy). Policy loss, whose second look at a row reads the L2: 202 us, 5.8 TB/s,
-// and 351 us, 5.3 TB/s. Gradient alone: 4048 rows of 152064 bf16, a quarter of them masked, 295 us, 6.7 TB/s with what
+// Bound by HBM. Log-probabilities: 6000 rows of 32000 fp32 118 us, 6.5 TB/s, 3000 of 152064 bf16 139 us, 6.5 TB/s
+// (where the exponential unit is 70 % busy). Policy loss, whose second look at a row reads the L2: 198 us, 5.8 TB/s,
+// and 338 us, 5.4 TB/s. Gradient alone: 4048 rows of 152064 bf16, a quarter of them masked, 295 us, 6.7 TB/s with what
 // the L2 still holds. What did not help the policy loss: a ring of shared memory that holds the row, filled by cp.async
-// (370 and 645 us), bulk prefetches of the next row into the L2 (272, 524), persistent blocks (210, 392).
+// (1.8 times as long), bulk prefetches of the next row into the L2 (1.3), persistent blocks (1.05).
 #include <algorithm>
 #include <cmath>
 
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
 }
 
 // Longer rows: a block a row, or, for very wide and for few rows, a cluster of blocks that split it by columns, with
-// two loads of a thread in flight (one: 240 us for 6144 rows of 32000 fp32, two 204, four at half the threads 266). The
+// two loads of a thread in flight (policy loss at 32000 fp32: one 1.18 times as long, four at half the threads 1.3). The
 // policy loss reads the row a second time, from the L2, for its gradient.
 // *p of block `rank` of the cluster = v.
 __device__ __forceinline__ void cluster_store(MaxSum* p, unsigned rank, const MaxSum& v) {
@@ -655,8 +655,8 @@ bool grad_ok(const TokenRows& g, int type) {
   return !spans_overlap(g.logits, g.ld, row_type_bytes(type), g.dlogits, g.ldd, 2, g.T, g.V);
 }
 // Blocks of a row. The policy loss: as many as keep the rows that are being worked on, two on an SM, within what the L2
-// holds of them (3072 rows of 152064 bf16, 304 KB: one block 370 us, two 347, four 437; 128 KB: one 202, two 272). Few
-// rows: as many as have 2048 columns each to do, up to two on an SM.
+// holds of them (3000 rows of 152064 bf16, 304 KB: one block 344 us, two 338, four 428; 6000 of 128 KB: one 198, two
+// 220). Few rows: as many as have 2048 columns each to do, up to two on an SM.
 constexpr int kShareBytes = 160 << 10;
 int row_blocks(int T, int V, int esz, bool policy) {
   int n = 1;
@@ -678,7 +678,7 @@ cudaError_t launch_rows(const TokenRows& g, cudaStream_t s) {
   const int blocks = row_blocks(g.T, g.V, sizeof(Z), POLICY);
   const int bytes = g.V / blocks * static_cast<int>(sizeof(Z));
   // About eight chunks a thread, so that the starts of many rows overlap (4127 rows of 10.5 KB: 256 threads 40 us with
-  // the call, 128 35), and, without a second look, sixteen and more (128 KB rows: 1024 threads 127 us, 512 121).
+  // the call, 128 35), and, without a second look, sixteen and more (128 KB rows: 1024 threads 127 us, 512 118).
   if (bytes <= 16 << 10) return launch_blocks<Z, POLICY, 128>(g, blocks, s);
   if (bytes <= 32 << 10) return launch_blocks<Z, POLICY, 256>(g, blocks, s);
   if (!POLICY || bytes <= 64 << 10) return launch_blocks<Z, POLICY, 512>(g, blocks, s);
