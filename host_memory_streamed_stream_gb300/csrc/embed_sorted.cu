@@ -528,8 +528,7 @@ cudaError_t embed_lookup_bwd(const int32_t* tok, const void* dx, int type, bf16*
       if (e != cudaSuccess) return e;
     }
   } else {
-    e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-    if (e == cudaSuccess) e = launch_following(sort_kernel, dim3(kSortBlocks), kSortThreads, kSortSmem, s, g);
+    e = launch_following(sort_kernel, dim3(kSortBlocks), kSortThreads, kSortSmem, s, g);
     if (e == cudaSuccess && !add) e = launch_following(zero_kernel, dim3(zero_blocks(T, V, h)), kZeroThreads, 0, s, g);
     if (e != cudaSuccess) return e;
   }

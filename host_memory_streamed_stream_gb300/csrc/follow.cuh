@@ -2,6 +2,9 @@
 // one before drains, set themselves up, and wait for its results only where they read them. Hides
 // the 2-4 us between dependent launches.
 #pragma once
+#include <atomic>
+#include <cstdint>
+
 #include <cuda_runtime.h>
 
 namespace mt {
@@ -11,6 +14,19 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 // Until the kernel before has completed and its writes are visible.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Let `kernel` ask for up to `bytes` of dynamic shared memory on the current device. `done` is the kernel's own, a bit a
+// device: the attribute costs a microsecond to set, and stays.
+template <class... P>
+cudaError_t allow_shared(void (*kernel)(P...), int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 // As below, in clusters of `cluster` blocks.
 template <class... P, class... A>
 cudaError_t launch_cluster_following(void (*kernel)(P...), dim3 grid, unsigned threads, unsigned cluster, size_t smem,

@@ -411,8 +411,8 @@ cudaError_t launch_fwd(LnFwd g, cudaStream_t s) {
   const int threads = n.group * n.groups, row = threads * kFwdCols * static_cast<int>(sizeof(X));
   g.group = n.group;
   g.stages = ring_stages(n, row);
-  const cudaError_t e =
-      cudaFuncSetAttribute(ln_fwd_kernel<X>, cudaFuncAttributeMaxDynamicSharedMemorySize, g.stages * row);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(ln_fwd_kernel<X>, kNormRing, done);
   if (e != cudaSuccess) return e;
   return launch_following(ln_fwd_kernel<X>, dim3(std::min((g.T + n.groups - 1) / n.groups, kSms * n.blocks)), threads,
                           g.stages * row, s, g);
@@ -436,7 +436,8 @@ cudaError_t launch_bwd(LnBwd g, const BwdShape& b, int parts, cudaStream_t s) {
   // at the end the ring holds the sums of all groups but one
   const int smem = std::max(g.stages * row, (b.n.groups - 1) * 2 * g.h * 4);
   auto* k = b.cluster > 1 ? ln_bwd_kernel<X, D, 2> : ln_bwd_kernel<X, D, 1>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = allow_shared(k, kNormRing, done[b.cluster > 1]);
   if (e != cudaSuccess) return e;
   return launch_cluster_following(k, dim3(parts * b.cluster), threads, b.cluster, smem, s, g);
 }

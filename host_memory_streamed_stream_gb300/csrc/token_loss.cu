@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
 }
 
 // Longer rows: a block a row, or, for very wide and for few rows, a cluster of blocks that split it by columns, with
-// two loads of a thread in flight (policy loss at 32000 fp32: one 1.18 times as long, four at half the threads 1.3). The
-// policy loss reads the row a second time, from the L2, for its gradient.
+// two loads of a thread in flight (policy loss at 32000 fp32: one 1.18 times as long, four at half the threads 1.3).
+// The policy loss reads the row a second time, from the L2, for its gradient.
 // *p of block `rank` of the cluster = v.
 __device__ __forceinline__ void cluster_store(MaxSum* p, unsigned rank, const MaxSum& v) {
   uint32_t a;
@@ -681,9 +681,11 @@ cudaError_t launch_rows(const TokenRows& g, cudaStream_t s) {
   // the call, 128 35), and, without a second look, sixteen and more (128 KB rows: 1024 threads 127 us, 512 118).
   if (bytes <= 16 << 10) return launch_blocks<Z, POLICY, 128>(g, blocks, s);
   if (bytes <= 32 << 10) return launch_blocks<Z, POLICY, 256>(g, blocks, s);
-  if (!POLICY || bytes <= 64 << 10) return launch_blocks<Z, POLICY, 512>(g, blocks, s);
-  return launch_blocks<Z, POLICY, 1024>(g, blocks, s);
+  if constexpr (POLICY)
+    if (bytes > 64 << 10) return launch_blocks<Z, POLICY, 1024>(g, blocks, s);
+  return launch_blocks<Z, POLICY, 512>(g, blocks, s);
 }
+
 }  // namespace
 
 cudaError_t token_logprobs(const void* logits, int type, int64_t ld, const int32_t* labels, float* logp, float* lse,

@@ -439,6 +439,11 @@ def layernorm_fwd(x, gamma, beta=None, eps=1e-5, out=None):
     return out, mean, rstd
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_parts(T, h):
+    return _lib.load().mtk_layernorm_bwd_parts(T, h)
+
+
 def layernorm_bwd(dy, x, gamma, mean, rstd, dres=None, bias=True):
     """(dx, dx_bf16, dgamma, dbeta) of layernorm_fwd: dx of x's type, with dres (of x's type, or None) added; dx_bf16
     the same rounded (None for bf16 rows); dbeta None without `bias`. dy f32 or bf16."""
@@ -449,24 +454,25 @@ def layernorm_bwd(dy, x, gamma, mean, rstd, dres=None, bias=True):
     pdy, dy_kind, lddy = _typed_rows(dy, T, h, "dy", dev)
     pres, res_kind, ldres = (None, kind, 0) if dres is None else _typed_rows(dres, T, h, "dres", dev)
     _need(res_kind == kind, "dres: of x's type")
-    lib = _lib.load()
-    dx = torch.empty((T, h), dtype=x.dtype, device=x.device)
-    dxb = torch.empty((T, h), dtype=torch.bfloat16, device=x.device) if kind == 0 else None
-    partial = torch.empty(2 * h * lib.mtk_layernorm_bwd_parts(T, h), dtype=torch.float32, device=x.device)
-    dg = torch.empty(h, dtype=torch.bfloat16, device=x.device)
-    db = torch.empty(h, dtype=torch.bfloat16, device=x.device) if bias else None
-    _ok(lib.mtk_layernorm_bwd(pdy, dy_kind, lddy, px, kind, ldx, _vec(gamma, h, torch.bfloat16, "gamma", dev),
-                              _vec(mean, T, torch.float32, "mean", dev), _vec(rstd, T, torch.float32, "rstd", dev),
-                              pres, ldres, dx.data_ptr(), _p(dxb), partial.data_ptr(), dg.data_ptr(), _p(db), T, h,
-                              _stream(dev)), "layernorm_bwd")
+    device, bf = x.device, torch.bfloat16
+    pg = _vec(gamma, h, bf, "gamma", dev)
+    dx = torch.empty((T, h), dtype=x.dtype, device=device)
+    dxb = torch.empty((T, h), dtype=bf, device=device) if kind == 0 else None
+    partial = torch.empty(2 * h * _norm_parts(T, h), dtype=torch.float32, device=device)
+    dg = torch.empty_like(gamma)
+    db = torch.empty_like(gamma) if bias else None
+    _ok(_lib.load().mtk_layernorm_bwd(pdy, dy_kind, lddy, px, kind, ldx, pg, _vec(mean, T, torch.float32, "mean", dev),
+                                      _vec(rstd, T, torch.float32, "rstd", dev), pres, ldres, dx.data_ptr(), _p(dxb),
+                                      partial.data_ptr(), dg.data_ptr(), _p(db), T, h, _stream(dev)), "layernorm_bwd")
     return dx, dxb, dg, db
 
 
 def _table_rows(t, what, dev, types=ROW_TYPES):
     """(rows, columns, type) of a contiguous matrix."""
-    _need(t.dim() == 2 and t.dtype in types and t.is_contiguous() and t.get_device() == dev,
-          f"{what}: a contiguous matrix on cuda:{dev} of {' or '.join(str(d) for d in types)}")
-    return t.shape[0], t.shape[1], ROW_TYPES[t.dtype]
+    shape, dtype = t.shape, t.dtype
+    if len(shape) != 2 or dtype not in types or not t.is_contiguous() or t.get_device() != dev:
+        raise MTError(-1, f"{what}: a contiguous matrix on cuda:{dev} of {' or '.join(str(d) for d in types)}")
+    return shape[0], shape[1], ROW_TYPES[dtype]
 
 
 def embed_lookup(tok, E, scale=1.0, dtype=torch.float32, err=None):
@@ -481,6 +487,11 @@ def embed_lookup(tok, E, scale=1.0, dtype=torch.float32, err=None):
     return x
 
 
+@functools.lru_cache(maxsize=256)
+def _embed_scratch(T, h):
+    return _lib.load().mtk_embed_lookup_bwd_scratch_bytes(T, h)
+
+
 def embed_lookup_bwd(tok, dx, V, scale=1.0, accumulate=None, err=None):
     """dE bf16 [V, h] of embed_lookup from dx f32 or bf16 [T, h], the same from run to run. accumulate: a dE to add to
     (its rows of no token stay), such as the gradient of a head that shares the table."""
@@ -492,11 +503,10 @@ def embed_lookup_bwd(tok, dx, V, scale=1.0, accumulate=None, err=None):
         dE = torch.empty((V, h), dtype=torch.bfloat16, device=dx.device)
     else:
         _need(_table_rows(dE, "accumulate", dev, (torch.bfloat16,))[:2] == (V, h), "accumulate: [V, h]")
-    lib = _lib.load()
-    scratch = torch.empty(lib.mtk_embed_lookup_bwd_scratch_bytes(T, h), dtype=torch.uint8, device=dx.device)
-    _ok(lib.mtk_embed_lookup_bwd(_vec(tok, T, torch.int32, "tok", dev), dx.data_ptr(), kind, dE.data_ptr(),
-                                 scratch.data_ptr(), T, h, V, scale, int(accumulate is not None), _flag(err, dev),
-                                 _stream(dev)), "embed_lookup_bwd")
+    scratch = torch.empty(_embed_scratch(T, h), dtype=torch.uint8, device=dx.device)
+    _ok(_lib.load().mtk_embed_lookup_bwd(_vec(tok, T, torch.int32, "tok", dev), dx.data_ptr(), kind, dE.data_ptr(),
+                                         scratch.data_ptr(), T, h, V, scale, accumulate is not None, _flag(err, dev),
+                                         _stream(dev)), "embed_lookup_bwd")
     return dE
 
 

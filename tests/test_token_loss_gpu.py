@@ -373,6 +373,32 @@ def test_preference_step(K):
         check(held)
 
 
+@pytest.mark.parametrize("T,V", [(5, 60000), (170, 40000), (3, 170000)])
+def test_wide_rows_in_a_graph(K, T, V):
+    """Rows split over clusters, captured and replayed with other logits and labels: what an eager call gives."""
+    rng = np.random.default_rng(T)
+    z = _logits(rng, T, V, "bf16")
+    lab = _dev(_labels(rng, T, V), torch.int32)
+    old, adv = _dev(rng.standard_normal(T) - 11), _dev(rng.standard_normal(T))
+    K.policy_loss(z, lab, old, adv)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = K.policy_loss(z, lab, old, adv)
+        logp, lse = K.token_logprobs(z, lab)
+        grad = K.token_logprobs_bwd(z, lab, lse, adv)
+    for _ in range(2):
+        z.copy_(_dev(rng.standard_normal((T, V)) * 2).to(z.dtype))
+        lab.copy_(_dev(_labels(rng, T, V), torch.int32))
+        adv.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, K.policy_loss(z, lab, old, adv)))
+        again = K.token_logprobs(z, lab)
+        assert torch.equal(again[0], logp) and torch.equal(again[1], lse)
+        assert torch.equal(K.token_logprobs_bwd(z, lab, lse, adv), grad)
+
+
 def test_two_calls_at_once(K):
     """Policy losses of different sizes on two streams at the same time give what they give alone."""
     rng = np.random.default_rng(12)
