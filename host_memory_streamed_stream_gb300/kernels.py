@@ -386,9 +386,9 @@ def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, weights=Non
     old_logp), w = weights (None: 1/T). logits, labels, scale as for token_logprobs; out as for its backward."""
     dev, T, V, z, kind, ld, lab = _logits(logits, labels)
     out, ldd = _grad_rows(out, T, V, dev)
-    f32 = torch.float32
-    logp, row_loss = torch.empty_like(labels, dtype=f32), torch.empty_like(labels, dtype=f32)
-    loss = torch.empty(1, dtype=f32, device=logits.device)
+    f32, device = torch.float32, logits.device
+    logp = torch.empty(T, dtype=f32, device=device)
+    row_loss, loss = torch.empty_like(logp), torch.empty(1, dtype=f32, device=device)
     _ok(_lib.load().mtk_policy_loss(z, kind, ld, lab, _vec(old_logp, T, f32, "old_logp", dev),
                                     _vec(advantages, T, f32, "advantages", dev),
                                     _opt(ref_logp, T, f32, "ref_logp", dev), _opt(weights, T, f32, "weights", dev),

@@ -144,10 +144,10 @@ def test_residual_in_place(K):
     assert rc == 0 and torch.equal(dres, want)
 
 
-def test_stream_and_graph(K):
+@pytest.mark.parametrize("T,h", [(300, 2056), (7, 12000), (900, 96)])
+def test_stream_and_graph(K, T, h):
     """Forward and backward on a stream of their own, and captured and replayed on other rows."""
     rng = np.random.default_rng(5)
-    T, h = 300, 2056
     x, dy = _rows(rng, T, h, "f32"), _rows(rng, T, h, "bf16", size=0.2)
     g, b = _gain(rng, h), _gain(rng, h, 0.0)
 
