@@ -281,7 +281,10 @@ __global__ void __launch_bounds__(kZeroThreads) zero_kernel(const SortArgs g) {
     for (int i0 = threadIdx.x; i0 < g.T; i0 += kZeroThreads * kSortAhead) {
       int v[kSortAhead];
 #pragma unroll
-      for (int j = 0; j < kSortAhead; ++j) v[j] = i0 + j * kZeroThreads < g.T ? g.tok[i0 + j * kZeroThreads] : -1;
+      for (int j = 0; j < kSortAhead; ++j) {
+        const int i = i0 + j * kZeroThreads;
+        v[j] = i < g.T ? __ldcg(g.tok + i) : -1;
+      }
 #pragma unroll
       for (int j = 0; j < kSortAhead; ++j)
         if (v[j] >= r0 && v[j] < r1) atomicOr(used + (v[j] - r0) / 32, 1u << ((v[j] - r0) & 31));
