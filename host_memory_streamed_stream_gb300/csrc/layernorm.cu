@@ -6,7 +6,7 @@
 // Bound by HBM: a row stays in the registers of its threads, so that every element is read once and the sum of
 // squares is taken of centred values. Measured at 8192 x 4096: forward of fp32 rows 35.1 us, 5.7 TB/s (a cast of the
 // same bytes takes 32), of bf16 ones 26.4; backward of fp32 rows with the residual's gradient 97.6 us, 6.2 TB/s with
-// the gains' sums, of bf16 ones 55.6, 4.8 TB/s, bound by its instructions. One row of 5120: 3 us on the device.
+// the gains' sums, of bf16 ones 49.4, 5.4 TB/s, bound by its instructions. One row of 5120: 3 us on the device.
 #include <algorithm>
 #include <cmath>
 
@@ -211,8 +211,10 @@ struct LnBwd {
 
 // The same with dy, x and dres of a row in the ring; dy n and dy add up in registers over a block's rows. dres is read
 // after the sums, when registers are free again (before them: 101.8 us, and 69.6 for bf16 rows). Rows wider than 512
-// threads hold are shared by two blocks of a cluster (CL = 2), by columns.
-template <class X, class D, int CL>
+// threads hold are shared by two blocks of a cluster (CL = 2), by columns. FULL: a row has
+// a multiple of 512 columns, so that no thread tests its own; for bf16 x and dy, bound by instructions (8192 x 4096:
+// 55.9 us with the tests, 49.4 without; of fp32 97.1 and 100.8).
+template <class X, class D, int CL, bool FULL>
 __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
   constexpr int W = sizeof(X) == 4 || sizeof(D) == 4 ? 4 : 8, K = kBwdCols / W;
   constexpr int BX = W * sizeof(X), BD = W * sizeof(D);
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (at + k * g.group) * W;
-      if (c < cols) {
+      if (FULL || c < cols) {
         copy_cols<D, W>(slot(st, 0, BD, k), dy + ahead * g.lddy + c);
         copy_cols<X, W>(slot(st, BD, BX, k), x + ahead * g.ldx + c);
       }
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           const int c = (at + k * g.group) * W;
-          if (c < cols) copy_cols<X, W>(slot(st, BD + BX, BX, k), res + ahead * g.lddres + c);
+          if (FULL || c < cols) copy_cols<X, W>(slot(st, BD + BX, BX, k), res + ahead * g.lddres + c);
         }
       }
       ahead += step;
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (at + k * g.group) * W;
-    if (c >= cols) break;
+    if (!FULL && c >= cols) break;
 #pragma unroll
     for (int j = 0; j < W / 2; ++j) gain[k][j] = reinterpret_cast<const uint32_t*>(g.gamma + c0 + c)[j];
   }
@@ -278,14 +280,14 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
     float2 n[K][W / 2], u[K][W / 2], sum[2] = {};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if ((at + k * g.group) * W >= cols) break;
+      if (!FULL && (at + k * g.group) * W >= cols) break;
       read_pairs<D, W>(reinterpret_cast<const D*>(slot(stage, 0, BD, k)), u[k]);
       read_pairs<X, W>(reinterpret_cast<const X*>(slot(stage, BD, BX, k)), n[k]);
     }
     load(stage);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if ((at + k * g.group) * W >= cols) break;
+      if (!FULL && (at + k * g.group) * W >= cols) break;
 #pragma unroll
       for (int j = 0; j < W / 2; ++j) {
         n[k][j] = __fmul2_rn(__fadd2_rn(n[k][j], both(-mean)), both(r));
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (at + k * g.group) * W;
-      if (c >= cols) break;
+      if (!FULL && c >= cols) break;
       float2 d[W / 2];
       if (res) read_pairs<X, W>(reinterpret_cast<const X*>(slot(stage, BD + BX, BX, k)), d);
 #pragma unroll
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = (at + k * g.group) * W;
-        if (c >= cols) break;
+        if (!FULL && c >= cols) break;
 #pragma unroll
         for (int j = 0; j < W / 2; ++j) {
           other[(id - 1) * g.h + c / 2 + j] = dg[k][j];
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (at + k * g.group) * W;
-    if (c >= cols) break;
+    if (!FULL && c >= cols) break;
     for (int o = 0; o < groups - 1; ++o)
 #pragma unroll
       for (int j = 0; j < W / 2; ++j) {
@@ -435,9 +437,12 @@ cudaError_t launch_bwd(LnBwd g, const BwdShape& b, int parts, cudaStream_t s) {
   g.stage_bytes = row;
   // at the end the ring holds the sums of all groups but one
   const int smem = std::max(g.stages * row, (b.n.groups - 1) * 2 * g.h * 4);
-  auto* k = b.cluster > 1 ? ln_bwd_kernel<X, D, 2> : ln_bwd_kernel<X, D, 1>;
-  static std::atomic<uint64_t> done[2];
-  const cudaError_t e = allow_shared(k, kNormRing, done[b.cluster > 1]);
+  auto* k = b.cluster > 1 ? ln_bwd_kernel<X, D, 2, false> : ln_bwd_kernel<X, D, 1, false>;
+  int which = b.cluster > 1;
+  if constexpr (sizeof(X) == 2 && sizeof(D) == 2)
+    if (b.cluster == 1 && g.h == b.n.group * kBwdCols) k = ln_bwd_kernel<X, D, 1, true>, which = 2;
+  static std::atomic<uint64_t> done[3];
+  const cudaError_t e = allow_shared(k, kNormRing, done[which]);
   if (e != cudaSuccess) return e;
   return launch_cluster_following(k, dim3(parts * b.cluster), threads, b.cluster, smem, s, g);
 }
