@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
   const X* res = g.dres ? static_cast<const X*>(g.dres) + c0 : nullptr;
   int turn = 0, stage = 0, half_turn = 0;
   int64_t t = static_cast<int64_t>(blockIdx.x / CL) * groups + id, ahead = t;
+  if constexpr (CL > 1) cluster_arrive();
   wait_for_previous();
   let_next_start();
   auto slot = [&](int st, int bytes_before, int bytes, int k) {
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kSmThreads) ln_bwd_kernel(const LnBwd g) {
   }
   float r = 0.f, mean = 0.f;
   if (t < g.T) r = g.rstd[t], mean = g.mean[t];
+  if constexpr (CL > 1) cluster_wait();  // both have started
   for (; t < g.T; t += step) {
     cp_async_wait_groups(g.stages - 1);
     float2 n[K][W / 2], u[K][W / 2], sum[2] = {};

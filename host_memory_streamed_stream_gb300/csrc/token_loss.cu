@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
     if (POLICY) zero_row(g.dlogits + t * g.ldd + c0, cols, threadIdx.x, NT);
     return;
   }
+  if (blocks > 1) cluster_arrive();
   const Z* z = static_cast<const Z*>(g.logits) + t * g.ld + c0;
   RowInputs<Z> in{};
   if (threadIdx.x == 0) in = row_inputs<Z, POLICY>(g, t, label);
@@ -376,12 +377,15 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
     add_terms<1>(r, &v, c);
   }
   int turn = 0;
+  bool started = false;  // all blocks of the cluster
   auto meet = [&](MaxSum v) {  // over the blocks of the row, in every thread
     v = merge_warp(v);
     if (lane == 0) part[turn][warp] = v;
     __syncthreads();
     v = merge_warp(lane < WARPS ? part[turn][lane] : MaxSum{-INFINITY, 0.f});
     if (blocks > 1) {
+      if (!started) cluster_wait();
+      started = true;
       if (warp == 0 && lane < static_cast<int>(blocks)) cluster_store(&others[turn][rank], lane, v);
       cluster_sync();
       v = merge_warp(lane < static_cast<int>(blocks) ? others[turn][lane] : MaxSum{-INFINITY, 0.f});
