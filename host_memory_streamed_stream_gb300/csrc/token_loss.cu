@@ -5,9 +5,9 @@
 //
 // Sums of exponentials run in fp32 as powers of two, 2^(c z - m) with c = a log2 e, against a whole number m that
 // is raised where a term would pass 1: rescaling is exact. What an approximation loses always in one direction adds up
-// over the tokens of a sequence, so that c is held as two floats, and the average error of the power is put back: a
-// token's logp is off by 1e-7 and its mean by less than 1e-8 (152064 columns, from 1.9e-7 without). The label's
-// logit, m and the logarithm meet in pairs of floats: a ratio of policies is exp of a small difference of numbers
+// over the tokens of a sequence, so that c is held as two floats (log2_factor.h), and the average error of the power is
+// put back: a token's logp is off by 1e-7 and its mean by less than 1e-8 (152064 columns, from 1.9e-7 without). The
+// label's logit, m and the logarithm meet in pairs of floats: a ratio of policies is exp of a small difference of numbers
 // of size 10, of which one float would lose 2^-21.
 //
 // Bound by HBM. Log-probabilities: 6000 rows of 32000 fp32 118 us, 6.5 TB/s, 3000 of 152064 bf16 139 us, 6.5 TB/s
@@ -20,6 +20,7 @@
 
 #include "follow.cuh"
 #include "kernels.h"
+#include "log2_factor.h"
 #include "mt_kernels.h"
 #include "rows.cuh"
 
@@ -28,7 +29,6 @@ namespace mt {
 namespace {
 
 constexpr float kMinScale = 0x1p-64f;
-constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);
 constexpr float kLn2 = 0.6931471805599453f, kLn2Low = 0.6931471805599453 - static_cast<double>(kLn2);
 
 __device__ __forceinline__ float pow2(float x) {
@@ -39,16 +39,6 @@ __device__ __forceinline__ float pow2(float x) {
 // The mean relative error of pow2 over any stretch of [-20, 0], measured against 64 bits: -4.9e-8 to -5.1e-8. (Above 0
 // it is 3.4e-8: exponents are kept at or below 0.)
 constexpr float kPow2Error = -5.0e-8f;
-// c = a log2 e. One float is off by up to 2^-25, which moves a row's logp by that times the label's distance from the
-// mean, always the same way (1e-7 a token, which a sequence of 1000 tokens adds up); hi + lo is not: hi has 12 bits, so
-// that what lo adds to c z is not below its last place, where it would always be lost.
-struct Factor {
-  float one, hi, lo;
-};
-__device__ __forceinline__ Factor factor(float scale) {
-  const float one = scale * kLog2e, hi = __uint_as_float(__float_as_uint(one) & 0xfffff000u);
-  return {one, hi, fmaf(scale, kLog2e, -hi) + scale * kLog2eLow};
-}
 
 // Sum of 2^(c z - m), m a whole number; -inf: nothing but -inf so far, sum 0. +inf: beyond the range of c z.
 struct MaxSum {
