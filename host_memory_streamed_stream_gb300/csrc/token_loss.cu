@@ -421,31 +421,69 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
 
 // dlogits of given dlogp and lse: a pass over the logits, from the last row to the first, since the L2 still holds some
 // of the last rows that token_logprobs read.
-constexpr int kGradChunks = 4;  // of a thread
+constexpr int kGradChunks = 4, kGradThreads = 256;  // chunks of a thread
+// Up to here p takes on lse's rounding, 2^-14 of it at most. Beyond, lse no longer has the sum's logarithm (or is out of
+// fp32's range), and one block takes the whole row, which it sums again with the largest logit subtracted (all rows of 2048
+// x 32000 bf16 far: 138 us for 44).
+constexpr float kFarLse = 1024.f;
+
+// A far row, in place or not: all of it is read before any of it is written.
 template <class Z>
-__global__ void __launch_bounds__(256) token_grad_kernel(const TokenRows g, const float* dlogp) {
-  constexpr int N = kChunk<Z>;
+__device__ __noinline__ void far_row_grad(const Z* z, bf16* d, int V, float scale, float k, int label) {
+  __shared__ float red[2][kGradThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float c = scale * kLog2e;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < V; i += kGradThreads) top = fmaxf(top, to_f32(z[i]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) red[0][warp] = top;
+  __syncthreads();
+  for (int w = 0; w < kGradThreads / 32; ++w) top = fmaxf(top, red[0][w]);
+#pragma unroll 8
+  for (int i = threadIdx.x; i < V; i += kGradThreads) sum += pow2((to_f32(z[i]) - top) * c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) red[1][warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+  for (int w = 0; w < kGradThreads / 32; ++w) sum += red[1][w];
+  const float kp = -k / sum;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < V; i += kGradThreads)
+    d[i] = __float2bfloat16_rn(kp * pow2((to_f32(z[i]) - top) * c) + (i == label ? k : 0.f));
+}
+template <class Z>
+__global__ void __launch_bounds__(kGradThreads) token_grad_kernel(const TokenRows g, const float* dlogp) {
+  constexpr int N = kChunk<Z>, STEP = kGradThreads * N;
   const int64_t t = gridDim.y - 1 - blockIdx.y;
   const Z* z = static_cast<const Z*>(g.logits) + t * g.ld;
   bf16* d = g.dlogits + t * g.ldd;
   wait_for_previous();
   let_next_start();
-  const int label = g.labels[t], whole = g.V / N * N, first = (blockIdx.x * 256 * kGradChunks + threadIdx.x) * N;
-  if (label < 0 || label >= g.V) {
-    const int c0 = blockIdx.x * 256 * kGradChunks * N;
-    zero_row(d + c0, min(256 * kGradChunks * N, g.V - c0), threadIdx.x, 256);
+  const int label = g.labels[t], whole = g.V / N * N, first = blockIdx.x * STEP * kGradChunks + threadIdx.x * N;
+  const float lse = g.lse[t];
+  const bool masked = label < 0 || label >= g.V, far = !(fabsf(lse) <= kFarLse);
+  if (masked | far) {  // one test, so that lse is not loaded behind the label's
+    if (masked) {
+      const int c0 = blockIdx.x * STEP * kGradChunks;
+      zero_row(d + c0, min(STEP * kGradChunks, g.V - c0), threadIdx.x, kGradThreads);
+    } else if (blockIdx.x == 0) {
+      far_row_grad(z, d, g.V, g.scale, dlogp[t] * g.scale, label);
+    }
     return;
   }
   uint4 raw[kGradChunks];
 #pragma unroll
   for (int j = 0; j < kGradChunks; ++j)
-    if (first + j * 256 * N < whole) raw[j] = __ldcs(reinterpret_cast<const uint4*>(z + first + j * 256 * N));
+    if (first + j * STEP < whole) raw[j] = __ldcs(reinterpret_cast<const uint4*>(z + first + j * STEP));
   const float k = dlogp[t] * g.scale;
-  const RowGrad q{g.lse[t] / g.scale, 0.f, k, -k};
+  const RowGrad q{lse / g.scale, 0.f, k, -k};
   const Factor c = factor(g.scale);
 #pragma unroll
   for (int j = 0; j < kGradChunks; ++j) {
-    const int i = first + j * 256 * N;
+    const int i = first + j * STEP;
     if (i < whole) {
       float v[N];
       unpack_chunk<Z>(raw[j], v);
@@ -699,7 +737,7 @@ cudaError_t token_logprobs_bwd(const void* logits, int type, int64_t ld, const i
   g.lse = const_cast<float*>(lse), g.dlogits = dlogits, g.ldd = ldd;
   if (!rows_args_ok(g, type) || !vec_ok(lse, 4) || !vec_ok(dlogp, 4) || !grad_ok(g, type)) return cudaErrorInvalidValue;
   auto* k = type == kRowF32 ? token_grad_kernel<float> : token_grad_kernel<bf16>;
-  const int columns = 256 * kGradChunks * (16 / row_type_bytes(type));
+  const int columns = kGradThreads * kGradChunks * (16 / row_type_bytes(type));
   for (int end = T; end > 0; end -= 65535) {
     TokenRows a = g;
     const int n = std::min(end, 65535), t = end - n;
@@ -707,7 +745,8 @@ cudaError_t token_logprobs_bwd(const void* logits, int type, int64_t ld, const i
     a.dlogits = dlogits + t * ldd;
     a.labels += t;
     a.lse += t;
-    const cudaError_t e = launch_following(k, dim3((V + columns - 1) / columns, n), 256, 0, s, a, dlogp + t);
+    const cudaError_t e = launch_following(k, dim3((V + columns - 1) / columns, n), kGradThreads, 0, s, a,
+                                           dlogp + t);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -236,8 +236,9 @@ int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, voi
  *
  * mtk_token_logprobs: logp f32 [T] and lse f32 [T].
  * mtk_token_logprobs_bwd: dlogits bf16 [T, V] (row stride ldd) = a dlogp_t ([v = label] - p_tv) from dlogp f32 [T] and
- *   the forward's lse (whose rounding p takes on: 2^-24 of lse's size). dlogits may be the bf16 logits themselves (the
- *   same address and stride), else they must not overlap (MT_EINVAL).
+ *   the forward's lse. p takes on its rounding, 2^-24 of its size, up to a size of 1024; a row further away is summed
+ *   again. dlogits may be the bf16 logits themselves (the same address and stride), else they must not overlap
+ *   (MT_EINVAL).
  * mtk_policy_loss: the clipped policy loss with a KL term, loss and gradient in one call. With r = exp(logp -
  *   old_logp), A = advantages, w = weights (f32 [T]; NULL: 1/T for every row):
  *     l_t = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(ref - logp) - (ref - logp) - 1)
