@@ -517,14 +517,13 @@ __global__ void __launch_bounds__(1024) sum_kernel(const float* v, int n, float 
   }
 }
 
-__device__ float block_total(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ Pair block_total(Pair v, Pair* red) {
+  v = add_warp(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.f;
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v += red[i];
+  v = {0.f, 0.f};
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v = add(v, red[i]);
   return v;
 }
 
@@ -537,9 +536,16 @@ struct Preference {
   float *pair_loss, *rewards, *dlogp;
 };
 
+// A row's part of its sequence's score, added to v where the row is trained. Scores are held in pairs of floats: two sums
+// of thousands, of which a float's step is 2^-11, differ by little.
+__device__ __forceinline__ Pair add_score(const Preference& g, Pair v, int i, bool on) {
+  const float a = g.logp[i], b = g.ref ? g.ref[i] : 0.f;
+  v = add(v, {on ? a : 0.f, 0.f});
+  return g.ref ? add(v, {on ? -b : 0.f, 0.f}) : v;
+}
 // A pair's loss from its two scores, and the derivative by their difference times beta (h).
-__device__ __forceinline__ float pair_loss(const Preference& g, float s0, float s1, float& d) {
-  const float h = g.beta * (s0 - s1) - g.margin;
+__device__ __forceinline__ float pair_loss(const Preference& g, const Pair& s0, const Pair& s1, float& d) {
+  const float h = g.beta * value(add(s0, negative(s1))) - g.margin;
   float loss;
   if (g.kind == MTK_PREF_SIGMOID) {
     const float e = expf(-fabsf(h)), l = log1pf(e);  // softplus(-|h|)
@@ -563,8 +569,9 @@ __device__ __forceinline__ int bound_of(const Preference& g, int j) { return min
 // 4 sequences 5.6 us, 4048 of 8 9.1; as two launches 6.1 and 2.9.)
 constexpr int kFewRows = 4096, kFewPairs = 1024;
 __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g, float* loss) {
-  __shared__ float score[2 * kFewPairs], share[2 * kFewPairs];
-  __shared__ float2 part[32];  // a warp's sum and count
+  __shared__ Pair score[2 * kFewPairs];
+  __shared__ float share[2 * kFewPairs];
+  __shared__ float4 part[32];  // a warp's sum and count
   __shared__ Pair red[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = 2 * g.pairs;
   const int team = n > 16 ? 1 : 32 / n, teams = 32 / team, mate = warp % team;  // team > 1: a team for each sequence
@@ -572,32 +579,32 @@ __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g
   let_next_start();
   for (int j0 = 0; j0 < n; j0 += teams) {
     const int j = j0 + warp / team;
-    float v = 0.f, count = 0.f;
+    Pair v{0.f, 0.f};
+    float count = 0.f;
     if (j < n) {
       const int lo = bound_of(g, j), hi = bound_of(g, j + 1);
 #pragma unroll 8
       for (int i = lo + mate * 32 + lane; i < hi; i += team * 32) {
         const bool on = !g.labels || g.labels[i] >= 0;
-        const float a = g.logp[i], b = g.ref ? g.ref[i] : 0.f;
-        v += on ? a - b : 0.f;
+        v = add_score(g, v, i, on);
         count += on ? 1.f : 0.f;
       }
     }
+    v = add_warp(v);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v += __shfl_xor_sync(0xffffffffu, v, o);
-      count += __shfl_xor_sync(0xffffffffu, count, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
     if (team > 1) {
-      if (lane == 0) part[warp] = make_float2(v, count);
+      if (lane == 0) part[warp] = make_float4(v.hi, v.lo, count, 0.f);
       __syncthreads();
-      v = count = 0.f;
-      for (int k = warp - mate; k < warp - mate + team && k < 32; ++k) v += part[k].x, count += part[k].y;
+      v = {0.f, 0.f};
+      count = 0.f;
+      for (int k = warp - mate; k < warp - mate + team && k < 32; ++k)
+        v = add(v, {part[k].x, part[k].y}), count += part[k].z;
     }
     if (lane == 0 && mate == 0 && j < n) {
       share[j] = g.average ? 1.f / fmaxf(count, 1.f) : 1.f;
-      score[j] = v * share[j];
-      g.rewards[j] = g.beta * score[j];
+      score[j] = product(v, share[j]);
+      g.rewards[j] = g.beta * value(score[j]);
     }
   }
   __syncthreads();
@@ -608,8 +615,8 @@ __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g
     g.pair_loss[p] = l;
     sum = add(sum, {l, 0.f});
     const float k = g.beta * d / static_cast<float>(g.pairs);
-    score[2 * p] = k * share[2 * p];
-    score[2 * p + 1] = -k * share[2 * p + 1];
+    share[2 * p] *= k;
+    share[2 * p + 1] *= -k;
   }
   sum = add_warp(sum);
   if (lane == 0) red[warp] = sum;
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g
   }
   for (int j = warp / team; j < n; j += teams) {
     const int lo = bound_of(g, j), hi = bound_of(g, j + 1);
-    const float k = score[j];
+    const float k = share[j];
 #pragma unroll 4
     for (int i = lo + mate * 32 + lane; i < hi; i += team * 32) g.dlogp[i] = g.labels && g.labels[i] < 0 ? 0.f : k;
   }
@@ -632,7 +639,7 @@ __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g
 // One block a pair: the sums of its two sequences, its loss, and its rows' dlogp. The last block zeroes the rows
 // of no sequence.
 __global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
-  __shared__ float red[16];
+  __shared__ Pair red[16];
   wait_for_previous();
   let_next_start();
   const int p = blockIdx.x;
@@ -642,29 +649,31 @@ __global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
     for (int i = last + threadIdx.x; i < g.T; i += blockDim.x) g.dlogp[i] = 0.f;
     return;
   }
-  float s[2], share[2];
+  Pair s[2];
+  float share[2];
   int lo[2], hi[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     lo[j] = bound_of(g, 2 * p + j);
     hi[j] = bound_of(g, 2 * p + j + 1);
-    float v = 0.f, n = 0.f;
+    Pair v{0.f, 0.f};
+    float n = 0.f;
     for (int i = lo[j] + threadIdx.x; i < hi[j]; i += blockDim.x) {
       if (g.labels && g.labels[i] < 0) continue;
-      v += g.ref ? g.logp[i] - g.ref[i] : g.logp[i];
+      v = add_score(g, v, i, true);
       n += 1.f;
     }
     v = block_total(v, red);
-    n = g.average ? block_total(n, red) : 1.f;
-    share[j] = 1.f / fmaxf(n, 1.f);
-    s[j] = v * share[j];
+    if (g.average) n = value(block_total({n, 0.f}, red));
+    share[j] = g.average ? 1.f / fmaxf(n, 1.f) : 1.f;
+    s[j] = product(v, share[j]);
   }
   float d;
   const float loss = pair_loss(g, s[0], s[1], d);
   if (threadIdx.x == 0) {
     g.pair_loss[p] = loss;
-    g.rewards[2 * p] = g.beta * s[0];
-    g.rewards[2 * p + 1] = g.beta * s[1];
+    g.rewards[2 * p] = g.beta * value(s[0]);
+    g.rewards[2 * p + 1] = g.beta * value(s[1]);
   }
   const float k = g.beta * d / static_cast<float>(g.pairs);
 #pragma unroll
