@@ -565,72 +565,58 @@ __device__ __forceinline__ float pair_loss(const Preference& g, const Pair& s0, 
 // The row at which sequence j begins, or the one before it ends.
 __device__ __forceinline__ int bound_of(const Preference& g, int j) { return min(max(g.bounds[j], 0), g.T); }
 
-// Few rows: one block does all of it; where there are fewer sequences than warps, several warps share one. (322 rows of
-// 4 sequences 5.6 us, 4048 of 8 9.1; as two launches 6.1 and 2.9.)
-constexpr int kFewRows = 4096, kFewPairs = 1024;
+// Few rows of few sequences: one block does all of it, several warps a sequence. Against a block a pair and another launch
+// for the mean, with a reference and labels: 322 rows of 4 sequences 2.7 and 4.7 us, 4096 of 2 3.9 and 7.6, of 8 3.9 and
+// 4.6, of 32 3.6 and 4.5. With warps that took more sequences in turn, 64 took 5.3 and 4.5, 2048 69 and 13.
+constexpr int kFewRows = 4096, kFewPairs = 16;
 __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g, float* loss) {
   __shared__ Pair score[2 * kFewPairs];
   __shared__ float share[2 * kFewPairs];
   __shared__ float4 part[32];  // a warp's sum and count
-  __shared__ Pair red[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = 2 * g.pairs;
-  const int team = n > 16 ? 1 : 32 / n, teams = 32 / team, mate = warp % team;  // team > 1: a team for each sequence
+  const int team = 32 / n, j = warp / team, mate = warp % team;  // a team of warps for each sequence
   wait_for_previous();
   let_next_start();
-  for (int j0 = 0; j0 < n; j0 += teams) {
-    const int j = j0 + warp / team;
-    Pair v{0.f, 0.f};
-    float count = 0.f;
-    if (j < n) {
-      const int lo = bound_of(g, j), hi = bound_of(g, j + 1);
+  int lo = 0, hi = 0;
+  if (j < n) lo = bound_of(g, j), hi = bound_of(g, j + 1);
+  Pair v{0.f, 0.f};
+  float count = 0.f;
 #pragma unroll 8
-      for (int i = lo + mate * 32 + lane; i < hi; i += team * 32) {
-        const bool on = !g.labels || g.labels[i] >= 0;
-        v = add_score(g, v, i, on);
-        count += on ? 1.f : 0.f;
-      }
-    }
-    v = add_warp(v);
+  for (int i = lo + mate * 32 + lane; i < hi; i += team * 32) {
+    const bool on = !g.labels || g.labels[i] >= 0;
+    v = add_score(g, v, i, on);
+    count += on ? 1.f : 0.f;
+  }
+  v = add_warp(v);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
-    if (team > 1) {
-      if (lane == 0) part[warp] = make_float4(v.hi, v.lo, count, 0.f);
-      __syncthreads();
-      v = {0.f, 0.f};
-      count = 0.f;
-      for (int k = warp - mate; k < warp - mate + team && k < 32; ++k)
-        v = add(v, {part[k].x, part[k].y}), count += part[k].z;
-    }
-    if (lane == 0 && mate == 0 && j < n) {
-      share[j] = g.average ? 1.f / fmaxf(count, 1.f) : 1.f;
-      score[j] = product(v, share[j]);
-      g.rewards[j] = g.beta * value(score[j]);
-    }
-  }
+  for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+  if (lane == 0) part[warp] = make_float4(v.hi, v.lo, count, 0.f);
   __syncthreads();
-  Pair sum{0.f, 0.f};
-  for (int p = threadIdx.x; p < g.pairs; p += 1024) {
-    float d;
-    const float l = pair_loss(g, score[2 * p], score[2 * p + 1], d);
-    g.pair_loss[p] = l;
-    sum = add(sum, {l, 0.f});
-    const float k = g.beta * d / static_cast<float>(g.pairs);
-    share[2 * p] *= k;
-    share[2 * p + 1] *= -k;
+  if (lane == 0 && mate == 0 && j < n) {
+    for (int k = warp + 1; k < warp + team; ++k) v = add(v, {part[k].x, part[k].y}), count += part[k].z;
+    share[j] = g.average ? 1.f / fmaxf(count, 1.f) : 1.f;
+    score[j] = product(v, share[j]);
+    g.rewards[j] = g.beta * value(score[j]);
   }
-  sum = add_warp(sum);
-  if (lane == 0) red[warp] = sum;
   __syncthreads();
   if (warp == 0) {
-    sum = add_warp(red[lane]);
+    Pair sum{0.f, 0.f};
+    if (lane < g.pairs) {
+      float d;
+      const float l = pair_loss(g, score[2 * lane], score[2 * lane + 1], d);
+      g.pair_loss[lane] = l;
+      sum = {l, 0.f};
+      const float k = g.beta * d / static_cast<float>(g.pairs);
+      share[2 * lane] *= k;
+      share[2 * lane + 1] *= -k;
+    }
+    sum = add_warp(sum);
     if (lane == 0) *loss = value(sum) / static_cast<float>(g.pairs);
   }
-  for (int j = warp / team; j < n; j += teams) {
-    const int lo = bound_of(g, j), hi = bound_of(g, j + 1);
-    const float k = share[j];
+  __syncthreads();
+  const float k = j < n ? share[j] : 0.f;
 #pragma unroll 4
-    for (int i = lo + mate * 32 + lane; i < hi; i += team * 32) g.dlogp[i] = g.labels && g.labels[i] < 0 ? 0.f : k;
-  }
+  for (int i = lo + mate * 32 + lane; i < hi; i += team * 32) g.dlogp[i] = g.labels && g.labels[i] < 0 ? 0.f : k;
   const int first = bound_of(g, 0), last = max(first, bound_of(g, n));
   for (int i = threadIdx.x; i < first; i += 1024) g.dlogp[i] = 0.f;
   for (int i = last + threadIdx.x; i < g.T; i += 1024) g.dlogp[i] = 0.f;

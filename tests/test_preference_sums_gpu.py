@@ -30,8 +30,9 @@ def _dev(a, dtype=torch.float32):
     return torch.tensor(np.asarray(a), dtype=dtype).cuda()
 
 
-# one launch for all of it, with several warps a sequence and with one; a block a pair
-@pytest.mark.parametrize("lengths", [[2000, 2001], [250] * 16, [40] * 100, [30000, 30011], [2500] * 6])
+# one launch for all of it, with several warps a sequence and with one, up to its largest; a block a pair
+@pytest.mark.parametrize("lengths", [[2000, 2001], [250] * 16, [40] * 100, [30000, 30011], [2500] * 6, [128] * 32,
+                                     [100] * 34, [0, 4096], [2048, 2049], [700] * 5 + [1]])
 @pytest.mark.parametrize("ref,masked,average", [(False, False, False), (True, True, False), (True, False, True)])
 def test_long_sums(K, lengths, ref, masked, average):
     rng = np.random.default_rng(len(lengths))
