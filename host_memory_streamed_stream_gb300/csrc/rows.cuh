@@ -154,12 +154,17 @@ inline bool rows_ok(const void* p, int64_t ld, int64_t cols) {
   return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld >= cols && ld % 8 == 0;
 }
 inline bool vec_ok(const void* p, uintptr_t bytes) { return p && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-// Whether two matrices share memory, from the first to the last element of each.
+// Whether two matrices may share an element: not if one ends before the other begins, nor if they lie beside each other in
+// rows of one buffer, the same number of bytes apart. What else interleaves counts as sharing.
 inline bool spans_overlap(const void* a, int64_t lda, int esz_a, const void* b, int64_t ldb, int esz_b, int64_t rows,
                           int64_t cols) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   const uintptr_t a1 = a0 + ((rows - 1) * lda + cols) * esz_a, b1 = b0 + ((rows - 1) * ldb + cols) * esz_b;
-  return a0 < b1 && b0 < a1;
+  if (a1 <= b0 || b1 <= a0) return false;
+  const uintptr_t row = lda * esz_a, wide_a = cols * esz_a, wide_b = cols * esz_b;
+  if (row != static_cast<uintptr_t>(ldb * esz_b)) return true;
+  const uintptr_t gap = b0 >= a0 ? (b0 - a0) % row : row - 1 - (a0 - b0 - 1) % row;  // from a row of a on to the next of b
+  return gap < wide_a || gap + wide_b > row;
 }
 
 inline bool ranges_overlap(const void* a, uint64_t bytes_a, const void* b, uint64_t bytes_b) {

@@ -238,7 +238,7 @@ int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, voi
  * mtk_token_logprobs_bwd: dlogits bf16 [T, V] (row stride ldd) = a dlogp_t ([v = label] - p_tv) from dlogp f32 [T] and
  *   the forward's lse. p takes on its rounding, 2^-24 of its size, up to a size of 1024; a row further away is summed
  *   again. dlogits may be the bf16 logits themselves (the same address and stride), else they must not overlap
- *   (MT_EINVAL).
+ *   (MT_EINVAL; matrices may interleave only beside each other in rows of one buffer, equally many bytes apart).
  * mtk_policy_loss: the clipped policy loss with a KL term, loss and gradient in one call. With r = exp(logp -
  *   old_logp), A = advantages, w = weights (f32 [T]; NULL: 1/T for every row):
  *     l_t = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(ref - logp) - (ref - logp) - 1)
@@ -278,7 +278,7 @@ int mtk_preference_loss(const void* logp, const void* ref_logp, const void* labe
  * Layer norm beside the RMSNorm: y bf16 = n gamma + beta, n = (x - mean) rstd, mean f32 [T] the row's mean and
  * rstd f32 [T] = 1/sqrt(mean((x - mean)^2) + eps). x [T, h] of `type` with row stride ldx, y with row stride
  * ldy; gamma, beta bf16 [h], 16-byte aligned (beta may be NULL). T <= 2^30, h a multiple of 8, at most 16384. y must
- * not overlap x.
+ * not overlap x (beside it in rows of one buffer it does not, if both are equally many bytes apart).
  *
  * mtk_layernorm_bwd: with u = dy gamma: dx = dres + rstd (u - mean(u) - n mean(u n)) over the h columns, from dy [T, h]
  * of dy_type (row stride lddy), the forward's x, mean and rstd and dres of x's type (row stride lddres, or
