@@ -185,7 +185,7 @@ __device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, con
     if (g.kl != 0.f) {
       const float far = value(add({in.ref, 0.f}, negative(logp)));
       const float em1 = expm1f(far);
-      loss += g.kl * (em1 - far);
+      loss += g.kl * (em1 < INFINITY ? em1 - far : em1);  // infinite, also where far itself is; NaN stays
       d -= g.kl * em1;
     }
     if (write) g.row_loss[t] = in.weight * loss;
