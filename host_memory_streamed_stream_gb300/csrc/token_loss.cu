@@ -16,6 +16,7 @@
 // the L2 still holds. What did not help the policy loss: a ring of shared memory that holds the row, filled by cp.async
 // (1.8 times as long), bulk prefetches of the next row into the L2 (1.3), persistent blocks (1.05).
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "follow.cuh"
@@ -175,7 +176,8 @@ __device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, con
     if (write) g.lse[t] = value(add(product({z0, 0.f}, g.scale), log_sum));
     return {};
   } else {
-    const float ratio = expf(value(add(logp, {-in.old_logp, 0.f})));
+    float ratio = expf(value(add(logp, {-in.old_logp, 0.f})));
+    if (ratio == INFINITY) ratio = FLT_MAX;  // times an advantage of 0 it is 0
     const float lo = 1.f - g.clip_low, hi = 1.f + g.clip_high;
     // comparisons rather than fminf, which would drop a NaN
     const float cut = ratio < lo ? lo : ratio > hi ? hi : ratio;
@@ -188,6 +190,7 @@ __device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, con
       loss += g.kl * (em1 < INFINITY ? em1 - far : em1);  // infinite, also where far itself is; NaN stays
       d -= g.kl * em1;
     }
+    if (in.weight == 0.f && loss == loss) loss = d = 0.f;  // where exp has passed fp32's range too
     if (write) g.row_loss[t] = in.weight * loss;
     const float k = in.weight * d * g.scale;
     return {z0, r.m == -INFINITY ? 0.f : r.m, k, -k / r.s};
