@@ -2,30 +2,11 @@
 // kernels of the losses, the layer norm and the embedding.
 #pragma once
 #include <cstdint>
-#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
 
 namespace mt {
-
-// Eight neighbouring columns. A thread's loads are issued first and unpacked where they are used.
-template <class T>
-struct Raw8;
-template <>
-struct Raw8<float> {
-  uint4 a, b;
-};
-template <>
-struct Raw8<bf16> {
-  uint4 a;
-};
-
-__device__ __forceinline__ Raw8<float> load8(const float* p) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
-  return {q[0], q[1]};
-}
-__device__ __forceinline__ Raw8<bf16> load8(const bf16* p) { return {*reinterpret_cast<const uint4*>(p)}; }
 
 __device__ __forceinline__ void unpack8(const uint4& u, float* v) {
   const uint32_t x[4] = {u.x, u.y, u.z, u.w};
@@ -35,24 +16,12 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* v) {
     v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void unpack8(const Raw8<bf16>& r, float* v) { unpack8(r.a, v); }
-__device__ __forceinline__ void unpack8(const Raw8<float>& r, float* v) {
-  const uint32_t x[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[i]);
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(bf16* p, const float* v) { *reinterpret_cast<uint4*>(p) = pack8(v); }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  float4* q = reinterpret_cast<float4*>(p);
-  q[0] = make_float4(v[0], v[1], v[2], v[3]);
-  q[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -81,19 +50,20 @@ template <class T, int W>
 __device__ __forceinline__ void write_cols(T* p, const float* v) {
   if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   else if constexpr (W == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-  else store8(p, v);
+  else *reinterpret_cast<uint4*>(p) = pack8(v);
 }
 
-// cp.async: 16 bytes (or 8) of global memory to shared memory, of which the first `bytes` are read and the rest is
-// zero. A thread waits for its own copies by groups.
-__device__ __forceinline__ void cp_async_chunk(void* dst, const void* src, int bytes = 16) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+// cp.async: 16 bytes (or 8) of global memory to shared memory. A thread waits for its own copies by groups.
+__device__ __forceinline__ void cp_async_chunk(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_half(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Until at most n of this thread's groups are in flight, n <= 24.
+// Until at most n of this thread's groups are in flight. Rings of 4 rows need n <= 3; the other cases make a jump table of
+// the switch, whose pace suits the layer norm's fp32 backward at 8192 x 4096 (97 us, 102 as a chain of tests), but not
+// at 8000 x 5120 (138, 113).
 __device__ __forceinline__ void cp_async_wait_groups(int n) {
 #define MT_WAIT(N) \
   case N: asm volatile("cp.async.wait_group " #N ";" ::: "memory"); break;
