@@ -8,9 +8,10 @@
 // cluster's, else beside the sums. No floating-point atomics: the result does not change from run to run.
 //
 // Bound by HBM, with a sort of 13 us (8192 tokens) and joins of 6 us that it cannot hide all of. Measured: 8192 tokens
-// x 4096 fp32, 32000 rows 73 us (zeros and sort 42, sums 24, joins 6), 5.2 TB/s; 131072 x 4096 bf16 227 us (sort 25,
-// sums 190, joins 12), 5.9 TB/s. Lookup of 4096 x 5120 to fp32: 18 us on the device, 20.5 in a row of calls, 5.3 TB/s.
-// Zeroing most rows beside the sums for few tokens too, which would hide the sort, measured 90 us.
+// x 4096 fp32, 32000 rows 71 us (zeros and sort 42, sums 24, joins 6), 5.4 TB/s; 131072 x 4096 bf16 227 us (sort 25,
+// sums 190, joins 12), 5.9 TB/s. Added to a gradient that is there: 60 us, of which the bytes take 28 (nothing hides
+// the sort), and 8192 x 256 19 us of 2. Lookup of 4096 x 5120 to fp32: 18 us on the device, 20.8 in a row of calls, 5.2
+// TB/s. Zeroing most rows beside the sums for few tokens too, which would hide the sort, measured 90 us.
 #include <algorithm>
 #include <cmath>
 #include <utility>
@@ -60,6 +61,10 @@ constexpr int kSortBits = 9;       // of a digit at most
 constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortAhead = 8;      // loads a thread has in flight
 constexpr int kSortSmem = kSortWarps * kSortBins * 4;  // counters
+// Up to here one cluster sorts, and zeros are written beside it; beyond, 128 blocks sort in two launches a pass and
+// zeros are written beside the sums. Both ways, 32000 rows of 4096 fp32: 8192 tokens 72 and 119 us, 16384 103 and 137,
+// 32768 150 and 155, 49152 208 and 189, 131072 428 and 380; 256 columns: 32768 33 and 36, 65536 50 and 38. Added to a
+// gradient, without zeros, they meet earlier: 16384 of 4096 99 and 96, of 256 24 and 26, 32768 33 and 29.
 constexpr int kClusterTokens = 32768;
 constexpr int kGapBlocks = 240;  // that write zeros in the launch of the sums (131072 x 4096: 120 244 us, 240 234)
 

@@ -3,10 +3,12 @@
 //   mean = sum x / h,  rstd = 1 / sqrt(sum (x - mean)^2 / h + eps),  n = (x - mean) rstd,  y = n gamma + beta
 //   u = dy gamma,  dx = dres + rstd (u - sum u / h - n sum(u n) / h),  dgamma = sum_t dy n,  dbeta = sum_t dy
 //
-// Bound by HBM: a row stays in the registers of its threads, so that every element is read once and the sum of
-// squares is taken of centred values. Measured at 8192 x 4096: forward of fp32 rows 35.1 us, 5.7 TB/s (a cast of the
-// same bytes takes 32), of bf16 ones 26.4; backward of fp32 rows with the residual's gradient 97.6 us, 6.2 TB/s with
-// the gains' sums, of bf16 ones 49.4, 5.4 TB/s, bound by its instructions. One row of 5120: 3 us on the device.
+// Bound by HBM: a row stays in the registers of its threads, so that every element is read once and the sum of squares
+// is taken of centred values. Measured at 8192 x 4096: forward of fp32 rows 35.2 us, 5.7 TB/s (a cast of the same bytes
+// takes 32), of bf16 ones 27 (20 for the bytes: four warps a scheduler, as 128 registers allow, fill half of its issue
+// slots between the latencies of a row's steps); backward of fp32 rows with the residual's gradient 97.2 us, 6.2 TB/s
+// with the gains' sums, of bf16 ones 50, 5.4 TB/s, bound by its instructions. At 8000 x 5120: forward 44 and 34 us,
+// backward 138 (one block of 320 threads an SM; 110 for the bytes) and 66. One row of 5120: 3 us on the device.
 #include <algorithm>
 #include <cmath>
 

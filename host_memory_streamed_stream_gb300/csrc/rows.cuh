@@ -61,9 +61,9 @@ __device__ __forceinline__ void cp_async_half(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Until at most n of this thread's groups are in flight. Rings of 4 rows need n <= 3; the other cases make a jump table of
-// the switch, whose pace suits the layer norm's fp32 backward at 8192 x 4096 (97 us, 102 as a chain of tests), but not
-// at 8000 x 5120 (138, 113).
+// Until at most n of this thread's groups are in flight. Rings of 4 rows need n <= 3; the other cases make a jump table
+// of the switch, whose pace suits the layer norm's fp32 backward at 8192 x 4096 (97 us, 102 as a chain of tests), but
+// not at 8000 x 5120 (138, 113).
 __device__ __forceinline__ void cp_async_wait_groups(int n) {
 #define MT_WAIT(N) \
   case N: asm volatile("cp.async.wait_group " #N ";" ::: "memory"); break;
@@ -124,8 +124,8 @@ inline bool rows_ok(const void* p, int64_t ld, int64_t cols) {
   return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld >= cols && ld % 8 == 0;
 }
 inline bool vec_ok(const void* p, uintptr_t bytes) { return p && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-// Whether two matrices may share an element: not if one ends before the other begins, nor if they lie beside each other in
-// rows of one buffer, the same number of bytes apart. What else interleaves counts as sharing.
+// Whether two matrices may share an element: not if one ends before the other begins, nor if they lie beside each other
+// in rows of one buffer, the same number of bytes apart. What else interleaves counts as sharing.
 inline bool spans_overlap(const void* a, int64_t lda, int esz_a, const void* b, int64_t ldb, int esz_b, int64_t rows,
                           int64_t cols) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
@@ -133,7 +133,8 @@ inline bool spans_overlap(const void* a, int64_t lda, int esz_a, const void* b, 
   if (a1 <= b0 || b1 <= a0) return false;
   const uintptr_t row = lda * esz_a, wide_a = cols * esz_a, wide_b = cols * esz_b;
   if (row != static_cast<uintptr_t>(ldb * esz_b)) return true;
-  const uintptr_t gap = b0 >= a0 ? (b0 - a0) % row : row - 1 - (a0 - b0 - 1) % row;  // from a row of a on to the next of b
+  // from the start of a row of a on to the next one of b
+  const uintptr_t gap = b0 >= a0 ? (b0 - a0) % row : row - 1 - (a0 - b0 - 1) % row;
   return gap < wide_a || gap + wide_b > row;
 }
 

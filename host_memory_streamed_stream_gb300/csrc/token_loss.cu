@@ -3,18 +3,21 @@
 //
 //   lse_t = log sum_v exp(a z_tv),  logp_t = a z_t,label - lse_t,  dlogits_tv = a dlogp_t ([v = label] - p_tv)
 //
-// Sums of exponentials run in fp32 as powers of two, 2^(c z - m) with c = a log2 e, against a whole number m that
-// is raised where a term would pass 1: rescaling is exact. What an approximation loses always in one direction adds up
+// Sums of exponentials run in fp32 as powers of two, 2^(c z - m) with c = a log2 e, against a whole number m that is
+// raised where a term would pass 1: rescaling is exact. What an approximation loses always in one direction adds up
 // over the tokens of a sequence, so that c is held as two floats (log2_factor.h), and the average error of the power is
-// put back: a token's logp is off by 1e-7 and its mean by less than 1e-8 (152064 columns, from 1.9e-7 without). The
-// label's logit, m and the logarithm meet in pairs of floats: a ratio of policies is exp of a small difference of numbers
-// of size 10, of which one float would lose 2^-21.
+// put back. Rows of 1001 to 152064 columns whose lse is near 0, so that its own rounding is nothing: off by 5e-8 in the
+// root mean square, 2.6e-7 at most, below 9e-9 in the mean (1.9e-7 without the two); storing a logp of 8 to 16 as fp32
+// adds 2.8e-7. The label's logit, m and the logarithm meet in pairs of floats: a ratio of policies is exp of a small
+// difference of numbers of size 10, of which one float would lose 2^-21.
 //
-// Bound by HBM. Log-probabilities: 6000 rows of 32000 fp32 118 us, 6.5 TB/s, 3000 of 152064 bf16 139 us, 6.5 TB/s
+// Bound by HBM. Log-probabilities: 6000 rows of 32000 fp32 114 us, 6.7 TB/s, 3000 of 152064 bf16 135 us, 6.8 TB/s
 // (where the exponential unit is 70 % busy). Policy loss, whose second look at a row reads the L2: 198 us, 5.8 TB/s,
-// and 338 us, 5.4 TB/s. Gradient alone: 4048 rows of 152064 bf16, a quarter of them masked, 295 us, 6.7 TB/s with what
-// the L2 still holds. What did not help the policy loss: a ring of shared memory that holds the row, filled by cp.async
-// (1.8 times as long), bulk prefetches of the next row into the L2 (1.3), persistent blocks (1.05).
+// and 343 us, 5.3 TB/s; rows of 3000 to 10000 columns 1.5 to 1.6 times their bytes' time (8192 x 5268 fp32 58 us of
+// 39), as a small block waits for its loads and at its barrier between two looks. Gradient alone: 4048 rows of 152064
+// bf16, a quarter of them masked, 313 us, 6.9 TB/s with what the L2 still holds. What did not help the policy loss: a
+// ring of shared memory that holds the row, filled by cp.async (1.8 times as long), bulk prefetches of the next row
+// into the L2 (1.3), persistent blocks (1.05).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -167,7 +170,8 @@ template <bool POLICY, class Z>
 __device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, const RowInputs<Z>& in, float z0,
                                               const MaxSum& r, bool write) {
   Pair log_sum = add(product({kLn2, kLn2Low}, r.m), log_pair(r.s));
-  // a power of two is a sum of exact terms
+  // A power of two is mostly a sum of exact terms. (Other sums of them, as of three equal logits of 0, are off by
+  // 5e-8.)
   if ((__float_as_uint(r.s) & 0x7fffffu) != 0) log_sum = add(log_sum, {-kPow2Error, 0.f});
   Pair logp = add(product(add({in.label(), 0.f}, {-z0, 0.f}), g.scale), negative(log_sum));
   if (logp.hi > 0.f) logp = {0.f, 0.f};  // by rounding, where the label has all of the probability
@@ -425,9 +429,9 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
 // dlogits of given dlogp and lse: a pass over the logits, from the last row to the first, since the L2 still holds some
 // of the last rows that token_logprobs read.
 constexpr int kGradChunks = 4, kGradThreads = 256;  // chunks of a thread
-// Up to here p takes on lse's rounding, 2^-14 of it at most. Beyond, lse no longer has the sum's logarithm (or is out of
-// fp32's range), and one block takes the whole row, which it sums again with the largest logit subtracted (all rows of 2048
-// x 32000 bf16 far: 138 us for 44).
+// Up to here p takes on lse's rounding, 2^-14 of it at most. Beyond, lse no longer has the sum's logarithm (or is out
+// of fp32's range), and one block takes the whole row, which it sums again with the largest logit subtracted (all rows
+// of 2048 x 32000 bf16 far: 138 us for 44).
 constexpr float kFarLse = 1024.f;
 
 // A far row, in place or not: all of it is read before any of it is written.
@@ -539,8 +543,8 @@ struct Preference {
   float *pair_loss, *rewards, *dlogp;
 };
 
-// A row's part of its sequence's score, added to v where the row is trained. Scores are held in pairs of floats: two sums
-// of thousands, of which a float's step is 2^-11, differ by little.
+// A row's part of its sequence's score, added to v where the row is trained. Scores are held in pairs of floats: two
+// sums of thousands, of which a float's step is 2^-11, differ by little.
 __device__ __forceinline__ Pair add_score(const Preference& g, Pair v, int i, bool on) {
   const float a = g.logp[i], b = g.ref ? g.ref[i] : 0.f;
   v = add(v, {on ? a : 0.f, 0.f});
@@ -568,9 +572,9 @@ __device__ __forceinline__ float pair_loss(const Preference& g, const Pair& s0, 
 // The row at which sequence j begins, or the one before it ends.
 __device__ __forceinline__ int bound_of(const Preference& g, int j) { return min(max(g.bounds[j], 0), g.T); }
 
-// Few rows of few sequences: one block does all of it, several warps a sequence. Against a block a pair and another launch
-// for the mean, with a reference and labels: 322 rows of 4 sequences 2.7 and 4.7 us, 4096 of 2 3.9 and 7.6, of 8 3.9 and
-// 4.6, of 32 3.6 and 4.5. With warps that took more sequences in turn, 64 took 5.3 and 4.5, 2048 69 and 13.
+// Few rows of few sequences: one block does all of it, several warps a sequence. Against a block a pair and another
+// launch for the mean, with a reference and labels: 322 rows of 4 sequences 2.7 and 4.7 us, 4096 of 2 3.9 and 7.6, of 8
+// 3.9 and 4.6, of 32 3.6 and 4.5. With warps that took more sequences in turn, 64 took 5.3 and 4.5, 2048 69 and 13.
 constexpr int kFewRows = 4096, kFewPairs = 16;
 __global__ void __launch_bounds__(1024) preference_few_kernel(const Preference g, float* loss) {
   __shared__ Pair score[2 * kFewPairs];

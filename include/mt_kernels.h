@@ -245,9 +245,10 @@ int mtk_cross_entropy(const void* logits, const void* labels, void* dlogits, voi
  *     loss = sum_t w l,  dlogits = w l' a ([v = label] - p),
  *     l' = -(r A, where that is the smaller or both are the same) + kl (1 - exp(ref - logp)).
  *   old_logp, advantages, ref_logp f32 [T] (ref_logp may be NULL where kl = 0); 0 <= clip_low <= 1, clip_high >= 0,
- *   kl >= 0. Where the label's logit is -inf and ref_logp is not, the KL term is +inf and the row's gradient not finite.
- *   An r beyond fp32's range counts as its largest number, and a row of weight 0 adds nothing whatever its r (NaN stays).
- *   Writes logp f32 [T], row_loss f32 [T] = w l, loss f32 [1] and dlogits (as above). The sum runs in a fixed order.
+ *   kl >= 0. Where the label's logit is -inf and ref_logp is not, the KL term is +inf and the row's gradient not
+ *   finite. An r beyond fp32's range counts as its largest number, and a row of weight 0 adds nothing whatever its r
+ *   (NaN stays). Writes logp f32 [T], row_loss f32 [T] = w l, loss f32 [1] and dlogits (as above). The sum runs in a
+ *   fixed order.
  * mtk_preference_loss: on pairs of sequences, 2i the preferred and 2i + 1 the other one. Sequence j holds the rows
  *   bounds[j] <= t < bounds[j+1] (DEVICE int32 [2 pairs + 1], not decreasing, clamped to [0, T]); its score s_j is the
  *   sum of logp - ref_logp over its rows with labels >= 0 (labels NULL: all; ref_logp NULL: 0; average != 0: their

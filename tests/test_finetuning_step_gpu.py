@@ -1,9 +1,9 @@
-"""Embedding, layer norm, the head's GEMM and the policy loss together, with ratios well away from the clip's borders: every
-row falls on the side that it falls on in float64, and the loss is compared.
+"""Embedding, layer norm, the head's GEMM and the policy loss together, with ratios well away from the clip's borders:
+every row falls on the side that it falls on in float64, and the loss is compared.
 
-Tolerances. y is rounded to bf16 (2^-8 of its size, at most) and meets W in a sum of h products, whose error has a deviation
-below sqrt(h) 2^-8 / 2 |y| |W| = D; over all T V logits the largest of them stays below 6 D, in lse as well, and logp has
-two of them: 12 D. A row's loss is A r (held: A times the border): it errs by exp(12 D) - 1 of its size.
+Tolerances. y is rounded to bf16 (2^-8 of its size, at most) and meets W in a sum of h products, whose error has a
+deviation below sqrt(h) 2^-8 / 2 |y| |W| = D; over all T V logits the largest of them stays below 6 D, in lse as well,
+and logp has two of them: 12 D. A row's loss is A r (held: A times the border): it errs by exp(12 D) - 1 of its size.
 """
 import numpy as np
 import pytest
@@ -62,8 +62,8 @@ def test_loss_of_a_step(K, kl):
     Y = K.layernorm_fwd(X, G, b)[0]
     Z = K.gemm(Y, False, W, False, T, V, h, epi=K.EPI_STORE_F32, err=err)
     loss, row, lp, _ = K.policy_loss(Z, lt, torch.tensor(old).cuda(), torch.tensor(adv).cuda(),
-                                     ref_logp=torch.tensor(ref).cuda() if kl else None, clip_low=0.2, clip_high=0.3, kl=kl,
-                                     err=err)
+                                     ref_logp=torch.tensor(ref).cuda() if kl else None, clip_low=0.2, clip_high=0.3,
+                                     kl=kl, err=err)
     K.check(err)
     assert np.all(np.abs(_np(lp) - logp)[on] <= room)
     far = np.abs(ref - logp)

@@ -1,10 +1,10 @@
-"""Layer norm where a block takes many rows in turn, several times what its ring holds, against float64: refilled slots, the
-sums that two blocks of a cluster exchange row after row, gains' sums over many rows.
+"""Layer norm where a block takes many rows in turn, several times what its ring holds, against float64: refilled
+slots, the sums that two blocks of a cluster exchange row after row, gains' sums over many rows.
 
-Tolerances. A sum over a row runs in chains of at most 32 terms a thread, 5 shuffles and 32 warps: C = 2^-17 of the sum of sizes
-bounds it. mean is within C mean|x|, n = (x - mean) rstd within C (|n| + mean|x| rstd), a bf16 result 2^-8 of its
-size. A gain's sum over T rows has chains of T / 76 rows (a block), at most 8 groups of a block, T / 76 / 16 blocks a
-warp and 16 warps: below T / 64 + 64 steps of 2^-24 of the sum of sizes.
+Tolerances. A sum over a row runs in chains of at most 32 terms a thread, 5 shuffles and 32 warps: C = 2^-17 of the
+sum of sizes bounds it. mean is within C mean|x|, n = (x - mean) rstd within C (|n| + mean|x| rstd), a bf16 result
+2^-8 of its size. A gain's sum over T rows has chains of T / 76 rows (a block), at most 8 groups of a block, T / 76 /
+16 blocks a warp and 16 warps: below T / 64 + 64 steps of 2^-24 of the sum of sizes.
 """
 import numpy as np
 import pytest

@@ -1,5 +1,5 @@
-"""The split of scale * log2(e) into two floats (csrc/log2_factor.h), compiled for the host, over all fp32 scales of an octave:
-powers of two change nothing but the exponent."""
+"""The split of scale * log2(e) into two floats (csrc/log2_factor.h), compiled for the host, over all fp32 scales of
+an octave: powers of two change nothing but the exponent."""
 import ctypes
 import os
 import shutil

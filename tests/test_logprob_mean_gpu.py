@@ -1,10 +1,11 @@
 """The mean error of the log-probabilities, which is what a sequence's sum adds up, against float64.
 
-Tolerance. Rounding a result of size 2^e to fp32 is an error of 2^(e - 23) / sqrt(12) in the root mean square, and its terms err
-by 1.5e-7 of their own, which a mean over T rows divides by sqrt(T). What does not average out is to stay below 1e-8: the
-factor's two floats (2^-34 of numbers of size 30: 2e-9), the mean error of the power as known (1e-9) and of the logarithm
-(at most 2^-25 a row, of either sign, 5e-9 in the mean). The bound is 1e-8 and 4.5 of the mean's own deviations, which is
-below 5e-8: the power's mean error left in place would pass it, and so would a factor rounded to one float (1e-7).
+Tolerance. Rounding a result of size 2^e to fp32 is an error of 2^(e - 23) / sqrt(12) in the root mean square, and its
+terms err by 1.5e-7 of their own, which a mean over T rows divides by sqrt(T). What does not average out is to stay
+below 1e-8: the factor's two floats (2^-34 of numbers of size 30: 2e-9), the mean error of the power as known (1e-9)
+and of the logarithm (at most 2^-25 a row, of either sign, 5e-9 in the mean). The bound is 1e-8 and 4.5 of the mean's
+own deviations, which is below 5e-8: the power's mean error left in place would pass it, and so would a factor rounded
+to one float (1e-7).
 """
 import numpy as np
 import pytest

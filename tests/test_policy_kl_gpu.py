@@ -1,4 +1,5 @@
-"""The policy loss's KL term at its end: a label that the policy cannot produce is infinitely far from a reference that can."""
+"""The policy loss's KL term at its end: a label that the policy cannot produce is infinitely far from a reference
+that can."""
 import pytest
 
 torch = pytest.importorskip("torch")

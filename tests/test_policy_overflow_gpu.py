@@ -1,5 +1,5 @@
-"""The policy loss where a ratio or a KL term passes the range of fp32: rows that weigh nothing or have no advantage add nothing,
-as in float64, where the exponential is finite.
+"""The policy loss where a ratio or a KL term passes the range of fp32: rows that weigh nothing or have no advantage
+add nothing, as in float64, where the exponential is finite.
 
 Tolerances as for near rows: logp is within 2^-24 (2 R + 20 + V / 128) with R <= 16 here, which exp and a few
 roundings pass on: 1e-4 of a row's size bounds it; bf16 gradients add 2^-8.

@@ -1,9 +1,9 @@
 """Preference loss of long sequences: scores of thousands whose difference decides, against float64 of the same numbers.
 
-Tolerances. Sums are held in pairs of floats, which are good to 2^-40 of the sums here, so that the difference of two scores
-is rounded once, and h = beta (s_0 - s_1) - margin takes three roundings of numbers below |h| + margin: 4 * 2^-24
-(|h| + 1). A mean divides each sum first, by a rounded reciprocal: 2 * 2^-24 of either mean. The loss (h - 1/2)^2 / beta^2
-and its derivative are smooth in h; what is computed from h takes eight roundings more.
+Tolerances. Sums are held in pairs of floats, which are good to 2^-40 of the sums here, so that the difference of two
+scores is rounded once, and h = beta (s_0 - s_1) - margin takes three roundings of numbers below |h| + margin: 4 *
+2^-24 (|h| + 1). A mean divides each sum first, by a rounded reciprocal: 2 * 2^-24 of either mean. The loss (h -
+1/2)^2 / beta^2 and its derivative are smooth in h; what is computed from h takes eight roundings more.
 """
 import numpy as np
 import pytest

@@ -1,5 +1,5 @@
-"""Inputs and outputs that lie beside each other in the rows of one buffer share no element: they are taken and give what they
-give in buffers of their own. Rows that do share elements are refused."""
+"""Inputs and outputs that lie beside each other in the rows of one buffer share no element: they are taken and give
+what they give in buffers of their own. Rows that do share elements are refused."""
 import pytest
 
 torch = pytest.importorskip("torch")

@@ -1,10 +1,11 @@
 """The gradient of the log-probabilities where a row's logits are far from 0 and its lse has lost the sum's logarithm,
 against float64 of the same logits.
 
-Tolerances. p is a ratio: its own power has a rounded factor and exponent, 2^-24 of the distance each, and the power's 2^-22;
-the sum's chain has at most V / 256 + 16 terms. Distances are from the row's largest logit where the row is far (beyond 110
-a term is below 2^-149), and from lse, itself rounded, changed in base and compared (3 * 2^-24 |lse|), where |lse| <=
-1024. Rounding to bf16 adds 2^-8, and the label's column is a difference of two numbers of size 1 (2 * 2^-24).
+Tolerances. p is a ratio: its own power has a rounded factor and exponent, 2^-24 of the distance each, and the power's
+2^-22; the sum's chain has at most V / 256 + 16 terms. Distances are from the row's largest logit where the row is far
+(beyond 110 a term is below 2^-149), and from lse, itself rounded, changed in base and compared (3 * 2^-24 |lse|),
+where |lse| <= 1024. Rounding to bf16 adds 2^-8, and the label's column is a difference of two numbers of size 1 (2 *
+2^-24).
 """
 import numpy as np
 import pytest

@@ -1,5 +1,5 @@
-"""Log-probabilities and the policy loss with -inf among the logits, at scales where the rounded scale * log2(e) has no bits
-beyond its twelfth, against float64.
+"""Log-probabilities and the policy loss with -inf among the logits, at scales where the rounded scale * log2(e) has
+no bits beyond its twelfth, against float64.
 
 Tolerances. Each term 2^(c z - max) has a rounded factor and exponent (2^-24 of |a z - lse| each, 2 R, R the largest
 |a z - lse| of the row) and the exponential's own error (2^-22); a sum of at most V / 128 + 16 terms in a chain, 2^-24
