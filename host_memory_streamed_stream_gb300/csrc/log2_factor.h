@@ -1,14 +1,8 @@
-// c = a log2 e as two floats, for powers 2^(c z). Plain C++: the device and the host compute the same.
+// c = a log2 e as two floats, for powers 2^(c z). Computed on the host, once a call.
 #pragma once
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-
-#ifdef __CUDACC__
-#define MT_HOST_DEVICE __host__ __device__ __forceinline__
-#else
-#define MT_HOST_DEVICE inline
-#endif
 
 namespace mt {
 
@@ -22,7 +16,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.4426950408889634 - s
 struct Factor {
   float one, hi, lo;
 };
-MT_HOST_DEVICE Factor factor(float scale) {
+inline Factor factor(float scale) {
   const float one = scale * kLog2e;
   uint32_t bits;
   std::memcpy(&bits, &one, sizeof(bits));

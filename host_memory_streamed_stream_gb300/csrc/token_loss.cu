@@ -13,7 +13,7 @@
 //
 // Bound by HBM. Log-probabilities: 6000 rows of 32000 fp32 114 us, 6.7 TB/s, 3000 of 152064 bf16 135 us, 6.8 TB/s
 // (where the exponential unit is 70 % busy). Policy loss, whose second look at a row reads the L2: 198 us, 5.8 TB/s,
-// and 343 us, 5.3 TB/s; rows of 3000 to 10000 columns 1.5 to 1.6 times their bytes' time (8192 x 5268 fp32 58 us of
+// and 341 us, 5.3 TB/s; rows of 3000 to 10000 columns 1.4 to 1.6 times their bytes' time (8192 x 5268 fp32 56 us of
 // 39), as a small block waits for its loads and at its barrier between two looks. Gradient alone: 4048 rows of 152064
 // bf16, a quarter of them masked, 313 us, 6.9 TB/s with what the L2 still holds. What did not help the policy loss: a
 // ring of shared memory that holds the row, filled by cp.async (1.8 times as long), bulk prefetches of the next row
@@ -130,6 +130,8 @@ struct TokenRows {
   const int32_t* labels;
   int T, V;
   float scale;
+  Factor c;     // of scale
+  float per_c;  // 1 / c
   float* logp;
   float* lse;  // token_logprobs
   // policy loss
@@ -164,6 +166,12 @@ __device__ __forceinline__ RowInputs<Z> row_inputs(const TokenRows& g, int64_t t
 struct RowGrad {
   float z0, m, k, kp;
 };
+// Of sums of 2^(c (z - z0) - m). The second look has c in one float, whose error times z would scale all of p (6e-4 at
+// logits of 40000): it subtracts about m / c from z first, and then what is left of m.
+__device__ __forceinline__ RowGrad row_grad(const TokenRows& g, float z0, float m, float k, float kp) {
+  const float near = m * g.per_c;  // 0 where z0 is not
+  return {z0 + near, fmaf(-g.c.lo, near, fmaf(-g.c.hi, near, m)), k, kp};
+}
 // The row's log-probability, and for the policy loss its loss and d loss / d logp, from the sum r of
 // 2^(c (z - z0) - m). `write`: of several callers, one.
 template <bool POLICY, class Z>
@@ -197,7 +205,7 @@ __device__ __forceinline__ RowGrad finish_row(const TokenRows& g, int64_t t, con
     if (in.weight == 0.f && loss == loss) loss = d = 0.f;  // where exp has passed fp32's range too
     if (write) g.row_loss[t] = in.weight * loss;
     const float k = in.weight * d * g.scale;
-    return {z0, r.m == -INFINITY ? 0.f : r.m, k, -k / r.s};
+    return row_grad(g, z0, r.m, k, -k / r.s);
   }
 }
 
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
     const int col = (j * 32 + lane) * N;
     if (col + N <= g.V) raw[j] = *reinterpret_cast<const uint4*>(z + col);
   }
-  const Factor c = factor(g.scale);
+  const Factor c = g.c;
   MaxSum r{-INFINITY, 0.f};
   float v[N];
 #pragma unroll
@@ -306,10 +314,7 @@ __global__ void __launch_bounds__(128) token_warp_kernel(const TokenRows g) {
   RowGrad q{};
   if (lane == 0) q = finish_row<POLICY>(g, t, in, z0, r, true);
   if constexpr (POLICY) {
-    q.z0 = z0;
-    q.m = __shfl_sync(0xffffffffu, q.m, 0);
-    q.k = __shfl_sync(0xffffffffu, q.k, 0);
-    q.kp = __shfl_sync(0xffffffffu, q.kp, 0);
+    q = row_grad(g, z0, r.m, __shfl_sync(0xffffffffu, q.k, 0), __shfl_sync(0xffffffffu, q.kp, 0));
 #pragma unroll
     for (int j = 0; j < kWarpChunks; ++j) {
       const int col = (j * 32 + lane) * N;
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(NT, 2048 / NT) token_rows_kernel(const TokenRo
   const Z* z = static_cast<const Z*>(g.logits) + t * g.ld + c0;
   RowInputs<Z> in{};
   if (threadIdx.x == 0) in = row_inputs<Z, POLICY>(g, t, label);
-  const Factor c = factor(g.scale);
+  const Factor c = g.c;
   MaxSum r{-INFINITY, 0.f};
   int i = threadIdx.x * N;
   for (; i + NT * N < whole; i += 2 * NT * N) {
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(kGradThreads) token_grad_kernel(const TokenRow
     if (first + j * STEP < whole) raw[j] = __ldcs(reinterpret_cast<const uint4*>(z + first + j * STEP));
   const float k = dlogp[t] * g.scale;
   const RowGrad q{lse / g.scale, 0.f, k, -k};
-  const Factor c = factor(g.scale);
+  const Factor c = g.c;
 #pragma unroll
   for (int j = 0; j < kGradChunks; ++j) {
     const int i = first + j * STEP;
@@ -677,6 +682,11 @@ __global__ void __launch_bounds__(512) preference_kernel(const Preference g) {
   }
 }
 
+void set_scale(TokenRows& g, float scale) {
+  g.scale = scale;
+  g.c = factor(scale);
+  g.per_c = 1.f / g.c.one;
+}
 bool rows_args_ok(const TokenRows& g, int type) {
   return row_type_ok(type) && g.T > 0 && g.T <= kMaxRows && g.V > 0 && g.V <= kMaxVocab &&
          rows_ok(g.logits, g.ld, g.V) && vec_ok(g.labels, 4) && g.scale >= kMinScale && g.scale <= 1.f / kMinScale &&
@@ -725,7 +735,8 @@ cudaError_t launch_rows(const TokenRows& g, cudaStream_t s) {
 cudaError_t token_logprobs(const void* logits, int type, int64_t ld, const int32_t* labels, float* logp, float* lse,
                            int T, int V, float scale, int* err, cudaStream_t s) {
   TokenRows g{};
-  g.logits = logits, g.ld = ld, g.labels = labels, g.T = T, g.V = V, g.scale = scale, g.logp = logp, g.lse = lse;
+  g.logits = logits, g.ld = ld, g.labels = labels, g.T = T, g.V = V, g.logp = logp, g.lse = lse;
+  set_scale(g, scale);
   g.err = err;
   if (!rows_args_ok(g, type) || !vec_ok(logp, 4) || !vec_ok(lse, 4)) return cudaErrorInvalidValue;
   return type == kRowF32 ? launch_rows<float, false>(g, s) : launch_rows<bf16, false>(g, s);
@@ -735,7 +746,8 @@ cudaError_t token_logprobs_bwd(const void* logits, int type, int64_t ld, const i
                                const float* dlogp, bf16* dlogits, int64_t ldd, int T, int V, float scale,
                                cudaStream_t s) {
   TokenRows g{};
-  g.logits = logits, g.ld = ld, g.labels = labels, g.T = T, g.V = V, g.scale = scale;
+  g.logits = logits, g.ld = ld, g.labels = labels, g.T = T, g.V = V;
+  set_scale(g, scale);
   g.lse = const_cast<float*>(lse), g.dlogits = dlogits, g.ldd = ldd;
   if (!rows_args_ok(g, type) || !vec_ok(lse, 4) || !vec_ok(dlogp, 4) || !grad_ok(g, type)) return cudaErrorInvalidValue;
   auto* k = type == kRowF32 ? token_grad_kernel<float> : token_grad_kernel<bf16>;
@@ -758,8 +770,12 @@ cudaError_t policy_loss(const void* logits, int type, int64_t ld, const int32_t*
                         const float* adv, const float* ref, const float* weights, float clip_low, float clip_high,
                         float kl, float scale, bf16* dlogits, int64_t ldd, float* logp, float* row_loss, float* loss,
                         int T, int V, int* err, cudaStream_t s) {
-  const TokenRows g{logits, ld, labels, T, V, scale, logp, nullptr, old_logp, adv, ref, weights, clip_low, clip_high,
-                    kl, dlogits, ldd, row_loss, err};
+  TokenRows g{};
+  g.logits = logits, g.ld = ld, g.labels = labels, g.T = T, g.V = V, g.logp = logp, g.err = err;
+  g.old_logp = old_logp, g.adv = adv, g.ref = ref, g.weights = weights;
+  g.clip_low = clip_low, g.clip_high = clip_high, g.kl = kl;
+  g.dlogits = dlogits, g.ldd = ldd, g.row_loss = row_loss;
+  set_scale(g, scale);
   if (!rows_args_ok(g, type) || !vec_ok(old_logp, 4) || !vec_ok(adv, 4) || !vec_ok(logp, 4) || !vec_ok(row_loss, 4) ||
       !vec_ok(loss, 4) || (weights && !vec_ok(weights, 4)) || (ref && !vec_ok(ref, 4)) || !grad_ok(g, type))
     return cudaErrorInvalidValue;
