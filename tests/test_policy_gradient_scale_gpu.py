@@ -42,3 +42,21 @@ def test_common_factor(K, V, scale, offset):
     rel[np.arange(T), lab] = 0.0
     assert np.abs(rel).max() <= 2.0 ** -8 + 2.0 ** -13
     assert abs(rel.sum() / (T * (V - 1))) <= 2.0 ** -13 + 6 * 2.0 ** -8 / np.sqrt(3.0 * T * V)
+
+
+@pytest.mark.parametrize("T,V", [(9, 1000), (300, 9000), (5, 60000), (3, 200000)])
+def test_far_rows_in_place(K, T, V):
+    """Rows that are summed again, beside near and masked ones: the gradient over bf16 logits is the one beside them."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn(T, V, device="cuda", generator=g) * 3
+    z[::2] = z[::2] * 2000 + 2.0e5
+    z = z.to(torch.bfloat16)
+    lab = torch.randint(0, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    lab[T // 2] = -1
+    adv = torch.randn(T, device="cuda", generator=g)
+    # advantages below 0 at a ratio of 1: no row is clipped
+    old = K.token_logprobs(z, lab)[0]
+    want = K.policy_loss(z, lab, old, -adv.abs())
+    assert bool(torch.isfinite(want[3].float()).all()) and bool((want[3] != 0).any())
+    got = K.policy_loss(z, lab, old, -adv.abs(), out=z)
+    assert got[3] is z and all(torch.equal(a, b) for a, b in zip(want, got))
